@@ -28,6 +28,10 @@ DEV_BAD_PAGE = 0x10
 
 PAGE_TOKENS = 128
 
+KV8_BLOCK = 64
+KV8_INT8 = 0
+KV8_E4M3 = 1
+
 # grok_status values (include/grok_attn.h)
 OK = 0
 ERR_INVALID_ARG = 1
@@ -73,6 +77,10 @@ EXPORTS = (
     "grok_kv_insert_slot",
     "grok_attn_decode_step_workspace",
     "grok_attn_decode_step",
+    "grok_kv8_append",
+    "grok_kv8_decode_workspace",
+    "grok_kv8_decode",
+    "grok_kv8_evict",
 )
 
 _lib: Optional[ctypes.CDLL] = None
@@ -163,6 +171,14 @@ def load() -> ctypes.CDLL:
     lib.grok_attn_decode_step_workspace.argtypes = [I, I, ctypes.POINTER(S)]
     lib.grok_attn_decode_step.restype = I
     lib.grok_attn_decode_step.argtypes = [P, P, P, P, I, I, P, P, P, S, P, P, P]
+    lib.grok_kv8_append.restype = I
+    lib.grok_kv8_append.argtypes = [P, P, P, P, P, P, P, I, P, P, I, P, P, P]
+    lib.grok_kv8_decode_workspace.restype = I
+    lib.grok_kv8_decode_workspace.argtypes = [I, I, I, ctypes.POINTER(S)]
+    lib.grok_kv8_decode.restype = I
+    lib.grok_kv8_decode.argtypes = [P, P, P, P, S, P, P, P, P, P]
+    lib.grok_kv8_evict.restype = I
+    lib.grok_kv8_evict.argtypes = [P, P, P, I, I, I, I, I, P, P, P, P, P]
     _lib = lib
     return lib
 
@@ -673,3 +689,7 @@ def decode_step_chained(q, k, v, start_pos, cache_k, cache_v, workspace, out, de
     _check(load().grok_attn_decode_step(_ptr(q), _ptr(k), _ptr(v), _ptr(start_pos), B, Tmax, _ptr(cache_k),
                                         _ptr(cache_v), _ptr(workspace), nbytes, _ptr(out), _ptr(dev_status),
                                         _stream(stream)))
+
+
+from .kv8 import (Kv8Cache, alloc_kv8_cache, alloc_kv8_decode_workspace, kv8_append, kv8_decode,  # noqa: E402,F401
+                  kv8_decode_workspace, kv8_evict)

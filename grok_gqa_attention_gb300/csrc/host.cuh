@@ -51,4 +51,7 @@ bool small_int8_ok(int M, int K, int N);
 grok_status linear_int8_small(const grok_bf16* x, const int8_t* w8, const float* scales, int M, int K, int N,
                               grok_bf16* y, int32_t* dev_status, void* stream);
 
+// Checks of an 8-bit cache's description (kv8_append.cu).
+grok_status kv8_check(const grok_kv8_cache* c, const char* who);
+
 }  // namespace grok

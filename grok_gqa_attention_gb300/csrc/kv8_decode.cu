@@ -1,0 +1,503 @@
+// Single-token attention over the 8-bit KV cache, and the blocks' weights.
+//
+// Code-reading guide ch. 4 §4.4.1, §4.5.2-§4.5.4 (decode over the cache, GQA
+// logits, cap, softmax, weighted sum), over codes with a scale per 64-token
+// block and KV head:
+//   x_j = (q . kcode_j) ks / sqrt(128),  z_j = log2(e) (30 tanh(x_j / 30) - 30),
+//   out = sum_j 2^(z_j - m) vs vcode_j / sum_j 2^(z_j - m).
+//
+// Memory-bound: 16 KB of codes per block of 64 tokens and KV head are read once.
+// Every warp is a worker of its own: the blocks of all (sequence, head) pairs, in
+// order, are dealt out in equal contiguous shares, so the load is even for any
+// lengths and no barrier joins warps. A worker streams its blocks through a
+// private K and a private V buffer in shared memory (one bulk copy each), and
+// writes one partial result (m, l, O) per pair that it touches; a second kernel,
+// launched as a dependent, joins a pair's partials.
+//
+// Per block, on fp16 tensor-core products (codes convert to fp16 exactly, q is
+// scaled to fp16 by a power of two per head):
+//   S^T [64 keys x 8 heads] = K q^T   (4 tiles of 16 keys; 6 of the 8 columns used)
+//   O^T [128 x 8] += V^T P^T          (8 tiles of 16 features)
+// The transposed form wastes 2 of 8 columns where rows of heads would waste 10 of
+// 16. S^T leaves the accumulators as P^T needs it but for one 8 x 8 transpose per
+// register (movmatrix). K rows and V columns are both contiguous bytes in a
+// block, so a thread reads operands as 16-byte words and the order of the
+// contracted index is chosen to fit them: thread t of a row's four holds
+// features (keys) 16 t .. 16 t + 15.
+// P is rounded once to fp16 (2^-12 relative) against a running reference that may
+// lag the maximum by 2^8; l, the weights and O stay in fp32.
+#include "host.cuh"
+#include "kv8.cuh"
+
+namespace grok {
+
+constexpr int kDqWarps = 14;
+constexpr int kDqThreads = kDqWarps * 32;
+constexpr int kDqBuf = 2 * kKv8Bytes;  // a warp's K and V buffers
+constexpr int kDqSmem = kDqWarps * kDqBuf + kDqWarps * 2 * 8 + 16;
+constexpr float kDqLag = 8.f;  // log2 units a weight may exceed the reference by
+
+struct DqParams {
+  grok_kv8_cache c;
+  const uint4* q;
+  const int32_t* kv_len;
+  float* part_o;    // [slot][6][128]
+  float2* part_ml;  // [slot][6]: reference (log2), sum
+  float* block_w;   // [B * 8][max_blocks][8]: a block's weights per head on the fixed reference 30
+  uint2* out;
+  const float* weight_in;
+  float* weight_out;
+  int workers;
+  int32_t* status;
+};
+
+// The sequences' blocks: total over the batch of ceil(kv_len / 64), by one warp.
+__device__ __forceinline__ int count_blocks(const DqParams& p, int lane) {
+  int total = 0;
+  for (int c = 0; c < p.c.B; c += 32)
+    total += __reduce_add_sync(0xffffffffu, c + lane < p.c.B ? kv8_blocks(__ldg(p.kv_len + c + lane), p.c.max_blocks) : 0);
+  return total;
+}
+
+template <int kKind, bool kWeights>
+__global__ void __launch_bounds__(kDqThreads, 1) kv8_decode_kernel(const DqParams p) {
+  extern __shared__ __align__(128) uint8_t smem[];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int row = lane >> 2, t = lane & 3;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kDqWarps * kDqBuf);
+  int* abort_flag = reinterpret_cast<int*>(bars + 2 * kDqWarps);
+  volatile int* abort = abort_flag;
+  uint64_t *k_bar = bars + 2 * warp, *v_bar = k_bar + 1;
+  uint8_t *k_buf = smem + warp * kDqBuf, *v_buf = k_buf + kKv8Bytes;
+  if (lane == 0) {
+    mbar_init(k_bar, 1);
+    mbar_init(v_bar, 1);
+    if (warp == 0) *abort_flag = 0;
+    fence_barrier_init();
+  }
+  __syncthreads();
+
+  const int n_total = kKVHeads * count_blocks(p, lane);
+  const int share = (n_total + p.workers - 1) / p.workers;
+  const int worker = warp * gridDim.x + blockIdx.x;  // few blocks spread over the SMs first
+  if (blockIdx.x == 0 && warp == 0)
+    for (int b = lane; b < p.c.B; b += 32)
+      if (kv8_blocks(__ldg(p.kv_len + b), p.c.max_blocks) == 0) report(p.status, GROK_DEV_BAD_KV_LEN);
+  const long long lo_ = (long long)worker * share;
+  if (lo_ >= n_total) return;
+  const int lo = int(lo_), hi = min(lo + share, n_total);
+
+  uint32_t qb[8][2];
+  float q_scale0 = 0.f, q_scale1 = 0.f;  // of heads 2 t, 2 t + 1
+  float o[8][4], m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
+  int pair = -1;
+  uint32_t phase = 0;                    // of both buffers, at the top of a block
+  uint32_t k_phase = 0;                  // of the K copy that is due
+  bool k_due = false, v_due = false;     // a copy was issued and not yet waited for
+  bool ok = true;
+
+  // One partial result: this worker's share of a pair.
+  auto flush = [&]() {
+#pragma unroll
+    for (int d = 4; d < 32; d *= 2) {
+      l0 += __shfl_xor_sync(0xffffffffu, l0, d);
+      l1 += __shfl_xor_sync(0xffffffffu, l1, d);
+    }
+    if (t < kGroup / 2) {
+      const size_t slot = (size_t)worker + pair;
+      float* po = p.part_o + (slot * kGroup + 2 * t) * kD + row;
+#pragma unroll
+      for (int mt = 0; mt < 8; ++mt) {
+        po[16 * mt] = o[mt][0];
+        po[16 * mt + kD] = o[mt][1];
+        po[16 * mt + 8] = o[mt][2];
+        po[16 * mt + 8 + kD] = o[mt][3];
+      }
+      if (row == 0) {
+        p.part_ml[slot * kGroup + 2 * t] = make_float2(m0, l0);
+        p.part_ml[slot * kGroup + 2 * t + 1] = make_float2(m1, l1);
+      }
+    }
+  };
+
+  for (int base = lo; base < hi && ok; base += 32) {
+    const int cnt = min(32, hi - base);
+    // Each lane finds one block of the batch: its pair, number, scales and visible keys.
+    int my_pair = 0, my_blk = 0, my_keys = 0;
+    {
+      const int idx = base + lane;
+      bool found = lane >= cnt;
+      int cum = 0;
+      for (int c = 0; c < p.c.B; c += 32) {
+        const int len = c + lane < p.c.B ? __ldg(p.kv_len + c + lane) : 0;
+        const int n = kv8_blocks(len, p.c.max_blocks);
+        int incl = n;
+#pragma unroll
+        for (int d = 1; d < 32; d *= 2) {
+          const int up = __shfl_up_sync(0xffffffffu, incl, d);
+          if (lane >= d) incl += up;
+        }
+        const int rest = idx - kKVHeads * cum;
+        int s = 0;  // the sequence of this chunk that holds block `rest`
+#pragma unroll
+        for (int step = 16; step; step /= 2)
+          if (kKVHeads * __shfl_sync(0xffffffffu, incl, s + step - 1) <= rest) s += step;
+        s = min(s, 31);
+        const int sn = __shfl_sync(0xffffffffu, n, s), si = __shfl_sync(0xffffffffu, incl, s);
+        const int sl = __shfl_sync(0xffffffffu, len, s);
+        const int chunk = __shfl_sync(0xffffffffu, incl, 31);
+        if (!found && rest < kKVHeads * chunk) {
+          const int in = rest - kKVHeads * (si - sn);
+          my_pair = (c + s) * kKVHeads + in / sn;
+          my_blk = in % sn;
+          my_keys = min(kKv8Block, sl - my_blk * kKv8Block);
+          found = true;
+        }
+        cum += chunk;
+        if (__all_sync(0xffffffffu, found)) break;
+      }
+    }
+    int my_id = 0;
+    float my_ks = 0.f, my_vs = 0.f;
+    if (lane < cnt) {
+      my_id = max(0, kv8_block_id(p.c.table, (size_t)my_pair * p.c.max_blocks + my_blk, p.c.n_blocks, p.status));
+      my_ks = __ldg(p.c.k_scale + my_id);
+      my_vs = __ldg(p.c.v_scale + my_id);
+    }
+    auto load = [&](int j, bool v) {
+      (v ? v_due : k_due) = true;
+      const int id = __shfl_sync(0xffffffffu, my_id, j);
+      if (lane == 0) {
+        uint64_t* bar = v ? v_bar : k_bar;
+        mbar_arrive_expect_tx(bar, kKv8Bytes);
+        bulk_load(v ? v_buf : k_buf, static_cast<const uint8_t*>(v ? p.c.v_pool : p.c.k_pool) + (size_t)id * kKv8Bytes,
+                  kKv8Bytes, bar);
+      }
+    };
+    load(0, false);
+    load(0, true);
+    for (int j = 0; j < cnt; ++j) {
+      const int jp = __shfl_sync(0xffffffffu, my_pair, j);
+      if (jp != pair) {  // the next pair: its partial starts empty, its six queries come in
+        if (pair >= 0) flush();
+        pair = jp;
+        m0 = m1 = -INFINITY;
+        l0 = l1 = 0.f;
+#pragma unroll
+        for (int mt = 0; mt < 8; ++mt) o[mt][0] = o[mt][1] = o[mt][2] = o[mt][3] = 0.f;
+        uint4 x[4];
+        uint32_t top = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          x[i] = make_uint4(0, 0, 0, 0);
+          if (row < kGroup) x[i] = __ldg(p.q + ((size_t)pair * kGroup + row) * 16 + (i >> 1) * 8 + 2 * t + (i & 1));
+          top = __vmaxu2(top, __vmaxu2(__vmaxu2(x[i].x & 0x7FFF7FFFu, x[i].y & 0x7FFF7FFFu),
+                                       __vmaxu2(x[i].z & 0x7FFF7FFFu, x[i].w & 0x7FFF7FFFu)));
+        }
+        top = max(top & 0xFFFFu, top >> 16);
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        // q / 2^e with the largest element in [1, 2): what falls below fp16's normal range is off by 2^-25 at most
+        const uint32_t e = min(max(top >> 7, 1u), 253u);
+        const float down = __uint_as_float((254u - e) << 23), up = __uint_as_float(e << 23);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const int u = (i >> 1) * 4 + (i & 1) * 2 + (c >> 1);  // product of the 16 features 64 (i >> 1) + 16 t + ..
+            qb[u][c & 1] = pack_f16x2(bf16lo_to_f32(w[c]) * down, bf16hi_to_f32(w[c]) * down);
+          }
+        }
+        q_scale0 = __shfl_sync(0xffffffffu, up, 8 * t) * (2.f * kY * kLog2e);
+        q_scale1 = __shfl_sync(0xffffffffu, up, 8 * t + 4) * (2.f * kY * kLog2e);
+      }
+      const float ks = __shfl_sync(0xffffffffu, my_ks, j), vs = __shfl_sync(0xffffffffu, my_vs, j);
+      const int keys = __shfl_sync(0xffffffffu, my_keys, j), blk = __shfl_sync(0xffffffffu, my_blk, j);
+
+      ok = __all_sync(0xffffffffu, mbar_wait(k_bar, phase, abort, p.status));
+      if (!ok) break;
+      k_due = false;
+      float s[4][4];
+#pragma unroll
+      for (int st = 0; st < 4; ++st) {
+        s[st][0] = s[st][1] = s[st][2] = s[st][3] = 0.f;
+        // row r of the tile is key 16 (r >> 1) + 4 st + (r & 1), row r + 8 two keys on: the order P^T is read in below
+        const uint8_t* k0 = k_buf + (16 * (row >> 1) + 4 * st + (row & 1)) * 64 + 16 * t;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint4 a = *reinterpret_cast<const uint4*>(k0 + h * (kKv8Bytes / 2));
+          const uint4 b = *reinterpret_cast<const uint4*>(k0 + h * (kKv8Bytes / 2) + 128);
+          const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            uint32_t a0, a1, a2, a3;
+            kv8_to_half<kKind>(aw[w], a0, a2);
+            kv8_to_half<kKind>(bw[w], a1, a3);
+            mma_f16_16816(s[st], a0, a1, a2, a3, qb[4 * h + w][0], qb[4 * h + w][1]);
+          }
+        }
+      }
+      __syncwarp();
+      k_phase = phase ^ 1;
+      if (j + 1 < cnt) load(j + 1, false);
+
+      // z = log2 of the weight against the fixed reference 30: -2 kT / (1 + e^(2 x / 30))
+      const float f0 = ks * q_scale0, f1 = ks * q_scale1;
+      float top0 = -INFINITY, top1 = -INFINITY;
+#pragma unroll
+      for (int st = 0; st < 4; ++st)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          float z = (-2.f * kT) * rcp_approx(1.f + ex2_approx(s[st][e] * (e & 1 ? f1 : f0)));
+          if (keys < kKv8Block && 16 * (row >> 1) + 4 * st + (row & 1) + (e & 2) >= keys) z = -INFINITY;
+          s[st][e] = z;
+          if (e & 1) top1 = fmaxf(top1, z); else top0 = fmaxf(top0, z);
+        }
+#pragma unroll
+      for (int d = 4; d < 32; d *= 2) {
+        top0 = fmaxf(top0, __shfl_xor_sync(0xffffffffu, top0, d));
+        top1 = fmaxf(top1, __shfl_xor_sync(0xffffffffu, top1, d));
+      }
+      if (__any_sync(0xffffffffu, top0 > m0 + kDqLag || top1 > m1 + kDqLag)) {
+        const float n0 = fmaxf(m0, top0), n1 = fmaxf(m1, top1);
+        const float c0 = m0 == -INFINITY ? 0.f : ex2_approx(m0 - n0), c1 = m1 == -INFINITY ? 0.f : ex2_approx(m1 - n1);
+        m0 = n0, m1 = n1;
+        l0 *= c0, l1 *= c1;
+#pragma unroll
+        for (int mt = 0; mt < 8; ++mt) o[mt][0] *= c0, o[mt][1] *= c1, o[mt][2] *= c0, o[mt][3] *= c1;
+      }
+      uint32_t pb[4][2];
+      float b0 = 0.f, b1 = 0.f;
+#pragma unroll
+      for (int st = 0; st < 4; ++st) {
+        const float p0 = ex2_approx(s[st][0] - m0), p1 = ex2_approx(s[st][1] - m1);
+        const float p2 = ex2_approx(s[st][2] - m0), p3 = ex2_approx(s[st][3] - m1);
+        b0 += p0 + p2, b1 += p1 + p3;
+        pb[st][0] = movmatrix_trans(pack_f16x2(p0, p1));
+        pb[st][1] = movmatrix_trans(pack_f16x2(p2, p3));
+      }
+      l0 += b0, l1 += b1;
+      if (kWeights) {
+#pragma unroll
+        for (int d = 4; d < 32; d *= 2) {
+          b0 += __shfl_xor_sync(0xffffffffu, b0, d);
+          b1 += __shfl_xor_sync(0xffffffffu, b1, d);
+        }
+        if (row == 0 && t < kGroup / 2)
+          *reinterpret_cast<float2*>(p.block_w + ((size_t)pair * p.c.max_blocks + blk) * 8 + 2 * t) =
+              make_float2(b0 * ex2_approx(m0), b1 * ex2_approx(m1));
+      }
+
+      ok = __all_sync(0xffffffffu, mbar_wait(v_bar, phase, abort, p.status));
+      if (!ok) break;
+      v_due = false;
+      k_phase = phase ^= 1;
+#pragma unroll
+      for (int mt = 0; mt < 8; ++mt) {
+        const uint4 a = *reinterpret_cast<const uint4*>(v_buf + (16 * mt + row) * 64 + 16 * t);
+        const uint4 b = *reinterpret_cast<const uint4*>(v_buf + (16 * mt + row + 8) * 64 + 16 * t);
+        uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w};
+        if (keys < kKv8Block) {  // codes behind the last row may be anything, NaN among them
+#pragma unroll
+          for (int st = 0; st < 4; ++st) {
+            const int left = keys - (16 * t + 4 * st);
+            const uint32_t mask = left >= 4 ? 0xFFFFFFFFu : left <= 0 ? 0u : (1u << (8 * left)) - 1u;
+            aw[st] &= mask;
+            bw[st] &= mask;
+          }
+        }
+        float acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int st = 0; st < 4; ++st) {
+          uint32_t a0, a1, a2, a3;
+          kv8_to_half<kKind>(aw[st], a0, a2);
+          kv8_to_half<kKind>(bw[st], a1, a3);
+          mma_f16_16816(acc, a0, a1, a2, a3, pb[st][0], pb[st][1]);
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[mt][e] = fmaf(acc[e], vs, o[mt][e]);
+      }
+      __syncwarp();
+      if (j + 1 < cnt) load(j + 1, true);
+    }
+  }
+  if (ok) {
+    flush();
+    return;
+  }
+  // A wait gave up: copies in flight land before the shared memory is released.
+  volatile int never = 0;
+  if (k_due) mbar_wait(k_bar, k_phase, &never, p.status);
+  if (v_due) mbar_wait(v_bar, phase, &never, p.status);
+}
+
+// Joins a pair's partials: CTA (pair, head) the output, CTA (pair, 6) the blocks' weights.
+constexpr int kDqJoinWarps = 4;
+
+__global__ void __launch_bounds__(kDqJoinWarps * 32) kv8_join_kernel(const DqParams p) {
+  __shared__ float4 s_o[kDqJoinWarps][32];
+  __shared__ float s_m[kDqJoinWarps], s_l[kDqJoinWarps], s_inv[8];
+  const int pair = blockIdx.x, head = blockIdx.y, b = pair / kKVHeads;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int blocks = kv8_blocks(__ldg(p.kv_len + b), p.c.max_blocks);
+  // where the pair's blocks lie in the order they were dealt out
+  int before = 0, total = 0;
+  for (int c = 0; c < p.c.B; c += 32) {
+    const int n = c + lane < p.c.B ? kv8_blocks(__ldg(p.kv_len + c + lane), p.c.max_blocks) : 0;
+    total += __reduce_add_sync(0xffffffffu, n);
+    before += __reduce_add_sync(0xffffffffu, c + lane < b ? n : 0);
+  }
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (blocks == 0) return;  // reported by the first kernel
+  const int share = (kKVHeads * total + p.workers - 1) / p.workers;
+  const int first = kKVHeads * before + (pair % kKVHeads) * blocks;
+  const int w0 = first / share, n_parts = (first + blocks - 1) / share - w0 + 1;
+  const size_t slot0 = (size_t)w0 + pair;
+
+  if (head < kGroup) {
+    float m = -INFINITY;
+    for (int k = threadIdx.x; k < n_parts; k += kDqJoinWarps * 32) m = fmaxf(m, p.part_ml[(slot0 + k) * kGroup + head].x);
+#pragma unroll
+    for (int d = 16; d; d /= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+    if (lane == 0) s_m[warp] = m;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kDqJoinWarps; ++w) m = fmaxf(m, s_m[w]);
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    float l = 0.f;
+#pragma unroll 4
+    for (int k = warp; k < n_parts; k += kDqJoinWarps) {
+      const float2 ml = p.part_ml[(slot0 + k) * kGroup + head];
+      const float4 v = *reinterpret_cast<const float4*>(p.part_o + ((slot0 + k) * kGroup + head) * kD + 4 * lane);
+      const float f = ex2_approx(ml.x - m);
+      l = fmaf(ml.y, f, l);
+      acc.x = fmaf(v.x, f, acc.x);
+      acc.y = fmaf(v.y, f, acc.y);
+      acc.z = fmaf(v.z, f, acc.z);
+      acc.w = fmaf(v.w, f, acc.w);
+    }
+    s_o[warp][lane] = acc;
+    if (lane == 0) s_l[warp] = l;
+    __syncthreads();
+    if (warp == 0) {
+#pragma unroll
+      for (int w = 1; w < kDqJoinWarps; ++w) {
+        const float4 v = s_o[w][lane];
+        acc.x += v.x, acc.y += v.y, acc.z += v.z, acc.w += v.w;
+        l += s_l[w];
+      }
+      const float inv = 1.f / l;
+      p.out[((size_t)pair * kGroup + head) * (kD / 4) + lane] =
+          make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+    }
+    return;
+  }
+  // The heads' sums on the fixed reference 30, then every block's share.
+  for (int h = warp; h < kGroup; h += kDqJoinWarps) {
+    float l = 0.f;
+    for (int k = lane; k < n_parts; k += 32) {
+      const float2 ml = p.part_ml[(slot0 + k) * kGroup + h];
+      l = fmaf(ml.y, ex2_approx(ml.x), l);
+    }
+#pragma unroll
+    for (int d = 16; d; d /= 2) l += __shfl_xor_sync(0xffffffffu, l, d);
+    if (lane == 0) s_inv[h] = 1.f / l;
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < p.c.max_blocks; i += kDqJoinWarps * 32) {
+    const size_t at = (size_t)pair * p.c.max_blocks + i;
+    float w = 0.f;
+    if (i < blocks) {
+      const float4 a = *reinterpret_cast<const float4*>(p.block_w + at * 8);
+      const float2 c = *reinterpret_cast<const float2*>(p.block_w + at * 8 + 4);
+      w = a.x * s_inv[0] + a.y * s_inv[1] + a.z * s_inv[2] + a.w * s_inv[3] + c.x * s_inv[4] + c.y * s_inv[5];
+    }
+    p.weight_out[at] = p.weight_in ? p.weight_in[at] + w : w;
+  }
+}
+
+}  // namespace grok
+
+using namespace grok;
+
+namespace {
+
+size_t up256(size_t n) { return (n + 255) & ~size_t(255); }
+// A worker's share touches a run of pairs, so (worker, pair) runs through fewer than workers + pairs values of their sum.
+size_t part_slots(int B, int sms) { return size_t(sms) * kDqWarps + size_t(B) * kKVHeads; }
+size_t part_o_bytes(int B, int sms) { return part_slots(B, sms) * kGroup * kD * sizeof(float); }
+size_t part_ml_bytes(int B, int sms) { return up256(part_slots(B, sms) * kGroup * sizeof(float2)); }
+size_t block_w_bytes(int B, int max_blocks) { return size_t(B) * kKVHeads * max_blocks * 8 * sizeof(float); }
+
+}  // namespace
+
+extern "C" grok_status grok_kv8_decode_workspace(int B, int max_blocks, int weights, size_t* bytes) {
+  if (!bytes) return fail(GROK_ERR_INVALID_ARG, "grok_kv8_decode_workspace: null pointer");
+  if (B < 1 || B > 65535 || max_blocks < 1 || max_blocks > kKv8MaxBlocks)
+    return fail(GROK_ERR_INVALID_ARG, "grok_kv8_decode_workspace: need 1 <= B <= 65535, 1 <= max_blocks <= %d",
+                kKv8MaxBlocks);
+  int sms = 0;
+  grok_status st = device_sm_count(&sms);
+  if (st != GROK_OK) return st;
+  *bytes = part_o_bytes(B, sms) + part_ml_bytes(B, sms) + (weights ? block_w_bytes(B, max_blocks) : 0);
+  return GROK_OK;
+}
+
+extern "C" grok_status grok_kv8_decode(const grok_kv8_cache* cache, const grok_bf16* q_rot, const int32_t* kv_len,
+                                       void* workspace, size_t workspace_bytes, grok_bf16* out,
+                                       const float* weight_in, float* weight_out, int32_t* dev_status, void* stream) {
+  grok_status st = kv8_check(cache, "grok_kv8_decode");
+  if (st != GROK_OK) return st;
+  if (!q_rot || !kv_len || !workspace || !out) return fail(GROK_ERR_INVALID_ARG, "grok_kv8_decode: null pointer");
+  if (weight_in && !weight_out) return fail(GROK_ERR_INVALID_ARG, "grok_kv8_decode: weight_in without weight_out");
+  if (!aligned16(q_rot) || !aligned16(out))
+    return fail(GROK_ERR_INVALID_ARG, "grok_kv8_decode: bf16 tensors must be 16-byte aligned");
+  if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
+    return fail(GROK_ERR_INVALID_ARG, "grok_kv8_decode: workspace must be 256-byte aligned");
+  int sms = 0, dev = 0;
+  if ((st = device_sm_count(&sms)) != GROK_OK || (st = device_index(&dev)) != GROK_OK) return st;
+  const int B = cache->B;
+  const size_t o_bytes = part_o_bytes(B, sms), ml_bytes = part_ml_bytes(B, sms);
+  const size_t need = o_bytes + ml_bytes + (weight_out ? block_w_bytes(B, cache->max_blocks) : 0);
+  if (workspace_bytes < need)
+    return fail(GROK_ERR_INVALID_ARG, "grok_kv8_decode: workspace of %zu bytes is smaller than the %zu needed",
+                workspace_bytes, need);
+  char* ws = static_cast<char*>(workspace);
+  const DqParams p{*cache,
+                   reinterpret_cast<const uint4*>(q_rot),
+                   kv_len,
+                   reinterpret_cast<float*>(ws),
+                   reinterpret_cast<float2*>(ws + o_bytes),
+                   weight_out ? reinterpret_cast<float*>(ws + o_bytes + ml_bytes) : nullptr,
+                   reinterpret_cast<uint2*>(out),
+                   weight_in,
+                   weight_out,
+                   sms * kDqWarps,
+                   dev_status};
+  const bool i8 = cache->kind == GROK_KV8_INT8;
+  auto kernel = i8 ? (weight_out ? kv8_decode_kernel<GROK_KV8_INT8, true> : kv8_decode_kernel<GROK_KV8_INT8, false>)
+                   : (weight_out ? kv8_decode_kernel<GROK_KV8_E4M3, true> : kv8_decode_kernel<GROK_KV8_E4M3, false>);
+  static bool attr_set[kMaxDevices][4] = {};  // per device and kernel; idempotent: every thread would set the same value
+  bool& set = attr_set[dev][(i8 ? 0 : 2) + (weight_out ? 1 : 0)];
+  if (!set) {
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kDqSmem);
+    if (e != cudaSuccess) return fail(cuda_status(e), "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
+    set = true;
+  }
+  kernel<<<sms, kDqThreads, kDqSmem, static_cast<cudaStream_t>(stream)>>>(p);
+  if ((st = check_launch("kv8_decode")) != GROK_OK) return st;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(B * kKVHeads, kGroup + (weight_out ? 1 : 0));
+  cfg.blockDim = dim3(kDqJoinWarps * 32);
+  cfg.stream = static_cast<cudaStream_t>(stream);
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cudaError_t e = cudaLaunchKernelEx(&cfg, kv8_join_kernel, p);
+  if (e != cudaSuccess) return fail(cuda_status(e), "kv8_join launch: %s", cudaGetErrorString(e));
+  return check_launch("kv8_join");
+}

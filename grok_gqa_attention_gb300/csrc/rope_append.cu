@@ -31,28 +31,6 @@ namespace grok {
 
 constexpr int kRopeThreads = 128;
 
-__device__ __forceinline__ void rotate8(const uint4& x1, const uint4& x2, const float* c, const float* s,
-                                        uint4& y1, uint4& y2) {
-  const uint32_t a[4] = {x1.x, x1.y, x1.z, x1.w};
-  const uint32_t b[4] = {x2.x, x2.y, x2.z, x2.w};
-  uint32_t o1[4], o2[4];
-#pragma unroll
-  for (int w = 0; w < 4; ++w) {
-    const float a0 = bf16lo_to_f32(a[w]), a1 = bf16hi_to_f32(a[w]);
-    const float b0 = bf16lo_to_f32(b[w]), b1 = bf16hi_to_f32(b[w]);
-    const float c0 = c[2 * w], c1 = c[2 * w + 1], s0 = s[2 * w], s1 = s[2 * w + 1];
-    // x'[j] = x[j] cos - x[j+64] sin ; x'[j+64] = x[j+64] cos + x[j] sin
-    const float y1a = __fadd_rn(__fmul_rn(a0, c0), -__fmul_rn(b0, s0));
-    const float y1b = __fadd_rn(__fmul_rn(a1, c1), -__fmul_rn(b1, s1));
-    const float y2a = __fadd_rn(__fmul_rn(b0, c0), __fmul_rn(a0, s0));
-    const float y2b = __fadd_rn(__fmul_rn(b1, c1), __fmul_rn(a1, s1));
-    o1[w] = pack_bf16x2(y1a, y1b);
-    o2[w] = pack_bf16x2(y2a, y2b);
-  }
-  y1 = make_uint4(o1[0], o1[1], o1[2], o1[3]);
-  y2 = make_uint4(o2[0], o2[1], o2[2], o2[3]);
-}
-
 // A team of `team` warps (1, 2, 4 or 8) per token, grid-stride over tokens
 // with no CTA-wide barrier. Warp w of the team takes the rotation units (8
 // pairs of one head) and value units whose index m satisfies m % team == w: it

@@ -1,5 +1,5 @@
-// RoPE constants evaluated on the device, shared by the kernels that rotate:
-// the fp32 inverse frequencies and the fp32 cos / sin of an fp32 phase.
+// RoPE on the device, shared by the kernels that rotate: the fp32 inverse
+// frequencies, the fp32 cos / sin of an fp32 phase, and the rotation itself.
 //
 // Grok-1 code-reading guide, ch. 4 "model.py close reading I", §4.3.1
 // RotaryEmbedding: inv_freq = 1 / 10000^(2j/128) in fp32, phase = t * inv_freq
@@ -66,6 +66,30 @@ __device__ __forceinline__ void rope_cos_sin(float phase, float& c_out, float& s
 __device__ __forceinline__ float rope_inv_freq(int j) {
   constexpr double kLog2Base = 13.287712379549449;  // log2(10000)
   return __fdiv_rn(1.0f, __double2float_rn(exp2(double(j) * (kLog2Base / 64.0))));
+}
+
+// Eight pairs of one head (features 8c .. 8c+7 in x1, 8c+64 .. in x2), rotated
+// with separately rounded products and sums (no contraction) and rounded to bf16.
+__device__ __forceinline__ void rotate8(const uint4& x1, const uint4& x2, const float* c, const float* s,
+                                        uint4& y1, uint4& y2) {
+  const uint32_t a[4] = {x1.x, x1.y, x1.z, x1.w};
+  const uint32_t b[4] = {x2.x, x2.y, x2.z, x2.w};
+  uint32_t o1[4], o2[4];
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    const float a0 = bf16lo_to_f32(a[w]), a1 = bf16hi_to_f32(a[w]);
+    const float b0 = bf16lo_to_f32(b[w]), b1 = bf16hi_to_f32(b[w]);
+    const float c0 = c[2 * w], c1 = c[2 * w + 1], s0 = s[2 * w], s1 = s[2 * w + 1];
+    // x'[j] = x[j] cos - x[j+64] sin ; x'[j+64] = x[j+64] cos + x[j] sin
+    const float y1a = __fadd_rn(__fmul_rn(a0, c0), -__fmul_rn(b0, s0));
+    const float y1b = __fadd_rn(__fmul_rn(a1, c1), -__fmul_rn(b1, s1));
+    const float y2a = __fadd_rn(__fmul_rn(b0, c0), __fmul_rn(a0, s0));
+    const float y2b = __fadd_rn(__fmul_rn(b1, c1), __fmul_rn(a1, s1));
+    o1[w] = pack_bf16x2(y1a, y1b);
+    o2[w] = pack_bf16x2(y2a, y2b);
+  }
+  y1 = make_uint4(o1[0], o1[1], o1[2], o1[3]);
+  y2 = make_uint4(o2[0], o2[1], o2[2], o2[3]);
 }
 
 }  // namespace grok

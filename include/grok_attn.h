@@ -29,6 +29,8 @@
  *   paged cache         grok_rope_kv_append_paged, grok_attn_prefill_paged, grok_attn_prefill_ws_paged,
  *                       grok_attn_decode_paged, grok_qkv_rope_append_paged
  *   continuous batching grok_kv_insert_slot
+ *   8-bit cache         grok_kv8_append, grok_kv8_decode(_workspace), grok_kv8_prefill(_workspace),
+ *                       grok_kv8_evict
  *   diagnostics         grok_abi_version, grok_last_error, grok_selftest_bounded_wait
  *
  * Conventions for every call:
@@ -103,6 +105,11 @@ typedef enum {
 
 /* Tokens per page of the paged KV cache (one prefill key tile). */
 #define GROK_PAGE_TOKENS 128
+
+/* The 8-bit KV cache: tokens per block, and the element types of its codes. */
+#define GROK_KV8_BLOCK 64
+#define GROK_KV8_INT8 0
+#define GROK_KV8_E4M3 1
 
 /* ABI version this library was built with (GROK_ATTN_ABI_VERSION). */
 int grok_abi_version(void);
@@ -538,6 +545,119 @@ grok_status grok_qkv_rope_append_paged(const grok_bf16* x, const grok_bf16* w, c
 grok_status grok_kv_insert_slot(grok_bf16* cache_k, grok_bf16* cache_v, int B, int Tmax, int slot,
                                 const grok_bf16* src_k, const grok_bf16* src_v, int src_rows, int n_rows,
                                 int32_t* step, int step_value, void* stream);
+
+/*
+ * KV cache in 8 bits, with one scale for each block of 64 tokens and KV head.
+ * The pages keep the cache in bf16 (ch. 6 §6.6) and the weights in 8 bits with
+ * a scale (ch. 4 §4.1.1); this cache is the second applied to the first: half
+ * the memory, and half the bytes that a decode step reads.
+ *
+ * A block holds 64 tokens' keys or values of one KV head:
+ *   k_pool [n_blocks][2][64][64]  (half of the 128 features, token, feature)
+ *   v_pool [n_blocks][128][64]    (feature, token)
+ * as one-byte codes (kind GROK_KV8_INT8 or GROK_KV8_E4M3), with one fp32 scale
+ * per block in k_scale, v_scale [n_blocks]; an element is code * scale. The
+ * block of rows [64 i, 64 i + 64) of sequence b and KV head g is
+ * table[(b * 8 + g) * max_blocks + i], in any order and at any place of the
+ * pools. A sequence's capacity is max_blocks * 64 rows, at most
+ * GROK_MAX_POSITION. Blocks may be shared between sequences except the one a
+ * sequence is still writing. Table entries past a sequence's rows are not read.
+ * open_k, open_v [B][8][64][128] bf16 hold, at row r % 64, the unrounded rows of
+ * the block that is not yet full (unused where a sequence's rows are a multiple
+ * of 64).
+ *
+ * Quantisation of a block whose rows so far are x: a = max |x|, scale =
+ * RN32(a / Q) with Q = 127 or 448, code = round(RN32(x * RN32(1 / scale))) to the
+ * nearest whole number or e4m3 value, ties to even. a < 2^-100 gives scale 0 and
+ * codes 0; a block that holds a NaN or an infinity gets scale NaN and codes 0,
+ * and attention over it gives NaN. The open block is always quantised as a
+ * whole from its bf16 rows, so each element is rounded once and the cache does
+ * not depend on the sizes of the appends that filled it.
+ *
+ * A sequence's rows (cache_len, kv_len) and its positions (start_pos) are
+ * separate: after an eviction a sequence has fewer rows than positions.
+ *
+ * The struct is host memory and is read during the call only. Device pointers
+ * are 16-byte aligned; B, n_blocks, max_blocks >= 1, max_blocks <= 1024,
+ * B <= 65535. A table entry outside [0, n_blocks) that a call needs sets
+ * GROK_DEV_BAD_PAGE; the append then skips that block, the attention calls read
+ * block 0 in its place (the sequence's results are meaningless).
+ */
+typedef struct {
+  void* k_pool;
+  void* v_pool;
+  float* k_scale;
+  float* v_scale;
+  const int32_t* table;
+  grok_bf16* open_k;
+  grok_bf16* open_v;
+  int kind;
+  int B;
+  int max_blocks;
+  int n_blocks;
+} grok_kv8_cache;
+
+/*
+ * RoPE on Q and K (bit for bit as grok_rope_kv_append_table, from the same
+ * tables; another table gives another rotation) and the append to the cache.
+ * Token i of sequence b has position start_pos[b] + i; tokens i < valid_len[b]
+ * become rows cache_len[b] + i. q_rot is written for all T tokens.
+ *   q [B,T,48,128], k, v [B,T,8,128]; start_pos, cache_len [B] int32; valid_len
+ *   [B] int32 or NULL (= T); cos_tab, sin_tab [tab_positions * 64] fp32.
+ * A sequence is skipped, with a bit in *dev_status, where start_pos[b] < 0 or
+ * start_pos[b] + T > tab_positions (GROK_DEV_BAD_START), cache_len[b] < 0 or
+ * cache_len[b] + valid_len[b] > max_blocks * 64 (GROK_DEV_BAD_KV_LEN), or
+ * valid_len[b] is outside [1, T] (GROK_DEV_BAD_VALID). Code rows behind a
+ * sequence's last are left as they were.
+ */
+grok_status grok_kv8_append(const grok_kv8_cache* cache, const grok_bf16* q, const grok_bf16* k, const grok_bf16* v,
+                            const int32_t* start_pos, const int32_t* cache_len, const int32_t* valid_len, int T,
+                            const float* cos_tab, const float* sin_tab, int tab_positions, grok_bf16* q_rot,
+                            int32_t* dev_status, void* stream);
+
+/*
+ * Attention of one token per sequence over rows [0, kv_len[b]) of the cache
+ * (the token's own row appended before): grok_attn_decode and grok_attn_combine
+ * over the 8-bit cache, in one call. The blocks of all sequences are dealt out
+ * evenly to the GPU's warps, whatever the lengths; a sequence's bits depend on
+ * the lengths in its batch through the places where its sums are split.
+ *   q_rot, out [B,48,128]; kv_len [B] int32 in [1, max_blocks * 64] (else
+ *   GROK_DEV_BAD_KV_LEN, and the sequence's outputs are left as they were).
+ *   weight_out [B,8,max_blocks] fp32 or NULL: weight_out = weight_in + the
+ *   softmax weight that each block received, summed over the KV head's six query
+ *   heads (so a head's blocks gain 6 in all). weight_in NULL counts as zero and
+ *   may be weight_out. Entries behind a sequence's last block are copied.
+ *   workspace: device memory, 256-byte aligned, of at least
+ *   grok_kv8_decode_workspace(B, max_blocks, weight_out != NULL) bytes for the
+ *   current device. Calls that overlap on the GPU need separate workspaces;
+ *   nothing in it is kept from call to call.
+ */
+grok_status grok_kv8_decode_workspace(int B, int max_blocks, int weights, size_t* bytes);
+grok_status grok_kv8_decode(const grok_kv8_cache* cache, const grok_bf16* q_rot, const int32_t* kv_len,
+                            void* workspace, size_t workspace_bytes, grok_bf16* out, const float* weight_in,
+                            float* weight_out, int32_t* dev_status, void* stream);
+
+/*
+ * Eviction by accumulated weight. For sequence b and KV head g with nc =
+ * kv_len[b] / 64 full blocks: where nc > keep, the first `sink` and the last
+ * `recent` full blocks stay, and of the others those with the largest weight
+ * (the lower index first among equals; NaN counts as minus infinity) until
+ * `keep` stay. The head's table row is permuted: the blocks that stay in their
+ * order, the entry of the open block (index nc), the evicted ones in their
+ * order, then the rest as it was; weights likewise, 0 for the evicted. No code
+ * moves: the rows that follow are written into the evicted blocks, and an
+ * owner of a shared pool finds their numbers behind the last block in use.
+ * kv_len_out[b] = keep * 64 + kv_len[b] % 64, or kv_len[b] where nc <= keep.
+ *   table, table_out [B,8,max_blocks] int32, weight, weight_out
+ *   [B,8,max_blocks] fp32, kv_len, kv_len_out [B] int32. table_out may be table and
+ *   weight_out weight; kv_len_out may not be kv_len (eight heads read it).
+ *   1 <= max_blocks <= 1024, 0 <= sink, 0 <= recent, sink + recent <= keep,
+ *   keep >= 1. kv_len[b] outside [0, max_blocks * 64] sets GROK_DEV_BAD_KV_LEN; the
+ *   sequence's rows of the outputs are copies of the inputs then.
+ */
+grok_status grok_kv8_evict(const int32_t* table, const float* weight, const int32_t* kv_len, int B, int max_blocks,
+                           int keep, int sink, int recent, int32_t* table_out, float* weight_out, int32_t* kv_len_out,
+                           int32_t* dev_status, void* stream);
 
 #ifdef __cplusplus
 }

@@ -1,0 +1,534 @@
+"""The 8-bit KV cache's calls against the oracle: append, decode with the blocks' weights, eviction, and a run of them."""
+import numpy as np
+import pytest
+import torch
+
+import grok_gqa_attention_gb300 as G
+from oracle import bf16, kv8
+from oracle import rope as R
+from tests.parity_util import assert_close
+
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda"
+DT = {"int8": torch.int8, "e4m3": torch.float8_e4m3fn}
+KINDS = ("int8", "e4m3")
+
+
+def _bits(t):
+    return t.detach().cpu().contiguous().view(torch.int16).numpy().view(np.uint16)
+
+
+def _bf16(x):
+    return torch.from_numpy(bf16.from_f32(np.asarray(x, np.float32)).view(np.int16)).view(torch.bfloat16)
+
+
+def _ints(v):
+    return torch.tensor(v, dtype=torch.int32, device=DEV)
+
+
+def make_cache(B, max_blocks, kind, seed=0, extra=5):
+    """A cache whose blocks lie in random order in a larger pool; every byte and scale that nothing writes is junk
+    (0x7f: the largest int8, an e4m3 NaN)."""
+    g = torch.Generator().manual_seed(seed)
+    n = B * 8 * max_blocks + extra
+    table = torch.randperm(n, generator=g)[:B * 8 * max_blocks].to(torch.int32).view(B, 8, max_blocks).to(DEV)
+    junk = lambda *s: torch.full((n,) + s, 0x7f, dtype=torch.uint8, device=DEV).view(DT[kind])  # noqa: E731
+    nan = lambda *s, d=torch.float32: torch.full(s, float("nan"), dtype=d, device=DEV)  # noqa: E731
+    return G.Kv8Cache(junk(2, 64, 64), junk(128, 64), nan(n), nan(n), table,
+                      nan(B, 8, 64, 128, d=torch.bfloat16), nan(B, 8, 64, 128, d=torch.bfloat16))
+
+
+def tables(n):
+    return G.rope_cos_sin(0, n)
+
+
+class Host:
+    """The oracle's side of a cache: each sequence's rotated keys and values, bf16 bits [L, 8, 128]."""
+
+    def __init__(self, B):
+        self.k = [np.zeros((0, 8, 128), np.uint16) for _ in range(B)]
+        self.v = [np.zeros((0, 8, 128), np.uint16) for _ in range(B)]
+
+    def append(self, q, k, v, start, valid):
+        k_rot = R.rotary_embedding(_bits(k), np.asarray(start))
+        for b, n in enumerate(valid):
+            self.k[b] = np.concatenate([self.k[b], k_rot[b, :n]])
+            self.v[b] = np.concatenate([self.v[b], _bits(v)[b, :n]])
+        return R.rotary_embedding(_bits(q), np.asarray(start))
+
+
+def block_of(cache, b, g, i):
+    """Codes [64, 128] (bytes) of K and V and the two scales of one block."""
+    at = int(cache.table[b, g, i])
+    k = cache.k_pool[at].view(torch.uint8).cpu().numpy()
+    v = cache.v_pool[at].view(torch.uint8).cpu().numpy()
+    return (np.concatenate([k[0], k[1]], 1), v.T, np.float32(cache.k_scale[at].item()),
+            np.float32(cache.v_scale[at].item()))
+
+
+def check_cache(cache, host, kind):
+    for b in range(cache.B):
+        L = len(host.k[b])
+        for g in range(8):
+            want_k, want_v = kv8.blocks(host.k[b][:, g], kind), kv8.blocks(host.v[b][:, g], kind)
+            for i in range(cache.max_blocks):
+                k, v, ks, vs = block_of(cache, b, g, i)
+                if i >= len(want_k):
+                    assert (k == 0x7f).all() and (v == 0x7f).all() and np.isnan(ks) and np.isnan(vs), (b, g, i)
+                    continue
+                (ck, sk), (cv, sv) = want_k[i], want_v[i]
+                r = len(ck)
+                assert np.array_equal(ks, sk, equal_nan=True) and np.array_equal(vs, sv, equal_nan=True), (b, g, i)
+                assert np.array_equal(k[:r], ck) and np.array_equal(v[:r], cv), (b, g, i)
+                assert (k[r:] == 0x7f).all() and (v[r:] == 0x7f).all(), (b, g, i)
+        r = L % 64
+        if r:
+            assert np.array_equal(_bits(cache.open_k[b])[:, :r], host.k[b][L - r:].transpose(1, 0, 2))
+            assert np.array_equal(_bits(cache.open_v[b])[:, :r], host.v[b][L - r:].transpose(1, 0, 2))
+
+
+def rows(rng, B, T, scale=3.0):
+    q, k, v = (_bf16(rng.standard_normal((B, T, h, 128)) * scale) for h in (48, 8, 8))
+    return q, k, v
+
+
+def append(cache, host, q, k, v, start, valid, tab, valid_given=True):
+    """One append on both sides; q_rot is compared."""
+    B, T = q.shape[:2]
+    lens = [len(x) for x in host.k]
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    q_rot = torch.zeros_like(q, device=DEV)
+    G.kv8_append(cache, q.to(DEV), k.to(DEV), v.to(DEV), _ints(start), _ints(lens), _ints(valid) if valid_given else None,
+                 *tab, q_rot, status)
+    want = host.append(q, k, v, start, valid)
+    assert int(status.item()) == 0
+    assert np.array_equal(_bits(q_rot), want)
+    return q_rot
+
+
+# ------------------------------------------------------------------------------------------------- append
+CHUNKS = {
+    "one_by_one": [1] * 67,
+    "whole": [200],
+    "odd": [63, 1, 1, 130, 5],
+    "closes_and_opens": [40, 100, 64, 3, 61, 65],
+    "exact": [64, 128, 64],
+}
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("chunks", list(CHUNKS))
+def test_append_any_chunks_give_the_rows_cache(kind, chunks):
+    sizes = CHUNKS[chunks]
+    rng = np.random.default_rng(len(sizes))
+    B, total = 2, sum(sizes)
+    cache, host, tab = make_cache(B, (total + 63) // 64 + 1, kind, seed=1), Host(B), tables(total + 1000)
+    pos = np.array([0, 777])
+    for T in sizes:
+        q, k, v = rows(rng, B, T)
+        append(cache, host, q, k, v, pos.tolist(), [T] * B, tab, valid_given=False)
+        pos += T
+    check_cache(cache, host, kind)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_append_padded_batch(kind):
+    rng = np.random.default_rng(5)
+    B, T = 5, 150
+    cache, host, tab = make_cache(B, 6, kind, seed=2), Host(B), tables(512)
+    for valid in ([150, 1, 64, 65, 127], [2, 63, 150, 100, 1], [1, 1, 1, 1, 1]):
+        q, k, v = rows(rng, B, T)
+        append(cache, host, q, k, v, [len(x) for x in host.k], valid, tab)
+    check_cache(cache, host, kind)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_append_scales_grow_stay_and_break(kind):
+    """Rows one by one whose magnitudes rise, fall, vanish and leave the finite numbers; each head its own."""
+    rng = np.random.default_rng(6)
+    cache, host, tab = make_cache(1, 3, kind, seed=3), Host(1), tables(256)
+    factor = [0.0, 2.0 ** -110, 1e-20, 1.0, 0.5, 1.0, 1e4, 3e4, 1e-3, 1e30, 1.0] + [1.0] * 60
+    for i, f in enumerate(factor):
+        q, k, v = rows(rng, 1, 1)
+        k, v = (k.float() * f).bfloat16(), (v.float() * f).bfloat16()
+        if i == 40:
+            k[0, 0, 2, 7] = float("nan")
+            v[0, 0, 3, 9] = float("inf")
+        append(cache, host, q, k, v, [i], [1], tab)
+    check_cache(cache, host, kind)
+    ks, vs = cache.k_scale[cache.table[0, 2, 0].long()], cache.v_scale[cache.table[0, 3, 0].long()]
+    assert torch.isnan(ks) and torch.isnan(vs)
+
+
+def test_append_skips_bad_sequences():
+    rng = np.random.default_rng(7)
+    B, T = 6, 3
+    tab = tables(64)
+    q, k, v = rows(rng, B, T)
+    for start, lens, valid, bit in (([0, -1, 0, 0, 0, 0], [0] * 6, [3] * 6, G.DEV_BAD_START),
+                                    ([0, 62, 0, 0, 0, 0], [0] * 6, [3] * 6, G.DEV_BAD_START),
+                                    ([0] * 6, [0, -1, 0, 0, 0, 0], [3] * 6, G.DEV_BAD_KV_LEN),
+                                    ([0] * 6, [0, 126, 0, 0, 0, 0], [3] * 6, G.DEV_BAD_KV_LEN),
+                                    ([0] * 6, [0] * 6, [3, 0, 3, 3, 3, 3], G.DEV_BAD_VALID),
+                                    ([0] * 6, [0] * 6, [3, 4, 3, 3, 3, 3], G.DEV_BAD_VALID)):
+        cache, host = make_cache(B, 2, "int8", seed=4), Host(B)
+        status = torch.zeros(1, dtype=torch.int32, device=DEV)
+        q_rot = torch.full_like(q, 7.0, device=DEV)
+        G.kv8_append(cache, q.to(DEV), k.to(DEV), v.to(DEV), _ints(start), _ints(lens), _ints(valid), *tab, q_rot, status)
+        assert int(status.item()) == bit
+        start, valid = list(start), list(valid)
+        start[1], valid[1] = 0, 0
+        want = host.append(q, k, v, start, valid)
+        got = _bits(q_rot)
+        assert (q_rot[1] == 7.0).all() and np.array_equal(got[[0, 2, 3, 4, 5]], want[[0, 2, 3, 4, 5]])
+        check_cache(cache, host, "int8")
+
+
+def test_append_skips_blocks_outside_the_pool():
+    rng = np.random.default_rng(8)
+    q, k, v = rows(rng, 1, 70)
+    for bad in (-1, 10 ** 6, 2 ** 31 - 1):
+        cache, host, tab = make_cache(1, 2, "int8", seed=5), Host(1), tables(128)
+        saved = cache.table.clone()
+        cache.table[0, 3, 1] = bad
+        status = torch.zeros(1, dtype=torch.int32, device=DEV)
+        q_rot = torch.zeros_like(q, device=DEV)
+        G.kv8_append(cache, q.to(DEV), k.to(DEV), v.to(DEV), _ints([0]), _ints([0]), None, *tab, q_rot, status)
+        assert int(status.item()) == G.DEV_BAD_PAGE
+        cache.table.copy_(saved)
+        host.append(q, k, v, [0], [70])
+        for g in range(8):
+            kk, vv, ks, _ = block_of(cache, 0, g, 1)
+            if g == 3:
+                assert (kk == 0x7f).all() and (vv == 0x7f).all() and np.isnan(ks)
+            else:
+                assert np.array_equal(kk[:6], kv8.blocks(host.k[0][:, g], "int8")[1][0])
+
+
+# ------------------------------------------------------------------------------------------------- decode
+def filled(rng, lens, kind, max_blocks, seed, scale=3.0, tab=None):
+    """A cache of lens[b] rows (0 allowed) and the oracle's rows."""
+    B, T = len(lens), max(max(lens), 1)
+    cache, host = make_cache(B, max_blocks, kind, seed=seed), Host(B)
+    q, k, v = rows(rng, B, T, scale)
+    lens1 = [max(n, 1) for n in lens]
+    append(cache, host, q, k, v, [0] * B, lens1, tab or tables(T))
+    return cache, host
+
+
+def decode_reference(host, q, lens, kind, max_blocks):
+    """Exact outputs, block weights, and per output the weighted sum of |v| (for the tolerance)."""
+    B = len(lens)
+    out, scale_v = np.zeros((B, 48, 128)), np.zeros((B, 48, 128))
+    weight = np.zeros((B, 8, max_blocks))
+    s_abs = 0.0
+    x = bf16.to_f64(_bits(q))
+    for b in range(B):
+        for g in range(8):
+            if lens[b] < 1:
+                continue
+            K, V = kv8.held(host.k[b][:lens[b], g], kind), kv8.held(host.v[b][:lens[b], g], kind)
+            qs = x[b, 6 * g:6 * g + 6]
+            o, w = kv8.attend(qs, K, V)
+            out[b, 6 * g:6 * g + 6], scale_v[b, 6 * g:6 * g + 6] = o, w @ np.abs(V)
+            weight[b, g] = kv8.block_weights(w, max_blocks)
+            s_abs = max(s_abs, (np.abs(qs) @ np.abs(K).T).max() / 128 ** 0.5)
+    return out, weight, scale_v, s_abs
+
+
+def check_decode(got, out, scale_v, s_abs, L, live):
+    """bf16 rounding of the result (half a step, 2^-8), and of a weight: its fp16 rounding (2^-11), its logit (a
+    128-term fp32 sum, 128 * 2^-23 of the sum of magnitudes), and three approximate functions on log2 weights up to
+    87 (2^-20 each of 87); a weight enters numerator and sum. fp16 below its normal range: 2^-25 of the largest
+    weight per key."""
+    got = got.float().cpu().numpy().astype(np.float64)
+    delta = 2.0 ** -11 + 2 * (128 * 2.0 ** -23 * s_abs + 3 * 87 * 2.0 ** -20)
+    tol = 2.0 ** -8 * np.abs(out) + delta * scale_v * (1 + 2.0 ** -8) + L * 2.0 ** -25 * scale_v.max()
+    bad = np.abs(got - out) > tol
+    assert not bad[live].any(), (np.abs(got - out) / tol)[live].max()
+
+
+def run_decode(cache, q, lens, weight_in=None, weights=True):
+    B = cache.B
+    out = torch.full((B, 48, 128), 7.0, dtype=torch.bfloat16, device=DEV)
+    w_out = torch.full((B, 8, cache.max_blocks), 7.0, device=DEV) if weights else None
+    ws = G.alloc_kv8_decode_workspace(cache, weights)
+    ws.fill_(0xff)
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    G.kv8_decode(cache, q, _ints(lens), ws, out, weight_in, w_out, status)
+    torch.cuda.synchronize()
+    return out, w_out, int(status.item())
+
+
+LENS = {
+    "short": [1, 2, 63, 64, 65, 128, 300],
+    "one": [1],
+    "one_long": [2000],
+    "mixed": [700, 1, 129, 64, 640, 5],
+    "many": [(37 * i) % 200 + 1 for i in range(70)],
+}
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("name", list(LENS))
+def test_decode(kind, name):
+    lens = LENS[name]
+    rng = np.random.default_rng(11)
+    max_blocks = (max(lens) + 63) // 64 + 1
+    cache, host = filled(rng, lens, kind, max_blocks, seed=6)
+    q = _bf16(rng.standard_normal((len(lens), 48, 128)) * 3).to(DEV)
+    before = torch.rand(len(lens), 8, max_blocks, device=DEV)
+    got, w, status = run_decode(cache, q, lens, before)
+    assert status == 0
+    out, weight, scale_v, s_abs = decode_reference(host, q, lens, kind, max_blocks)
+    live = np.ones(len(lens), bool)
+    check_decode(got, out, scale_v, s_abs, max(lens), live)
+    assert_close(_bits(got), bf16.from_f64(out), f"kv8 decode {kind} {name}")
+    # the weights are sums of fp32 weights: the same errors but for the fp16 rounding, and one fp32 sum
+    exact = before.double().cpu().numpy() + weight
+    delta = 2 * (128 * 2.0 ** -23 * s_abs + 3 * 87 * 2.0 ** -20) + 2.0 ** -20
+    assert (np.abs(w.double().cpu().numpy() - exact) <= delta * weight + 2.0 ** -23 * exact).all()
+    assert torch.equal(run_decode(cache, q, lens, weights=False)[0], got)
+    # in place
+    G.kv8_decode(cache, q, _ints(lens), G.alloc_kv8_decode_workspace(cache), got, before, before)
+    assert torch.equal(before, w)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("scale", [1e-6, 0.02, 8.0])
+def test_decode_flat_and_peaked_logits(kind, scale):
+    """Weights all alike, and logits far beyond the cap."""
+    lens = [517, 64]
+    rng = np.random.default_rng(12)
+    cache, host = filled(rng, lens, kind, 9, seed=7, scale=scale)
+    q = _bf16(rng.standard_normal((2, 48, 128)) * scale).to(DEV)
+    got, _, _ = run_decode(cache, q, lens)
+    out, _, scale_v, s_abs = decode_reference(host, q, lens, kind, 9)
+    check_decode(got, out, scale_v, s_abs, 517, np.ones(2, bool))
+
+
+def test_decode_unequal_query_heads():
+    """Queries of very different magnitudes, one zero: each head is scaled to fp16 by its own power of two."""
+    lens = [200]
+    rng = np.random.default_rng(13)
+    cache, host = filled(rng, lens, "int8", 4, seed=8)
+    mag = 2.0 ** np.linspace(-40, 3, 48)[None, :, None]
+    mag[0, 5] = 0
+    q = _bf16(rng.standard_normal((1, 48, 128)) * mag).to(DEV)
+    got, _, _ = run_decode(cache, q, lens)
+    out, _, scale_v, s_abs = decode_reference(host, q, lens, "int8", 4)
+    check_decode(got, out, scale_v, s_abs, 200, np.ones(1, bool))
+
+
+def test_decode_bad_lengths_leave_the_outputs():
+    rng = np.random.default_rng(14)
+    lens = [100, 70, 3, 128]
+    cache, host = filled(rng, lens, "e4m3", 2, seed=9)
+    q = _bf16(rng.standard_normal((4, 48, 128)) * 3).to(DEV)
+    given = [100, 0, 129, 128]
+    got, w, status = run_decode(cache, q, given)
+    assert status == G.DEV_BAD_KV_LEN
+    assert (got[[1, 2]] == 7.0).all() and (w[[1, 2]] == 7.0).all()
+    out, _, scale_v, s_abs = decode_reference(host, q, [100, 0, 0, 128], "e4m3", 2)
+    check_decode(got, out, scale_v, s_abs, 128, np.array([True, False, False, True]))
+    got, _, status = run_decode(cache, q, [0, -5, 2 ** 31 - 1, -2 ** 31])
+    assert status == G.DEV_BAD_KV_LEN and (got == 7.0).all()
+
+
+def test_decode_reports_blocks_outside_the_pool():
+    rng = np.random.default_rng(15)
+    cache, _ = filled(rng, [100, 100], "int8", 2, seed=10)
+    q = _bf16(rng.standard_normal((2, 48, 128)) * 3).to(DEV)
+    good, _, _ = run_decode(cache, q, [100, 100])
+    for bad in (-1, cache.n_blocks, 2 ** 31 - 1):
+        cache.table[1, 0, 1] = bad
+        got, _, status = run_decode(cache, q, [100, 100])
+        assert status == G.DEV_BAD_PAGE
+        assert torch.equal(got[0], good[0]) and torch.equal(got[1, 6:], good[1, 6:])
+
+
+def test_decode_of_a_non_finite_block_is_nan_for_its_head_alone():
+    rng = np.random.default_rng(16)
+    cache, host = filled(rng, [200, 200], "int8", 4, seed=11)
+    q = _bf16(rng.standard_normal((2, 48, 128)) * 3).to(DEV)
+    good, _, _ = run_decode(cache, q, [200, 200])
+    cache.k_scale[cache.table[0, 1, 2].long()] = float("nan")
+    cache.v_scale[cache.table[1, 4, 0].long()] = float("nan")
+    got, _, _ = run_decode(cache, q, [200, 200])
+    nan = torch.isnan(got).all(-1)
+    want = torch.zeros_like(nan)
+    want[0, 6:12] = True
+    want[1, 24:30] = True
+    assert torch.equal(nan, want) and torch.equal(got[~want], good[~want])
+
+
+def test_decode_pool_past_2_gb():
+    """Blocks behind byte 2^31 of both pools."""
+    rng = np.random.default_rng(17)
+    small, host = filled(rng, [150], "int8", 3, seed=12)
+    n = 300000
+    k = torch.empty((n, 2, 64, 64), dtype=torch.int8, device=DEV)
+    v = torch.empty((n, 128, 64), dtype=torch.int8, device=DEV)
+    ks, vs = torch.empty(n, device=DEV), torch.empty(n, device=DEV)
+    shift = n - small.n_blocks
+    k[shift:], v[shift:], ks[shift:], vs[shift:] = small.k_pool, small.v_pool, small.k_scale, small.v_scale
+    cache = G.Kv8Cache(k, v, ks, vs, small.table + shift, small.open_k, small.open_v)
+    q = _bf16(rng.standard_normal((1, 48, 128)) * 3).to(DEV)
+    assert torch.equal(run_decode(cache, q, [150])[0], run_decode(small, q, [150])[0])
+    del host
+
+
+def test_workspace_too_small_is_refused():
+    rng = np.random.default_rng(18)
+    cache, _ = filled(rng, [10], "int8", 1, seed=13)
+    q = _bf16(rng.standard_normal((1, 48, 128))).to(DEV)
+    out = torch.empty(1, 48, 128, dtype=torch.bfloat16, device=DEV)
+    w = torch.empty(1, 8, 1, device=DEV)
+    ws = G.alloc_kv8_decode_workspace(cache, weights=False)
+    with pytest.raises(G.GrokError, match="smaller"):
+        G.kv8_decode(cache, q, _ints([10]), ws, out, None, w)
+    with pytest.raises(G.GrokError, match="smaller"):
+        G.kv8_decode(cache, q, _ints([10]), ws[:-256], out)
+
+
+# ------------------------------------------------------------------------------------------------- evict
+EVICTS = [dict(B=3, n=9, keep=4, sink=1, recent=2), dict(B=2, n=40, keep=33, sink=0, recent=0),
+          dict(B=2, n=1024, keep=500, sink=4, recent=60), dict(B=4, n=33, keep=1, sink=0, recent=1),
+          dict(B=2, n=64, keep=8, sink=4, recent=4), dict(B=1, n=1, keep=1, sink=0, recent=0),
+          dict(B=3, n=5, keep=64, sink=3, recent=9)]
+
+
+@pytest.mark.parametrize("case", EVICTS, ids=str)
+@pytest.mark.parametrize("values", ["random", "ties", "special"])
+def test_evict(case, values):
+    B, n, keep, sink, recent = (case[x] for x in ("B", "n", "keep", "sink", "recent"))
+    rng = np.random.default_rng(20)
+    w = rng.standard_normal((B, 8, n)).astype(np.float32)
+    if values == "ties":
+        w = np.round(w).astype(np.float32) * np.float32(1.0)
+    if values == "special":
+        w = rng.choice(np.array([np.nan, np.inf, -np.inf, 0.0, -0.0, 1.0, 3.4e38, 1e-45], np.float32), (B, 8, n))
+    lens = rng.integers(0, n * 64 + 1, B)
+    lens[0] = n * 64
+    if B > 2:
+        lens[2] = min(keep, n) * 64
+    table = torch.from_numpy(rng.permutation(B * 8 * n).astype(np.int32).reshape(B, 8, n)).to(DEV)
+    weight, length = torch.from_numpy(w).to(DEV), _ints(lens.tolist())
+    t_out, w_out, l_out = torch.empty_like(table), torch.empty_like(weight), torch.empty_like(length)
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    G.kv8_evict(table, weight, length, keep, sink, recent, t_out, w_out, l_out, status)
+    assert int(status.item()) == 0
+    for b in range(B):
+        for g in range(8):
+            t, ww, m = kv8.evict(table[b, g].tolist(), w[b, g], int(lens[b]), keep, sink, recent)
+            assert t_out[b, g].tolist() == t, (b, g)
+            assert np.array_equal(w_out[b, g].cpu().numpy(), np.array(ww, np.float32), equal_nan=True)
+            assert int(l_out[b]) == m
+    # in place
+    G.kv8_evict(table, weight, length, keep, sink, recent, table, weight, l_out, status)
+    assert torch.equal(table, t_out) and torch.equal(torch.nan_to_num(weight), torch.nan_to_num(w_out))
+
+
+def test_evict_bad_lengths_copy():
+    table = torch.arange(2 * 8 * 3, dtype=torch.int32, device=DEV).view(2, 8, 3)
+    weight = torch.rand(2, 8, 3, device=DEV)
+    t_out, w_out, l_out = torch.empty_like(table), torch.empty_like(weight), _ints([0, 0])
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    G.kv8_evict(table, weight, _ints([-1, 193]), 1, 0, 0, t_out, w_out, l_out, status)
+    assert int(status.item()) == G.DEV_BAD_KV_LEN
+    assert torch.equal(table, t_out) and torch.equal(weight, w_out) and l_out.tolist() == [-1, 193]
+
+
+# ------------------------------------------------------------------------------------------------- together
+@pytest.mark.parametrize("kind", KINDS)
+def test_a_conversation_within_a_budget(kind):
+    """Prompt, steps, eviction, and steps on: rows and positions part, the blocks that were freed are written again."""
+    rng = np.random.default_rng(30)
+    B, max_blocks, tab = 2, 8, tables(1024)
+    cache, host = make_cache(B, max_blocks, kind, seed=20), Host(B)
+    pos, valid = [0, 0], [450, 333]
+    append(cache, host, *rows(rng, B, 450), pos, valid, tab)
+    pos = list(valid)
+    weight = torch.zeros(B, 8, max_blocks, device=DEV)
+    total = np.zeros((B, 8, max_blocks))
+    # per head from here on: the rows a head holds
+    held = [[(host.k[b][:, g], host.v[b][:, g]) for g in range(8)] for b in range(B)]
+    length = list(valid)
+    ws = G.alloc_kv8_decode_workspace(cache)
+    for step in range(70):
+        q, k, v = rows(rng, B, 1)
+        q_rot = torch.empty_like(q, device=DEV)
+        G.kv8_append(cache, q.to(DEV), k.to(DEV), v.to(DEV), _ints(pos), _ints(length), None, *tab, q_rot)
+        k_rot = R.rotary_embedding(_bits(k), np.array(pos))
+        for b in range(B):
+            held[b] = [(np.concatenate([kk, k_rot[b, :, g]]), np.concatenate([vv, _bits(v)[b, :, g]]))
+                       for g, (kk, vv) in enumerate(held[b])]
+            pos[b] += 1
+            length[b] += 1
+        out = torch.empty(B, 48, 128, dtype=torch.bfloat16, device=DEV)
+        G.kv8_decode(cache, q_rot[:, 0], _ints(length), ws, out, weight, weight)
+        if step % 23 == 0 or step == 69:
+            got = out.float().cpu().numpy()
+            x = bf16.to_f64(_bits(q_rot))[:, 0]
+            exact = np.zeros((B, 48, 128))
+            for b in range(B):
+                for g in range(8):
+                    K, V = (kv8.held(h, kind) for h in held[b][g])
+                    exact[b, 6 * g:6 * g + 6], _ = kv8.attend(x[b, 6 * g:6 * g + 6], K, V)
+            assert_close(_bits(out), bf16.from_f64(exact), f"conversation {kind} step {step}")
+            assert np.isfinite(got).all()
+        if step in (20, 55):
+            keep = 4 if step == 20 else 2
+            old, w = cache.table.clone(), weight.cpu().numpy()
+            t_out, l_out = torch.empty_like(old), _ints(length)
+            G.kv8_evict(old, weight, _ints(length), keep, 1, 1, t_out, weight, l_out)
+            cache = cache.with_table(t_out)
+            for b in range(B):
+                for g in range(8):
+                    t, _, m = kv8.evict(old[b, g].tolist(), w[b, g], length[b], keep, 1, 1)
+                    assert t_out[b, g].tolist() == t
+                    order = [old[b, g].tolist().index(x) for x in t[:(m + 63) // 64]]
+                    held[b][g] = tuple(np.concatenate([h[64 * i:64 * i + 64] for i in order]) for h in held[b][g])
+                    assert len(held[b][g][0]) == m
+            length = l_out.tolist()
+    del total
+
+
+def test_a_captured_step_on_another_stream():
+    """Append, decode and accumulation captured once and replayed with new inputs, on a side stream, equal the eager calls."""
+    rng = np.random.default_rng(31)
+    B, tab = 3, tables(512)
+    lens = [100, 63, 300]
+    cache, host = filled(rng, lens, "int8", 6, seed=21)
+    twin = G.Kv8Cache(*(x.clone() for x in (cache.k_pool, cache.v_pool, cache.k_scale, cache.v_scale, cache.table,
+                                            cache.open_k, cache.open_v)))
+    ws, ws2 = G.alloc_kv8_decode_workspace(cache), G.alloc_kv8_decode_workspace(cache)
+    q, k, v = (x.to(DEV) for x in rows(rng, B, 1))
+    q_rot, out = torch.zeros_like(q), torch.zeros(B, 48, 128, dtype=torch.bfloat16, device=DEV)
+    length, rows_now, weight = _ints(lens), _ints([n + 1 for n in lens]), torch.zeros(B, 8, 6, device=DEV)
+
+    def step(c, w, x, o, wt, stream=None):
+        G.kv8_append(c, q, k, v, length, length, None, *tab, x, stream=stream)
+        G.kv8_decode(c, x[:, 0], rows_now, w, o, wt, wt, stream=stream)
+
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        step(cache, ws, q_rot, out, weight)
+    eager_x, eager_out, eager_w = torch.zeros_like(q), torch.zeros_like(out), torch.zeros_like(weight)
+    for _ in range(4):
+        q.copy_(rows(rng, B, 1)[0])
+        k.copy_(rows(rng, B, 1)[1])
+        v.copy_(rows(rng, B, 1)[2])
+        graph.replay()
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            step(twin, ws2, eager_x, eager_out, eager_w, stream=side)
+        torch.cuda.synchronize()
+        assert torch.equal(out, eager_out) and torch.equal(weight, eager_w) and torch.equal(q_rot, eager_x)
+        length += 1
+        rows_now += 1
+    for a in ("k_pool", "v_pool"):
+        assert torch.equal(getattr(cache, a).view(torch.uint8), getattr(twin, a).view(torch.uint8))
