@@ -80,6 +80,8 @@ EXPORTS = (
     "grok_kv8_append",
     "grok_kv8_decode_workspace",
     "grok_kv8_decode",
+    "grok_kv8_prefill_workspace",
+    "grok_kv8_prefill",
     "grok_kv8_evict",
 )
 
@@ -177,6 +179,10 @@ def load() -> ctypes.CDLL:
     lib.grok_kv8_decode_workspace.argtypes = [I, I, I, ctypes.POINTER(S)]
     lib.grok_kv8_decode.restype = I
     lib.grok_kv8_decode.argtypes = [P, P, P, P, S, P, P, P, P, P]
+    lib.grok_kv8_prefill_workspace.restype = I
+    lib.grok_kv8_prefill_workspace.argtypes = [I, I, ctypes.POINTER(S)]
+    lib.grok_kv8_prefill.restype = I
+    lib.grok_kv8_prefill.argtypes = [P, P, P, P, I, P, P, S, P, P]
     lib.grok_kv8_evict.restype = I
     lib.grok_kv8_evict.argtypes = [P, P, P, I, I, I, I, I, P, P, P, P, P]
     _lib = lib
@@ -691,5 +697,5 @@ def decode_step_chained(q, k, v, start_pos, cache_k, cache_v, workspace, out, de
                                         _stream(stream)))
 
 
-from .kv8 import (Kv8Cache, alloc_kv8_cache, alloc_kv8_decode_workspace, kv8_append, kv8_decode,  # noqa: E402,F401
-                  kv8_decode_workspace, kv8_evict)
+from .kv8 import (Kv8Cache, alloc_kv8_cache, alloc_kv8_decode_workspace, alloc_kv8_prefill_workspace,  # noqa: E402,F401
+                  kv8_append, kv8_decode, kv8_decode_workspace, kv8_evict, kv8_prefill, kv8_prefill_workspace)

@@ -2,6 +2,8 @@
 // conversions between codes and 16-bit floating point.
 #pragma once
 
+#include <cuda_fp16.h>
+
 #include "common.cuh"
 
 namespace grok {

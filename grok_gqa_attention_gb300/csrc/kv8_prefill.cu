@@ -1,0 +1,329 @@
+// Attention of many tokens over the 8-bit KV cache.
+//
+// Code-reading guide ch. 4 §4.5.2-§4.5.4, ch. 6 §6.4.2, over code * scale. A first
+// kernel lays the blocks that the call sees out for the tensor cores: K codes
+// as bf16 (exact) and V as fp16, rows of a sequence and head in order. The
+// attention kernel (prefill_kernel.cuh, kQ8) multiplies the logits of each 64-key
+// step by the block's K scale and the outputs by the head's V scale: a V value is
+// rounded once to fp16 on the scale vs / max vs of its block, 2^-12 relative.
+//
+// Tensor-bound for all but short calls: the copies cost 1 byte read, 2 written
+// and 2 read per code against 24 products of it for every 128 new tokens.
+#include "host.cuh"
+#include "kv8.cuh"
+#include "prefill_kernel.cuh"
+
+namespace grok {
+
+constexpr int kUnThreads = 256;
+
+struct UnParams {
+  grok_kv8_cache c;
+  const int32_t *cache_len, *valid_len;
+  int T, rows;         // rows of a sequence's copies
+  uint4 *k_copy, *v_copy;  // [B][rows][8][128] bf16, fp16
+  float* k_scale;      // [B][8][rows / 64]
+  float* o_scale;      // [B][8]
+  int32_t* zero;       // words that the attention passes expect to be zero
+  int n_zero;
+  int32_t* status;
+};
+
+// V values on the copy's common scale: codes up to 127 or 448 times vs / max vs times this stay below 65504.
+constexpr float kVTop = 128.f;
+
+// Four int8 or e4m3 codes to bf16 pairs, exactly. int8: the seven low bits b behind 0x43 are 128 + b, the sign bit there
+// is 128 or 256, and the difference is the code.
+template <int kKind>
+__device__ __forceinline__ void kv8_to_bf16(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  if (kKind == GROK_KV8_INT8) {
+    const uint32_t a = __byte_perm(w, 0x43434343u, 0x4140), b = __byte_perm(w, 0x43434343u, 0x4342);
+    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(lo) : "r"(a & 0xFF7FFF7Fu), "r"(a & 0xFF80FF80u));
+    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(hi) : "r"(b & 0xFF7FFF7Fu), "r"(b & 0xFF80FF80u));
+  } else {
+    uint32_t x[2];
+    kv8_to_half<kKind>(w, x[0], x[1]);
+    const float2 a = __half22float2(reinterpret_cast<const __half2&>(x[0]));
+    const float2 b = __half22float2(reinterpret_cast<const __half2&>(x[1]));
+    lo = pack_bf16x2(a.x, a.y);
+    hi = pack_bf16x2(b.x, b.y);
+  }
+}
+
+__device__ __forceinline__ uint32_t scale_half2(uint32_t x, float f) {
+  const float2 a = __half22float2(reinterpret_cast<const __half2&>(x));
+  return pack_f16x2(a.x * f, a.y * f);
+}
+
+// Grid (parts, KV head, sequence): a CTA takes every parts-th block of its head.
+template <int kKind>
+__global__ void __launch_bounds__(kUnThreads) kv8_unpack_kernel(const UnParams p) {
+  __shared__ float s_top[kUnThreads / 32];
+  const int g = blockIdx.y, b = blockIdx.z, tid = threadIdx.x;
+  if (blockIdx.x == 0 && g == 0 && b == 0)
+    for (int i = tid; i < p.n_zero; i += kUnThreads) p.zero[i] = 0;
+  const int s = __ldg(p.cache_len + b), n = p.valid_len ? __ldg(p.valid_len + b) : p.T;
+  if (s < 0 || n < 1 || n > p.T || (long long)s + n > (long long)p.c.max_blocks * kKv8Block) return;  // reported later
+  const int len = s + n, blocks = (len + kKv8Block - 1) / kKv8Block;
+  const size_t head = (size_t)b * kKVHeads + g;
+  const int32_t* table = p.c.table + head * p.c.max_blocks;
+  // The head's scales: the largest V scale, and every block's K scale. A block whose values are not finite shows it
+  // in the logits (a NaN in the copy of V would reach rows that do not see the block).
+  float top = 0.f;
+  for (int i = tid; i < blocks; i += kUnThreads) {
+    const int id = max(0, kv8_block_id(table, i, p.c.n_blocks, p.status));
+    const float vs = __ldg(p.c.v_scale + id);
+    if (vs == vs) top = fmaxf(top, vs);
+    if (blockIdx.x == 0) p.k_scale[head * (p.rows / kKv8Block) + i] = vs == vs ? __ldg(p.c.k_scale + id) : vs;
+  }
+#pragma unroll
+  for (int d = 16; d; d /= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+  if ((tid & 31) == 0) s_top[tid >> 5] = top;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kUnThreads / 32; ++w) top = fmaxf(top, s_top[w]);
+  if (blockIdx.x == 0 && tid == 0) p.o_scale[head] = top / kVTop;
+  const float per = top > 0.f ? kVTop / top : 0.f;
+
+  // Rows up to the next multiple of 128: those behind the last are zeros (in V they meet zero weights).
+  const int pad = (blocks + 1) / 2 * 2;
+  uint4* k_out = p.k_copy + ((size_t)b * p.rows * kKVHeads + g) * 16;
+  uint4* v_out = p.v_copy + ((size_t)b * p.rows * kKVHeads + g) * 16;
+  for (int i = blockIdx.x; i < pad; i += gridDim.x) {
+    const int left = min(kKv8Block, len - i * kKv8Block);  // rows of this block (negative in the padding)
+    const int id = left > 0 ? max(0, kv8_block_id(table, i, p.c.n_blocks, nullptr)) : 0;
+    const uint8_t* k_src = static_cast<const uint8_t*>(p.c.k_pool) + (size_t)id * kKv8Bytes;
+    const uint8_t* v_src = static_cast<const uint8_t*>(p.c.v_pool) + (size_t)id * kKv8Bytes;
+    float f = left > 0 ? __ldg(p.c.v_scale + id) : 0.f;
+    f = f == f ? f * per : 0.f;
+    // K: thread = (row, 8 codes) of one half, four passes
+#pragma unroll
+    for (int m = 0; m < 4; ++m) {
+      const int e = tid + m * kUnThreads, row = (e >> 3) & 63, c = e & 7, h = e >> 9;
+      uint4 x = make_uint4(0, 0, 0, 0);
+      if (row < left) {
+        const uint2 w = __ldg(reinterpret_cast<const uint2*>(k_src + h * (kKv8Bytes / 2) + row * 64 + c * 8));
+        kv8_to_bf16<kKind>(w.x, x.x, x.y);
+        kv8_to_bf16<kKind>(w.y, x.z, x.w);
+      }
+      k_out[(size_t)(i * kKv8Block + row) * (kKVHeads * 16) + h * 8 + c] = x;
+    }
+    // V: thread = four rows of eight features, turned in registers
+    const int q = tid & 15, c = tid >> 4;
+    uint32_t w[8];
+#pragma unroll
+    for (int d = 0; d < 8; ++d) w[d] = left > 4 * q ? __ldg(reinterpret_cast<const uint32_t*>(v_src + (8 * c + d) * 64 + 4 * q)) : 0u;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      uint4 x = make_uint4(0, 0, 0, 0);
+      if (4 * q + r < left) {
+        uint32_t a, z;
+        const uint32_t sel = r | (r + 4) << 4;
+        const uint32_t w0 = __byte_perm(__byte_perm(w[0], w[1], sel), __byte_perm(w[2], w[3], sel), 0x5410);
+        const uint32_t w1 = __byte_perm(__byte_perm(w[4], w[5], sel), __byte_perm(w[6], w[7], sel), 0x5410);
+        kv8_to_half<kKind>(w0, a, z);
+        x.x = scale_half2(a, f), x.y = scale_half2(z, f);
+        kv8_to_half<kKind>(w1, a, z);
+        x.z = scale_half2(a, f), x.w = scale_half2(z, f);
+      }
+      v_out[(size_t)(i * kKv8Block + 4 * q + r) * (kKVHeads * 16) + c] = x;
+    }
+  }
+}
+
+// The fallback pass multiplies bf16: when an item is listed, the copy of V is rounded to bf16 in its place.
+__global__ void __launch_bounds__(256) kv8_v_to_bf16_kernel(const int32_t* fb_count, uint4* v, long long n) {
+  if (__ldg(fb_count) == 0) return;
+  for (long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += (long long)gridDim.x * blockDim.x) {
+    uint4 x = v[i];
+    uint32_t* w = reinterpret_cast<uint32_t*>(&x);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float2 a = __half22float2(reinterpret_cast<const __half2&>(w[e]));
+      w[e] = pack_bf16x2(a.x, a.y);
+    }
+    v[i] = x;
+  }
+}
+
+}  // namespace grok
+
+using namespace grok;
+
+namespace {
+
+size_t up256(size_t n) { return (n + 255) & ~size_t(255); }
+
+// Workspace: fallback count and list, K scales, output factors, the copies of K and V, the split's area.
+struct Layout {
+  int rows;
+  size_t k_scale, o_scale, k_copy, v_copy, split, bytes;
+};
+
+Layout layout(int B, int max_blocks, int sms) {
+  Layout w;
+  w.rows = (max_blocks + 1) / 2 * 2 * kKv8Block;
+  w.k_scale = up256((1 + size_t(ws_fb_cap(B, w.rows))) * sizeof(int32_t));
+  w.o_scale = w.k_scale + up256(size_t(B) * kKVHeads * (w.rows / kKv8Block) * sizeof(float));
+  w.k_copy = w.o_scale + up256(size_t(B) * kKVHeads * sizeof(float));
+  const size_t copy = size_t(B) * w.rows * kKVHeads * kD * 2;
+  w.v_copy = w.k_copy + copy;
+  w.split = w.v_copy + copy;
+  w.bytes = w.split + (split_allowed(w.rows) ? split_area_bytes(sms) : 0);
+  return w;
+}
+
+grok_status sizes_ok(int B, int max_blocks, const char* who) {
+  if (B < 1 || B > 65535 || max_blocks < 1 || max_blocks > kKv8MaxBlocks || (long long)B * max_blocks > (1 << 21))
+    return fail(GROK_ERR_INVALID_ARG, "%s: need 1 <= B <= 65535, 1 <= max_blocks <= %d, B * max_blocks <= %d", who,
+                kKv8MaxBlocks, 1 << 21);
+  return GROK_OK;
+}
+
+struct Maps {
+  CUtensorMap q, k, v, v_bf16, out;
+};
+
+template <typename Kernel>
+grok_status launch(Kernel kernel, int which, int grid, const Maps& m, const CUtensorMap& v, const PfParams& p, bool dependent,
+                   cudaStream_t s) {
+  static bool attr_set[kMaxDevices][3] = {};  // per device and kernel; idempotent: every thread would set the same value
+  int dev = 0;
+  grok_status st = device_index(&dev);
+  if (st != GROK_OK) return st;
+  if (!attr_set[dev][which]) {
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kPfSmem);
+    if (e != cudaSuccess) return fail(cuda_status(e), "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
+    attr_set[dev][which] = true;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(kPfThreads);
+  cfg.dynamicSmemBytes = kPfSmem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = dependent ? 1 : 0;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, m.q, m.k, v, m.out, p);
+  if (e != cudaSuccess) return fail(cuda_status(e), "kv8_prefill launch: %s", cudaGetErrorString(e));
+  return check_launch("kv8_prefill");
+}
+
+}  // namespace
+
+extern "C" grok_status grok_kv8_prefill_workspace(int B, int max_blocks, size_t* bytes) {
+  if (!bytes) return fail(GROK_ERR_INVALID_ARG, "grok_kv8_prefill_workspace: null pointer");
+  grok_status st = sizes_ok(B, max_blocks, "grok_kv8_prefill_workspace");
+  if (st != GROK_OK) return st;
+  int sms = 0;
+  if ((st = device_sm_count(&sms)) != GROK_OK) return st;
+  *bytes = layout(B, max_blocks, sms).bytes;
+  return GROK_OK;
+}
+
+extern "C" grok_status grok_kv8_prefill(const grok_kv8_cache* cache, const grok_bf16* q_rot, const int32_t* cache_len,
+                                        const int32_t* valid_len, int T, grok_bf16* out, void* workspace,
+                                        size_t workspace_bytes, int32_t* dev_status, void* stream) {
+  grok_status st = kv8_check(cache, "grok_kv8_prefill");
+  if (st != GROK_OK) return st;
+  if (!q_rot || !cache_len || !out || !workspace)
+    return fail(GROK_ERR_INVALID_ARG, "grok_kv8_prefill: null pointer");
+  if (!aligned16(q_rot) || !aligned16(out))
+    return fail(GROK_ERR_INVALID_ARG, "grok_kv8_prefill: bf16 tensors must be 16-byte aligned");
+  if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
+    return fail(GROK_ERR_INVALID_ARG, "grok_kv8_prefill: workspace must be 256-byte aligned");
+  const int B = cache->B, max_blocks = cache->max_blocks;
+  if ((st = sizes_ok(B, max_blocks, "grok_kv8_prefill")) != GROK_OK) return st;
+  if (T < 1 || T > max_blocks * kKv8Block)
+    return fail(GROK_ERR_INVALID_ARG, "grok_kv8_prefill: need 1 <= T <= max_blocks * %d (T=%d max_blocks=%d)", kKv8Block,
+                T, max_blocks);
+  int sms = 0;
+  if ((st = device_sm_count(&sms)) != GROK_OK) return st;
+  const Layout w = layout(B, max_blocks, sms);
+  if (workspace_bytes < w.bytes)
+    return fail(GROK_ERR_INVALID_ARG, "grok_kv8_prefill: workspace of %zu bytes is smaller than the %zu needed",
+                workspace_bytes, w.bytes);
+  char* ws = static_cast<char*>(workspace);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const int n_items = prefill_items(B, T);
+  int n_whole, n_parts;
+  split_plan(n_items, sms, split_allowed(w.rows), n_whole, n_parts);
+  const int n_split = n_items - n_whole;
+
+  Maps m;
+  const uint32_t box[4] = {64, 1, 128, 1}, obox[4] = {64, 1, 32, 1};
+  const uint64_t qdims[4] = {kD, kQHeads, uint64_t(T), uint64_t(B)};
+  const uint64_t qstrides[3] = {kD * 2, uint64_t(kQHeads) * kD * 2, uint64_t(T) * kQHeads * kD * 2};
+  const uint64_t dims[4] = {kD, kKVHeads, uint64_t(w.rows), uint64_t(B)};
+  const uint64_t strides[3] = {kD * 2, uint64_t(kKVHeads) * kD * 2, uint64_t(w.rows) * kKVHeads * kD * 2};
+  if ((st = encode_tmap_bf16_4d(&m.q, q_rot, qdims, qstrides, box)) != GROK_OK ||
+      (st = encode_tmap_bf16_4d(&m.out, out, qdims, qstrides, obox)) != GROK_OK ||
+      (st = encode_tmap_bf16_4d(&m.k, ws + w.k_copy, dims, strides, box)) != GROK_OK ||
+      (st = encode_tmap_f16_4d(&m.v, ws + w.v_copy, dims, strides, box)) != GROK_OK ||
+      (st = encode_tmap_bf16_4d(&m.v_bf16, ws + w.v_copy, dims, strides, box)) != GROK_OK)
+    return st;
+
+  int32_t* fb_count = reinterpret_cast<int32_t*>(ws);
+  // The fallback count comes first and the split's counters are apart: the first is cleared here, the second there.
+  cudaError_t e = cudaMemsetAsync(fb_count, 0, sizeof(int32_t), s);
+  if (e != cudaSuccess) return fail(cuda_status(e), "cudaMemsetAsync: %s", cudaGetErrorString(e));
+  const UnParams u{*cache,
+                   cache_len,
+                   valid_len,
+                   T,
+                   w.rows,
+                   reinterpret_cast<uint4*>(ws + w.k_copy),
+                   reinterpret_cast<uint4*>(ws + w.v_copy),
+                   reinterpret_cast<float*>(ws + w.k_scale),
+                   reinterpret_cast<float*>(ws + w.o_scale),
+                   reinterpret_cast<int32_t*>(ws + w.split),
+                   2 * n_split,
+                   dev_status};
+  const int heads = B * kKVHeads;
+  const int parts = std::max(1, std::min((max_blocks + 1) / 2 * 2, (sms * 6 + heads - 1) / heads));
+  auto unpack = cache->kind == GROK_KV8_INT8 ? kv8_unpack_kernel<GROK_KV8_INT8> : kv8_unpack_kernel<GROK_KV8_E4M3>;
+  unpack<<<dim3(parts, kKVHeads, B), kUnThreads, 0, s>>>(u);
+  if ((st = check_launch("kv8_unpack")) != GROK_OK) return st;
+
+  PfParams p = {};
+  p.B = B;
+  p.T = T;
+  p.Tmax = max_blocks * kKv8Block;
+  p.n_qt = (T + kPfRows - 1) / kPfRows;
+  p.n_items = n_items;
+  p.pm = PageMap{nullptr, 0, 0};
+  p.start_pos = cache_len;
+  p.valid_len = valid_len;
+  p.status = dev_status;
+  p.fb_count = fb_count;
+  p.fb_list = fb_count + 1;
+  p.fb_cap = ws_fb_cap(B, w.rows);
+  p.n_parts = 1;
+  p.k_scale = u.k_scale;
+  p.k_scale_stride = w.rows / kKv8Block;
+  p.o_scale = u.o_scale;
+  if (n_whole > 0) {
+    p.n_units = n_whole;
+    if ((st = launch(prefill_kernel<true, false, false, true>, 0, std::min(n_whole, sms), m, m.v, p, false, s)) != GROK_OK)
+      return st;
+  }
+  if (n_split > 0) {
+    PfParams ps = p;
+    ps.item_base = n_whole;
+    ps.n_parts = n_parts;
+    ps.n_units = n_split * n_parts;
+    ps.part_cnt = reinterpret_cast<int32_t*>(ws + w.split);
+    ps.part_lm = reinterpret_cast<float2*>(ws + w.split + split_cnt_bytes(sms));
+    ps.part_o = reinterpret_cast<float4*>(ws + w.split + split_cnt_bytes(sms) + split_lm_bytes(sms));
+    if ((st = launch(prefill_kernel<true, false, true, true>, 1, std::min(ps.n_units, sms), m, m.v, ps, false, s)) != GROK_OK)
+      return st;
+  }
+  kv8_v_to_bf16_kernel<<<sms, 256, 0, s>>>(fb_count, u.v_copy, (long long)B * w.rows * kKVHeads * (kD / 8));
+  if ((st = check_launch("kv8_v_to_bf16")) != GROK_OK) return st;
+  p.item_list = p.fb_list;
+  p.item_count = fb_count;
+  p.n_units = n_items;
+  return launch(prefill_kernel<false, true, false, true>, 2, sms, m, m.v_bf16, p, true, s);
+}

@@ -173,6 +173,38 @@ def kv8_decode(cache: Kv8Cache, q_rot, kv_len, workspace, out, weight_in=None, w
           workspace.numel(), _ptr(out), _ptr(weight_in), _ptr(weight_out), _ptr(dev_status))
 
 
+def kv8_prefill_workspace(B: int, max_blocks: int) -> int:
+    """Bytes of workspace for kv8_prefill() on the current device."""
+    n = ctypes.c_size_t(0)
+    _check(load().grok_kv8_prefill_workspace(int(B), int(max_blocks), ctypes.byref(n)))
+    return n.value
+
+
+def alloc_kv8_prefill_workspace(cache: Kv8Cache) -> torch.Tensor:
+    with _on(cache.device):
+        return torch.empty(kv8_prefill_workspace(cache.B, cache.max_blocks), dtype=torch.uint8, device=cache.device)
+
+
+def kv8_prefill(cache: Kv8Cache, q_rot, cache_len, valid_len, out, workspace, dev_status=None, stream=None) -> None:
+    """out [B, T, 48, 128]: token i of sequence b attends rows j <= cache_len[b] + i, j < cache_len[b] + valid_len[b].
+
+    The tokens' own rows are in the cache already (kv8_append with the same cache_len and valid_len, which may be None).
+    """
+    B, T = cache.B, q_rot.shape[1]
+    _want(q_rot, "q_rot", torch.bfloat16, (B, T, N_Q_HEADS, HEAD_DIM))
+    _want(cache_len, "cache_len", torch.int32, (B,))
+    if valid_len is not None:
+        _want(valid_len, "valid_len", torch.int32, (B,))
+    _want(out, "out", torch.bfloat16, (B, T, N_Q_HEADS, HEAD_DIM))
+    _want(workspace, "workspace", torch.uint8, (workspace.numel(),))
+    if dev_status is not None:
+        _want(dev_status, "dev_status", torch.int32, (1,))
+    _same_device(cache.device, q_rot=q_rot, cache_len=cache_len, valid_len=valid_len, out=out, workspace=workspace,
+                 dev_status=dev_status)
+    _call(cache.device, stream, "grok_kv8_prefill", cache._ref, _ptr(q_rot), _ptr(cache_len), _ptr(valid_len), T,
+          _ptr(out), _ptr(workspace), workspace.numel(), _ptr(dev_status))
+
+
 def kv8_evict(table, weight, kv_len, keep: int, sink: int, recent: int, table_out, weight_out, kv_len_out,
               dev_status=None, stream=None) -> None:
     """Down to `keep` full blocks per sequence and head: the first `sink`, the last `recent`, then by weight.

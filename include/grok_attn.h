@@ -638,6 +638,31 @@ grok_status grok_kv8_decode(const grok_kv8_cache* cache, const grok_bf16* q_rot,
                             float* weight_out, int32_t* dev_status, void* stream);
 
 /*
+ * Attention of T tokens per sequence over the cache that holds them already:
+ * grok_attn_prefill_ws over the 8-bit cache. Token i of sequence b attends rows
+ * j <= cache_len[b] + i, j < cache_len[b] + valid_len[b]; padding tokens (i >=
+ * valid_len[b]) are computed too.
+ *   q_rot, out [B,T,48,128]; cache_len [B] int32: rows before these tokens;
+ *   valid_len [B] int32 or NULL (= T); 1 <= T <= max_blocks * 64.
+ * valid_len[b] outside [1, T] sets GROK_DEV_BAD_VALID, cache_len[b] < 0 or
+ * cache_len[b] + valid_len[b] > max_blocks * 64 GROK_DEV_BAD_KV_LEN; the sequence's
+ * outputs are left as they were.
+ * The rows are first copied to the workspace, K codes as bf16 (exact), V as fp16
+ * on a common scale per sequence and head (2^-12 relative for values down to
+ * 2^-28 of the head's largest); softmax weights are rounded to fp16 as in
+ * grok_attn_prefill_ws. Items whose weights leave fp16's range are recomputed with
+ * bf16 hi + lo weights and V rounded to bf16.
+ *   workspace: device memory, 256-byte aligned, of at least
+ *   grok_kv8_prefill_workspace(B, max_blocks) bytes for the current device (4 KB
+ *   per row of the cache and sequence, B * max_blocks <= 2^21, and about 20 MB).
+ *   Calls that overlap on the GPU need separate workspaces; nothing is kept.
+ */
+grok_status grok_kv8_prefill_workspace(int B, int max_blocks, size_t* bytes);
+grok_status grok_kv8_prefill(const grok_kv8_cache* cache, const grok_bf16* q_rot, const int32_t* cache_len,
+                             const int32_t* valid_len, int T, grok_bf16* out, void* workspace, size_t workspace_bytes,
+                             int32_t* dev_status, void* stream);
+
+/*
  * Eviction by accumulated weight. For sequence b and KV head g with nc =
  * kv_len[b] / 64 full blocks: where nc > keep, the first `sink` and the last
  * `recent` full blocks stay, and of the others those with the largest weight

@@ -392,6 +392,174 @@ def test_workspace_too_small_is_refused():
         G.kv8_decode(cache, q, _ints([10]), ws[:-256], out)
 
 
+# ------------------------------------------------------------------------------------------------- prefill
+def run_prefill(cache, q_rot, lens, valid, T):
+    out = torch.full((cache.B, T, 48, 128), 7.0, dtype=torch.bfloat16, device=DEV)
+    ws = G.alloc_kv8_prefill_workspace(cache)
+    ws.fill_(0xff)
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    G.kv8_prefill(cache, q_rot, _ints(lens), _ints(valid) if valid else None, out, ws, status)
+    torch.cuda.synchronize()
+    return out, int(status.item())
+
+
+def check_prefill(host, q_rot, got, lens, valid, kind, what, picks=None, heads=range(48)):
+    """The rows `picks` (default: edges of the tiles and the sequence) of every sequence against the oracle."""
+    T = q_rot.shape[1]
+    x, y = bf16.to_f64(_bits(q_rot)), _bits(got)
+    want, have = [], []
+    for b in range(len(lens)):
+        n = valid[b]
+        rows_ = sorted({i for i in (picks or (0, 1, 31, 63, 64, 65, 127, 128, 129, 200, 255, 256, n - 1, n, T - 1))
+                        if 0 <= i < T})
+        last = np.minimum(lens[b] + np.array(rows_), lens[b] + n - 1)
+        for g in sorted({h // 6 for h in heads}):
+            K, V = kv8.held(host.k[b][:, g], kind), kv8.held(host.v[b][:, g], kind)
+            for h in range(6 * g, 6 * g + 6):
+                o, _ = kv8.attend(x[b, rows_, h], K, V, last)
+                want.append(o)
+                have.append(y[b, rows_, h])
+    return assert_close(np.concatenate(have), bf16.from_f64(np.concatenate(want)), what)
+
+
+def logit_error(q, K):
+    """A 128-term fp32 sum: at most 128 * 2^-23 of the sum of the terms' magnitudes."""
+    return 128 * 2.0 ** -23 * (np.abs(q) @ np.abs(K).T).max() / 128 ** 0.5
+
+
+PREFILLS = {
+    # warm rows, valid tokens, padded T
+    "tiny": ([0], [1], 1),
+    "one_tile": ([0], [128], 128),
+    "odd": ([0, 5, 64], [200, 77, 131], 200),
+    "warm": ([130, 700, 63], [90, 33, 1], 90),
+    "chunk_split": ([2100, 1900], [150, 61], 150),
+    "ragged": ([0, 0, 0, 0], [300, 1, 64, 129], 300),
+}
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("name", list(PREFILLS))
+def test_prefill(kind, name):
+    lens, valid, T = PREFILLS[name]
+    rng = np.random.default_rng(40)
+    B = len(lens)
+    max_blocks, tab = (max(lens) + T + 63) // 64, tables(max(lens) + T + 1)
+    cache, host = make_cache(B, max_blocks, kind, seed=30), Host(B)
+    if max(lens):
+        warm = [max(n, 1) for n in lens]
+        append(cache, host, *rows(rng, B, max(lens)), [0] * B, warm, tab)
+        lens = warm
+    q_rot = append(cache, host, *rows(rng, B, T), lens, valid, tab)
+    got, status = run_prefill(cache, q_rot, lens, valid, T)
+    assert status == 0
+    check_prefill(host, q_rot, got, lens, valid, kind, f"kv8 prefill {kind} {name}")
+    assert torch.equal(run_prefill(cache, q_rot, lens, valid, T)[0], got)
+
+
+def test_prefill_of_one_token_is_the_decode():
+    rng = np.random.default_rng(41)
+    cache, host = filled(rng, [300, 65], "int8", 5, seed=31)
+    q = _bf16(rng.standard_normal((2, 1, 48, 128)) * 3).to(DEV)
+    a, _ = run_prefill(cache, q, [299, 64], [1, 1], 1)
+    b, _, _ = run_decode(cache, q[:, 0].contiguous(), [300, 65])
+    assert_close(_bits(a[:, 0]), _bits(b), "kv8 prefill against decode")
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_prefill_block_magnitudes_apart(kind):
+    """V blocks 2^-12 to 2^12 of one another, keys 2^-3 to 2^1: each element still within its own block's share."""
+    rng = np.random.default_rng(42)
+    L = 400
+    cache, host, tab = make_cache(1, 7, kind, seed=32), Host(1), tables(512)
+    q, k, v = rows(rng, 1, L)
+    vm = 2.0 ** rng.integers(-12, 13, (1, 7, 8, 1)).repeat(64, 1)[:, :L]
+    km = 2.0 ** rng.integers(-3, 2, (1, 7, 8, 1)).repeat(64, 1)[:, :L]
+    v, k = (v.float() * torch.from_numpy(vm).float()).bfloat16(), (k.float() * torch.from_numpy(km).float()).bfloat16()
+    q_rot = append(cache, host, q, k, v, [0], [L], tab)
+    got, _ = run_prefill(cache, q_rot, [0], [L], L)
+    x, y = bf16.to_f64(_bits(q_rot)), got.float().cpu().numpy().astype(np.float64)
+    for h in range(0, 48, 5):
+        K, V = kv8.held(host.k[0][:, h // 6], kind), kv8.held(host.v[0][:, h // 6], kind)
+        o, w = kv8.attend(x[0, :, h], K, V, np.arange(L))
+        # half a step of bf16; a weight is off by its fp16 rounding (2^-11), by tanh and exp2 (1e-5 of 30, that is 3e-4)
+        # and by its logit (a 128-term fp32 sum), in the sum too; below fp16's normal range by 2^-17 of the row's
+        # largest; V by 2^-11, or 2^-40 of the head's largest
+        rel = 2.0 ** -11 + 2 * (3e-4 + logit_error(x[0, :, h], K)) + 2.0 ** -11
+        tol = 2.0 ** -8 * np.abs(o) + rel * (w @ np.abs(V)) + 2.0 ** -17 * np.abs(V).sum(0) * w.max(1, keepdims=True) \
+            + 2.0 ** -40 * np.abs(V).max()
+        assert (np.abs(y[0, :, h] - o) <= tol).all(), h
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_prefill_weights_that_outgrow_fp16(kind):
+    """A first tile of small logits and a later key at the cap: those items are computed again in bf16, V rounded to
+    bf16 there (2^-9 of each value, within the tolerance of one bf16 step of the result)."""
+    rng = np.random.default_rng(43)
+    L = 300
+    cache, host, tab = make_cache(2, 5, kind, seed=33), Host(2), tables(512)
+    q, k, v = rows(rng, 2, L)
+    k[0] = (k[0].float() * 0.02).bfloat16()
+    q[0, :, :6] = q[0, 200, 0]
+    k[0, 200, 0] = q[0, 200, 0]
+    # the rotation keeps q . k only at equal positions: rotate by none
+    tab = (torch.ones_like(tab[0]), torch.zeros_like(tab[1]))
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    q_rot = torch.zeros_like(q, device=DEV)
+    G.kv8_append(cache, q.to(DEV), k.to(DEV), v.to(DEV), _ints([0, 0]), _ints([0, 0]), None, *tab, q_rot, status)
+    assert torch.equal(q_rot.cpu(), q)
+    for b in range(2):
+        host.k[b], host.v[b] = _bits(k)[b], _bits(v)[b]
+    got, st = run_prefill(cache, q_rot, [0, 0], [L, L], L)
+    assert st == 0
+    x, y = bf16.to_f64(_bits(q_rot)), got.float().cpu().numpy().astype(np.float64)
+    for b in range(2):
+        for h in (0, 5, 7, 47):
+            K, V = kv8.held(host.k[b][:, h // 6], kind), kv8.held(host.v[b][:, h // 6], kind)
+            o, w = kv8.attend(x[b, :, h], K, V, np.arange(L))
+            # half a step of the result, 2^-8; of V 2^-8; weights as above (bf16 hi + lo: 2^-16)
+            rel = 2.0 ** -8 + 2.0 ** -11 + 2 * (3e-4 + logit_error(x[b, :, h], K))
+            tol = 2.0 ** -8 * np.abs(o) + rel * (w @ np.abs(V)) \
+                + 2.0 ** -17 * np.abs(V).sum(0) * w.max(1, keepdims=True)
+            assert (np.abs(y[b, :, h] - o) <= tol).all(), (b, h)
+
+
+def test_prefill_non_finite_blocks_reach_their_rows_alone():
+    rng = np.random.default_rng(44)
+    cache, host = filled(rng, [300, 300], "int8", 5, seed=34)
+    q = _bf16(rng.standard_normal((2, 300, 48, 128)) * 3).to(DEV)
+    good, _ = run_prefill(cache, q, [0, 0], None, 300)
+    for scale, b, g, blk in ((cache.k_scale, 0, 1, 1), (cache.v_scale, 1, 3, 2), (cache.v_scale, 1, 5, 4)):
+        at = cache.table[b, g, blk].long()
+        saved = scale[at].clone()
+        scale[at] = float("nan")
+        got, _ = run_prefill(cache, q, [0, 0], None, 300)
+        scale[at] = saved
+        nan = torch.isnan(got).all(-1)
+        want = torch.zeros_like(nan)
+        want[b, 64 * blk:, 6 * g:6 * g + 6] = True
+        assert torch.equal(nan, want)
+        assert torch.equal(got[~want], good[~want])
+
+
+def test_prefill_bad_integers_leave_the_outputs():
+    rng = np.random.default_rng(45)
+    cache, host = filled(rng, [128] * 3, "int8", 2, seed=35)
+    q = _bf16(rng.standard_normal((3, 28, 48, 128))).to(DEV)
+    good, _ = run_prefill(cache, q, [100] * 3, [28] * 3, 28)
+    for lens, valid, bit in (([100, -1, 100], [28] * 3, G.DEV_BAD_KV_LEN), ([100, 101, 100], [28] * 3, G.DEV_BAD_KV_LEN),
+                             ([100] * 3, [28, 0, 28], G.DEV_BAD_VALID), ([100] * 3, [28, 29, 28], G.DEV_BAD_VALID | G.DEV_BAD_KV_LEN)):
+        got, status = run_prefill(cache, q, lens, valid, 28)
+        assert status == bit
+        assert (got[1] == 7.0).all() and torch.equal(got[[0, 2]], good[[0, 2]])
+    # padding tokens past the capacity are no error
+    got, status = run_prefill(cache, q, [110] * 3, [18, 1, 10], 28)
+    assert status == 0
+    cache.table[1, 7, 1] = cache.n_blocks
+    got, status = run_prefill(cache, q, [100] * 3, [28] * 3, 28)
+    assert status == G.DEV_BAD_PAGE and torch.equal(got[[0, 2]], good[[0, 2]])
+
+
 # ------------------------------------------------------------------------------------------------- evict
 EVICTS = [dict(B=3, n=9, keep=4, sink=1, recent=2), dict(B=2, n=40, keep=33, sink=0, recent=0),
           dict(B=2, n=1024, keep=500, sink=4, recent=60), dict(B=4, n=33, keep=1, sink=0, recent=1),

@@ -36,6 +36,10 @@ def _evict(lib, table=A, w=A, length=A, B=2, n=4, keep=2, sink=0, recent=0, t_ou
     return lib.grok_kv8_evict(table, w, length, B, n, keep, sink, recent, t_out, w_out, l_out, None, None)
 
 
+def _prefill(lib, cache=None, q=A, length=A, valid=None, T=4, out=A, ws=A, nbytes=1 << 40):
+    return lib.grok_kv8_prefill(_cache() if cache is None else cache, q, length, valid, T, out, ws, nbytes, None, None)
+
+
 BAD_CACHES = [dict(k_pool=None), dict(v_pool=None), dict(k_scale=None), dict(v_scale=None), dict(table=None),
               dict(open_k=None), dict(open_v=None), dict(k_pool=A + 8), dict(open_v=A + 2), dict(table=A + 4),
               dict(kind=2), dict(kind=-1), dict(B=0), dict(B=65536), dict(max_blocks=0), dict(max_blocks=1025),
@@ -46,6 +50,7 @@ BAD_CACHES = [dict(k_pool=None), dict(v_pool=None), dict(k_scale=None), dict(v_s
 def test_bad_caches(lib, bad):
     assert _append(lib, _cache(**bad)) == 1
     assert _decode(lib, _cache(**bad)) == 1
+    assert _prefill(lib, _cache(**bad)) == 1
 
 
 @pytest.mark.parametrize("bad", [dict(q=None), dict(k=None), dict(v=None), dict(start=None), dict(length=None),
@@ -63,6 +68,13 @@ def test_bad_decodes(lib, bad):
     assert b"grok_kv8_decode" in lib.grok_last_error()
 
 
+@pytest.mark.parametrize("bad", [dict(q=None), dict(length=None), dict(ws=None), dict(out=None), dict(q=A + 8),
+                                 dict(out=A + 8), dict(ws=A + 16), dict(T=0), dict(T=257)], ids=str)
+def test_bad_prefills(lib, bad):
+    assert _prefill(lib, **bad) == 1
+    assert b"grok_kv8_prefill" in lib.grok_last_error()
+
+
 @pytest.mark.parametrize("bad", [dict(table=None), dict(w=None), dict(length=None), dict(t_out=None), dict(w_out=None),
                                  dict(l_out=None), dict(l_out=A), dict(B=0), dict(B=65536), dict(n=0), dict(n=1025),
                                  dict(keep=0), dict(sink=-1), dict(recent=-1), dict(sink=2, recent=1)], ids=str)
@@ -77,6 +89,9 @@ def test_null_cache_and_workspace_sizes(lib):
     assert lib.grok_kv8_decode_workspace(0, 4, 0, ctypes.byref(n)) == 1
     assert lib.grok_kv8_decode_workspace(1, 1025, 0, ctypes.byref(n)) == 1
     assert lib.grok_kv8_decode_workspace(1, 4, 0, None) == 1
+    assert lib.grok_kv8_prefill_workspace(0, 4, ctypes.byref(n)) == 1
+    assert lib.grok_kv8_prefill_workspace(65535, 1024, ctypes.byref(n)) == 1
+    assert lib.grok_kv8_prefill_workspace(1, 4, None) == 1
 
 
 def test_binding_constants_and_cpu_tensors():
