@@ -3,7 +3,7 @@
 // Code-reading guide ch. 4 §4.5.2-§4.5.4, ch. 6 §6.4.2, over code * scale. A first
 // kernel lays the blocks that the call sees out for the tensor cores: K codes
 // as bf16 (exact) and V as fp16, rows of a sequence and head in order. The
-// attention kernel (prefill_kernel.cuh, kQ8) multiplies the logits of each 64-key
+// attention kernel (prefill.cu, kQ8) multiplies the logits of each 64-key
 // step by the block's K scale and the outputs by the head's V scale: a V value is
 // rounded once to fp16 on the scale vs / max vs of its block, 2^-12 relative.
 //
@@ -11,7 +11,7 @@
 // and 2 read per code against 24 products of it for every 128 new tokens.
 #include "host.cuh"
 #include "kv8.cuh"
-#include "prefill_kernel.cuh"
+#include "prefill.cuh"
 
 namespace grok {
 
@@ -180,37 +180,6 @@ grok_status sizes_ok(int B, int max_blocks, const char* who) {
   return GROK_OK;
 }
 
-struct Maps {
-  CUtensorMap q, k, v, v_bf16, out;
-};
-
-template <typename Kernel>
-grok_status launch(Kernel kernel, int which, int grid, const Maps& m, const CUtensorMap& v, const PfParams& p, bool dependent,
-                   cudaStream_t s) {
-  static bool attr_set[kMaxDevices][3] = {};  // per device and kernel; idempotent: every thread would set the same value
-  int dev = 0;
-  grok_status st = device_index(&dev);
-  if (st != GROK_OK) return st;
-  if (!attr_set[dev][which]) {
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kPfSmem);
-    if (e != cudaSuccess) return fail(cuda_status(e), "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
-    attr_set[dev][which] = true;
-  }
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(kPfThreads);
-  cfg.dynamicSmemBytes = kPfSmem;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = dependent ? 1 : 0;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, m.q, m.k, v, m.out, p);
-  if (e != cudaSuccess) return fail(cuda_status(e), "kv8_prefill launch: %s", cudaGetErrorString(e));
-  return check_launch("kv8_prefill");
-}
-
 }  // namespace
 
 extern "C" grok_status grok_kv8_prefill_workspace(int B, int max_blocks, size_t* bytes) {
@@ -252,19 +221,6 @@ extern "C" grok_status grok_kv8_prefill(const grok_kv8_cache* cache, const grok_
   split_plan(n_items, sms, split_allowed(w.rows), n_whole, n_parts);
   const int n_split = n_items - n_whole;
 
-  Maps m;
-  const uint32_t box[4] = {64, 1, 128, 1}, obox[4] = {64, 1, 32, 1};
-  const uint64_t qdims[4] = {kD, kQHeads, uint64_t(T), uint64_t(B)};
-  const uint64_t qstrides[3] = {kD * 2, uint64_t(kQHeads) * kD * 2, uint64_t(T) * kQHeads * kD * 2};
-  const uint64_t dims[4] = {kD, kKVHeads, uint64_t(w.rows), uint64_t(B)};
-  const uint64_t strides[3] = {kD * 2, uint64_t(kKVHeads) * kD * 2, uint64_t(w.rows) * kKVHeads * kD * 2};
-  if ((st = encode_tmap_bf16_4d(&m.q, q_rot, qdims, qstrides, box)) != GROK_OK ||
-      (st = encode_tmap_bf16_4d(&m.out, out, qdims, qstrides, obox)) != GROK_OK ||
-      (st = encode_tmap_bf16_4d(&m.k, ws + w.k_copy, dims, strides, box)) != GROK_OK ||
-      (st = encode_tmap_f16_4d(&m.v, ws + w.v_copy, dims, strides, box)) != GROK_OK ||
-      (st = encode_tmap_bf16_4d(&m.v_bf16, ws + w.v_copy, dims, strides, box)) != GROK_OK)
-    return st;
-
   int32_t* fb_count = reinterpret_cast<int32_t*>(ws);
   // The fallback count comes first and the split's counters are apart: the first is cleared here, the second there.
   cudaError_t e = cudaMemsetAsync(fb_count, 0, sizeof(int32_t), s);
@@ -287,43 +243,28 @@ extern "C" grok_status grok_kv8_prefill(const grok_kv8_cache* cache, const grok_
   unpack<<<dim3(parts, kKVHeads, B), kUnThreads, 0, s>>>(u);
   if ((st = check_launch("kv8_unpack")) != GROK_OK) return st;
 
-  PfParams p = {};
-  p.B = B;
-  p.T = T;
-  p.Tmax = max_blocks * kKv8Block;
-  p.n_qt = (T + kPfRows - 1) / kPfRows;
-  p.n_items = n_items;
-  p.pm = PageMap{nullptr, 0, 0};
-  p.start_pos = cache_len;
-  p.valid_len = valid_len;
-  p.status = dev_status;
-  p.fb_count = fb_count;
-  p.fb_list = fb_count + 1;
-  p.fb_cap = ws_fb_cap(B, w.rows);
-  p.n_parts = 1;
-  p.k_scale = u.k_scale;
-  p.k_scale_stride = w.rows / kKv8Block;
-  p.o_scale = u.o_scale;
-  if (n_whole > 0) {
-    p.n_units = n_whole;
-    if ((st = launch(prefill_kernel<true, false, false, true>, 0, std::min(n_whole, sms), m, m.v, p, false, s)) != GROK_OK)
-      return st;
-  }
-  if (n_split > 0) {
-    PfParams ps = p;
-    ps.item_base = n_whole;
-    ps.n_parts = n_parts;
-    ps.n_units = n_split * n_parts;
-    ps.part_cnt = reinterpret_cast<int32_t*>(ws + w.split);
-    ps.part_lm = reinterpret_cast<float2*>(ws + w.split + split_cnt_bytes(sms));
-    ps.part_o = reinterpret_cast<float4*>(ws + w.split + split_cnt_bytes(sms) + split_lm_bytes(sms));
-    if ((st = launch(prefill_kernel<true, false, true, true>, 1, std::min(ps.n_units, sms), m, m.v, ps, false, s)) != GROK_OK)
-      return st;
-  }
+  const Q8Prefill a{q_rot,
+                    out,
+                    u.k_copy,
+                    u.v_copy,
+                    w.rows,
+                    u.k_scale,
+                    u.o_scale,
+                    cache_len,
+                    valid_len,
+                    B,
+                    T,
+                    max_blocks * kKv8Block,
+                    sms,
+                    fb_count,
+                    fb_count + 1,
+                    ws_fb_cap(B, w.rows),
+                    n_whole,
+                    n_parts,
+                    ws + w.split,
+                    dev_status};
+  if ((st = prefill_q8_passes(a, false, s)) != GROK_OK) return st;
   kv8_v_to_bf16_kernel<<<sms, 256, 0, s>>>(fb_count, u.v_copy, (long long)B * w.rows * kKVHeads * (kD / 8));
   if ((st = check_launch("kv8_v_to_bf16")) != GROK_OK) return st;
-  p.item_list = p.fb_list;
-  p.item_count = fb_count;
-  p.n_units = n_items;
-  return launch(prefill_kernel<false, true, false, true>, 2, sms, m, m.v_bf16, p, true, s);
+  return prefill_q8_passes(a, true, s);
 }
