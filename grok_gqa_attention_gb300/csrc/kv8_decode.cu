@@ -31,10 +31,16 @@
 
 namespace grok {
 
-constexpr int kDqWarps = 14;
+#ifndef KDQ_WARPS
+#define KDQ_WARPS 10
+#define KDQ_BUFS 2
+#endif
+constexpr int kDqWarps = KDQ_WARPS;
+constexpr int kDqBufs = KDQ_BUFS;      // a warp's ring: K and V of its blocks in turn
 constexpr int kDqThreads = kDqWarps * 32;
-constexpr int kDqBuf = 2 * kKv8Bytes;  // a warp's K and V buffers
-constexpr int kDqSmem = kDqWarps * kDqBuf + kDqWarps * 2 * 8 + 16;
+constexpr int kDqRing = kDqBufs * kKv8Bytes;
+constexpr int kDqSmem = kDqWarps * kDqRing + kDqWarps * kDqBufs * 8 + 16;
+static_assert(kDqSmem <= 232448, "shared memory per CTA");
 constexpr float kDqLag = 8.f;  // log2 units a weight may exceed the reference by
 
 struct DqParams {
@@ -43,6 +49,7 @@ struct DqParams {
   const int32_t* kv_len;
   float* part_o;    // [slot][6][128]
   float2* part_ml;  // [slot][6]: reference (log2), sum
+  int2* pair_parts; // [B * 8]: a pair's first slot and number of slots
   float* block_w;   // [B * 8][max_blocks][8]: a block's weights per head on the fixed reference 30
   uint2* out;
   const float* weight_in;
@@ -50,6 +57,23 @@ struct DqParams {
   int workers;
   int32_t* status;
 };
+
+// Four codes as two fp16 pairs of an A operand. int8: code + 128 in the low byte of
+// an fp16 is the subnormal (code + 128) 2^-24; three instructions for four codes,
+// and the offset is taken off where the sums start (a product's 128 more is a
+// few units of 2^-24 of the sum of |q| or of P). e4m3: converted.
+template <int kKind>
+__device__ __forceinline__ void operand(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  if (kKind == GROK_KV8_INT8) {
+    const uint32_t u = w ^ 0x80808080u;
+    lo = __byte_perm(u, 0u, 0x4140);
+    hi = __byte_perm(u, 0u, 0x4342);
+  } else {
+    kv8_to_half<kKind>(w, lo, hi);
+  }
+}
+
+__device__ __forceinline__ uint32_t word_of(const uint4& x, int w) { return w == 0 ? x.x : w == 1 ? x.y : w == 2 ? x.z : x.w; }
 
 // The sequences' blocks: total over the batch of ceil(kv_len / 64), by one warp.
 __device__ __forceinline__ int count_blocks(const DqParams& p, int lane) {
@@ -62,42 +86,43 @@ __device__ __forceinline__ int count_blocks(const DqParams& p, int lane) {
 template <int kKind, bool kWeights>
 __global__ void __launch_bounds__(kDqThreads, 1) kv8_decode_kernel(const DqParams p) {
   extern __shared__ __align__(128) uint8_t smem[];
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int row = lane >> 2, t = lane & 3;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kDqWarps * kDqBuf);
-  int* abort_flag = reinterpret_cast<int*>(bars + 2 * kDqWarps);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kDqWarps * kDqRing);
+  int* abort_flag = reinterpret_cast<int*>(bars + kDqBufs * kDqWarps);
   volatile int* abort = abort_flag;
-  uint64_t *k_bar = bars + 2 * warp, *v_bar = k_bar + 1;
-  uint8_t *k_buf = smem + warp * kDqBuf, *v_buf = k_buf + kKv8Bytes;
+  bars += kDqBufs * warp;
+  uint8_t* ring = smem + warp * kDqRing;
   if (lane == 0) {
-    mbar_init(k_bar, 1);
-    mbar_init(v_bar, 1);
+    for (int i = 0; i < kDqBufs; ++i) mbar_init(&bars[i], 1);
     if (warp == 0) *abort_flag = 0;
     fence_barrier_init();
   }
   __syncthreads();
-
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int n_total = kKVHeads * count_blocks(p, lane);
   const int share = (n_total + p.workers - 1) / p.workers;
-  const int worker = warp * gridDim.x + blockIdx.x;  // few blocks spread over the SMs first
-  if (blockIdx.x == 0 && warp == 0)
+  const int item = warp * gridDim.x + blockIdx.x;  // few blocks spread over the SMs first
+  if (item == 0)
     for (int b = lane; b < p.c.B; b += 32)
       if (kv8_blocks(__ldg(p.kv_len + b), p.c.max_blocks) == 0) report(p.status, GROK_DEV_BAD_KV_LEN);
-  const long long lo_ = (long long)worker * share;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const long long lo_ = (long long)item * share;
   if (lo_ >= n_total) return;
   const int lo = int(lo_), hi = min(lo + share, n_total);
 
   uint32_t qb[8][2];
   float q_scale0 = 0.f, q_scale1 = 0.f;  // of heads 2 t, 2 t + 1
+  float q_off0 = 0.f, q_off1 = 0.f;
+  constexpr float kUnit = kKind == GROK_KV8_INT8 ? 0x1p24f : 1.f;  // the operands' scale
   float o[8][4], m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
   int pair = -1;
-  uint32_t phase = 0;                    // of both buffers, at the top of a block
-  uint32_t k_phase = 0;                  // of the K copy that is due
-  bool k_due = false, v_due = false;     // a copy was issued and not yet waited for
+  int buf = 0, next_buf = 0;         // buffers of the next piece to read and to load (a piece: a block's K or V)
+  uint32_t phase = 0;                // of buffer `buf`
+  int due = 0;                       // pieces loaded and not yet waited for
   bool ok = true;
 
-  // One partial result: this worker's share of a pair.
+  // One partial result: this item's share of a pair.
   auto flush = [&]() {
 #pragma unroll
     for (int d = 4; d < 32; d *= 2) {
@@ -105,7 +130,7 @@ __global__ void __launch_bounds__(kDqThreads, 1) kv8_decode_kernel(const DqParam
       l1 += __shfl_xor_sync(0xffffffffu, l1, d);
     }
     if (t < kGroup / 2) {
-      const size_t slot = (size_t)worker + pair;
+      const size_t slot = (size_t)item + pair;
       float* po = p.part_o + (slot * kGroup + 2 * t) * kD + row;
 #pragma unroll
       for (int mt = 0; mt < 8; ++mt) {
@@ -153,6 +178,7 @@ __global__ void __launch_bounds__(kDqThreads, 1) kv8_decode_kernel(const DqParam
           my_blk = in % sn;
           my_keys = min(kKv8Block, sl - my_blk * kKv8Block);
           found = true;
+          if (my_blk == 0) p.pair_parts[my_pair] = make_int2(item + my_pair, (idx + sn - 1) / share - item + 1);
         }
         cum += chunk;
         if (__all_sync(0xffffffffu, found)) break;
@@ -165,18 +191,37 @@ __global__ void __launch_bounds__(kDqThreads, 1) kv8_decode_kernel(const DqParam
       my_ks = __ldg(p.c.k_scale + my_id);
       my_vs = __ldg(p.c.v_scale + my_id);
     }
-    auto load = [&](int j, bool v) {
-      (v ? v_due : k_due) = true;
-      const int id = __shfl_sync(0xffffffffu, my_id, j);
+    int loaded = 0;  // pieces of this batch
+    auto load = [&]() {
+      const bool v = loaded & 1;
+      const int id = __shfl_sync(0xffffffffu, my_id, loaded >> 1);
       if (lane == 0) {
-        uint64_t* bar = v ? v_bar : k_bar;
-        mbar_arrive_expect_tx(bar, kKv8Bytes);
-        bulk_load(v ? v_buf : k_buf, static_cast<const uint8_t*>(v ? p.c.v_pool : p.c.k_pool) + (size_t)id * kKv8Bytes,
-                  kKv8Bytes, bar);
+        mbar_arrive_expect_tx(&bars[next_buf], kKv8Bytes);
+        bulk_load(ring + next_buf * kKv8Bytes,
+                  static_cast<const uint8_t*>(v ? p.c.v_pool : p.c.k_pool) + (size_t)id * kKv8Bytes, kKv8Bytes,
+                  &bars[next_buf]);
       }
+      next_buf = next_buf + 1 == kDqBufs ? 0 : next_buf + 1;
+      ++loaded;
+      ++due;
     };
-    load(0, false);
-    load(0, true);
+    auto wait = [&]() {
+      ok = __all_sync(0xffffffffu, mbar_wait(&bars[buf], phase, abort, p.status));
+      return ok;
+    };
+    // The piece in `buf` is read by every lane: its place takes the next one.
+    auto release = [&]() {
+      __syncwarp();
+      --due;
+      if (buf + 1 == kDqBufs) {
+        buf = 0;
+        phase ^= 1;
+      } else {
+        ++buf;
+      }
+      if (loaded < 2 * cnt) load();
+    };
+    for (int i = 0; i < kDqBufs && i < 2 * cnt; ++i) load();
     for (int j = 0; j < cnt; ++j) {
       const int jp = __shfl_sync(0xffffffffu, my_pair, j);
       if (jp != pair) {  // the next pair: its partial starts empty, its six queries come in
@@ -210,38 +255,41 @@ __global__ void __launch_bounds__(kDqThreads, 1) kv8_decode_kernel(const DqParam
             qb[u][c & 1] = pack_f16x2(bf16lo_to_f32(w[c]) * down, bf16hi_to_f32(w[c]) * down);
           }
         }
+        if (kKind == GROK_KV8_INT8) {  // minus 128 x 2^-24 x the sum of q, for every key
+          float off[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int u = 0; u < 8; ++u) mma_f16_16816(off, 0x80808080u, 0x80808080u, 0x80808080u, 0x80808080u, qb[u][0], qb[u][1]);
+          q_off0 = off[0], q_off1 = off[1];
+        }
         q_scale0 = __shfl_sync(0xffffffffu, up, 8 * t) * (2.f * kY * kLog2e);
         q_scale1 = __shfl_sync(0xffffffffu, up, 8 * t + 4) * (2.f * kY * kLog2e);
       }
-      const float ks = __shfl_sync(0xffffffffu, my_ks, j), vs = __shfl_sync(0xffffffffu, my_vs, j);
+      const float ks = __shfl_sync(0xffffffffu, my_ks, j) * kUnit, vs = __shfl_sync(0xffffffffu, my_vs, j) * kUnit;
       const int keys = __shfl_sync(0xffffffffu, my_keys, j), blk = __shfl_sync(0xffffffffu, my_blk, j);
 
-      ok = __all_sync(0xffffffffu, mbar_wait(k_bar, phase, abort, p.status));
-      if (!ok) break;
-      k_due = false;
+      if (!wait()) break;
+      const uint8_t* k_buf = ring + buf * kKv8Bytes;
       float s[4][4];
 #pragma unroll
       for (int st = 0; st < 4; ++st) {
-        s[st][0] = s[st][1] = s[st][2] = s[st][3] = 0.f;
+        s[st][0] = s[st][2] = q_off0;
+        s[st][1] = s[st][3] = q_off1;
         // row r of the tile is key 16 (r >> 1) + 4 st + (r & 1), row r + 8 two keys on: the order P^T is read in below
         const uint8_t* k0 = k_buf + (16 * (row >> 1) + 4 * st + (row & 1)) * 64 + 16 * t;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const uint4 a = *reinterpret_cast<const uint4*>(k0 + h * (kKv8Bytes / 2));
           const uint4 b = *reinterpret_cast<const uint4*>(k0 + h * (kKv8Bytes / 2) + 128);
-          const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
           for (int w = 0; w < 4; ++w) {
             uint32_t a0, a1, a2, a3;
-            kv8_to_half<kKind>(aw[w], a0, a2);
-            kv8_to_half<kKind>(bw[w], a1, a3);
+            operand<kKind>(word_of(a, w), a0, a2);
+            operand<kKind>(word_of(b, w), a1, a3);
             mma_f16_16816(s[st], a0, a1, a2, a3, qb[4 * h + w][0], qb[4 * h + w][1]);
           }
         }
       }
-      __syncwarp();
-      k_phase = phase ^ 1;
-      if (j + 1 < cnt) load(j + 1, false);
+      release();
 
       // z = log2 of the weight against the fixed reference 30: -2 kT / (1 + e^(2 x / 30))
       const float f0 = ks * q_scale0, f1 = ks * q_scale1;
@@ -290,37 +338,39 @@ __global__ void __launch_bounds__(kDqThreads, 1) kv8_decode_kernel(const DqParam
               make_float2(b0 * ex2_approx(m0), b1 * ex2_approx(m1));
       }
 
-      ok = __all_sync(0xffffffffu, mbar_wait(v_bar, phase, abort, p.status));
-      if (!ok) break;
-      v_due = false;
-      k_phase = phase ^= 1;
+      if (!wait()) break;
+      const uint8_t* v_buf = ring + buf * kKv8Bytes;
+      float off[4] = {0.f, 0.f, 0.f, 0.f};
+      if (kKind == GROK_KV8_INT8) {
+        constexpr uint32_t c = 0x80808080u;  // fp16 -2^-17, twice: the operands' offset of 128 times 2^-24
+#pragma unroll
+        for (int st = 0; st < 4; ++st) mma_f16_16816(off, c, c, c, c, pb[st][0], pb[st][1]);
+      }
 #pragma unroll
       for (int mt = 0; mt < 8; ++mt) {
-        const uint4 a = *reinterpret_cast<const uint4*>(v_buf + (16 * mt + row) * 64 + 16 * t);
-        const uint4 b = *reinterpret_cast<const uint4*>(v_buf + (16 * mt + row + 8) * 64 + 16 * t);
-        uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w};
-        if (keys < kKv8Block) {  // codes behind the last row may be anything, NaN among them
+        uint4 a = *reinterpret_cast<const uint4*>(v_buf + (16 * mt + row) * 64 + 16 * t);
+        uint4 b = *reinterpret_cast<const uint4*>(v_buf + (16 * mt + row + 8) * 64 + 16 * t);
+        if (kKind == GROK_KV8_E4M3 && keys < kKv8Block) {  // codes behind the last row may be NaN
 #pragma unroll
           for (int st = 0; st < 4; ++st) {
             const int left = keys - (16 * t + 4 * st);
             const uint32_t mask = left >= 4 ? 0xFFFFFFFFu : left <= 0 ? 0u : (1u << (8 * left)) - 1u;
-            aw[st] &= mask;
-            bw[st] &= mask;
+            reinterpret_cast<uint32_t*>(&a)[st] &= mask;
+            reinterpret_cast<uint32_t*>(&b)[st] &= mask;
           }
         }
-        float acc[4] = {0.f, 0.f, 0.f, 0.f};
+        float acc[4] = {off[0], off[1], off[2], off[3]};
 #pragma unroll
         for (int st = 0; st < 4; ++st) {
           uint32_t a0, a1, a2, a3;
-          kv8_to_half<kKind>(aw[st], a0, a2);
-          kv8_to_half<kKind>(bw[st], a1, a3);
+          operand<kKind>(word_of(a, st), a0, a2);
+          operand<kKind>(word_of(b, st), a1, a3);
           mma_f16_16816(acc, a0, a1, a2, a3, pb[st][0], pb[st][1]);
         }
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[mt][e] = fmaf(acc[e], vs, o[mt][e]);
       }
-      __syncwarp();
-      if (j + 1 < cnt) load(j + 1, true);
+      release();
     }
   }
   if (ok) {
@@ -329,84 +379,101 @@ __global__ void __launch_bounds__(kDqThreads, 1) kv8_decode_kernel(const DqParam
   }
   // A wait gave up: copies in flight land before the shared memory is released.
   volatile int never = 0;
-  if (k_due) mbar_wait(k_bar, k_phase, &never, p.status);
-  if (v_due) mbar_wait(v_bar, phase, &never, p.status);
+  for (; due > 0; --due) {
+    mbar_wait(&bars[buf], phase, &never, p.status);
+    if (++buf == kDqBufs) {
+      buf = 0;
+      phase ^= 1;
+    }
+  }
 }
 
-// Joins a pair's partials: CTA (pair, head) the output, CTA (pair, 6) the blocks' weights.
-constexpr int kDqJoinWarps = 4;
+// Joins a pair's partials. A CTA takes kHeads of the pair's six query heads,
+// kSplit warps to a head; the blocks' weights are done by the pair's CTA (kHeads 6)
+// or by one CTA more (kHeads 1).
+__device__ __forceinline__ float warp_max(float x) {
+#pragma unroll
+  for (int d = 16; d; d /= 2) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
+  return x;
+}
+__device__ __forceinline__ float warp_sum(float x) {
+#pragma unroll
+  for (int d = 16; d; d /= 2) x += __shfl_xor_sync(0xffffffffu, x, d);
+  return x;
+}
 
-__global__ void __launch_bounds__(kDqJoinWarps * 32) kv8_join_kernel(const DqParams p) {
-  __shared__ float4 s_o[kDqJoinWarps][32];
-  __shared__ float s_m[kDqJoinWarps], s_l[kDqJoinWarps], s_inv[8];
-  const int pair = blockIdx.x, head = blockIdx.y, b = pair / kKVHeads;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int blocks = kv8_blocks(__ldg(p.kv_len + b), p.c.max_blocks);
-  // where the pair's blocks lie in the order they were dealt out
-  int before = 0, total = 0;
-  for (int c = 0; c < p.c.B; c += 32) {
-    const int n = c + lane < p.c.B ? kv8_blocks(__ldg(p.kv_len + c + lane), p.c.max_blocks) : 0;
-    total += __reduce_add_sync(0xffffffffu, n);
-    before += __reduce_add_sync(0xffffffffu, c + lane < b ? n : 0);
-  }
+template <int kHeads, int kSplit>
+__global__ void __launch_bounds__(kHeads * kSplit * 32) kv8_join_kernel(const DqParams p) {
+  constexpr int kThreads = kHeads * kSplit * 32;
+  __shared__ float4 s_o[kHeads * kSplit][32];
+  __shared__ float s_inv[8];
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (blocks == 0) return;  // reported by the first kernel
-  const int share = (kKVHeads * total + p.workers - 1) / p.workers;
-  const int first = kKVHeads * before + (pair % kKVHeads) * blocks;
-  const int w0 = first / share, n_parts = (first + blocks - 1) / share - w0 + 1;
-  const size_t slot0 = (size_t)w0 + pair;
+  const int pair = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int blocks = kv8_blocks(__ldg(p.kv_len + pair / kKVHeads), p.c.max_blocks);
+  const int2 parts = p.pair_parts[pair];  // first slot, number (not written for a bad length)
+  if (blocks == 0) return;                // reported by the first kernel
+  const size_t slot0 = parts.x;
+  const int n_parts = parts.y;
 
-  if (head < kGroup) {
-    float m = -INFINITY;
-    for (int k = threadIdx.x; k < n_parts; k += kDqJoinWarps * 32) m = fmaxf(m, p.part_ml[(slot0 + k) * kGroup + head].x);
-#pragma unroll
-    for (int d = 16; d; d /= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-    if (lane == 0) s_m[warp] = m;
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < kDqJoinWarps; ++w) m = fmaxf(m, s_m[w]);
+  const bool weights_only = kHeads == 1 && blockIdx.y == kGroup;
+  if (!weights_only) {
+    const int head = kHeads == 1 ? blockIdx.y : warp / kSplit, sub = warp % kSplit;
+    float m = -INFINITY, l = 0.f;
+    for (int k = lane; k < n_parts; k += 32) m = fmaxf(m, p.part_ml[(slot0 + k) * kGroup + head].x);
+    m = warp_max(m);
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    float l = 0.f;
-#pragma unroll 4
-    for (int k = warp; k < n_parts; k += kDqJoinWarps) {
-      const float2 ml = p.part_ml[(slot0 + k) * kGroup + head];
-      const float4 v = *reinterpret_cast<const float4*>(p.part_o + ((slot0 + k) * kGroup + head) * kD + 4 * lane);
-      const float f = ex2_approx(ml.x - m);
-      l = fmaf(ml.y, f, l);
-      acc.x = fmaf(v.x, f, acc.x);
-      acc.y = fmaf(v.y, f, acc.y);
-      acc.z = fmaf(v.z, f, acc.z);
-      acc.w = fmaf(v.w, f, acc.w);
-    }
-    s_o[warp][lane] = acc;
-    if (lane == 0) s_l[warp] = l;
-    __syncthreads();
-    if (warp == 0) {
-#pragma unroll
-      for (int w = 1; w < kDqJoinWarps; ++w) {
-        const float4 v = s_o[w][lane];
-        acc.x += v.x, acc.y += v.y, acc.z += v.z, acc.w += v.w;
-        l += s_l[w];
+    for (int k0 = 0; k0 < n_parts; k0 += 32) {
+      float my_f = 0.f;
+      if (k0 + lane < n_parts) {
+        const float2 ml = p.part_ml[(slot0 + k0 + lane) * kGroup + head];
+        my_f = ex2_approx(ml.x - m);
+        l = fmaf(ml.y, my_f, l);
       }
+      const float* po = p.part_o + ((slot0 + k0) * kGroup + head) * kD + 4 * lane;
+      const int n = min(32, n_parts - k0);
+#pragma unroll 8
+      for (int k = sub; k < n; k += kSplit) {
+        const float4 v = *reinterpret_cast<const float4*>(po + (size_t)k * (kGroup * kD));
+        const float f = __shfl_sync(0xffffffffu, my_f, k);
+        acc.x = fmaf(v.x, f, acc.x);
+        acc.y = fmaf(v.y, f, acc.y);
+        acc.z = fmaf(v.z, f, acc.z);
+        acc.w = fmaf(v.w, f, acc.w);
+      }
+    }
+    l = warp_sum(l);
+    if (kSplit > 1) {
+      s_o[warp][lane] = acc;
+      __syncthreads();
+      if (sub == 0) {
+#pragma unroll
+        for (int w = 1; w < kSplit; ++w) {
+          const float4 v = s_o[warp + w][lane];
+          acc.x += v.x, acc.y += v.y, acc.z += v.z, acc.w += v.w;
+        }
+      }
+    }
+    if (sub == 0) {
       const float inv = 1.f / l;
       p.out[((size_t)pair * kGroup + head) * (kD / 4) + lane] =
           make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+      if (kHeads > 1 && lane == 0) s_inv[head] = 1.f / (l * ex2_approx(m));
     }
-    return;
-  }
-  // The heads' sums on the fixed reference 30, then every block's share.
-  for (int h = warp; h < kGroup; h += kDqJoinWarps) {
-    float l = 0.f;
-    for (int k = lane; k < n_parts; k += 32) {
-      const float2 ml = p.part_ml[(slot0 + k) * kGroup + h];
-      l = fmaf(ml.y, ex2_approx(ml.x), l);
+    if (kHeads == 1 || !p.weight_out) return;
+  } else {
+    // the heads' sums on the fixed reference 30
+    for (int h = warp; h < kGroup; h += kSplit) {
+      float l = 0.f;
+      for (int k = lane; k < n_parts; k += 32) {
+        const float2 ml = p.part_ml[(slot0 + k) * kGroup + h];
+        l = fmaf(ml.y, ex2_approx(ml.x), l);
+      }
+      l = warp_sum(l);
+      if (lane == 0) s_inv[h] = 1.f / l;
     }
-#pragma unroll
-    for (int d = 16; d; d /= 2) l += __shfl_xor_sync(0xffffffffu, l, d);
-    if (lane == 0) s_inv[h] = 1.f / l;
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < p.c.max_blocks; i += kDqJoinWarps * 32) {
+  for (int i = threadIdx.x; i < p.c.max_blocks; i += kThreads) {
     const size_t at = (size_t)pair * p.c.max_blocks + i;
     float w = 0.f;
     if (i < blocks) {
@@ -425,10 +492,11 @@ using namespace grok;
 namespace {
 
 size_t up256(size_t n) { return (n + 255) & ~size_t(255); }
-// A worker's share touches a run of pairs, so (worker, pair) runs through fewer than workers + pairs values of their sum.
+// A worker's blocks touch a run of pairs, so (worker, pair) runs through fewer than workers + pairs values of their sum.
 size_t part_slots(int B, int sms) { return size_t(sms) * kDqWarps + size_t(B) * kKVHeads; }
 size_t part_o_bytes(int B, int sms) { return part_slots(B, sms) * kGroup * kD * sizeof(float); }
 size_t part_ml_bytes(int B, int sms) { return up256(part_slots(B, sms) * kGroup * sizeof(float2)); }
+size_t pairs_bytes(int B) { return up256(size_t(B) * kKVHeads * sizeof(int2)); }
 size_t block_w_bytes(int B, int max_blocks) { return size_t(B) * kKVHeads * max_blocks * 8 * sizeof(float); }
 
 }  // namespace
@@ -441,7 +509,7 @@ extern "C" grok_status grok_kv8_decode_workspace(int B, int max_blocks, int weig
   int sms = 0;
   grok_status st = device_sm_count(&sms);
   if (st != GROK_OK) return st;
-  *bytes = part_o_bytes(B, sms) + part_ml_bytes(B, sms) + (weights ? block_w_bytes(B, max_blocks) : 0);
+  *bytes = part_o_bytes(B, sms) + part_ml_bytes(B, sms) + pairs_bytes(B) + (weights ? block_w_bytes(B, max_blocks) : 0);
   return GROK_OK;
 }
 
@@ -460,7 +528,7 @@ extern "C" grok_status grok_kv8_decode(const grok_kv8_cache* cache, const grok_b
   if ((st = device_sm_count(&sms)) != GROK_OK || (st = device_index(&dev)) != GROK_OK) return st;
   const int B = cache->B;
   const size_t o_bytes = part_o_bytes(B, sms), ml_bytes = part_ml_bytes(B, sms);
-  const size_t need = o_bytes + ml_bytes + (weight_out ? block_w_bytes(B, cache->max_blocks) : 0);
+  const size_t need = o_bytes + ml_bytes + pairs_bytes(B) + (weight_out ? block_w_bytes(B, cache->max_blocks) : 0);
   if (workspace_bytes < need)
     return fail(GROK_ERR_INVALID_ARG, "grok_kv8_decode: workspace of %zu bytes is smaller than the %zu needed",
                 workspace_bytes, need);
@@ -470,7 +538,8 @@ extern "C" grok_status grok_kv8_decode(const grok_kv8_cache* cache, const grok_b
                    kv_len,
                    reinterpret_cast<float*>(ws),
                    reinterpret_cast<float2*>(ws + o_bytes),
-                   weight_out ? reinterpret_cast<float*>(ws + o_bytes + ml_bytes) : nullptr,
+                   reinterpret_cast<int2*>(ws + o_bytes + ml_bytes),
+                   weight_out ? reinterpret_cast<float*>(ws + o_bytes + ml_bytes + pairs_bytes(B)) : nullptr,
                    reinterpret_cast<uint2*>(out),
                    weight_in,
                    weight_out,
@@ -486,18 +555,27 @@ extern "C" grok_status grok_kv8_decode(const grok_kv8_cache* cache, const grok_b
     if (e != cudaSuccess) return fail(cuda_status(e), "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
     set = true;
   }
-  kernel<<<sms, kDqThreads, kDqSmem, static_cast<cudaStream_t>(stream)>>>(p);
-  if ((st = check_launch("kv8_decode")) != GROK_OK) return st;
+  // Both kernels are launched as dependents of the one before them: each begins with a wait for all of it.
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(B * kKVHeads, kGroup + (weight_out ? 1 : 0));
-  cfg.blockDim = dim3(kDqJoinWarps * 32);
+  cfg.gridDim = dim3(sms);
+  cfg.blockDim = dim3(kDqThreads);
+  cfg.dynamicSmemBytes = kDqSmem;
   cfg.stream = static_cast<cudaStream_t>(stream);
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  cudaError_t e = cudaLaunchKernelEx(&cfg, kv8_join_kernel, p);
+  cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, p);
+  if (e != cudaSuccess) return fail(cuda_status(e), "kv8_decode launch: %s", cudaGetErrorString(e));
+  if ((st = check_launch("kv8_decode")) != GROK_OK) return st;
+  // Many pairs have few partials each: a CTA per pair, a warp per head. Few pairs have many (workers / pairs and
+  // two more at most): a CTA per pair and head.
+  const bool few = B * kKVHeads * 8 < p.workers;
+  cfg.gridDim = few ? dim3(B * kKVHeads, kGroup + (weight_out ? 1 : 0)) : dim3(B * kKVHeads);
+  cfg.blockDim = dim3(few ? 256 : kGroup * 32);
+  cfg.dynamicSmemBytes = 0;
+  e = cudaLaunchKernelEx(&cfg, few ? kv8_join_kernel<1, 8> : kv8_join_kernel<kGroup, 1>, p);
   if (e != cudaSuccess) return fail(cuda_status(e), "kv8_join launch: %s", cudaGetErrorString(e));
   return check_launch("kv8_join");
 }

@@ -1,10 +1,11 @@
 // Eviction from the 8-bit KV cache by accumulated attention weight.
 //
-// One CTA per (sequence, KV head), one thread per table entry (at most 1024).
-// The threshold weight is found bit by bit from the top: a block-wide count of
-// the candidates at or above a trial value per bit, 32 barriers, no memory
-// traffic. Ranks among equals and the places in the new row are prefix counts.
-// The codes stay where they are; what is read and written is 16 bytes per entry.
+// One warp per (sequence, KV head): it holds the head's row of the table and its
+// weights in registers (up to 1024 entries, 32 a lane), finds the threshold weight
+// bit by bit from the top (a count of the candidates at or above a trial value per
+// bit, until the count is the one wanted), and writes each entry to its place in
+// the new row, a prefix count of ballots. No shared memory and no barrier; the
+// codes stay where they are. What is read and written is 16 bytes per entry.
 #include "host.cuh"
 #include "kv8.cuh"
 
@@ -17,64 +18,93 @@ __device__ __forceinline__ uint32_t order_key(float w) {
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-// Number of earlier threads of the CTA with `flag`; counts is shared, one per warp.
-__device__ __forceinline__ int prefix_count(bool flag, int* counts) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t ballot = __ballot_sync(0xffffffffu, flag);
-  if (lane == 0) counts[warp] = __popc(ballot);
-  __syncthreads();
-  const int n_warps = blockDim.x >> 5;
-  const int before = __reduce_add_sync(0xffffffffu, lane < warp && lane < n_warps ? counts[lane] : 0);
-  return before + __popc(ballot & ((1u << lane) - 1u));
-}
+constexpr int kEvWarps = 4;
 
-__global__ void __launch_bounds__(1024) kv8_evict_kernel(const int32_t* table, const float* weight,
-                                                         const int32_t* kv_len, int max_blocks, int keep, int sink,
-                                                         int recent, int32_t* table_out, float* weight_out,
-                                                         int32_t* kv_len_out, int32_t* status) {
-  __shared__ int counts[2][32];
-  const int g = blockIdx.x, b = blockIdx.y, i = threadIdx.x;
-  const size_t row = ((size_t)b * kKVHeads + g) * max_blocks;
+// kPer: entries a lane holds; entry 32 e + lane of the row is e of the lane.
+template <int kPer>
+__global__ void __launch_bounds__(kEvWarps * 32) kv8_evict_kernel(const int32_t* table, const float* weight,
+                                                                  const int32_t* kv_len, int n_rows, int max_blocks,
+                                                                  int keep, int sink, int recent, int32_t* table_out,
+                                                                  float* weight_out, int32_t* kv_len_out,
+                                                                  int32_t* status) {
+  const int r = blockIdx.x * kEvWarps + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  if (r >= n_rows) return;
+  const int b = r / kKVHeads;
+  const size_t row = (size_t)r * max_blocks;
   const int len = kv_len[b];
+  int id[kPer];
+  float w[kPer];
+#pragma unroll
+  for (int e = 0; e < kPer; ++e) {
+    const int i = 32 * e + lane;
+    id[e] = i < max_blocks ? table[row + i] : 0;
+    w[e] = i < max_blocks ? weight[row + i] : 0.f;
+  }
   const bool bad = len < 0 || len > max_blocks * kKv8Block;
   const int closed = bad ? 0 : len / kKv8Block;
   const bool cut = closed > keep;
-  if (i == 0 && g == 0) {
+  if (lane == 0 && r % kKVHeads == 0) {
     if (bad) report(status, GROK_DEV_BAD_KV_LEN);
     kv_len_out[b] = cut ? keep * kKv8Block + len % kKv8Block : len;
   }
-  const bool in = i < max_blocks;
-  const int id = in ? table[row + i] : 0;
-  const float w = in ? weight[row + i] : 0.f;
-  int to = i;
-  bool gone = false;
-  if (cut) {  // uniform over the CTA
-    const bool must = i < closed && (i < sink || i >= closed - recent);
-    const bool free = i < closed && !must;
-    const uint32_t key = free ? order_key(w) : 0u;
-    const int quota = keep - __syncthreads_count(must);
-    // the quota-th largest key among the free blocks (there are more than quota of them)
-    uint32_t edge = 0;
+  __syncwarp();  // the row is read before it is written (the outputs may be the inputs)
+  if (!cut) {
+#pragma unroll
+    for (int e = 0; e < kPer; ++e)
+      if (32 * e + lane < max_blocks) {
+        table_out[row + 32 * e + lane] = id[e];
+        weight_out[row + 32 * e + lane] = w[e];
+      }
+    return;
+  }
+  // Blocks [sink, free_end) are chosen by weight: the `quota` largest of them (there are more).
+  const int free_end = closed - recent, quota = keep - min(sink, closed) - recent;
+  uint32_t edge = 0;
+  int above = 0;  // candidates at or above `edge`
+  auto key_of = [&](int e) {
+    const int i = 32 * e + lane;
+    return i >= sink && i < free_end ? order_key(w[e]) : 0u;  // (a candidate's key is never 0)
+  };
+  if (quota > 0) {
     for (int bit = 31; bit >= 0; --bit) {
       const uint32_t trial = edge | (1u << bit);
-      if (__syncthreads_count(free && key >= trial) >= quota) edge = trial;
+      int n = 0;
+#pragma unroll
+      for (int e = 0; e < kPer; ++e) n += key_of(e) >= trial;
+      n = __reduce_add_sync(0xffffffffu, n);
+      if (n >= quota) {
+        edge = trial;
+        above = n;
+        if (n == quota) break;  // exactly those at or above it
+      }
     }
-    const int ties = quota - __syncthreads_count(free && key > edge);
-    const bool tie = free && key == edge;
-    const int tie_rank = prefix_count(tie, counts[0]);
-    const bool stays = must || (free && quota > 0 && (key > edge || (tie && tie_rank < ties)));
-    const int rank = prefix_count(stays, counts[1]);
-    gone = i < closed && !stays;
-    if (i < closed)
-      to = stays ? rank : keep + (closed < max_blocks ? 1 : 0) + i - rank;
-    else if (i == closed)
-      to = keep;
   } else {
-    __syncthreads();  // every entry is read before one is written (the outputs may be the inputs)
+    edge = 0xFFFFFFFFu;
   }
-  if (in) {
-    table_out[row + to] = id;
-    weight_out[row + to] = gone ? 0.f : w;
+  // Unless the search ended early, the blocks equal to `edge` are too many by above - quota: the last ones go.
+  int equal = 0;
+#pragma unroll
+  for (int e = 0; e < kPer; ++e) equal += key_of(e) == edge;
+  equal = __reduce_add_sync(0xffffffffu, equal);
+  int ties = quota > 0 ? equal - (above - quota) : 0;
+  int rank = 0;  // blocks that stay, before this run of 32
+#pragma unroll
+  for (int e = 0; e < kPer; ++e) {
+    const int i = 32 * e + lane;
+    const uint32_t key = key_of(e), lower = (1u << lane) - 1u;
+    const bool tie = quota > 0 && key != 0 && key == edge;
+    const uint32_t tied = __ballot_sync(0xffffffffu, tie);
+    const bool stays = i < closed && (i < sink || i >= free_end || (key > edge) || (tie && __popc(tied & lower) < ties));
+    ties -= min(ties, __popc(tied));
+    const uint32_t staying = __ballot_sync(0xffffffffu, stays);
+    const int before = rank + __popc(staying & lower);
+    rank += __popc(staying);
+    if (i < max_blocks) {
+      const bool gone = i < closed && !stays;
+      const int to = i > closed ? i : i == closed ? keep : stays ? before : keep + (closed < max_blocks ? 1 : 0) + i - before;
+      table_out[row + to] = id[e];
+      weight_out[row + to] = gone ? 0.f : w[e];
+    }
   }
 }
 
@@ -98,8 +128,12 @@ extern "C" grok_status grok_kv8_evict(const int32_t* table, const float* weight,
   int sms = 0;
   grok_status st = device_sm_count(&sms);
   if (st != GROK_OK) return st;
-  const int threads = (max_blocks + 31) / 32 * 32;
-  kv8_evict_kernel<<<dim3(kKVHeads, B), threads, 0, static_cast<cudaStream_t>(stream)>>>(
-      table, weight, kv_len, max_blocks, keep, sink, recent, table_out, weight_out, kv_len_out, dev_status);
+  const int n_rows = B * kKVHeads;
+  auto kernel = max_blocks <= 128   ? kv8_evict_kernel<4>
+                : max_blocks <= 256 ? kv8_evict_kernel<8>
+                : max_blocks <= 512 ? kv8_evict_kernel<16>
+                                    : kv8_evict_kernel<32>;
+  kernel<<<(n_rows + kEvWarps - 1) / kEvWarps, kEvWarps * 32, 0, static_cast<cudaStream_t>(stream)>>>(
+      table, weight, kv_len, n_rows, max_blocks, keep, sink, recent, table_out, weight_out, kv_len_out, dev_status);
   return check_launch("kv8_evict");
 }
