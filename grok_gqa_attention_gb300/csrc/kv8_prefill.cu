@@ -21,10 +21,11 @@ struct UnParams {
   grok_kv8_cache c;
   const int32_t *cache_len, *valid_len;
   int T, rows;         // rows of a sequence's copies
-  uint4 *k_copy, *v_copy;  // [B][rows][8][128] bf16, fp16
+  uint4 *k_copy, *v_copy;  // [B][8][rows][128] bf16, fp16
   float* k_scale;      // [B][8][rows / 64]
   float* o_scale;      // [B][8]
-  int32_t* zero;       // words that the attention passes expect to be zero
+  int32_t* fb_count;   // words that the attention passes expect to be zero: the fallback count and the split's
+  int32_t* zero;
   int n_zero;
   int32_t* status;
 };
@@ -59,9 +60,12 @@ __device__ __forceinline__ uint32_t scale_half2(uint32_t x, float f) {
 template <int kKind>
 __global__ void __launch_bounds__(kUnThreads) kv8_unpack_kernel(const UnParams p) {
   __shared__ float s_top[kUnThreads / 32];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int g = blockIdx.y, b = blockIdx.z, tid = threadIdx.x;
-  if (blockIdx.x == 0 && g == 0 && b == 0)
+  if (blockIdx.x == 0 && g == 0 && b == 0) {
+    if (tid == 0) *p.fb_count = 0;
     for (int i = tid; i < p.n_zero; i += kUnThreads) p.zero[i] = 0;
+  }
   const int s = __ldg(p.cache_len + b), n = p.valid_len ? __ldg(p.valid_len + b) : p.T;
   if (s < 0 || n < 1 || n > p.T || (long long)s + n > (long long)p.c.max_blocks * kKv8Block) return;  // reported later
   const int len = s + n, blocks = (len + kKv8Block - 1) / kKv8Block;
@@ -87,53 +91,57 @@ __global__ void __launch_bounds__(kUnThreads) kv8_unpack_kernel(const UnParams p
 
   // Rows up to the next multiple of 128: those behind the last are zeros (in V they meet zero weights).
   const int pad = (blocks + 1) / 2 * 2;
-  uint4* k_out = p.k_copy + ((size_t)b * p.rows * kKVHeads + g) * 16;
-  uint4* v_out = p.v_copy + ((size_t)b * p.rows * kKVHeads + g) * 16;
+  uint4* k_out = p.k_copy + head * p.rows * 16;
+  uint4* v_out = p.v_copy + head * p.rows * 16;
+  const int q = tid & 15, c = tid >> 4;
   for (int i = blockIdx.x; i < pad; i += gridDim.x) {
     const int left = min(kKv8Block, len - i * kKv8Block);  // rows of this block (negative in the padding)
     const int id = left > 0 ? max(0, kv8_block_id(table, i, p.c.n_blocks, nullptr)) : 0;
     const uint8_t* k_src = static_cast<const uint8_t*>(p.c.k_pool) + (size_t)id * kKv8Bytes;
     const uint8_t* v_src = static_cast<const uint8_t*>(p.c.v_pool) + (size_t)id * kKv8Bytes;
     float f = left > 0 ? __ldg(p.c.v_scale + id) : 0.f;
-    f = f == f ? f * per : 0.f;
-    // K: thread = (row, 8 codes) of one half, four passes
+    // K: 8 codes of a row of one half, four times; V: four rows (4 q ..) of eight features (8 c ..)
+    uint2 kw[4];
+    uint32_t vw[8];
 #pragma unroll
     for (int m = 0; m < 4; ++m) {
-      const int e = tid + m * kUnThreads, row = (e >> 3) & 63, c = e & 7, h = e >> 9;
-      uint4 x = make_uint4(0, 0, 0, 0);
-      if (row < left) {
-        const uint2 w = __ldg(reinterpret_cast<const uint2*>(k_src + h * (kKv8Bytes / 2) + row * 64 + c * 8));
-        kv8_to_bf16<kKind>(w.x, x.x, x.y);
-        kv8_to_bf16<kKind>(w.y, x.z, x.w);
-      }
-      k_out[(size_t)(i * kKv8Block + row) * (kKVHeads * 16) + h * 8 + c] = x;
+      const int e = tid + m * kUnThreads, row = (e >> 3) & 63;
+      kw[m] = row < left ? __ldg(reinterpret_cast<const uint2*>(k_src + 8 * e)) : make_uint2(0, 0);
     }
-    // V: thread = four rows of eight features, turned in registers
-    const int q = tid & 15, c = tid >> 4;
-    uint32_t w[8];
 #pragma unroll
-    for (int d = 0; d < 8; ++d) w[d] = left > 4 * q ? __ldg(reinterpret_cast<const uint32_t*>(v_src + (8 * c + d) * 64 + 4 * q)) : 0u;
+    for (int d = 0; d < 8; ++d)
+      vw[d] = left > 4 * q ? __ldg(reinterpret_cast<const uint32_t*>(v_src + (8 * c + d) * 64 + 4 * q)) : 0u;
+    f = f == f ? f * per : 0.f;
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
+    for (int m = 0; m < 4; ++m) {
+      const int e = tid + m * kUnThreads, row = (e >> 3) & 63;
+      uint4 x;
+      kv8_to_bf16<kKind>(kw[m].x, x.x, x.y);
+      kv8_to_bf16<kKind>(kw[m].y, x.z, x.w);
+      k_out[(size_t)(i * kKv8Block + row) * 16 + (e >> 9) * 8 + (e & 7)] = x;
+    }
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {  // turned in registers
       uint4 x = make_uint4(0, 0, 0, 0);
       if (4 * q + r < left) {
         uint32_t a, z;
         const uint32_t sel = r | (r + 4) << 4;
-        const uint32_t w0 = __byte_perm(__byte_perm(w[0], w[1], sel), __byte_perm(w[2], w[3], sel), 0x5410);
-        const uint32_t w1 = __byte_perm(__byte_perm(w[4], w[5], sel), __byte_perm(w[6], w[7], sel), 0x5410);
+        const uint32_t w0 = __byte_perm(__byte_perm(vw[0], vw[1], sel), __byte_perm(vw[2], vw[3], sel), 0x5410);
+        const uint32_t w1 = __byte_perm(__byte_perm(vw[4], vw[5], sel), __byte_perm(vw[6], vw[7], sel), 0x5410);
         kv8_to_half<kKind>(w0, a, z);
         x.x = scale_half2(a, f), x.y = scale_half2(z, f);
         kv8_to_half<kKind>(w1, a, z);
         x.z = scale_half2(a, f), x.w = scale_half2(z, f);
       }
-      v_out[(size_t)(i * kKv8Block + 4 * q + r) * (kKVHeads * 16) + c] = x;
+      v_out[(size_t)(i * kKv8Block + 4 * q + r) * 16 + c] = x;
     }
   }
 }
 
 // The fallback pass multiplies bf16: when an item is listed, the copy of V is rounded to bf16 in its place.
 __global__ void __launch_bounds__(256) kv8_v_to_bf16_kernel(const int32_t* fb_count, uint4* v, long long n) {
-  if (__ldg(fb_count) == 0) return;
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the fp16 passes, which list the items
+  if (*fb_count == 0) return;
   for (long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += (long long)gridDim.x * blockDim.x) {
     uint4 x = v[i];
     uint32_t* w = reinterpret_cast<uint32_t*>(&x);
@@ -222,9 +230,6 @@ extern "C" grok_status grok_kv8_prefill(const grok_kv8_cache* cache, const grok_
   const int n_split = n_items - n_whole;
 
   int32_t* fb_count = reinterpret_cast<int32_t*>(ws);
-  // The fallback count comes first and the split's counters are apart: the first is cleared here, the second there.
-  cudaError_t e = cudaMemsetAsync(fb_count, 0, sizeof(int32_t), s);
-  if (e != cudaSuccess) return fail(cuda_status(e), "cudaMemsetAsync: %s", cudaGetErrorString(e));
   const UnParams u{*cache,
                    cache_len,
                    valid_len,
@@ -234,6 +239,7 @@ extern "C" grok_status grok_kv8_prefill(const grok_kv8_cache* cache, const grok_
                    reinterpret_cast<uint4*>(ws + w.v_copy),
                    reinterpret_cast<float*>(ws + w.k_scale),
                    reinterpret_cast<float*>(ws + w.o_scale),
+                   fb_count,
                    reinterpret_cast<int32_t*>(ws + w.split),
                    2 * n_split,
                    dev_status};
@@ -264,7 +270,20 @@ extern "C" grok_status grok_kv8_prefill(const grok_kv8_cache* cache, const grok_
                     ws + w.split,
                     dev_status};
   if ((st = prefill_q8_passes(a, false, s)) != GROK_OK) return st;
-  kv8_v_to_bf16_kernel<<<sms, 256, 0, s>>>(fb_count, u.v_copy, (long long)B * w.rows * kKVHeads * (kD / 8));
+  // No weight of a single key tile outgrows the reference that the tile itself sets.
+  if (w.rows <= kPfKeys) return GROK_OK;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(sms);
+  cfg.blockDim = dim3(256);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cudaError_t e = cudaLaunchKernelEx(&cfg, kv8_v_to_bf16_kernel, static_cast<const int32_t*>(fb_count), u.v_copy,
+                                     (long long)B * w.rows * kKVHeads * (kD / 8));
+  if (e != cudaSuccess) return fail(cuda_status(e), "kv8_v_to_bf16 launch: %s", cudaGetErrorString(e));
   if ((st = check_launch("kv8_v_to_bf16")) != GROK_OK) return st;
   return prefill_q8_passes(a, true, s);
 }

@@ -550,7 +550,9 @@ __global__ void __launch_bounds__(kPfThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   // The fallback pass runs as a programmatic dependent of the fp16 pass: wait
   // for that grid's writes (the list, the outputs it replaces). A no-op otherwise.
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  // (8-bit cache: the whole-item pass is a dependent of the kernel that makes the copies, and each pass of the one
+  // before it; the wait is below, after what reads nothing of theirs.)
+  if (!kQ8) asm volatile("griddepcontrol.wait;" ::: "memory");
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sQ = smem;
   uint8_t* sK = smem + kQBytes;                           // K ring
@@ -606,6 +608,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = bars->tmem_base;
+  if (kQ8) asm volatile("griddepcontrol.wait;" ::: "memory");
 
   if (warp == 0) {
     // ------------------------------------------------------------ TMA producer
@@ -1281,7 +1284,7 @@ extern "C" grok_status grok_attn_prefill_ws_paged(const grok_bf16* q_rot, const 
 // The attention passes over copies of an 8-bit cache.
 template <typename Kernel>
 static grok_status q8_launch(Kernel kernel, int which, int grid, const CUtensorMap (&m)[4], const PfParams& p,
-                             bool dependent, cudaStream_t stream) {
+                             cudaStream_t stream) {
   static bool attr_set[kMaxDevices][3] = {};  // per device and kernel instance; idempotent
   int dev = 0;
   grok_status st = device_index(&dev);
@@ -1298,7 +1301,7 @@ static grok_status q8_launch(Kernel kernel, int which, int grid, const CUtensorM
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = dependent ? 1 : 0;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, m[0], m[1], m[2], m[3], p);
@@ -1313,7 +1316,7 @@ grok_status grok::prefill_q8_passes(const Q8Prefill& a, bool fallback, cudaStrea
   const uint64_t qdims[4] = {kD, kQHeads, uint64_t(a.T), uint64_t(a.B)};
   const uint64_t qstrides[3] = {kD * 2, uint64_t(kQHeads) * kD * 2, uint64_t(a.T) * kQHeads * kD * 2};
   const uint64_t dims[4] = {kD, kKVHeads, uint64_t(a.rows), uint64_t(a.B)};
-  const uint64_t strides[3] = {kD * 2, uint64_t(kKVHeads) * kD * 2, uint64_t(a.rows) * kKVHeads * kD * 2};
+  const uint64_t strides[3] = {uint64_t(a.rows) * kD * 2, kD * 2, uint64_t(a.rows) * kKVHeads * kD * 2};
   if ((st = encode_tmap_bf16_4d(&m[0], a.q, qdims, qstrides, box)) != GROK_OK ||
       (st = encode_tmap_bf16_4d(&m[1], a.k_copy, dims, strides, box)) != GROK_OK ||
       (st = fallback ? encode_tmap_bf16_4d(&m[2], a.v_copy, dims, strides, box)
@@ -1341,11 +1344,11 @@ grok_status grok::prefill_q8_passes(const Q8Prefill& a, bool fallback, cudaStrea
     p.item_list = a.fb_list;
     p.item_count = a.fb_count;
     p.n_units = p.n_items;
-    return q8_launch(prefill_kernel<false, true, false, true>, 2, a.sms, m, p, true, stream);
+    return q8_launch(prefill_kernel<false, true, false, true>, 2, a.sms, m, p, stream);
   }
   if (a.n_whole > 0) {
     p.n_units = a.n_whole;
-    if ((st = q8_launch(prefill_kernel<true, false, false, true>, 0, std::min(a.n_whole, a.sms), m, p, false, stream)) !=
+    if ((st = q8_launch(prefill_kernel<true, false, false, true>, 0, std::min(a.n_whole, a.sms), m, p, stream)) !=
         GROK_OK)
       return st;
   }
@@ -1357,5 +1360,5 @@ grok_status grok::prefill_q8_passes(const Q8Prefill& a, bool fallback, cudaStrea
   p.part_cnt = reinterpret_cast<int32_t*>(a.split_area);
   p.part_lm = reinterpret_cast<float2*>(a.split_area + split_cnt_bytes(a.sms));
   p.part_o = reinterpret_cast<float4*>(a.split_area + split_cnt_bytes(a.sms) + split_lm_bytes(a.sms));
-  return q8_launch(prefill_kernel<true, false, true, true>, 1, std::min(p.n_units, a.sms), m, p, false, stream);
+  return q8_launch(prefill_kernel<true, false, true, true>, 1, std::min(p.n_units, a.sms), m, p, stream);
 }

@@ -52,7 +52,7 @@ inline void split_plan(int n_items, int sms, bool allowed, int& n_whole, int& n_
 }
 
 // Attention over copies of an 8-bit cache (kv8_prefill.cu makes them): k_copy
-// [B][rows][8][128] bf16 codes, v_copy the same in fp16 (fp16 passes) or bf16
+// [B][8][rows][128] bf16 codes, v_copy the same in fp16 (fp16 passes) or bf16
 // (fallback pass), K scales [B][8][rows / 64], the outputs' factors [B][8].
 struct Q8Prefill {
   const grok_bf16* q;
@@ -68,8 +68,8 @@ struct Q8Prefill {
   char* split_area;
   int32_t* status;
 };
-// fallback false: the fp16 passes; true: the listed items with bf16 weights, as
-// the programmatic dependent of the kernel before it.
+// fallback false: the fp16 passes; true: the listed items with bf16 weights. Every
+// pass is launched as the programmatic dependent of the kernel before it.
 grok_status prefill_q8_passes(const Q8Prefill& a, bool fallback, cudaStream_t stream);
 
 }  // namespace grok

@@ -6,13 +6,12 @@ the device of its tensors, on that device's current stream unless one is given.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 from typing import Optional
 
 import torch
 
-from . import (HEAD_DIM, KV8_BLOCK, KV8_E4M3, KV8_INT8, MAX_POSITION, N_KV_HEADS, N_Q_HEADS, _check, _ptr, _want, load)
+from . import HEAD_DIM, KV8_BLOCK, KV8_E4M3, KV8_INT8, MAX_POSITION, N_KV_HEADS, N_Q_HEADS, _check, _want, load
 
 _KINDS = {torch.int8: KV8_INT8, torch.float8_e4m3fn: KV8_E4M3}
 
@@ -24,29 +23,41 @@ class _Cache(ctypes.Structure):
                 ("n_blocks", ctypes.c_int)]
 
 
-def _same_device(device: torch.device, **tensors: Optional[torch.Tensor]) -> None:
-    for name, t in tensors.items():
-        if t is not None and t.device != device:
-            raise ValueError(f"{name} is on {t.device}, the other tensors on {device}")
+def _need(t, name: str, dtype: torch.dtype, shape: tuple, index: int) -> int:
+    """The address of t, which must be a contiguous tensor of this type and shape on CUDA device `index`.
+
+    One pass of cheap comparisons (a decode step's calls are short); _want says what is wrong otherwise.
+    """
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == index \
+            and t.is_contiguous():
+        return t.data_ptr()
+    _want(t, name, dtype, shape)
+    raise ValueError(f"{name} is on {t.device}, the cache's or the other tensors on cuda:{index}")
 
 
-@contextlib.contextmanager
-def _on(device: torch.device):
-    with torch.cuda.device(device):
-        yield
+def _maybe(t, name: str, dtype: torch.dtype, shape: tuple, index: int) -> Optional[int]:
+    return None if t is None else _need(t, name, dtype, shape, index)
 
 
-def _call(device: torch.device, stream: Optional[torch.cuda.Stream], name: str, *args) -> None:
-    """fn(*args, stream) with the tensors' device current."""
-    lib = load()
-    if stream is not None and stream.device != device:
-        raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
-    s = (stream if stream is not None else torch.cuda.current_stream(device)).cuda_stream
-    if torch.cuda.current_device() == device.index:
-        _check(getattr(lib, name)(*args, ctypes.c_void_p(s)))
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _call(index: int, stream: Optional[torch.cuda.Stream], name: str, *args) -> None:
+    """The library's call `name` on `stream` (None: the device's current one), with device `index` current."""
+    if stream is not None:
+        if stream.device.index != index:
+            raise ValueError(f"stream is on {stream.device}, the tensors on cuda:{index}")
+        s = stream.cuda_stream
     else:
-        with _on(device):
-            _check(getattr(lib, name)(*args, ctypes.c_void_p(s)))
+        s = _raw_stream(index) if _raw_stream is not None else torch.cuda.current_stream(index).cuda_stream
+    fn = getattr(load(), name)
+    if torch.cuda.current_device() == index:
+        status = fn(*args, s)
+    else:
+        with torch.cuda.device(index):
+            status = fn(*args, s)
+    if status:
+        _check(status)
 
 
 class Kv8Cache:
@@ -59,7 +70,7 @@ class Kv8Cache:
     """
 
     __slots__ = ("k_pool", "v_pool", "k_scale", "v_scale", "table", "open_k", "open_v", "B", "max_blocks", "n_blocks",
-                 "device", "_c", "_ref")
+                 "index", "_c", "_ref")
 
     def __init__(self, k_pool, v_pool, k_scale, v_scale, table, open_k, open_v):
         if k_pool.dtype not in _KINDS:
@@ -67,24 +78,21 @@ class Kv8Cache:
         if table.dim() != 3:
             raise ValueError("table must be [B, 8, max_blocks]")
         n, (B, _, max_blocks) = k_pool.shape[0], table.shape
-        half = HEAD_DIM // 2
-        _want(k_pool, "k_pool", k_pool.dtype, (n, 2, KV8_BLOCK, half))
-        _want(v_pool, "v_pool", k_pool.dtype, (n, HEAD_DIM, KV8_BLOCK))
-        _want(k_scale, "k_scale", torch.float32, (n,))
-        _want(v_scale, "v_scale", torch.float32, (n,))
-        _want(table, "table", torch.int32, (B, N_KV_HEADS, max_blocks))
-        _want(open_k, "open_k", torch.bfloat16, (B, N_KV_HEADS, KV8_BLOCK, HEAD_DIM))
-        _want(open_v, "open_v", torch.bfloat16, (B, N_KV_HEADS, KV8_BLOCK, HEAD_DIM))
+        half, pool = HEAD_DIM // 2, k_pool.dtype
+        _want(k_pool, "k_pool", pool, (n, 2, KV8_BLOCK, half))
         if not 1 <= max_blocks <= MAX_POSITION // KV8_BLOCK:
             raise ValueError(f"max_blocks must be 1 to {MAX_POSITION // KV8_BLOCK}, got {max_blocks}")
-        self.device = k_pool.device
-        _same_device(self.device, v_pool=v_pool, k_scale=k_scale, v_scale=v_scale, table=table, open_k=open_k,
-                     open_v=open_v)
+        rows, index = (B, N_KV_HEADS, KV8_BLOCK, HEAD_DIM), k_pool.get_device()
+        self.index = index
+        self._c = _Cache(k_pool.data_ptr(), _need(v_pool, "v_pool", pool, (n, HEAD_DIM, KV8_BLOCK), index),
+                         _need(k_scale, "k_scale", torch.float32, (n,), index),
+                         _need(v_scale, "v_scale", torch.float32, (n,), index),
+                         _need(table, "table", torch.int32, (B, N_KV_HEADS, max_blocks), index),
+                         _need(open_k, "open_k", torch.bfloat16, rows, index),
+                         _need(open_v, "open_v", torch.bfloat16, rows, index), _KINDS[pool], B, max_blocks, n)
         self.k_pool, self.v_pool, self.k_scale, self.v_scale = k_pool, v_pool, k_scale, v_scale
         self.table, self.open_k, self.open_v = table, open_k, open_v
         self.B, self.max_blocks, self.n_blocks = B, max_blocks, n
-        self._c = _Cache(k_pool.data_ptr(), v_pool.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
-                         table.data_ptr(), open_k.data_ptr(), open_v.data_ptr(), _KINDS[k_pool.dtype], B, max_blocks, n)
         self._ref = ctypes.byref(self._c)
 
     def __setattr__(self, name, value):
@@ -117,23 +125,15 @@ def kv8_append(cache: Kv8Cache, q, k, v, start_pos, cache_len, valid_len, cos_ta
     valid_len may be None (all T tokens). cos_tab, sin_tab [n, 64] as from rope_cos_sin(0, n). The caller advances
     cache_len and start_pos (see grok_kv8_append).
     """
-    B, T, n = cache.B, q.shape[1], cos_tab.shape[0]
-    _want(q, "q", torch.bfloat16, (B, T, N_Q_HEADS, HEAD_DIM))
-    _want(k, "k", torch.bfloat16, (B, T, N_KV_HEADS, HEAD_DIM))
-    _want(v, "v", torch.bfloat16, (B, T, N_KV_HEADS, HEAD_DIM))
-    _want(start_pos, "start_pos", torch.int32, (B,))
-    _want(cache_len, "cache_len", torch.int32, (B,))
-    if valid_len is not None:
-        _want(valid_len, "valid_len", torch.int32, (B,))
-    _want(cos_tab, "cos_tab", torch.float32, (n, 64))
-    _want(sin_tab, "sin_tab", torch.float32, (n, 64))
-    _want(q_rot, "q_rot", torch.bfloat16, (B, T, N_Q_HEADS, HEAD_DIM))
-    if dev_status is not None:
-        _want(dev_status, "dev_status", torch.int32, (1,))
-    _same_device(cache.device, q=q, k=k, v=v, start_pos=start_pos, cache_len=cache_len, valid_len=valid_len,
-                 cos_tab=cos_tab, sin_tab=sin_tab, q_rot=q_rot, dev_status=dev_status)
-    _call(cache.device, stream, "grok_kv8_append", cache._ref, _ptr(q), _ptr(k), _ptr(v), _ptr(start_pos),
-          _ptr(cache_len), _ptr(valid_len), T, _ptr(cos_tab), _ptr(sin_tab), n, _ptr(q_rot), _ptr(dev_status))
+    B, T, n, at = cache.B, q.shape[1], cos_tab.shape[0], cache.index
+    kv = (B, T, N_KV_HEADS, HEAD_DIM)
+    heads = (B, T, N_Q_HEADS, HEAD_DIM)
+    _call(at, stream, "grok_kv8_append", cache._ref, _need(q, "q", torch.bfloat16, heads, at),
+          _need(k, "k", torch.bfloat16, kv, at), _need(v, "v", torch.bfloat16, kv, at),
+          _need(start_pos, "start_pos", torch.int32, (B,), at), _need(cache_len, "cache_len", torch.int32, (B,), at),
+          _maybe(valid_len, "valid_len", torch.int32, (B,), at), T,
+          _need(cos_tab, "cos_tab", torch.float32, (n, 64), at), _need(sin_tab, "sin_tab", torch.float32, (n, 64), at),
+          n, _need(q_rot, "q_rot", torch.bfloat16, heads, at), _maybe(dev_status, "dev_status", torch.int32, (1,), at))
 
 
 def kv8_decode_workspace(B: int, max_blocks: int, weights: bool = True) -> int:
@@ -144,9 +144,8 @@ def kv8_decode_workspace(B: int, max_blocks: int, weights: bool = True) -> int:
 
 
 def alloc_kv8_decode_workspace(cache: Kv8Cache, weights: bool = True) -> torch.Tensor:
-    with _on(cache.device):
-        return torch.empty(kv8_decode_workspace(cache.B, cache.max_blocks, weights), dtype=torch.uint8,
-                           device=cache.device)
+    with torch.cuda.device(cache.index):
+        return torch.empty(kv8_decode_workspace(cache.B, cache.max_blocks, weights), dtype=torch.uint8, device="cuda")
 
 
 def kv8_decode(cache: Kv8Cache, q_rot, kv_len, workspace, out, weight_in=None, weight_out=None, dev_status=None,
@@ -156,21 +155,15 @@ def kv8_decode(cache: Kv8Cache, q_rot, kv_len, workspace, out, weight_in=None, w
     weight_out [B, 8, max_blocks] float32 (optional): weight_in (None: zero; may be weight_out) plus the softmax
     weight each block received, summed over the KV head's query heads.
     """
-    B = cache.B
-    _want(q_rot, "q_rot", torch.bfloat16, (B, N_Q_HEADS, HEAD_DIM))
-    _want(kv_len, "kv_len", torch.int32, (B,))
-    _want(out, "out", torch.bfloat16, (B, N_Q_HEADS, HEAD_DIM))
-    _want(workspace, "workspace", torch.uint8, (workspace.numel(),))
-    if weight_in is not None:
-        _want(weight_in, "weight_in", torch.float32, (B, N_KV_HEADS, cache.max_blocks))
-    if weight_out is not None:
-        _want(weight_out, "weight_out", torch.float32, (B, N_KV_HEADS, cache.max_blocks))
-    if dev_status is not None:
-        _want(dev_status, "dev_status", torch.int32, (1,))
-    _same_device(cache.device, q_rot=q_rot, kv_len=kv_len, out=out, workspace=workspace, weight_in=weight_in,
-                 weight_out=weight_out, dev_status=dev_status)
-    _call(cache.device, stream, "grok_kv8_decode", cache._ref, _ptr(q_rot), _ptr(kv_len), _ptr(workspace),
-          workspace.numel(), _ptr(out), _ptr(weight_in), _ptr(weight_out), _ptr(dev_status))
+    B, at = cache.B, cache.index
+    heads, blocks = (B, N_Q_HEADS, HEAD_DIM), (B, N_KV_HEADS, cache.max_blocks)
+    nbytes = workspace.numel()
+    _call(at, stream, "grok_kv8_decode", cache._ref, _need(q_rot, "q_rot", torch.bfloat16, heads, at),
+          _need(kv_len, "kv_len", torch.int32, (B,), at), _need(workspace, "workspace", torch.uint8, (nbytes,), at),
+          nbytes, _need(out, "out", torch.bfloat16, heads, at),
+          _maybe(weight_in, "weight_in", torch.float32, blocks, at),
+          _maybe(weight_out, "weight_out", torch.float32, blocks, at),
+          _maybe(dev_status, "dev_status", torch.int32, (1,), at))
 
 
 def kv8_prefill_workspace(B: int, max_blocks: int) -> int:
@@ -181,8 +174,8 @@ def kv8_prefill_workspace(B: int, max_blocks: int) -> int:
 
 
 def alloc_kv8_prefill_workspace(cache: Kv8Cache) -> torch.Tensor:
-    with _on(cache.device):
-        return torch.empty(kv8_prefill_workspace(cache.B, cache.max_blocks), dtype=torch.uint8, device=cache.device)
+    with torch.cuda.device(cache.index):
+        return torch.empty(kv8_prefill_workspace(cache.B, cache.max_blocks), dtype=torch.uint8, device="cuda")
 
 
 def kv8_prefill(cache: Kv8Cache, q_rot, cache_len, valid_len, out, workspace, dev_status=None, stream=None) -> None:
@@ -190,19 +183,12 @@ def kv8_prefill(cache: Kv8Cache, q_rot, cache_len, valid_len, out, workspace, de
 
     The tokens' own rows are in the cache already (kv8_append with the same cache_len and valid_len, which may be None).
     """
-    B, T = cache.B, q_rot.shape[1]
-    _want(q_rot, "q_rot", torch.bfloat16, (B, T, N_Q_HEADS, HEAD_DIM))
-    _want(cache_len, "cache_len", torch.int32, (B,))
-    if valid_len is not None:
-        _want(valid_len, "valid_len", torch.int32, (B,))
-    _want(out, "out", torch.bfloat16, (B, T, N_Q_HEADS, HEAD_DIM))
-    _want(workspace, "workspace", torch.uint8, (workspace.numel(),))
-    if dev_status is not None:
-        _want(dev_status, "dev_status", torch.int32, (1,))
-    _same_device(cache.device, q_rot=q_rot, cache_len=cache_len, valid_len=valid_len, out=out, workspace=workspace,
-                 dev_status=dev_status)
-    _call(cache.device, stream, "grok_kv8_prefill", cache._ref, _ptr(q_rot), _ptr(cache_len), _ptr(valid_len), T,
-          _ptr(out), _ptr(workspace), workspace.numel(), _ptr(dev_status))
+    B, T, at = cache.B, q_rot.shape[1], cache.index
+    heads, nbytes = (B, T, N_Q_HEADS, HEAD_DIM), workspace.numel()
+    _call(at, stream, "grok_kv8_prefill", cache._ref, _need(q_rot, "q_rot", torch.bfloat16, heads, at),
+          _need(cache_len, "cache_len", torch.int32, (B,), at), _maybe(valid_len, "valid_len", torch.int32, (B,), at), T,
+          _need(out, "out", torch.bfloat16, heads, at), _need(workspace, "workspace", torch.uint8, (nbytes,), at), nbytes,
+          _maybe(dev_status, "dev_status", torch.int32, (1,), at))
 
 
 def kv8_evict(table, weight, kv_len, keep: int, sink: int, recent: int, table_out, weight_out, kv_len_out,
@@ -214,15 +200,12 @@ def kv8_evict(table, weight, kv_len, keep: int, sink: int, recent: int, table_ou
     if table.dim() != 3:
         raise ValueError("table must be [B, 8, max_blocks]")
     B, _, n = table.shape
-    _want(table, "table", torch.int32, (B, N_KV_HEADS, n))
-    _want(weight, "weight", torch.float32, (B, N_KV_HEADS, n))
-    _want(kv_len, "kv_len", torch.int32, (B,))
-    _want(table_out, "table_out", torch.int32, (B, N_KV_HEADS, n))
-    _want(weight_out, "weight_out", torch.float32, (B, N_KV_HEADS, n))
-    _want(kv_len_out, "kv_len_out", torch.int32, (B,))
-    if dev_status is not None:
-        _want(dev_status, "dev_status", torch.int32, (1,))
-    _same_device(table.device, weight=weight, kv_len=kv_len, table_out=table_out, weight_out=weight_out,
-                 kv_len_out=kv_len_out, dev_status=dev_status)
-    _call(table.device, stream, "grok_kv8_evict", _ptr(table), _ptr(weight), _ptr(kv_len), B, n, int(keep), int(sink),
-          int(recent), _ptr(table_out), _ptr(weight_out), _ptr(kv_len_out), _ptr(dev_status))
+    row, at = (B, N_KV_HEADS, n), table.get_device()
+    if at < 0:
+        raise ValueError("table must be a CUDA tensor")
+    _call(at, stream, "grok_kv8_evict", _need(table, "table", torch.int32, row, at),
+          _need(weight, "weight", torch.float32, row, at), _need(kv_len, "kv_len", torch.int32, (B,), at), B, n,
+          int(keep), int(sink), int(recent), _need(table_out, "table_out", torch.int32, row, at),
+          _need(weight_out, "weight_out", torch.float32, row, at),
+          _need(kv_len_out, "kv_len_out", torch.int32, (B,), at),
+          _maybe(dev_status, "dev_status", torch.int32, (1,), at))
