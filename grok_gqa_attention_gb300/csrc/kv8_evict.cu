@@ -22,7 +22,7 @@ constexpr int kEvWarps = 4;
 
 // kPer: entries a lane holds; entry 32 e + lane of the row is e of the lane.
 template <int kPer>
-__global__ void __launch_bounds__(kEvWarps * 32) kv8_evict_kernel(const int32_t* table, const float* weight,
+__global__ void __launch_bounds__(kEvWarps * 32, 4) kv8_evict_kernel(const int32_t* table, const float* weight,
                                                                   const int32_t* kv_len, int n_rows, int max_blocks,
                                                                   int keep, int sink, int recent, int32_t* table_out,
                                                                   float* weight_out, int32_t* kv_len_out,
@@ -61,16 +61,15 @@ __global__ void __launch_bounds__(kEvWarps * 32) kv8_evict_kernel(const int32_t*
   const int free_end = closed - recent, quota = keep - min(sink, closed) - recent;
   uint32_t edge = 0;
   int above = 0;  // candidates at or above `edge`
-  auto key_of = [&](int e) {
-    const int i = 32 * e + lane;
-    return i >= sink && i < free_end ? order_key(w[e]) : 0u;  // (a candidate's key is never 0)
-  };
+  uint32_t key[kPer];  // 0 for the others (a candidate's key is not)
+#pragma unroll
+  for (int e = 0; e < kPer; ++e) key[e] = 32 * e + lane >= sink && 32 * e + lane < free_end ? order_key(w[e]) : 0u;
   if (quota > 0) {
     for (int bit = 31; bit >= 0; --bit) {
       const uint32_t trial = edge | (1u << bit);
       int n = 0;
 #pragma unroll
-      for (int e = 0; e < kPer; ++e) n += key_of(e) >= trial;
+      for (int e = 0; e < kPer; ++e) n += key[e] >= trial;
       n = __reduce_add_sync(0xffffffffu, n);
       if (n >= quota) {
         edge = trial;
@@ -82,28 +81,36 @@ __global__ void __launch_bounds__(kEvWarps * 32) kv8_evict_kernel(const int32_t*
     edge = 0xFFFFFFFFu;
   }
   // Unless the search ended early, the blocks equal to `edge` are too many by above - quota: the last ones go.
-  int equal = 0;
+  int ties = 0x7FFFFFFF;
+  if (above > quota) {
+    int equal = 0;
 #pragma unroll
-  for (int e = 0; e < kPer; ++e) equal += key_of(e) == edge;
-  equal = __reduce_add_sync(0xffffffffu, equal);
-  int ties = quota > 0 ? equal - (above - quota) : 0;
+    for (int e = 0; e < kPer; ++e) equal += key[e] == edge;
+    ties = __reduce_add_sync(0xffffffffu, equal) - (above - quota);
+  }
+  const uint32_t lower = (1u << lane) - 1u;
+  int32_t* t_out = table_out + row;
+  float* w_out = weight_out + row;
+  const int gone_at = keep + (closed < max_blocks ? 1 : 0);  // behind the open block
   int rank = 0;  // blocks that stay, before this run of 32
 #pragma unroll
   for (int e = 0; e < kPer; ++e) {
     const int i = 32 * e + lane;
-    const uint32_t key = key_of(e), lower = (1u << lane) - 1u;
-    const bool tie = quota > 0 && key != 0 && key == edge;
-    const uint32_t tied = __ballot_sync(0xffffffffu, tie);
-    const bool stays = i < closed && (i < sink || i >= free_end || (key > edge) || (tie && __popc(tied & lower) < ties));
-    ties -= min(ties, __popc(tied));
+    bool stays = i < closed && (i < sink || i >= free_end || key[e] >= edge);
+    if (ties < kPer * 32) {
+      const bool tie = key[e] == edge;  // (edge is not 0 here)
+      const uint32_t tied = __ballot_sync(0xffffffffu, tie);
+      stays = stays && !(tie && __popc(tied & lower) >= ties);
+      ties -= min(ties, __popc(tied));
+    }
     const uint32_t staying = __ballot_sync(0xffffffffu, stays);
     const int before = rank + __popc(staying & lower);
     rank += __popc(staying);
+    int to = before;
+    if (!stays) to = i < closed ? gone_at + i - before : i == closed ? keep : i;
     if (i < max_blocks) {
-      const bool gone = i < closed && !stays;
-      const int to = i > closed ? i : i == closed ? keep : stays ? before : keep + (closed < max_blocks ? 1 : 0) + i - before;
-      table_out[row + to] = id[e];
-      weight_out[row + to] = gone ? 0.f : w[e];
+      t_out[to] = id[e];
+      w_out[to] = i < closed && !stays ? 0.f : w[e];
     }
   }
 }
