@@ -31,12 +31,8 @@
 
 namespace grok {
 
-#ifndef KDQ_WARPS
-#define KDQ_WARPS 10
-#define KDQ_BUFS 2
-#endif
-constexpr int kDqWarps = KDQ_WARPS;
-constexpr int kDqBufs = KDQ_BUFS;      // a warp's ring: K and V of its blocks in turn
+constexpr int kDqWarps = 10;
+constexpr int kDqBufs = 2;  // a warp's ring: K and V of its blocks in turn
 constexpr int kDqThreads = kDqWarps * 32;
 constexpr int kDqRing = kDqBufs * kKv8Bytes;
 constexpr int kDqSmem = kDqWarps * kDqRing + kDqWarps * kDqBufs * 8 + 16;
@@ -405,51 +401,80 @@ __device__ __forceinline__ float warp_sum(float x) {
 template <int kHeads, int kSplit>
 __global__ void __launch_bounds__(kHeads * kSplit * 32) kv8_join_kernel(const DqParams p) {
   constexpr int kThreads = kHeads * kSplit * 32;
+  constexpr int kBatch = 12;  // partial outputs in flight per warp
   __shared__ float4 s_o[kHeads * kSplit][32];
   __shared__ float s_inv[8];
-  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int pair = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int blocks = kv8_blocks(__ldg(p.kv_len + pair / kKVHeads), p.c.max_blocks);
-  const int2 parts = p.pair_parts[pair];  // first slot, number (not written for a bad length)
+  const bool weights = p.weight_out && (kHeads > 1 || blockIdx.y == kGroup);
+  // The first blocks' old weights do not depend on the first kernel.
+  const size_t at0 = (size_t)pair * p.c.max_blocks + threadIdx.x;
+  float w_in = 0.f;
+  if (weights && p.weight_in && threadIdx.x < p.c.max_blocks) w_in = p.weight_in[at0];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   if (blocks == 0) return;                // reported by the first kernel
-  const size_t slot0 = parts.x;
+  const int2 parts = p.pair_parts[pair];  // first slot, number
   const int n_parts = parts.y;
+  const float2* ml = p.part_ml + (size_t)parts.x * kGroup;
+  float4 wa = make_float4(0.f, 0.f, 0.f, 0.f);
+  float2 wb = make_float2(0.f, 0.f);
+  if (weights && threadIdx.x < blocks) {
+    wa = *reinterpret_cast<const float4*>(p.block_w + at0 * 8);
+    wb = *reinterpret_cast<const float2*>(p.block_w + at0 * 8 + 4);
+  }
 
-  const bool weights_only = kHeads == 1 && blockIdx.y == kGroup;
-  if (!weights_only) {
+  if (kHeads > 1 || blockIdx.y < kGroup) {
+    // Everything is loaded before anything is used: the partials' sums, a lane to each, and this warp's first outputs.
     const int head = kHeads == 1 ? blockIdx.y : warp / kSplit, sub = warp % kSplit;
-    float m = -INFINITY, l = 0.f;
-    for (int k = lane; k < n_parts; k += 32) m = fmaxf(m, p.part_ml[(slot0 + k) * kGroup + head].x);
-    m = warp_max(m);
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int k0 = 0; k0 < n_parts; k0 += 32) {
-      float my_f = 0.f;
-      if (k0 + lane < n_parts) {
-        const float2 ml = p.part_ml[(slot0 + k0 + lane) * kGroup + head];
-        my_f = ex2_approx(ml.x - m);
-        l = fmaf(ml.y, my_f, l);
-      }
-      const float* po = p.part_o + ((slot0 + k0) * kGroup + head) * kD + 4 * lane;
-      const int n = min(32, n_parts - k0);
-#pragma unroll 8
-      for (int k = sub; k < n; k += kSplit) {
-        const float4 v = *reinterpret_cast<const float4*>(po + (size_t)k * (kGroup * kD));
-        const float f = __shfl_sync(0xffffffffu, my_f, k);
-        acc.x = fmaf(v.x, f, acc.x);
-        acc.y = fmaf(v.y, f, acc.y);
-        acc.z = fmaf(v.z, f, acc.z);
-        acc.w = fmaf(v.w, f, acc.w);
+    const float* po = p.part_o + ((size_t)parts.x * kGroup + head) * kD + 4 * lane;
+    const float2 mine = lane < n_parts ? ml[lane * kGroup + head] : make_float2(-INFINITY, 0.f);
+    float4 v[kBatch];
+    float vm[kBatch];
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const int k = sub + u * kSplit;
+      v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+      vm[u] = -INFINITY;
+      if (k < n_parts) {
+        v[u] = *reinterpret_cast<const float4*>(po + (size_t)k * (kGroup * kD));
+        vm[u] = ml[k * kGroup + head].x;
       }
     }
+    float m = mine.x;
+    for (int k = lane + 32; k < n_parts; k += 32) m = fmaxf(m, ml[k * kGroup + head].x);
+    m = warp_max(m);
+    float l = mine.y * ex2_approx(mine.x - m);
+    for (int k = lane + 32; k < n_parts; k += 32) {
+      const float2 x = ml[k * kGroup + head];
+      l = fmaf(x.y, ex2_approx(x.x - m), l);
+    }
     l = warp_sum(l);
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const float f = ex2_approx(vm[u] - m);
+      acc.x = fmaf(v[u].x, f, acc.x);
+      acc.y = fmaf(v[u].y, f, acc.y);
+      acc.z = fmaf(v[u].z, f, acc.z);
+      acc.w = fmaf(v[u].w, f, acc.w);
+    }
+#pragma unroll 8
+    for (int k = sub + kBatch * kSplit; k < n_parts; k += kSplit) {
+      const float4 x = *reinterpret_cast<const float4*>(po + (size_t)k * (kGroup * kD));
+      const float f = ex2_approx(ml[k * kGroup + head].x - m);
+      acc.x = fmaf(x.x, f, acc.x);
+      acc.y = fmaf(x.y, f, acc.y);
+      acc.z = fmaf(x.z, f, acc.z);
+      acc.w = fmaf(x.w, f, acc.w);
+    }
     if (kSplit > 1) {
       s_o[warp][lane] = acc;
       __syncthreads();
       if (sub == 0) {
 #pragma unroll
         for (int w = 1; w < kSplit; ++w) {
-          const float4 v = s_o[warp + w][lane];
-          acc.x += v.x, acc.y += v.y, acc.z += v.z, acc.w += v.w;
+          const float4 x = s_o[warp + w][lane];
+          acc.x += x.x, acc.y += x.y, acc.z += x.z, acc.w += x.w;
         }
       }
     }
@@ -457,31 +482,31 @@ __global__ void __launch_bounds__(kHeads * kSplit * 32) kv8_join_kernel(const Dq
       const float inv = 1.f / l;
       p.out[((size_t)pair * kGroup + head) * (kD / 4) + lane] =
           make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
-      if (kHeads > 1 && lane == 0) s_inv[head] = 1.f / (l * ex2_approx(m));
+      if (kHeads > 1 && lane == 0) s_inv[head] = 1.f / (l * ex2_approx(m));  // on the fixed reference 30
     }
-    if (kHeads == 1 || !p.weight_out) return;
   } else {
-    // the heads' sums on the fixed reference 30
     for (int h = warp; h < kGroup; h += kSplit) {
       float l = 0.f;
-      for (int k = lane; k < n_parts; k += 32) {
-        const float2 ml = p.part_ml[(slot0 + k) * kGroup + h];
-        l = fmaf(ml.y, ex2_approx(ml.x), l);
-      }
+      for (int k = lane; k < n_parts; k += 32) l = fmaf(ml[k * kGroup + h].y, ex2_approx(ml[k * kGroup + h].x), l);
       l = warp_sum(l);
       if (lane == 0) s_inv[h] = 1.f / l;
     }
   }
+  if (!weights) return;
   __syncthreads();
   for (int i = threadIdx.x; i < p.c.max_blocks; i += kThreads) {
     const size_t at = (size_t)pair * p.c.max_blocks + i;
-    float w = 0.f;
-    if (i < blocks) {
-      const float4 a = *reinterpret_cast<const float4*>(p.block_w + at * 8);
-      const float2 c = *reinterpret_cast<const float2*>(p.block_w + at * 8 + 4);
-      w = a.x * s_inv[0] + a.y * s_inv[1] + a.z * s_inv[2] + a.w * s_inv[3] + c.x * s_inv[4] + c.y * s_inv[5];
+    if (i >= kThreads) {
+      w_in = p.weight_in ? p.weight_in[at] : 0.f;
+      if (i < blocks) {
+        wa = *reinterpret_cast<const float4*>(p.block_w + at * 8);
+        wb = *reinterpret_cast<const float2*>(p.block_w + at * 8 + 4);
+      }
     }
-    p.weight_out[at] = p.weight_in ? p.weight_in[at] + w : w;
+    float w = 0.f;
+    if (i < blocks)
+      w = wa.x * s_inv[0] + wa.y * s_inv[1] + wa.z * s_inv[2] + wa.w * s_inv[3] + wb.x * s_inv[4] + wb.y * s_inv[5];
+    p.weight_out[at] = w_in + w;
   }
 }
 
