@@ -226,7 +226,7 @@ extern "C" grok_status grok_kv8_prefill(const grok_kv8_cache* cache, const grok_
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const int n_items = prefill_items(B, T);
   int n_whole, n_parts;
-  split_plan(n_items, sms, split_allowed(w.rows), n_whole, n_parts);
+  split_plan(n_items, sms, split_allowed(w.rows), kPfMaxPartsQ8, n_whole, n_parts);
   const int n_split = n_items - n_whole;
 
   int32_t* fb_count = reinterpret_cast<int32_t*>(ws);

@@ -451,6 +451,7 @@ __device__ __forceinline__ float pf_rowmax_half(uint32_t trow, int half, int rel
 // on which unit finishes last) and stages the output rows. Returns 1 when this
 // warp staged output rows, 0 when it has none to write, -1 when a bounded wait
 // gave up. Out of line: its registers stay out of the softmax loop's.
+template <int kMaxParts>
 static __device__ __noinline__ int pf_split_epilogue(const PfParams& p, PfBars* bars, volatile int* abort, int unit,
                                               int item, int parts, int slot, int half, int quad, int lane,
                                               uint32_t trow, float lt, float mref, float o_scale, bool over,
@@ -495,18 +496,18 @@ static __device__ __noinline__ int pf_split_epilogue(const PfParams& p, PfBars* 
   // Part k's weights are 2^(t - m_k) (m_k its reference); on the common
   // reference mx they are scaled by 2^(m_k - mx) <= 1.
   const size_t su0 = size_t(item) * p.n_parts * 2 + slot;  // part 0 of the item, this slot
-  float2 lm[kPfMaxParts];
+  float2 lm[kMaxParts];
   float mx = -INFINITY;
 #pragma unroll
-  for (int k = 0; k < kPfMaxParts; ++k)
+  for (int k = 0; k < kMaxParts; ++k)
     if (k < parts) {
       lm[k] = __ldcg(p.part_lm + (su0 + 2 * k) * kPfRows + r);
       mx = fmaxf(mx, lm[k].y);
     }
-  float fk[kPfMaxParts];
+  float fk[kMaxParts];
   float lsum = 0.f;
 #pragma unroll
-  for (int k = 0; k < kPfMaxParts; ++k)
+  for (int k = 0; k < kMaxParts; ++k)
     if (k < parts) {
       fk[k] = ex2_approx(lm[k].y - mx);
       lsum = fmaf(lm[k].x, fk[k], lsum);
@@ -518,7 +519,7 @@ static __device__ __noinline__ int pf_split_epilogue(const PfParams& p, PfBars* 
 #pragma unroll
     for (int e = 0; e < 8; ++e) acc[e] = 0.f;
 #pragma unroll
-    for (int k = 0; k < kPfMaxParts; ++k)
+    for (int k = 0; k < kMaxParts; ++k)
       if (k < parts) {
         const float4* pk4 = p.part_o + ((su0 + 2 * k) * 2 + half) * (16 * kPfRows) + r;
         const float4 v0 = __ldcg(pk4 + (2 * c) * kPfRows), v1 = __ldcg(pk4 + (2 * c + 1) * kPfRows);
@@ -776,6 +777,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
       bool ok = true;
       for (int u = half; u < it.n_sub; u += 2) {
         const int j = u >> 1;
+        const float ks = kQ8 ? __ldg(k_scale + u) : 1.f;  // (block 2 j + half: arrives while the products run)
         ok = mbar_wait(&bars->s_full[slot][half], sub_cnt & 1, abort, p.status);
         ++sub_cnt;
         if (!__all_sync(0xffffffffu, ok)) {  // leave together: the TMEM ops below are warp-collective
@@ -787,7 +789,6 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         // The choice must be warp-uniform: the TMEM loads and stores inside
         // are warp-collective (.sync.aligned).
         const bool unmasked = __all_sync(0xffffffffu, rel >= 64 * half + 63);
-        const float ks = kQ8 ? __ldg(k_scale + 2 * j + half) : 1.f;
         // (a block that holds a NaN has a NaN scale; the exp2 polynomial may lose it)
         if (kQ8 && rel >= 64 * half) l0 = fmaf(ks, 0.f, l0);
         if (kF16 && j == 0) {
@@ -892,7 +893,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         mbar_arrive(&bars->o_empty[slot]);  // O is read: the next item's products may overwrite it
       } else {
         const int res =
-            pf_split_epilogue(p, bars, abort, item, it.item - p.item_base, it.parts, slot, half, quad, lane, trow, lt,
+            pf_split_epilogue<kQ8 ? kPfMaxPartsQ8 : kPfMaxParts>(p, bars, abort, item, it.item - p.item_base, it.parts, slot, half, quad, lane, trow, lt,
                               mref, o_scale, __any_sync(0xffffffffu, over), stage,
                               uint32_t(split_cnt & 1));
         ++split_cnt;
@@ -1176,7 +1177,8 @@ static grok_status prefill_ws_run(const grok_bf16* q_rot, const grok_bf16* k_src
   // items [0, n_whole) run whole; the rest, if the split applies, n_parts units each
   const int n_items = prefill_items(B, T);
   int n_whole, n_parts;
-  split_plan(n_items, sms, split_allowed(Tmax) && workspace_bytes >= need + split_area_bytes(sms), n_whole, n_parts);
+  split_plan(n_items, sms, split_allowed(Tmax) && workspace_bytes >= need + split_area_bytes(sms), kPfMaxParts, n_whole,
+             n_parts);
   const int n_split = n_items - n_whole;
   char* split_area = static_cast<char*>(workspace) + need;
   const int vh_rows = ws_vh_rows(Tmax);

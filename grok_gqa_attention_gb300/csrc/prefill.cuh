@@ -12,6 +12,7 @@ namespace grok {
 constexpr int kPfRows = 128;   // query rows per tile (MMA M)
 constexpr int kPfKeys = 128;   // keys per K/V tile (MMA N for Q K^T, K for P V)
 constexpr int kPfMaxParts = 4;       // key-range split: most units one item's key tiles are shared among
+constexpr int kPfMaxPartsQ8 = 8;     // the same over an 8-bit cache (24 items, 8192 rows behind: 6 parts, not 4)
 constexpr int kPfMinPartTiles = 8;   // key-range split: fewest key tiles per unit
 
 inline int prefill_items(int B, int T) { return B * ((T + kPfRows - 1) / kPfRows) * GROK_N_KV_HEADS * 3; }
@@ -38,12 +39,12 @@ inline int ws_fb_cap(int B, int Tmax) {
 }
 
 // How many items run whole and how many units share each of the rest.
-inline void split_plan(int n_items, int sms, bool allowed, int& n_whole, int& n_parts) {
+inline void split_plan(int n_items, int sms, bool allowed, int max_parts, int& n_whole, int& n_parts) {
   n_whole = n_items;
   n_parts = 1;
   if (n_items < 2 * sms && allowed) {
     const int rest = n_items % sms;
-    const int parts = rest > 0 ? std::min(kPfMaxParts, sms / rest) : 1;
+    const int parts = rest > 0 ? std::min(max_parts, sms / rest) : 1;
     if (parts > 1) {
       n_whole = n_items - rest;
       n_parts = parts;

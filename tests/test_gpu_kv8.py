@@ -435,6 +435,10 @@ PREFILLS = {
     "warm": ([130, 700, 63], [90, 33, 1], 90),
     "chunk_split": ([2100, 1900], [150, 61], 150),
     "ragged": ([0, 0, 0, 0], [300, 1, 64, 129], 300),
+    # items split over the key range
+    "split_few": ([2500], [1], 1),
+    "split_unequal": ([2000, 64, 900], [300, 500, 7], 500),
+    "split_causal": ([700], [1400], 1400),
 }
 
 
@@ -540,6 +544,25 @@ def test_prefill_non_finite_blocks_reach_their_rows_alone():
         want[b, 64 * blk:, 6 * g:6 * g + 6] = True
         assert torch.equal(nan, want)
         assert torch.equal(got[~want], good[~want])
+
+
+def test_prefill_split_items_of_good_and_bad_sequences():
+    """A key-range split with a sequence that takes no part: its outputs stay."""
+    rng = np.random.default_rng(46)
+    cache, host = filled(rng, [1500, 1100, 1300], "int8", 32, seed=36)
+    q = _bf16(rng.standard_normal((3, 140, 48, 128)) * 3).to(DEV)
+    lens, valid = [1360, 960, 1160], [140, 130, 140]
+    good, status = run_prefill(cache, q, lens, valid, 140)
+    assert status == 0
+    host.k[1], host.v[1] = host.k[1][:1090], host.v[1][:1090]
+    check_prefill(host, q, good, lens, valid, "int8", "kv8 prefill shared", heads=(0, 47))
+    for bad in (-1, 2 ** 31 - 1, 2000):
+        got, status = run_prefill(cache, q, [1360, bad, 1160], valid, 140)
+        assert status == G.DEV_BAD_KV_LEN and (got[1] == 7.0).all()
+        # the split may fall elsewhere: the same within one bf16 step
+        assert_close(_bits(got[[0, 2]]), _bits(good[[0, 2]]), "beside a bad sequence")
+    got, status = run_prefill(cache, q, [-1, -1, -1], valid, 140)
+    assert status == G.DEV_BAD_KV_LEN and (got == 7.0).all()
 
 
 def test_prefill_bad_integers_leave_the_outputs():
