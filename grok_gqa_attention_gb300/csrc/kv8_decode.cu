@@ -54,21 +54,6 @@ struct DqParams {
   int32_t* status;
 };
 
-// Four codes as two fp16 pairs of an A operand. int8: code + 128 in the low byte of
-// an fp16 is the subnormal (code + 128) 2^-24; three instructions for four codes,
-// and the offset is taken off where the sums start (a product's 128 more is a
-// few units of 2^-24 of the sum of |q| or of P). e4m3: converted.
-template <int kKind>
-__device__ __forceinline__ void operand(uint32_t w, uint32_t& lo, uint32_t& hi) {
-  if (kKind == GROK_KV8_INT8) {
-    const uint32_t u = w ^ 0x80808080u;
-    lo = __byte_perm(u, 0u, 0x4140);
-    hi = __byte_perm(u, 0u, 0x4342);
-  } else {
-    kv8_to_half<kKind>(w, lo, hi);
-  }
-}
-
 __device__ __forceinline__ uint32_t word_of(const uint4& x, int w) { return w == 0 ? x.x : w == 1 ? x.y : w == 2 ? x.z : x.w; }
 
 // The sequences' blocks: total over the batch of ceil(kv_len / 64), by one warp.
@@ -109,8 +94,6 @@ __global__ void __launch_bounds__(kDqThreads, 1) kv8_decode_kernel(const DqParam
 
   uint32_t qb[8][2];
   float q_scale0 = 0.f, q_scale1 = 0.f;  // of heads 2 t, 2 t + 1
-  float q_off0 = 0.f, q_off1 = 0.f;
-  constexpr float kUnit = kKind == GROK_KV8_INT8 ? 0x1p24f : 1.f;  // the operands' scale
   float o[8][4], m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
   int pair = -1;
   int buf = 0, next_buf = 0;         // buffers of the next piece to read and to load (a piece: a block's K or V)
@@ -251,16 +234,10 @@ __global__ void __launch_bounds__(kDqThreads, 1) kv8_decode_kernel(const DqParam
             qb[u][c & 1] = pack_f16x2(bf16lo_to_f32(w[c]) * down, bf16hi_to_f32(w[c]) * down);
           }
         }
-        if (kKind == GROK_KV8_INT8) {  // minus 128 x 2^-24 x the sum of q, for every key
-          float off[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-          for (int u = 0; u < 8; ++u) mma_f16_16816(off, 0x80808080u, 0x80808080u, 0x80808080u, 0x80808080u, qb[u][0], qb[u][1]);
-          q_off0 = off[0], q_off1 = off[1];
-        }
         q_scale0 = __shfl_sync(0xffffffffu, up, 8 * t) * (2.f * kY * kLog2e);
         q_scale1 = __shfl_sync(0xffffffffu, up, 8 * t + 4) * (2.f * kY * kLog2e);
       }
-      const float ks = __shfl_sync(0xffffffffu, my_ks, j) * kUnit, vs = __shfl_sync(0xffffffffu, my_vs, j) * kUnit;
+      const float ks = __shfl_sync(0xffffffffu, my_ks, j), vs = __shfl_sync(0xffffffffu, my_vs, j);
       const int keys = __shfl_sync(0xffffffffu, my_keys, j), blk = __shfl_sync(0xffffffffu, my_blk, j);
 
       if (!wait()) break;
@@ -268,8 +245,7 @@ __global__ void __launch_bounds__(kDqThreads, 1) kv8_decode_kernel(const DqParam
       float s[4][4];
 #pragma unroll
       for (int st = 0; st < 4; ++st) {
-        s[st][0] = s[st][2] = q_off0;
-        s[st][1] = s[st][3] = q_off1;
+        s[st][0] = s[st][1] = s[st][2] = s[st][3] = 0.f;
         // row r of the tile is key 16 (r >> 1) + 4 st + (r & 1), row r + 8 two keys on: the order P^T is read in below
         const uint8_t* k0 = k_buf + (16 * (row >> 1) + 4 * st + (row & 1)) * 64 + 16 * t;
 #pragma unroll
@@ -279,8 +255,8 @@ __global__ void __launch_bounds__(kDqThreads, 1) kv8_decode_kernel(const DqParam
 #pragma unroll
           for (int w = 0; w < 4; ++w) {
             uint32_t a0, a1, a2, a3;
-            operand<kKind>(word_of(a, w), a0, a2);
-            operand<kKind>(word_of(b, w), a1, a3);
+            kv8_to_half<kKind>(word_of(a, w), a0, a2);
+            kv8_to_half<kKind>(word_of(b, w), a1, a3);
             mma_f16_16816(s[st], a0, a1, a2, a3, qb[4 * h + w][0], qb[4 * h + w][1]);
           }
         }
@@ -336,12 +312,6 @@ __global__ void __launch_bounds__(kDqThreads, 1) kv8_decode_kernel(const DqParam
 
       if (!wait()) break;
       const uint8_t* v_buf = ring + buf * kKv8Bytes;
-      float off[4] = {0.f, 0.f, 0.f, 0.f};
-      if (kKind == GROK_KV8_INT8) {
-        constexpr uint32_t c = 0x80808080u;  // fp16 -2^-17, twice: the operands' offset of 128 times 2^-24
-#pragma unroll
-        for (int st = 0; st < 4; ++st) mma_f16_16816(off, c, c, c, c, pb[st][0], pb[st][1]);
-      }
 #pragma unroll
       for (int mt = 0; mt < 8; ++mt) {
         uint4 a = *reinterpret_cast<const uint4*>(v_buf + (16 * mt + row) * 64 + 16 * t);
@@ -355,12 +325,12 @@ __global__ void __launch_bounds__(kDqThreads, 1) kv8_decode_kernel(const DqParam
             reinterpret_cast<uint32_t*>(&b)[st] &= mask;
           }
         }
-        float acc[4] = {off[0], off[1], off[2], off[3]};
+        float acc[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int st = 0; st < 4; ++st) {
           uint32_t a0, a1, a2, a3;
-          operand<kKind>(word_of(a, st), a0, a2);
-          operand<kKind>(word_of(b, st), a1, a3);
+          kv8_to_half<kKind>(word_of(a, st), a0, a2);
+          kv8_to_half<kKind>(word_of(b, st), a1, a3);
           mma_f16_16816(acc, a0, a1, a2, a3, pb[st][0], pb[st][1]);
         }
 #pragma unroll
