@@ -10,9 +10,17 @@
 // Every warp is a worker of its own: the blocks of all (sequence, head) pairs, in
 // order, are dealt out in equal contiguous shares, so the load is even for any
 // lengths and no barrier joins warps. A worker streams its blocks through a
-// private K and a private V buffer in shared memory (one bulk copy each), and
-// writes one partial result (m, l, O) per pair that it touches; a second kernel,
-// launched as a dependent, joins a pair's partials.
+// private K and a private V buffer in shared memory (one bulk copy each, of 8 KB),
+// and writes one partial result (m, l, O) per pair that it touches; a second
+// kernel, launched as a dependent, joins a pair's partials. Which blocks make a
+// partial follows from the lengths alone, so the bits do too.
+//
+// Measured (graph replays, one GB300): 32 sequences of up to 8192 rows (274 MB of
+// codes) 52.1 us, 5.26 TB/s, 0.78 of the copy rate; 16 of up to 65536 (1.14 GB) 179 us,
+// 6.38 TB/s, 0.94; one of 300 rows 6.2 us. Of the 52 us about 3 are the join, 45 the
+// loads alone, the rest what the products do not hide. Ten warps with two buffers
+// read as fast as any other split of the shared memory tried (14 x 2, 12 x 2, 9 x 3,
+// 8 x 3, 7 x 4, within 3 %).
 //
 // Per block, on fp16 tensor-core products (codes convert to fp16 exactly, q is
 // scaled to fp16 by a power of two per head):
@@ -31,12 +39,14 @@
 
 namespace grok {
 
-constexpr int kDqWarps = 10;
+constexpr int kDqWarps = 5;
+constexpr int kDqCtas = 2;  // CTAs resident on an SM
 constexpr int kDqBufs = 2;  // a warp's ring: K and V of its blocks in turn
 constexpr int kDqThreads = kDqWarps * 32;
 constexpr int kDqRing = kDqBufs * kKv8Bytes;
 constexpr int kDqSmem = kDqWarps * kDqRing + kDqWarps * kDqBufs * 8 + 16;
-static_assert(kDqSmem <= 232448, "shared memory per CTA");
+static_assert(kDqCtas * (kDqSmem + 1024) <= 233472, "shared memory per SM");
+constexpr int kDqLong = 24;  // blocks per worker from which a second wave of small shares pays
 constexpr float kDqLag = 8.f;  // log2 units a weight may exceed the reference by
 
 struct DqParams {
@@ -50,8 +60,31 @@ struct DqParams {
   uint2* out;
   const float* weight_in;
   float* weight_out;
-  int workers;
+  int wave, second;  // workers of the CTAs resident at a time, and of those behind them
   int32_t* status;
+};
+
+// How `total` blocks are dealt out. The SMs do not all read at the same rate (with
+// equal shares the mean SM is done at 0.82 of the slowest's time). Where shares are
+// long, 7/8 of the blocks are dealt to the `wave` workers that start at once and the
+// rest, in small shares, to a second wave of CTAs that take SMs as they come free
+// (128 sequences of up to 8192 rows: 184.6 -> 178.7 us; 16 of 65536: 185.1 -> 179.1).
+// With short shares the second wave's start costs more than it evens out (32
+// sequences: 52.2 us without, 56.2 with).
+struct Deal {
+  int first, big, small;
+  __device__ __forceinline__ Deal(int total, int wave, int second) {
+    big = second && total >= kDqLong * wave ? int((long long)total * 7 / 8 / wave) : 0;
+    first = big > 0 ? wave : 0;
+    const int slots = first ? second : wave;
+    small = max(1, (total - big * first + slots - 1) / slots);
+  }
+  __device__ __forceinline__ int start(int item) const {
+    return item < first ? item * big : first * big + (item - first) * small;
+  }
+  __device__ __forceinline__ int item_of(int block) const {
+    return block < first * big ? block / big : first + (block - first * big) / small;
+  }
 };
 
 __device__ __forceinline__ uint32_t word_of(const uint4& x, int w) { return w == 0 ? x.x : w == 1 ? x.y : w == 2 ? x.z : x.w; }
@@ -65,7 +98,7 @@ __device__ __forceinline__ int count_blocks(const DqParams& p, int lane) {
 }
 
 template <int kKind, bool kWeights>
-__global__ void __launch_bounds__(kDqThreads, 1) kv8_decode_kernel(const DqParams p) {
+__global__ void __launch_bounds__(kDqThreads, kDqCtas) kv8_decode_kernel(const DqParams p) {
   extern __shared__ __align__(128) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int row = lane >> 2, t = lane & 3;
@@ -82,15 +115,16 @@ __global__ void __launch_bounds__(kDqThreads, 1) kv8_decode_kernel(const DqParam
   __syncthreads();
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int n_total = kKVHeads * count_blocks(p, lane);
-  const int share = (n_total + p.workers - 1) / p.workers;
-  const int item = warp * gridDim.x + blockIdx.x;  // few blocks spread over the SMs first
+  const Deal deal(n_total, p.wave, p.second);
+  const int n_first = p.wave / kDqWarps, cta = blockIdx.x;
+  const int item = cta < n_first ? warp * n_first + cta : cta * kDqWarps + warp;  // (few blocks: over the SMs first)
   if (item == 0)
     for (int b = lane; b < p.c.B; b += 32)
       if (kv8_blocks(__ldg(p.kv_len + b), p.c.max_blocks) == 0) report(p.status, GROK_DEV_BAD_KV_LEN);
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const long long lo_ = (long long)item * share;
-  if (lo_ >= n_total) return;
-  const int lo = int(lo_), hi = min(lo + share, n_total);
+  // (item * small passes n_total by less than a wave of shares: no overflow below 2^31)
+  const int lo = min(deal.start(item), n_total), hi = min(deal.start(item + 1), n_total);
+  if (lo >= hi) return;
 
   uint32_t qb[8][2];
   float q_scale0 = 0.f, q_scale1 = 0.f;  // of heads 2 t, 2 t + 1
@@ -157,7 +191,7 @@ __global__ void __launch_bounds__(kDqThreads, 1) kv8_decode_kernel(const DqParam
           my_blk = in % sn;
           my_keys = min(kKv8Block, sl - my_blk * kKv8Block);
           found = true;
-          if (my_blk == 0) p.pair_parts[my_pair] = make_int2(item + my_pair, (idx + sn - 1) / share - item + 1);
+          if (my_blk == 0) p.pair_parts[my_pair] = make_int2(item + my_pair, deal.item_of(idx + sn - 1) - item + 1);
         }
         cum += chunk;
         if (__all_sync(0xffffffffu, found)) break;
@@ -487,8 +521,9 @@ using namespace grok;
 namespace {
 
 size_t up256(size_t n) { return (n + 255) & ~size_t(255); }
-// A worker's blocks touch a run of pairs, so (worker, pair) runs through fewer than workers + pairs values of their sum.
-size_t part_slots(int B, int sms) { return size_t(sms) * kDqWarps + size_t(B) * kKVHeads; }
+int wave_of(int sms) { return sms * kDqCtas * kDqWarps; }  // workers resident at a time
+// A share touches a run of pairs, so (share, pair) runs through fewer than shares + pairs values of their sum.
+size_t part_slots(int B, int sms) { return size_t(2) * wave_of(sms) + size_t(B) * kKVHeads; }
 size_t part_o_bytes(int B, int sms) { return part_slots(B, sms) * kGroup * kD * sizeof(float); }
 size_t part_ml_bytes(int B, int sms) { return up256(part_slots(B, sms) * kGroup * sizeof(float2)); }
 size_t pairs_bytes(int B) { return up256(size_t(B) * kKVHeads * sizeof(int2)); }
@@ -528,6 +563,8 @@ extern "C" grok_status grok_kv8_decode(const grok_kv8_cache* cache, const grok_b
     return fail(GROK_ERR_INVALID_ARG, "grok_kv8_decode: workspace of %zu bytes is smaller than the %zu needed",
                 workspace_bytes, need);
   char* ws = static_cast<char*>(workspace);
+  const int wave = wave_of(sms);
+  const int second = (long long)B * kKVHeads * cache->max_blocks >= (long long)kDqLong * wave ? wave : 0;
   const DqParams p{*cache,
                    reinterpret_cast<const uint4*>(q_rot),
                    kv_len,
@@ -538,7 +575,8 @@ extern "C" grok_status grok_kv8_decode(const grok_kv8_cache* cache, const grok_b
                    reinterpret_cast<uint2*>(out),
                    weight_in,
                    weight_out,
-                   sms * kDqWarps,
+                   wave,
+                   second,
                    dev_status};
   const bool i8 = cache->kind == GROK_KV8_INT8;
   auto kernel = i8 ? (weight_out ? kv8_decode_kernel<GROK_KV8_INT8, true> : kv8_decode_kernel<GROK_KV8_INT8, false>)
@@ -552,7 +590,7 @@ extern "C" grok_status grok_kv8_decode(const grok_kv8_cache* cache, const grok_b
   }
   // Both kernels are launched as dependents of the one before them: each begins with a wait for all of it.
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(sms);
+  cfg.gridDim = dim3((p.wave + p.second) / kDqWarps);
   cfg.blockDim = dim3(kDqThreads);
   cfg.dynamicSmemBytes = kDqSmem;
   cfg.stream = static_cast<cudaStream_t>(stream);
@@ -566,7 +604,7 @@ extern "C" grok_status grok_kv8_decode(const grok_kv8_cache* cache, const grok_b
   if ((st = check_launch("kv8_decode")) != GROK_OK) return st;
   // Many pairs have few partials each: a CTA per pair, a warp per head. Few pairs have many (workers / pairs and
   // two more at most): a CTA per pair and head.
-  const bool few = B * kKVHeads * 8 < p.workers;
+  const bool few = B * kKVHeads * 8 < p.wave;
   cfg.gridDim = few ? dim3(B * kKVHeads, kGroup + (weight_out ? 1 : 0)) : dim3(B * kKVHeads);
   cfg.blockDim = dim3(few ? 256 : kGroup * 32);
   cfg.dynamicSmemBytes = 0;

@@ -379,6 +379,44 @@ def test_decode_pool_past_2_gb():
     del host
 
 
+@pytest.mark.parametrize("kind", KINDS)
+def test_decode_long_shares_in_two_waves(kind):
+    """Enough blocks (24 and more for every resident warp) for the second wave of small shares; three sequences and the
+    shortest against 64 bits."""
+    g = torch.Generator(DEV).manual_seed(50)
+    B, max_blocks = 80, 72
+    lens = torch.randint(4000, max_blocks * 64 + 1, (B,), generator=g, device=DEV)
+    lens[7], lens[40] = 1, 65
+    n = B * 8 * max_blocks
+    k, v = (torch.randint(0, 256, shape, generator=g, device=DEV, dtype=torch.uint8)
+            for shape in ((n, 2, 64, 64), (n, 128, 64)))
+    if kind == "e4m3":
+        k, v = (torch.where((x & 0x7f) == 0x7f, 0x11, x) for x in (k, v))  # no NaN
+    scale = torch.rand(n, generator=g, device=DEV) * (3 / 127 if kind == "int8" else 3 / 448) + 1e-3
+    table = torch.randperm(n, generator=g, device=DEV).to(torch.int32).view(B, 8, max_blocks)
+    rows_open = torch.zeros(B, 8, 64, 128, dtype=torch.bfloat16, device=DEV)
+    cache = G.Kv8Cache(k.view(DT[kind]), v.view(DT[kind]), scale, scale.flip(0).contiguous(), table, rows_open, rows_open)
+    q = (torch.randn(B, 48, 128, generator=g, device=DEV) * 3).bfloat16()
+    got, w, status = run_decode(cache, q, lens.tolist())
+    assert status == 0
+    out, exact = torch.zeros(B, 48, 128, dtype=torch.float64), torch.zeros(B, 8, max_blocks, dtype=torch.float64)
+    for b in (0, 7, 40, 79):
+        L = int(lens[b])
+        for h in range(8):
+            ids = table[b, h, :(L + 63) // 64].long()
+            K = cache.k_pool[ids].float().double().transpose(1, 2).flatten(2) * cache.k_scale[ids].double()[:, None, None]
+            V = cache.v_pool[ids].float().double().transpose(1, 2) * cache.v_scale[ids].double()[:, None, None]
+            K, V = K.reshape(-1, 128)[:L].cpu().numpy(), V.reshape(-1, 128)[:L].cpu().numpy()
+            o, p = kv8.attend(q[b, 6 * h:6 * h + 6].double().cpu().numpy(), K, V)
+            out[b, 6 * h:6 * h + 6] = torch.from_numpy(o)
+            exact[b, h] = torch.from_numpy(kv8.block_weights(p, max_blocks))
+    pick = [0, 7, 40, 79]
+    assert_close(_bits(got[pick]), bf16.from_f64(out[pick].numpy()), f"kv8 decode two waves {kind}")
+    assert torch.allclose(w[pick].double().cpu(), exact[pick], rtol=2e-3, atol=1e-7)
+    assert (w.sum(-1) - 6).abs().max() < 1e-3  # every head's weights add up to one, every block was read once
+    assert torch.equal(run_decode(cache, q, lens.tolist(), weights=False)[0], got)
+
+
 def test_workspace_too_small_is_refused():
     rng = np.random.default_rng(18)
     cache, _ = filled(rng, [10], "int8", 1, seed=13)
