@@ -552,8 +552,9 @@ __global__ void __launch_bounds__(kPfThreads, 1)
   // The fallback pass runs as a programmatic dependent of the fp16 pass: wait
   // for that grid's writes (the list, the outputs it replaces). A no-op otherwise.
   // (8-bit cache: the whole-item pass is a dependent of the kernel that makes the copies, and each pass of the one
-  // before it; the wait is below, after what reads nothing of theirs.)
-  if (!kQ8) asm volatile("griddepcontrol.wait;" ::: "memory");
+  // before it. Its producer waits before the first K tile, its softmax warps before the first scale; the set-up and
+  // the first Q tile need nothing of theirs.)
+  if (!kQ8 || kList) asm volatile("griddepcontrol.wait;" ::: "memory");
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sQ = smem;
   uint8_t* sK = smem + kQBytes;                           // K ring
@@ -609,7 +610,6 @@ __global__ void __launch_bounds__(kPfThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = bars->tmem_base;
-  if (kQ8) asm volatile("griddepcontrol.wait;" ::: "memory");
 
   if (warp == 0) {
     // ------------------------------------------------------------ TMA producer
@@ -626,6 +626,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
             tma_load_4d(sQ + (hs * 2 + half) * kBox, &tm_q, &bars->q_full, half * 64, h, it.qt * kPfRows, it.b);
         }
         ++q_it;
+        if (kQ8 && !kList && q_it == 1) asm volatile("griddepcontrol.wait;" ::: "memory");
         bool ok = true;
         for (int j = 0; j < it.n_kv; ++j, ++kv_it) {
           const int st = kv_it % kPfStages;
@@ -759,6 +760,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
     const int r = quad * 32 + lane;            // query row within the tile
     const uint32_t trow = tmem + (uint32_t(quad * 32) << 16) + slot * 256;
     int tile_cnt = 0, item_it = 0, sub_cnt = 0, xch_cnt = 0, split_cnt = 0;
+    if (kQ8 && !kList) asm volatile("griddepcontrol.wait;" ::: "memory");
     for (int rd = 0, item; (item = pf_item_index<kList>(p, rd)) >= 0; ++rd) {
       const PfItem it = pf_item<kF16, kSplit, kQ8>(p, bars, item);
       if (it.n_kv == 0) {
