@@ -451,7 +451,6 @@ __device__ __forceinline__ float pf_rowmax_half(uint32_t trow, int half, int rel
 // on which unit finishes last) and stages the output rows. Returns 1 when this
 // warp staged output rows, 0 when it has none to write, -1 when a bounded wait
 // gave up. Out of line: its registers stay out of the softmax loop's.
-template <int kMaxParts>
 static __device__ __noinline__ int pf_split_epilogue(const PfParams& p, PfBars* bars, volatile int* abort, int unit,
                                               int item, int parts, int slot, int half, int quad, int lane,
                                               uint32_t trow, float lt, float mref, float o_scale, bool over,
@@ -496,18 +495,18 @@ static __device__ __noinline__ int pf_split_epilogue(const PfParams& p, PfBars* 
   // Part k's weights are 2^(t - m_k) (m_k its reference); on the common
   // reference mx they are scaled by 2^(m_k - mx) <= 1.
   const size_t su0 = size_t(item) * p.n_parts * 2 + slot;  // part 0 of the item, this slot
-  float2 lm[kMaxParts];
+  float2 lm[kPfMaxParts];
   float mx = -INFINITY;
 #pragma unroll
-  for (int k = 0; k < kMaxParts; ++k)
+  for (int k = 0; k < kPfMaxParts; ++k)
     if (k < parts) {
       lm[k] = __ldcg(p.part_lm + (su0 + 2 * k) * kPfRows + r);
       mx = fmaxf(mx, lm[k].y);
     }
-  float fk[kMaxParts];
+  float fk[kPfMaxParts];
   float lsum = 0.f;
 #pragma unroll
-  for (int k = 0; k < kMaxParts; ++k)
+  for (int k = 0; k < kPfMaxParts; ++k)
     if (k < parts) {
       fk[k] = ex2_approx(lm[k].y - mx);
       lsum = fmaf(lm[k].x, fk[k], lsum);
@@ -519,7 +518,7 @@ static __device__ __noinline__ int pf_split_epilogue(const PfParams& p, PfBars* 
 #pragma unroll
     for (int e = 0; e < 8; ++e) acc[e] = 0.f;
 #pragma unroll
-    for (int k = 0; k < kMaxParts; ++k)
+    for (int k = 0; k < kPfMaxParts; ++k)
       if (k < parts) {
         const float4* pk4 = p.part_o + ((su0 + 2 * k) * 2 + half) * (16 * kPfRows) + r;
         const float4 v0 = __ldcg(pk4 + (2 * c) * kPfRows), v1 = __ldcg(pk4 + (2 * c + 1) * kPfRows);
@@ -893,9 +892,30 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         }
         tc_fence_before();
         mbar_arrive(&bars->o_empty[slot]);  // O is read: the next item's products may overwrite it
+      } else if (kQ8) {
+        // the unit's part; a kernel of its own adds the parts (prefill_join_kernel)
+        const size_t su = size_t(item) * 2 + slot;
+        float4* po = p.part_o + (su * 2 + half) * (16 * kPfRows) + r;
+#pragma unroll
+        for (int cc = 0; cc < 2; ++cc) {
+          uint32_t ov[32];
+          tmem_ld32(trow + 128 + half * 64 + cc * 32, ov);
+          tmem_wait_ld_dep(ov);
+#pragma unroll
+          for (int q = 0; q < 8; ++q)
+            po[(cc * 8 + q) * kPfRows] = make_float4(__uint_as_float(ov[4 * q]), __uint_as_float(ov[4 * q + 1]),
+                                                     __uint_as_float(ov[4 * q + 2]), __uint_as_float(ov[4 * q + 3]));
+        }
+        if (half == 0) p.part_lm[su * kPfRows + r] = make_float2(lt, mref);
+        tc_fence_before();
+        mbar_arrive(&bars->o_empty[slot]);
+        if (__any_sync(0xffffffffu, over) && half == 0 && lane == 0 &&
+            atomicExch(p.part_cnt + (it.item - p.item_base) * 2, 1) == 0)
+          pf_fallback(p, it.item);  // once per item
+        store = false;
       } else {
         const int res =
-            pf_split_epilogue<kQ8 ? kPfMaxPartsQ8 : kPfMaxParts>(p, bars, abort, item, it.item - p.item_base, it.parts, slot, half, quad, lane, trow, lt,
+            pf_split_epilogue(p, bars, abort, item, it.item - p.item_base, it.parts, slot, half, quad, lane, trow, lt,
                               mref, o_scale, __any_sync(0xffffffffu, over), stage,
                               uint32_t(split_cnt & 1));
         ++split_cnt;
@@ -1286,6 +1306,77 @@ extern "C" grok_status grok_attn_prefill_ws_paged(const grok_bf16* q_rot, const 
 
 // ----------------------------------------------------------------------------
 // The attention passes over copies of an 8-bit cache.
+
+// Adds the parts of the split items: CTA (item and slot, 32 query rows). A part is
+// read a row to a lane, 512 bytes at a time; the sum turns in shared memory and is
+// written a row at a time. (The item's last unit could add them, as it does over
+// the bf16 cache, but one SM reading eight parts of 131 KB holds the pass up: 128
+// tokens behind 8192 rows 65.9 us with that, 50.9 with this kernel.)
+static __global__ void __launch_bounds__(256) prefill_join_kernel(const PfParams p, uint4* __restrict__ out) {
+  __shared__ uint2 s_row[32][33];
+  __shared__ float s_f[kPfMaxPartsQ8][32];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // (every CTA: what follows this kernel relies on the pass before it)
+  const int local = blockIdx.x >> 1, slot = blockIdx.x & 1, r0 = blockIdx.y * 32;
+  const int item = p.item_base + local, hp = item % 3, g = item / 3 % kKVHeads, rest = item / 24;
+  const int b = rest % p.B, qt = p.n_qt - 1 - rest / p.B;
+  const int s = __ldg(p.start_pos + b), n = p.valid_len ? __ldg(p.valid_len + b) : p.T;
+  if (s < 0 || n < 1 || n > p.T || (long long)s + n > p.Tmax) return;  // (as in pf_item)
+  const int n_kv = (min(s + min(qt * kPfRows + kPfRows, p.T), s + n) + kPfKeys - 1) / kPfKeys;
+  const int parts = max(1, min(p.n_parts, n_kv / kPfMinPartTiles));
+  if (parts == 1 || qt * kPfRows + r0 >= p.T) return;  // a whole unit wrote its rows
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const size_t su0 = size_t(local) * p.n_parts * 2 + slot;
+  if (warp == 0) {  // each row's factors: 2^(reference - largest reference) / sum, times the head's V scale
+    float2 lm[kPfMaxPartsQ8];
+    float mx = -INFINITY, l = 0.f;
+#pragma unroll
+    for (int k = 0; k < kPfMaxPartsQ8; ++k)
+      if (k < parts) {
+        lm[k] = p.part_lm[(su0 + 2 * k) * kPfRows + r0 + lane];
+        mx = fmaxf(mx, lm[k].y);
+      }
+#pragma unroll
+    for (int k = 0; k < kPfMaxPartsQ8; ++k)
+      if (k < parts) {
+        lm[k].y = ex2_approx(lm[k].y - mx);
+        l = fmaf(lm[k].x, lm[k].y, l);
+      }
+    const float inv = __ldg(p.o_scale + b * kKVHeads + g) / l;
+#pragma unroll
+    for (int k = 0; k < kPfMaxPartsQ8; ++k)
+      if (k < parts) s_f[k][lane] = lm[k].y * inv;
+  }
+  __syncthreads();
+  // warp w: feature quads w, w + 8, .. of the row's 32 (16 in each half)
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    const int quad = warp + 8 * u;
+    const float4* po = p.part_o + ((su0 * 2 + (quad >> 4)) * 16 + (quad & 15)) * kPfRows + r0 + lane;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int k = 0; k < kPfMaxPartsQ8; ++k)
+      if (k < parts) {
+        const float4 v = po[size_t(k) * (2 * 2 * 16 * kPfRows)];
+        const float f = s_f[k][lane];
+        acc.x = fmaf(v.x, f, acc.x);
+        acc.y = fmaf(v.y, f, acc.y);
+        acc.z = fmaf(v.z, f, acc.z);
+        acc.w = fmaf(v.w, f, acc.w);
+      }
+    s_row[lane][quad] = make_uint2(pack_bf16x2(acc.x, acc.y), pack_bf16x2(acc.z, acc.w));
+  }
+  __syncthreads();
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    const int e = threadIdx.x + 256 * u, row = e >> 4, c = e & 15, i = qt * kPfRows + r0 + row;
+    if (i < p.T) {
+      const uint2 a = s_row[row][2 * c], d = s_row[row][2 * c + 1];
+      out[(((size_t)b * p.T + i) * kQHeads + g * kGroup + hp * 2 + slot) * 16 + c] = make_uint4(a.x, a.y, d.x, d.y);
+    }
+  }
+}
+
 template <typename Kernel>
 static grok_status q8_launch(Kernel kernel, int which, int grid, const CUtensorMap (&m)[4], const PfParams& p,
                              cudaStream_t stream) {
@@ -1364,5 +1455,18 @@ grok_status grok::prefill_q8_passes(const Q8Prefill& a, bool fallback, cudaStrea
   p.part_cnt = reinterpret_cast<int32_t*>(a.split_area);
   p.part_lm = reinterpret_cast<float2*>(a.split_area + split_cnt_bytes(a.sms));
   p.part_o = reinterpret_cast<float4*>(a.split_area + split_cnt_bytes(a.sms) + split_lm_bytes(a.sms));
-  return q8_launch(prefill_kernel<true, false, true, true>, 1, std::min(p.n_units, a.sms), m, p, stream);
+  if ((st = q8_launch(prefill_kernel<true, false, true, true>, 1, std::min(p.n_units, a.sms), m, p, stream)) != GROK_OK)
+    return st;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2 * n_split, kPfRows / 32);
+  cfg.blockDim = dim3(256);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cudaError_t e = cudaLaunchKernelEx(&cfg, prefill_join_kernel, p, reinterpret_cast<uint4*>(a.out));
+  if (e != cudaSuccess) return fail(cuda_status(e), "prefill join launch: %s", cudaGetErrorString(e));
+  return check_launch("prefill join");
 }
