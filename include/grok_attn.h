@@ -572,7 +572,8 @@ grok_status grok_kv_insert_slot(grok_bf16* cache_k, grok_bf16* cache_v, int B, i
  * codes 0; a block that holds a NaN or an infinity gets scale NaN and codes 0,
  * and attention over it gives NaN. The open block is always quantised as a
  * whole from its bf16 rows, so each element is rounded once and the cache does
- * not depend on the sizes of the appends that filled it.
+ * not depend on the sizes of the appends that filled it. No code of a row is a
+ * NaN; behind a sequence's last row the codes may be anything.
  *
  * A sequence's rows (cache_len, kv_len) and its positions (start_pos) are
  * separate: after an eviction a sequence has fewer rows than positions.

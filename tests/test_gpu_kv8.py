@@ -379,14 +379,9 @@ def test_decode_pool_past_2_gb():
     del host
 
 
-@pytest.mark.parametrize("kind", KINDS)
-def test_decode_long_shares_in_two_waves(kind):
-    """Enough blocks (24 and more for every resident warp) for the second wave of small shares; three sequences and the
-    shortest against 64 bits."""
-    g = torch.Generator(DEV).manual_seed(50)
-    B, max_blocks = 80, 72
-    lens = torch.randint(4000, max_blocks * 64 + 1, (B,), generator=g, device=DEV)
-    lens[7], lens[40] = 1, 65
+def random_cache(B, max_blocks, kind, seed):
+    """A cache of random codes and scales in random order (no rows behind it: for long caches)."""
+    g = torch.Generator(DEV).manual_seed(seed)
     n = B * 8 * max_blocks
     k, v = (torch.randint(0, 256, shape, generator=g, device=DEV, dtype=torch.uint8)
             for shape in ((n, 2, 64, 64), (n, 128, 64)))
@@ -395,26 +390,88 @@ def test_decode_long_shares_in_two_waves(kind):
     scale = torch.rand(n, generator=g, device=DEV) * (3 / 127 if kind == "int8" else 3 / 448) + 1e-3
     table = torch.randperm(n, generator=g, device=DEV).to(torch.int32).view(B, 8, max_blocks)
     rows_open = torch.zeros(B, 8, 64, 128, dtype=torch.bfloat16, device=DEV)
-    cache = G.Kv8Cache(k.view(DT[kind]), v.view(DT[kind]), scale, scale.flip(0).contiguous(), table, rows_open, rows_open)
-    q = (torch.randn(B, 48, 128, generator=g, device=DEV) * 3).bfloat16()
-    got, w, status = run_decode(cache, q, lens.tolist())
+    return G.Kv8Cache(k.view(DT[kind]), v.view(DT[kind]), scale, scale.flip(0).contiguous(), table, rows_open, rows_open)
+
+
+def cache_values(cache, b, h, L):
+    """Keys and values [L, 128] of one head in fp64."""
+    ids = cache.table[b, h, :(L + 63) // 64].long()
+    k = cache.k_pool.view(torch.uint8)[ids].view(cache.k_pool.dtype)
+    v = cache.v_pool.view(torch.uint8)[ids].view(cache.v_pool.dtype)
+    K = k.float().double().transpose(1, 2).flatten(2) * cache.k_scale[ids].double()[:, None, None]
+    V = v.float().double().transpose(1, 2) * cache.v_scale[ids].double()[:, None, None]
+    return K.reshape(-1, 128)[:L].cpu().numpy(), V.reshape(-1, 128)[:L].cpu().numpy()
+
+
+def check_random_cache_decode(cache, lens, pick, what):
+    q = (torch.randn(cache.B, 48, 128, generator=torch.Generator(DEV).manual_seed(9), device=DEV) * 3).bfloat16()
+    got, w, status = run_decode(cache, q, lens)
     assert status == 0
-    out, exact = torch.zeros(B, 48, 128, dtype=torch.float64), torch.zeros(B, 8, max_blocks, dtype=torch.float64)
-    for b in (0, 7, 40, 79):
-        L = int(lens[b])
+    want, exact = [], []
+    for b in pick:
         for h in range(8):
-            ids = table[b, h, :(L + 63) // 64].long()
-            K = cache.k_pool[ids].float().double().transpose(1, 2).flatten(2) * cache.k_scale[ids].double()[:, None, None]
-            V = cache.v_pool[ids].float().double().transpose(1, 2) * cache.v_scale[ids].double()[:, None, None]
-            K, V = K.reshape(-1, 128)[:L].cpu().numpy(), V.reshape(-1, 128)[:L].cpu().numpy()
-            o, p = kv8.attend(q[b, 6 * h:6 * h + 6].double().cpu().numpy(), K, V)
-            out[b, 6 * h:6 * h + 6] = torch.from_numpy(o)
-            exact[b, h] = torch.from_numpy(kv8.block_weights(p, max_blocks))
-    pick = [0, 7, 40, 79]
-    assert_close(_bits(got[pick]), bf16.from_f64(out[pick].numpy()), f"kv8 decode two waves {kind}")
-    assert torch.allclose(w[pick].double().cpu(), exact[pick], rtol=2e-3, atol=1e-7)
-    assert (w.sum(-1) - 6).abs().max() < 1e-3  # every head's weights add up to one, every block was read once
-    assert torch.equal(run_decode(cache, q, lens.tolist(), weights=False)[0], got)
+            o, p = kv8.attend(q[b, 6 * h:6 * h + 6].double().cpu().numpy(), *cache_values(cache, b, h, lens[b]))
+            want.append(o)
+            exact.append(kv8.block_weights(p, cache.max_blocks))
+    assert_close(_bits(got[pick]).reshape(-1, 6, 128), bf16.from_f64(np.stack(want)), what)
+    # sums of |q k| are about 40 here: logits off by at most 128 * 2^-23 * 40, weights by the functions' 3 * 87 * 2^-20, twice
+    assert np.allclose(w[pick].double().cpu().numpy().reshape(-1, cache.max_blocks), np.stack(exact), rtol=2e-3, atol=1e-7)
+    assert (w.sum(-1) - 6).abs().max() < 1e-3  # every head's weights add up to one: every block was read once
+    assert torch.equal(run_decode(cache, q, lens, weights=False)[0], got)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_decode_long_shares_in_two_waves(kind):
+    """Enough blocks (24 and more for every resident warp) for the second wave of small shares."""
+    lens = np.random.default_rng(50).integers(4000, 72 * 64 + 1, 80).tolist()
+    lens[7], lens[40] = 1, 65
+    check_random_cache_decode(random_cache(80, 72, kind, 50), lens, [0, 7, 40, 79], f"kv8 decode two waves {kind}")
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("rows_", [65536, 40001])
+def test_decode_longest_cache(kind, rows_):
+    """One sequence over the whole range: over a hundred partials for each head."""
+    check_random_cache_decode(random_cache(1, 1024, kind, 51), [rows_], [0], f"kv8 decode {rows_} rows {kind}")
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_prefill_behind_the_longest_cache(kind):
+    """Few tokens behind 65000 rows: items in eight parts, kernels over 510 key tiles."""
+    cache = random_cache(1, 1024, kind, 52)
+    T, start = 3, 65000
+    q = (torch.randn(1, T, 48, 128, generator=torch.Generator(DEV).manual_seed(10), device=DEV) * 3).bfloat16()
+    got, status = run_prefill(cache, q, [start], [T], T)
+    assert status == 0
+    want = []
+    for h in range(8):
+        K, V = cache_values(cache, 0, h, start + T)
+        for r in range(6):
+            want.append(kv8.attend(q[0, :, 6 * h + r].double().cpu().numpy(), K, V, start + np.arange(T))[0])
+    assert_close(_bits(got[0]), bf16.from_f64(np.stack(want, 1)), f"kv8 prefill behind 65000 rows {kind}")
+
+
+def test_calls_on_two_streams_at_once():
+    """Decode and prefill over one cache from two streams, each with its own workspace and outputs."""
+    cache = random_cache(4, 40, "int8", 53)
+    lens = [2500, 700, 64, 1]
+    gen = torch.Generator(DEV).manual_seed(11)
+    q = (torch.randn(4, 48, 128, generator=gen, device=DEV) * 3).bfloat16()
+    qp = (torch.randn(4, 130, 48, 128, generator=gen, device=DEV) * 3).bfloat16()
+    want_d = run_decode(cache, q, lens, weights=False)[0]
+    want_p = run_prefill(cache, qp, [2000, 500, 64, 1], None, 130)[0]
+    kv, cl = _ints(lens), _ints([2000, 500, 64, 1])
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    outs = [(torch.zeros_like(q), torch.zeros_like(qp), G.alloc_kv8_decode_workspace(cache),
+             G.alloc_kv8_prefill_workspace(cache)) for _ in streams]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for s, (d, p, wd, wp) in zip(streams, outs):
+            G.kv8_decode(cache, q, kv, wd, d, stream=s)
+            G.kv8_prefill(cache, qp, cl, None, p, wp, stream=s)
+    torch.cuda.synchronize()
+    for d, p, _, _ in outs:
+        assert torch.equal(d, want_d) and torch.equal(p, want_p)
 
 
 def test_workspace_too_small_is_refused():
@@ -761,3 +818,28 @@ def test_a_captured_step_on_another_stream():
         rows_now += 1
     for a in ("k_pool", "v_pool"):
         assert torch.equal(getattr(cache, a).view(torch.uint8), getattr(twin, a).view(torch.uint8))
+
+
+def test_readme_example_runs():
+    import os
+    import re
+    text = open(os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "README.md")).read()
+    scope = {}
+    for block in re.findall(r"```python\n(.*?)```", text, re.S):
+        exec(block, scope)  # noqa: S102
+    torch.cuda.synchronize()
+    assert int(scope["status"].item()) == 0
+    assert scope["left"].tolist() == [48 * 64 + 1] and torch.isfinite(scope["out1"].float()).all()
+
+
+def test_cache_tensors_are_fixed():
+    cache = G.alloc_kv8_cache(1, 2)
+    with pytest.raises(AttributeError, match="with_table"):
+        cache.table = cache.table.clone()
+    other = cache.table.flip(2).contiguous()
+    assert cache.with_table(other).table is other and cache.with_table(other).k_pool is cache.k_pool
+    with pytest.raises(ValueError, match="shape"):
+        cache.with_table(other[:, :4].contiguous())
+    with pytest.raises(ValueError, match="contiguous"):
+        G.Kv8Cache(cache.k_pool, cache.v_pool, cache.k_scale, cache.v_scale, cache.table, cache.open_k.transpose(2, 3)
+                   .contiguous().transpose(2, 3), cache.open_v)
