@@ -23,14 +23,19 @@ class _Cache(ctypes.Structure):
                 ("n_blocks", ctypes.c_int)]
 
 
+_BF16, _F32, _I32, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
+
+
 def _need(t, name: str, dtype: torch.dtype, shape: tuple, index: int) -> int:
     """The address of t, which must be a contiguous tensor of this type and shape on CUDA device `index`.
 
     One pass of cheap comparisons (a decode step's calls are short); _want says what is wrong otherwise.
     """
-    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == index \
-            and t.is_contiguous():
-        return t.data_ptr()
+    try:
+        if t.dtype is dtype and t.shape == shape and t.get_device() == index and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
     _want(t, name, dtype, shape)
     raise ValueError(f"{name} is on {t.device}, the cache's or the other tensors on cuda:{index}")
 
@@ -39,19 +44,24 @@ def _maybe(t, name: str, dtype: torch.dtype, shape: tuple, index: int) -> Option
     return None if t is None else _need(t, name, dtype, shape, index)
 
 
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+# The raw forms of torch.cuda.current_stream(i).cuda_stream and torch.cuda.current_device(), where torch has them.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda i: torch.cuda.current_stream(i).cuda_stream)
+_raw_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+_calls: dict = {}
 
 
 def _call(index: int, stream: Optional[torch.cuda.Stream], name: str, *args) -> None:
     """The library's call `name` on `stream` (None: the device's current one), with device `index` current."""
-    if stream is not None:
-        if stream.device.index != index:
-            raise ValueError(f"stream is on {stream.device}, the tensors on cuda:{index}")
+    fn = _calls.get(name)
+    if fn is None:
+        fn = _calls[name] = getattr(load(), name)
+    if stream is None:
+        s = _raw_stream(index)
+    elif stream.device.index == index:
         s = stream.cuda_stream
     else:
-        s = _raw_stream(index) if _raw_stream is not None else torch.cuda.current_stream(index).cuda_stream
-    fn = getattr(load(), name)
-    if torch.cuda.current_device() == index:
+        raise ValueError(f"stream is on {stream.device}, the tensors on cuda:{index}")
+    if _raw_device() == index:
         status = fn(*args, s)
     else:
         with torch.cuda.device(index):
@@ -128,12 +138,12 @@ def kv8_append(cache: Kv8Cache, q, k, v, start_pos, cache_len, valid_len, cos_ta
     B, T, n, at = cache.B, q.shape[1], cos_tab.shape[0], cache.index
     kv = (B, T, N_KV_HEADS, HEAD_DIM)
     heads = (B, T, N_Q_HEADS, HEAD_DIM)
-    _call(at, stream, "grok_kv8_append", cache._ref, _need(q, "q", torch.bfloat16, heads, at),
-          _need(k, "k", torch.bfloat16, kv, at), _need(v, "v", torch.bfloat16, kv, at),
-          _need(start_pos, "start_pos", torch.int32, (B,), at), _need(cache_len, "cache_len", torch.int32, (B,), at),
-          _maybe(valid_len, "valid_len", torch.int32, (B,), at), T,
-          _need(cos_tab, "cos_tab", torch.float32, (n, 64), at), _need(sin_tab, "sin_tab", torch.float32, (n, 64), at),
-          n, _need(q_rot, "q_rot", torch.bfloat16, heads, at), _maybe(dev_status, "dev_status", torch.int32, (1,), at))
+    _call(at, stream, "grok_kv8_append", cache._ref, _need(q, "q", _BF16, heads, at),
+          _need(k, "k", _BF16, kv, at), _need(v, "v", _BF16, kv, at),
+          _need(start_pos, "start_pos", _I32, (B,), at), _need(cache_len, "cache_len", _I32, (B,), at),
+          _maybe(valid_len, "valid_len", _I32, (B,), at), T,
+          _need(cos_tab, "cos_tab", _F32, (n, 64), at), _need(sin_tab, "sin_tab", _F32, (n, 64), at),
+          n, _need(q_rot, "q_rot", _BF16, heads, at), _maybe(dev_status, "dev_status", _I32, (1,), at))
 
 
 def kv8_decode_workspace(B: int, max_blocks: int, weights: bool = True) -> int:
@@ -158,12 +168,12 @@ def kv8_decode(cache: Kv8Cache, q_rot, kv_len, workspace, out, weight_in=None, w
     B, at = cache.B, cache.index
     heads, blocks = (B, N_Q_HEADS, HEAD_DIM), (B, N_KV_HEADS, cache.max_blocks)
     nbytes = workspace.numel()
-    _call(at, stream, "grok_kv8_decode", cache._ref, _need(q_rot, "q_rot", torch.bfloat16, heads, at),
-          _need(kv_len, "kv_len", torch.int32, (B,), at), _need(workspace, "workspace", torch.uint8, (nbytes,), at),
-          nbytes, _need(out, "out", torch.bfloat16, heads, at),
-          _maybe(weight_in, "weight_in", torch.float32, blocks, at),
-          _maybe(weight_out, "weight_out", torch.float32, blocks, at),
-          _maybe(dev_status, "dev_status", torch.int32, (1,), at))
+    _call(at, stream, "grok_kv8_decode", cache._ref, _need(q_rot, "q_rot", _BF16, heads, at),
+          _need(kv_len, "kv_len", _I32, (B,), at), _need(workspace, "workspace", _U8, (nbytes,), at),
+          nbytes, _need(out, "out", _BF16, heads, at),
+          _maybe(weight_in, "weight_in", _F32, blocks, at),
+          _maybe(weight_out, "weight_out", _F32, blocks, at),
+          _maybe(dev_status, "dev_status", _I32, (1,), at))
 
 
 def kv8_prefill_workspace(B: int, max_blocks: int) -> int:
@@ -185,10 +195,10 @@ def kv8_prefill(cache: Kv8Cache, q_rot, cache_len, valid_len, out, workspace, de
     """
     B, T, at = cache.B, q_rot.shape[1], cache.index
     heads, nbytes = (B, T, N_Q_HEADS, HEAD_DIM), workspace.numel()
-    _call(at, stream, "grok_kv8_prefill", cache._ref, _need(q_rot, "q_rot", torch.bfloat16, heads, at),
-          _need(cache_len, "cache_len", torch.int32, (B,), at), _maybe(valid_len, "valid_len", torch.int32, (B,), at), T,
-          _need(out, "out", torch.bfloat16, heads, at), _need(workspace, "workspace", torch.uint8, (nbytes,), at), nbytes,
-          _maybe(dev_status, "dev_status", torch.int32, (1,), at))
+    _call(at, stream, "grok_kv8_prefill", cache._ref, _need(q_rot, "q_rot", _BF16, heads, at),
+          _need(cache_len, "cache_len", _I32, (B,), at), _maybe(valid_len, "valid_len", _I32, (B,), at), T,
+          _need(out, "out", _BF16, heads, at), _need(workspace, "workspace", _U8, (nbytes,), at), nbytes,
+          _maybe(dev_status, "dev_status", _I32, (1,), at))
 
 
 def kv8_evict(table, weight, kv_len, keep: int, sink: int, recent: int, table_out, weight_out, kv_len_out,
@@ -203,9 +213,9 @@ def kv8_evict(table, weight, kv_len, keep: int, sink: int, recent: int, table_ou
     row, at = (B, N_KV_HEADS, n), table.get_device()
     if at < 0:
         raise ValueError("table must be a CUDA tensor")
-    _call(at, stream, "grok_kv8_evict", _need(table, "table", torch.int32, row, at),
-          _need(weight, "weight", torch.float32, row, at), _need(kv_len, "kv_len", torch.int32, (B,), at), B, n,
-          int(keep), int(sink), int(recent), _need(table_out, "table_out", torch.int32, row, at),
-          _need(weight_out, "weight_out", torch.float32, row, at),
-          _need(kv_len_out, "kv_len_out", torch.int32, (B,), at),
-          _maybe(dev_status, "dev_status", torch.int32, (1,), at))
+    _call(at, stream, "grok_kv8_evict", _need(table, "table", _I32, row, at),
+          _need(weight, "weight", _F32, row, at), _need(kv_len, "kv_len", _I32, (B,), at), B, n,
+          int(keep), int(sink), int(recent), _need(table_out, "table_out", _I32, row, at),
+          _need(weight_out, "weight_out", _F32, row, at),
+          _need(kv_len_out, "kv_len_out", _I32, (B,), at),
+          _maybe(dev_status, "dev_status", _I32, (1,), at))
