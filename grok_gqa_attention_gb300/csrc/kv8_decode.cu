@@ -13,7 +13,8 @@
 // private K and a private V buffer in shared memory (one bulk copy each, of 8 KB),
 // and writes one partial result (m, l, O) per pair that it touches; a second
 // kernel, launched as a dependent, joins a pair's partials. Which blocks make a
-// partial follows from the lengths alone, so the bits do too.
+// partial follows from the lengths alone, so the bits do too. Calls of a few tokens
+// run here as well, every token a query with a length of its own (few_tokens).
 //
 // Measured (graph replays, one GB300): 32 sequences of up to 8192 rows (274 MB of
 // codes) 52.1 us, 5.26 TB/s, 0.78 of the copy rate; 16 of up to 65536 (1.14 GB) 179 us,
@@ -32,8 +33,10 @@
 // block, so a thread reads operands as 16-byte words and the order of the
 // contracted index is chosen to fit them: thread t of a row's four holds
 // features (keys) 16 t .. 16 t + 15.
-// P is rounded once to fp16 (2^-12 relative) against a running reference that may
+// P is rounded once to fp16 (2^-11 relative) against a running reference that may
 // lag the maximum by 2^8; l, the weights and O stay in fp32.
+#include <algorithm>
+
 #include "host.cuh"
 #include "kv8.cuh"
 
@@ -52,7 +55,10 @@ constexpr float kDqLag = 8.f;  // log2 units a weight may exceed the reference b
 struct DqParams {
   grok_kv8_cache c;
   const uint4* q;
-  const int32_t* kv_len;
+  const int32_t* kv_len;     // rows that a query sees; with few_tokens, rows before the call's tokens
+  const int32_t* valid_len;  // few_tokens: valid tokens of a sequence, or null (all)
+  int few_tokens;  // 0: one query per sequence. T: T tokens per sequence, each a query of its own
+  int n_seq;       // queries: B, or B * T
   float* part_o;    // [slot][6][128]
   float2* part_ml;  // [slot][6]: reference (log2), sum
   int2* pair_parts; // [B * 8]: a pair's first slot and number of slots
@@ -89,11 +95,31 @@ struct Deal {
 
 __device__ __forceinline__ uint32_t word_of(const uint4& x, int w) { return w == 0 ? x.x : w == 1 ? x.y : w == 2 ? x.z : x.w; }
 
-// The sequences' blocks: total over the batch of ceil(kv_len / 64), by one warp.
+// Rows that query v sees: 0 when its sequence's integers are bad. With few_tokens
+// token i of a sequence sees those before the call and the valid ones up to itself.
+__device__ __forceinline__ int rows_of(const DqParams& p, int v) {
+  if (!p.few_tokens) return __ldg(p.kv_len + v);
+  const int b = v / p.few_tokens, i = v % p.few_tokens;
+  const int s = __ldg(p.kv_len + b), n = p.valid_len ? __ldg(p.valid_len + b) : p.few_tokens;
+  if (s < 0 || n < 1 || n > p.few_tokens || (long long)s + n > (long long)p.c.max_blocks * kKv8Block) return 0;
+  return s + min(i + 1, n);
+}
+__device__ __forceinline__ int blocks_of(const DqParams& p, int v) { return kv8_blocks(rows_of(p, v), p.c.max_blocks); }
+
+// Bits for a query whose sequence's integers are bad (as the many-token kernel reports them).
+__device__ __forceinline__ int bad_bits(const DqParams& p, int v) {
+  if (!p.few_tokens) return GROK_DEV_BAD_KV_LEN;
+  const int b = v / p.few_tokens;
+  const int s = __ldg(p.kv_len + b), n = p.valid_len ? __ldg(p.valid_len + b) : p.few_tokens;
+  return (n < 1 || n > p.few_tokens ? GROK_DEV_BAD_VALID : 0) |
+         (s < 0 || (long long)s + max(n, 0) > (long long)p.c.max_blocks * kKv8Block ? GROK_DEV_BAD_KV_LEN : 0);
+}
+
+// The queries' blocks: total over the batch of ceil(rows / 64), by one warp.
 __device__ __forceinline__ int count_blocks(const DqParams& p, int lane) {
   int total = 0;
-  for (int c = 0; c < p.c.B; c += 32)
-    total += __reduce_add_sync(0xffffffffu, c + lane < p.c.B ? kv8_blocks(__ldg(p.kv_len + c + lane), p.c.max_blocks) : 0);
+  for (int c = 0; c < p.n_seq; c += 32)
+    total += __reduce_add_sync(0xffffffffu, c + lane < p.n_seq ? blocks_of(p, c + lane) : 0);
   return total;
 }
 
@@ -119,8 +145,8 @@ __global__ void __launch_bounds__(kDqThreads, kDqCtas) kv8_decode_kernel(const D
   const int n_first = p.wave / kDqWarps, cta = blockIdx.x;
   const int item = cta < n_first ? warp * n_first + cta : cta * kDqWarps + warp;  // (few blocks: over the SMs first)
   if (item == 0)
-    for (int b = lane; b < p.c.B; b += 32)
-      if (kv8_blocks(__ldg(p.kv_len + b), p.c.max_blocks) == 0) report(p.status, GROK_DEV_BAD_KV_LEN);
+    for (int v = lane; v < p.n_seq; v += 32)
+      if (blocks_of(p, v) == 0) report(p.status, bad_bits(p, v));
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   // (item * small passes n_total by less than a wave of shares: no overflow below 2^31)
   const int lo = min(deal.start(item), n_total), hi = min(deal.start(item + 1), n_total);
@@ -167,8 +193,8 @@ __global__ void __launch_bounds__(kDqThreads, kDqCtas) kv8_decode_kernel(const D
       const int idx = base + lane;
       bool found = lane >= cnt;
       int cum = 0;
-      for (int c = 0; c < p.c.B; c += 32) {
-        const int len = c + lane < p.c.B ? __ldg(p.kv_len + c + lane) : 0;
+      for (int c = 0; c < p.n_seq; c += 32) {
+        const int len = c + lane < p.n_seq ? rows_of(p, c + lane) : 0;
         const int n = kv8_blocks(len, p.c.max_blocks);
         int incl = n;
 #pragma unroll
@@ -200,7 +226,9 @@ __global__ void __launch_bounds__(kDqThreads, kDqCtas) kv8_decode_kernel(const D
     int my_id = 0;
     float my_ks = 0.f, my_vs = 0.f;
     if (lane < cnt) {
-      my_id = max(0, kv8_block_id(p.c.table, (size_t)my_pair * p.c.max_blocks + my_blk, p.c.n_blocks, p.status));
+      size_t row_of = my_pair;  // of the table
+      if (p.few_tokens) row_of = (size_t)(my_pair / kKVHeads / p.few_tokens) * kKVHeads + my_pair % kKVHeads;
+      my_id = max(0, kv8_block_id(p.c.table, row_of * p.c.max_blocks + my_blk, p.c.n_blocks, p.status));
       my_ks = __ldg(p.c.k_scale + my_id);
       my_vs = __ldg(p.c.v_scale + my_id);
     }
@@ -409,7 +437,7 @@ __global__ void __launch_bounds__(kHeads * kSplit * 32) kv8_join_kernel(const Dq
   __shared__ float4 s_o[kHeads * kSplit][32];
   __shared__ float s_inv[8];
   const int pair = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int blocks = kv8_blocks(__ldg(p.kv_len + pair / kKVHeads), p.c.max_blocks);
+  const int blocks = blocks_of(p, pair / kKVHeads);
   const bool weights = p.weight_out && (kHeads > 1 || blockIdx.y == kGroup);
   // The first blocks' old weights do not depend on the first kernel.
   const size_t at0 = (size_t)pair * p.c.max_blocks + threadIdx.x;
@@ -531,54 +559,39 @@ size_t block_w_bytes(int B, int max_blocks) { return size_t(B) * kKVHeads * max_
 
 }  // namespace
 
-extern "C" grok_status grok_kv8_decode_workspace(int B, int max_blocks, int weights, size_t* bytes) {
-  if (!bytes) return fail(GROK_ERR_INVALID_ARG, "grok_kv8_decode_workspace: null pointer");
-  if (B < 1 || B > 65535 || max_blocks < 1 || max_blocks > kKv8MaxBlocks)
-    return fail(GROK_ERR_INVALID_ARG, "grok_kv8_decode_workspace: need 1 <= B <= 65535, 1 <= max_blocks <= %d",
-                kKv8MaxBlocks);
-  int sms = 0;
-  grok_status st = device_sm_count(&sms);
-  if (st != GROK_OK) return st;
-  *bytes = part_o_bytes(B, sms) + part_ml_bytes(B, sms) + pairs_bytes(B) + (weights ? block_w_bytes(B, max_blocks) : 0);
-  return GROK_OK;
+size_t grok::kv8_decode_bytes(int n_seq, int max_blocks, bool weights, int sms) {
+  return part_o_bytes(n_seq, sms) + part_ml_bytes(n_seq, sms) + pairs_bytes(n_seq) +
+         (weights ? block_w_bytes(n_seq, max_blocks) : 0);
 }
 
-extern "C" grok_status grok_kv8_decode(const grok_kv8_cache* cache, const grok_bf16* q_rot, const int32_t* kv_len,
-                                       void* workspace, size_t workspace_bytes, grok_bf16* out,
-                                       const float* weight_in, float* weight_out, int32_t* dev_status, void* stream) {
-  grok_status st = kv8_check(cache, "grok_kv8_decode");
+grok_status grok::kv8_decode_run(const grok_kv8_cache& cache, const grok_bf16* q_rot, const int32_t* len,
+                                 const int32_t* valid_len, int few_tokens, char* ws, grok_bf16* out,
+                                 const float* weight_in, float* weight_out, int sms, int32_t* dev_status,
+                                 cudaStream_t stream) {
+  int dev = 0;
+  grok_status st = device_index(&dev);
   if (st != GROK_OK) return st;
-  if (!q_rot || !kv_len || !workspace || !out) return fail(GROK_ERR_INVALID_ARG, "grok_kv8_decode: null pointer");
-  if (weight_in && !weight_out) return fail(GROK_ERR_INVALID_ARG, "grok_kv8_decode: weight_in without weight_out");
-  if (!aligned16(q_rot) || !aligned16(out))
-    return fail(GROK_ERR_INVALID_ARG, "grok_kv8_decode: bf16 tensors must be 16-byte aligned");
-  if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
-    return fail(GROK_ERR_INVALID_ARG, "grok_kv8_decode: workspace must be 256-byte aligned");
-  int sms = 0, dev = 0;
-  if ((st = device_sm_count(&sms)) != GROK_OK || (st = device_index(&dev)) != GROK_OK) return st;
-  const int B = cache->B;
-  const size_t o_bytes = part_o_bytes(B, sms), ml_bytes = part_ml_bytes(B, sms);
-  const size_t need = o_bytes + ml_bytes + pairs_bytes(B) + (weight_out ? block_w_bytes(B, cache->max_blocks) : 0);
-  if (workspace_bytes < need)
-    return fail(GROK_ERR_INVALID_ARG, "grok_kv8_decode: workspace of %zu bytes is smaller than the %zu needed",
-                workspace_bytes, need);
-  char* ws = static_cast<char*>(workspace);
+  const int n_seq = cache.B * std::max(1, few_tokens);
+  const size_t o_bytes = part_o_bytes(n_seq, sms), ml_bytes = part_ml_bytes(n_seq, sms);
   const int wave = wave_of(sms);
-  const int second = (long long)B * kKVHeads * cache->max_blocks >= (long long)kDqLong * wave ? wave : 0;
-  const DqParams p{*cache,
+  const int second = (long long)n_seq * kKVHeads * cache.max_blocks >= (long long)kDqLong * wave ? wave : 0;
+  const DqParams p{cache,
                    reinterpret_cast<const uint4*>(q_rot),
-                   kv_len,
+                   len,
+                   valid_len,
+                   few_tokens,
+                   n_seq,
                    reinterpret_cast<float*>(ws),
                    reinterpret_cast<float2*>(ws + o_bytes),
                    reinterpret_cast<int2*>(ws + o_bytes + ml_bytes),
-                   weight_out ? reinterpret_cast<float*>(ws + o_bytes + ml_bytes + pairs_bytes(B)) : nullptr,
+                   weight_out ? reinterpret_cast<float*>(ws + o_bytes + ml_bytes + pairs_bytes(n_seq)) : nullptr,
                    reinterpret_cast<uint2*>(out),
                    weight_in,
                    weight_out,
                    wave,
                    second,
                    dev_status};
-  const bool i8 = cache->kind == GROK_KV8_INT8;
+  const bool i8 = cache.kind == GROK_KV8_INT8;
   auto kernel = i8 ? (weight_out ? kv8_decode_kernel<GROK_KV8_INT8, true> : kv8_decode_kernel<GROK_KV8_INT8, false>)
                    : (weight_out ? kv8_decode_kernel<GROK_KV8_E4M3, true> : kv8_decode_kernel<GROK_KV8_E4M3, false>);
   static bool attr_set[kMaxDevices][4] = {};  // per device and kernel; idempotent: every thread would set the same value
@@ -593,7 +606,7 @@ extern "C" grok_status grok_kv8_decode(const grok_kv8_cache* cache, const grok_b
   cfg.gridDim = dim3((p.wave + p.second) / kDqWarps);
   cfg.blockDim = dim3(kDqThreads);
   cfg.dynamicSmemBytes = kDqSmem;
-  cfg.stream = static_cast<cudaStream_t>(stream);
+  cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -604,11 +617,45 @@ extern "C" grok_status grok_kv8_decode(const grok_kv8_cache* cache, const grok_b
   if ((st = check_launch("kv8_decode")) != GROK_OK) return st;
   // Many pairs have few partials each: a CTA per pair, a warp per head. Few pairs have many (workers / pairs and
   // two more at most): a CTA per pair and head.
-  const bool few = B * kKVHeads * 8 < p.wave;
-  cfg.gridDim = few ? dim3(B * kKVHeads, kGroup + (weight_out ? 1 : 0)) : dim3(B * kKVHeads);
+  const int pairs = n_seq * kKVHeads;
+  const bool few = pairs * 8 < p.wave;
+  cfg.gridDim = few ? dim3(pairs, kGroup + (weight_out ? 1 : 0)) : dim3(pairs);
   cfg.blockDim = dim3(few ? 256 : kGroup * 32);
   cfg.dynamicSmemBytes = 0;
   e = cudaLaunchKernelEx(&cfg, few ? kv8_join_kernel<1, 8> : kv8_join_kernel<kGroup, 1>, p);
   if (e != cudaSuccess) return fail(cuda_status(e), "kv8_join launch: %s", cudaGetErrorString(e));
   return check_launch("kv8_join");
+}
+
+extern "C" grok_status grok_kv8_decode_workspace(int B, int max_blocks, int weights, size_t* bytes) {
+  if (!bytes) return fail(GROK_ERR_INVALID_ARG, "grok_kv8_decode_workspace: null pointer");
+  if (B < 1 || B > 65535 || max_blocks < 1 || max_blocks > kKv8MaxBlocks)
+    return fail(GROK_ERR_INVALID_ARG, "grok_kv8_decode_workspace: need 1 <= B <= 65535, 1 <= max_blocks <= %d",
+                kKv8MaxBlocks);
+  int sms = 0;
+  grok_status st = device_sm_count(&sms);
+  if (st != GROK_OK) return st;
+  *bytes = kv8_decode_bytes(B, max_blocks, weights != 0, sms);
+  return GROK_OK;
+}
+
+extern "C" grok_status grok_kv8_decode(const grok_kv8_cache* cache, const grok_bf16* q_rot, const int32_t* kv_len,
+                                       void* workspace, size_t workspace_bytes, grok_bf16* out,
+                                       const float* weight_in, float* weight_out, int32_t* dev_status, void* stream) {
+  grok_status st = kv8_check(cache, "grok_kv8_decode");
+  if (st != GROK_OK) return st;
+  if (!q_rot || !kv_len || !workspace || !out) return fail(GROK_ERR_INVALID_ARG, "grok_kv8_decode: null pointer");
+  if (weight_in && !weight_out) return fail(GROK_ERR_INVALID_ARG, "grok_kv8_decode: weight_in without weight_out");
+  if (!aligned16(q_rot) || !aligned16(out))
+    return fail(GROK_ERR_INVALID_ARG, "grok_kv8_decode: bf16 tensors must be 16-byte aligned");
+  if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
+    return fail(GROK_ERR_INVALID_ARG, "grok_kv8_decode: workspace must be 256-byte aligned");
+  int sms = 0;
+  if ((st = device_sm_count(&sms)) != GROK_OK) return st;
+  const size_t need = kv8_decode_bytes(cache->B, cache->max_blocks, weight_out != nullptr, sms);
+  if (workspace_bytes < need)
+    return fail(GROK_ERR_INVALID_ARG, "grok_kv8_decode: workspace of %zu bytes is smaller than the %zu needed",
+                workspace_bytes, need);
+  return kv8_decode_run(*cache, q_rot, kv_len, nullptr, 0, static_cast<char*>(workspace), out, weight_in, weight_out, sms,
+                        dev_status, static_cast<cudaStream_t>(stream));
 }

@@ -5,10 +5,13 @@
 // as bf16 (exact) and V as fp16, rows of a sequence and head in order. The
 // attention kernel (prefill.cu, kQ8) multiplies the logits of each 64-key
 // step by the block's K scale and the outputs by the head's V scale: a V value is
-// rounded once to fp16 on the scale vs / max vs of its block, 2^-12 relative.
+// rounded once to fp16 on the scale vs / max vs of its block, 2^-11 relative.
 //
 // Tensor-bound for all but short calls: the copies cost 1 byte read, 2 written
-// and 2 read per code against 24 products of it for every 128 new tokens.
+// and 2 read per code. Measured (graph replays, one GB300): 8192 tokens in an empty
+// cache 678 us, 1217 TFLOP/s, 0.63 of the library GEMM's rate, of which the copies
+// are 12 us; 4 x 256 tokens behind 6144 rows 180 us, 26 of them the copies (52 MB of
+// codes read, 105 MB written, 6 TB/s); 128 tokens behind 8192 rows 51 us.
 #include "host.cuh"
 #include "kv8.cuh"
 #include "prefill.cuh"
@@ -162,6 +165,14 @@ namespace {
 
 size_t up256(size_t n) { return (n + 255) & ~size_t(255); }
 
+// Up to here every token runs as a query of its own over the codes (kv8_decode.cu): no copies of the cache, its codes
+// read (mostly from L2) once per token, and the split over the key range that single tokens have. Above, the copies
+// cost less than the tokens' reads. Measured, us, own queries against copies: 1 sequence behind 16000 rows 13 against
+// 79 for 1 token, 39 against 79 for 8, 53 against 78 for 12, 71 against 79 for 16; 8 behind 8000 137 against 257 for 8,
+// 256 against 257 for 16; 32 behind 4000 276 against 519 for 8, 534 against 520 for 16; 256 behind 1000 763 against
+// 1019 for 8, 1269 against 1020 for 12.
+constexpr int kFewTokens = 8;
+
 // Workspace: fallback count and list, K scales, output factors, the copies of K and V, the split's area.
 struct Layout {
   int rows;
@@ -178,6 +189,7 @@ Layout layout(int B, int max_blocks, int sms) {
   w.v_copy = w.k_copy + copy;
   w.split = w.v_copy + copy;
   w.bytes = w.split + (split_allowed(w.rows) ? split_area_bytes(sms) : 0);
+  w.bytes = std::max(w.bytes, kv8_decode_bytes(B * kFewTokens, max_blocks, false, sms));
   return w;
 }
 
@@ -222,6 +234,9 @@ extern "C" grok_status grok_kv8_prefill(const grok_kv8_cache* cache, const grok_
   if (workspace_bytes < w.bytes)
     return fail(GROK_ERR_INVALID_ARG, "grok_kv8_prefill: workspace of %zu bytes is smaller than the %zu needed",
                 workspace_bytes, w.bytes);
+  if (T <= kFewTokens)
+    return kv8_decode_run(*cache, q_rot, cache_len, valid_len, T, static_cast<char*>(workspace), out, nullptr, nullptr, sms,
+                          dev_status, static_cast<cudaStream_t>(stream));
   char* ws = static_cast<char*>(workspace);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const int n_items = prefill_items(B, T);

@@ -648,8 +648,9 @@ grok_status grok_kv8_decode(const grok_kv8_cache* cache, const grok_bf16* q_rot,
  * valid_len[b] outside [1, T] sets GROK_DEV_BAD_VALID, cache_len[b] < 0 or
  * cache_len[b] + valid_len[b] > max_blocks * 64 GROK_DEV_BAD_KV_LEN; the sequence's
  * outputs are left as they were.
- * The rows are first copied to the workspace, K codes as bf16 (exact), V as fp16
- * on a common scale per sequence and head (2^-12 relative for values down to
+ * T <= 8: each token is computed as grok_kv8_decode computes it, from the codes.
+ * More: the rows are first copied to the workspace, K codes as bf16 (exact), V as fp16
+ * on a common scale per sequence and head (2^-11 relative for values down to
  * 2^-28 of the head's largest); softmax weights are rounded to fp16 as in
  * grok_attn_prefill_ws. Items whose weights leave fp16's range are recomputed with
  * bf16 hi + lo weights and V rounded to bf16.

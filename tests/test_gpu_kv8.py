@@ -534,6 +534,11 @@ PREFILLS = {
     "split_few": ([2500], [1], 1),
     "split_unequal": ([2000, 64, 900], [300, 500, 7], 500),
     "split_causal": ([700], [1400], 1400),
+    # the longest call that runs as single tokens, and the shortest that does not
+    "last_few": ([2500, 63, 120], [8, 4, 7], 8),
+    "first_many": ([2500, 63, 120], [9, 4, 7], 9),
+    "few_over_many_shares": ([9000, 60, 0, 7000], [5, 7, 1, 2], 7),
+    "few_over_many_sequences": (list(range(0, 320, 5)), [1 + i % 3 for i in range(64)], 3),
 }
 
 
@@ -563,6 +568,39 @@ def test_prefill_of_one_token_is_the_decode():
     a, _ = run_prefill(cache, q, [299, 64], [1, 1], 1)
     b, _, _ = run_decode(cache, q[:, 0].contiguous(), [300, 65])
     assert_close(_bits(a[:, 0]), _bits(b), "kv8 prefill against decode")
+
+
+def test_prefill_of_few_tokens_is_that_of_many():
+    """The same valid tokens in calls of 8 and of 9 tokens, which take different kernels."""
+    rng = np.random.default_rng(48)
+    cache, host = filled(rng, [700, 64, 12, 300], "e4m3", 11, seed=38)
+    q = _bf16(rng.standard_normal((4, 9, 48, 128)) * 3).to(DEV)
+    lens, valid = [692, 60, 4, 293], [8, 4, 8, 7]
+    a, sa = run_prefill(cache, q[:, :8].contiguous(), lens, valid, 8)
+    b, sb = run_prefill(cache, q, lens, valid, 9)
+    assert sa == sb == 0
+    assert_close(_bits(a), _bits(b[:, :8]), "kv8 prefill of 8 tokens against 9")
+
+
+def test_prefill_of_few_tokens_bad_integers():
+    rng = np.random.default_rng(49)
+    cache, host = filled(rng, [128] * 3, "int8", 2, seed=39)
+    q = _bf16(rng.standard_normal((3, 5, 48, 128))).to(DEV)
+    good, _ = run_prefill(cache, q, [100] * 3, [5] * 3, 5)
+    for start, n, bit in ((-1, 5, G.DEV_BAD_KV_LEN), (124, 5, G.DEV_BAD_KV_LEN), (2 ** 31 - 1, 5, G.DEV_BAD_KV_LEN),
+                          (100, 0, G.DEV_BAD_VALID), (100, -7, G.DEV_BAD_VALID), (100, 6, G.DEV_BAD_VALID),
+                          (125, 6, G.DEV_BAD_VALID | G.DEV_BAD_KV_LEN),
+                          (-1, 2 ** 31 - 1, G.DEV_BAD_VALID | G.DEV_BAD_KV_LEN)):
+        got, status = run_prefill(cache, q, [100, start, 100], [5, n, 5], 5)
+        assert status == bit
+        assert (got[1] == 7.0).all() and torch.equal(got[[0, 2]], good[[0, 2]])
+    got, status = run_prefill(cache, q, [110] * 3, [5, 1, 3], 5)
+    assert status == 0
+    got, status = run_prefill(cache, q, [-1] * 3, [5] * 3, 5)
+    assert status == G.DEV_BAD_KV_LEN and (got == 7.0).all()
+    cache.table[1, 7, 1] = cache.n_blocks
+    got, status = run_prefill(cache, q, [100] * 3, [5] * 3, 5)
+    assert status == G.DEV_BAD_PAGE and torch.equal(got[[0, 2]], good[[0, 2]])
 
 
 @pytest.mark.parametrize("kind", KINDS)
