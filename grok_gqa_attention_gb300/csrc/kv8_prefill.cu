@@ -223,6 +223,7 @@ extern "C" grok_status grok_kv8_prefill(const grok_kv8_cache* cache, const grok_
     return fail(GROK_ERR_INVALID_ARG, "grok_kv8_prefill: bf16 tensors must be 16-byte aligned");
   if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
     return fail(GROK_ERR_INVALID_ARG, "grok_kv8_prefill: workspace must be 256-byte aligned");
+  if (q_rot == out) return fail(GROK_ERR_INVALID_ARG, "grok_kv8_prefill: out may not alias q_rot");
   const int B = cache->B, max_blocks = cache->max_blocks;
   if ((st = sizes_ok(B, max_blocks, "grok_kv8_prefill")) != GROK_OK) return st;
   if (T < 1 || T > max_blocks * kKv8Block)

@@ -643,7 +643,8 @@ grok_status grok_kv8_decode(const grok_kv8_cache* cache, const grok_bf16* q_rot,
  * grok_attn_prefill_ws over the 8-bit cache. Token i of sequence b attends rows
  * j <= cache_len[b] + i, j < cache_len[b] + valid_len[b]; padding tokens (i >=
  * valid_len[b]) are computed too.
- *   q_rot, out [B,T,48,128]; cache_len [B] int32: rows before these tokens;
+ *   q_rot, out [B,T,48,128] (out may not alias q_rot: items computed again read
+ *   their queries again); cache_len [B] int32: rows before these tokens;
  *   valid_len [B] int32 or NULL (= T); 1 <= T <= max_blocks * 64.
  * valid_len[b] outside [1, T] sets GROK_DEV_BAD_VALID, cache_len[b] < 0 or
  * cache_len[b] + valid_len[b] > max_blocks * 64 GROK_DEV_BAD_KV_LEN; the sequence's
@@ -673,7 +674,9 @@ grok_status grok_kv8_prefill(const grok_kv8_cache* cache, const grok_bf16* q_rot
  * order, the entry of the open block (index nc), the evicted ones in their
  * order, then the rest as it was; weights likewise, 0 for the evicted. No code
  * moves: the rows that follow are written into the evicted blocks, and an
- * owner of a shared pool finds their numbers behind the last block in use.
+ * owner of a shared pool finds their numbers behind the last block in use (where
+ * an evicted block is another sequence's too, the caller puts a free one in its
+ * place before rows are appended there).
  * kv_len_out[b] = keep * 64 + kv_len[b] % 64, or kv_len[b] where nc <= keep.
  *   table, table_out [B,8,max_blocks] int32, weight, weight_out
  *   [B,8,max_blocks] fp32, kv_len, kv_len_out [B] int32. table_out may be table and

@@ -858,6 +858,62 @@ def test_a_captured_step_on_another_stream():
         assert torch.equal(getattr(cache, a).view(torch.uint8), getattr(twin, a).view(torch.uint8))
 
 
+def test_captured_turns_that_share_workspaces():
+    """A turn (12 and 3 tokens, a single one, an eviction in place) as two graphs over the same workspaces, by turns."""
+    rng = np.random.default_rng(50)
+    B, tab, keep = 2, tables(1024), 5
+    cache, host = filled(rng, [400, 330], "e4m3", 8, seed=40)
+    twin = G.Kv8Cache(*(x.clone() for x in (cache.k_pool, cache.v_pool, cache.k_scale, cache.v_scale, cache.table,
+                                            cache.open_k, cache.open_v)))
+
+    def state():
+        return dict(pos=_ints([400, 330]), rows=_ints([400, 330]), next=_ints([0, 0]), weight=torch.zeros(B, 8, 8, device=DEV),
+                    out=[torch.zeros(B, t, 48, 128, dtype=torch.bfloat16, device=DEV) for t in (12, 3, 1)],
+                    status=torch.zeros(1, dtype=torch.int32, device=DEV))
+
+    x = [[r.to(DEV) for r in rows(rng, B, t)] for t in (12, 3, 1)]
+    rot = [torch.zeros_like(q) for q, _, _ in x]
+    before = cache.table.clone()
+    pre, dec = G.alloc_kv8_prefill_workspace(cache), G.alloc_kv8_decode_workspace(cache)
+
+    def prompt(c, s):
+        for i in (0, 1):
+            G.kv8_append(c, *x[i], s["pos"], s["rows"], None, *tab, rot[i], s["status"])
+            G.kv8_prefill(c, rot[i], s["rows"], None, s["out"][i], pre, s["status"])
+            s["pos"] += x[i][0].shape[1]
+            s["rows"] += x[i][0].shape[1]
+
+    def answer(c, s):
+        G.kv8_append(c, *x[2], s["pos"], s["rows"], None, *tab, rot[2], s["status"])
+        s["pos"] += 1
+        s["rows"] += 1
+        G.kv8_decode(c, rot[2][:, 0], s["rows"], dec, s["out"][2][:, 0], s["weight"], s["weight"], s["status"])
+        G.kv8_evict(c.table, s["weight"], s["rows"], keep, 1, 2, c.table, s["weight"], s["next"], s["status"])
+        s["rows"].copy_(s["next"])
+
+    mine, theirs = state(), state()
+    torch.cuda.synchronize()
+    graphs = [torch.cuda.CUDAGraph() for _ in range(2)]
+    for graph, call in zip(graphs, (prompt, answer)):
+        with torch.cuda.graph(graph):
+            call(cache, mine)
+    for turn in range(3):
+        for q, k, v in x:
+            a, b, c = rows(rng, B, q.shape[1])
+            q.copy_(a), k.copy_(b), v.copy_(c)
+        for graph in graphs:
+            graph.replay()
+        prompt(twin, theirs)
+        answer(twin, theirs)
+        torch.cuda.synchronize()
+        for name in ("pos", "rows", "weight", "status"):
+            assert torch.equal(mine[name], theirs[name]), (turn, name)
+        assert all(torch.equal(a, b) and bool(a.any()) for a, b in zip(mine["out"], theirs["out"]))
+        assert torch.equal(cache.table, twin.table)
+        assert int(mine["status"].item()) == 0 and mine["rows"].max().item() < (keep + 1) * 64
+    assert not torch.equal(cache.table, before)
+
+
 def test_readme_example_runs():
     import os
     import re

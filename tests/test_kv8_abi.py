@@ -36,7 +36,7 @@ def _evict(lib, table=A, w=A, length=A, B=2, n=4, keep=2, sink=0, recent=0, t_ou
     return lib.grok_kv8_evict(table, w, length, B, n, keep, sink, recent, t_out, w_out, l_out, None, None)
 
 
-def _prefill(lib, cache=None, q=A, length=A, valid=None, T=4, out=A, ws=A, nbytes=1 << 40):
+def _prefill(lib, cache=None, q=A, length=A, valid=None, T=4, out=2 * A, ws=A, nbytes=1 << 40):
     return lib.grok_kv8_prefill(_cache() if cache is None else cache, q, length, valid, T, out, ws, nbytes, None, None)
 
 
@@ -69,7 +69,7 @@ def test_bad_decodes(lib, bad):
 
 
 @pytest.mark.parametrize("bad", [dict(q=None), dict(length=None), dict(ws=None), dict(out=None), dict(q=A + 8),
-                                 dict(out=A + 8), dict(ws=A + 16), dict(T=0), dict(T=257)], ids=str)
+                                 dict(out=A + 8), dict(out=A), dict(ws=A + 16), dict(T=0), dict(T=257)], ids=str)
 def test_bad_prefills(lib, bad):
     assert _prefill(lib, **bad) == 1
     assert b"grok_kv8_prefill" in lib.grok_last_error()
