@@ -616,9 +616,12 @@ grok_status grok::kv8_decode_run(const grok_kv8_cache& cache, const grok_bf16* q
   if (e != cudaSuccess) return fail(cuda_status(e), "kv8_decode launch: %s", cudaGetErrorString(e));
   if ((st = check_launch("kv8_decode")) != GROK_OK) return st;
   // Many pairs have few partials each: a CTA per pair, a warp per head. Few pairs have many (workers / pairs and
-  // two more at most): a CTA per pair and head.
+  // two more at most): a CTA per pair and head, where all of them run at once (two on an SM). Whole calls, us, CTA per
+  // pair and head against CTA per pair: 2 sequences of 5120 rows 9.8 against 15.0, 4 14.9 against 18.0, 8 22.4 against
+  // 21.9; of 300 rows 1 6.9 against 6.9, 8 9.0 against 7.6, 16 11.0 against 8.3.
+  // (With or without weights the same join adds the outputs, in the same order.)
   const int pairs = n_seq * kKVHeads;
-  const bool few = pairs * 8 < p.wave;
+  const bool few = pairs * (kGroup + 1) <= 2 * sms;
   cfg.gridDim = few ? dim3(pairs, kGroup + (weight_out ? 1 : 0)) : dim3(pairs);
   cfg.blockDim = dim3(few ? 256 : kGroup * 32);
   cfg.dynamicSmemBytes = 0;
