@@ -55,9 +55,9 @@ constexpr float kDqLag = 8.f;  // log2 units a weight may exceed the reference b
 struct DqParams {
   grok_kv8_cache c;
   const uint4* q;
-  const int32_t* kv_len;     // rows that a query sees; with few_tokens, rows before the call's tokens
-  const int32_t* valid_len;  // few_tokens: valid tokens of a sequence, or null (all)
-  int few_tokens;  // 0: one query per sequence. T: T tokens per sequence, each a query of its own
+  const int32_t* kv_len;     // rows that a query sees; kFew: rows before the call's tokens
+  const int32_t* valid_len;  // kFew: valid tokens of a sequence, or null (all)
+  int few_tokens;  // kFew: tokens per sequence, each a query of its own
   int n_seq;       // queries: B, or B * T
   float* part_o;    // [slot][6][128]
   float2* part_ml;  // [slot][6]: reference (log2), sum
@@ -95,20 +95,26 @@ struct Deal {
 
 __device__ __forceinline__ uint32_t word_of(const uint4& x, int w) { return w == 0 ? x.x : w == 1 ? x.y : w == 2 ? x.z : x.w; }
 
-// Rows that query v sees: 0 when its sequence's integers are bad. With few_tokens
-// token i of a sequence sees those before the call and the valid ones up to itself.
+// Rows that query v sees: 0 when its sequence's integers are bad. kFew: token i of a
+// sequence sees those before the call and the valid ones up to itself. (A template:
+// the choice at run time costs a call over 300 rows 0.3 of its 6.2 us.)
+template <bool kFew>
 __device__ __forceinline__ int rows_of(const DqParams& p, int v) {
-  if (!p.few_tokens) return __ldg(p.kv_len + v);
+  if (!kFew) return __ldg(p.kv_len + v);
   const int b = v / p.few_tokens, i = v % p.few_tokens;
   const int s = __ldg(p.kv_len + b), n = p.valid_len ? __ldg(p.valid_len + b) : p.few_tokens;
   if (s < 0 || n < 1 || n > p.few_tokens || (long long)s + n > (long long)p.c.max_blocks * kKv8Block) return 0;
   return s + min(i + 1, n);
 }
-__device__ __forceinline__ int blocks_of(const DqParams& p, int v) { return kv8_blocks(rows_of(p, v), p.c.max_blocks); }
+template <bool kFew>
+__device__ __forceinline__ int blocks_of(const DqParams& p, int v) {
+  return kv8_blocks(rows_of<kFew>(p, v), p.c.max_blocks);
+}
 
 // Bits for a query whose sequence's integers are bad (as the many-token kernel reports them).
+template <bool kFew>
 __device__ __forceinline__ int bad_bits(const DqParams& p, int v) {
-  if (!p.few_tokens) return GROK_DEV_BAD_KV_LEN;
+  if (!kFew) return GROK_DEV_BAD_KV_LEN;
   const int b = v / p.few_tokens;
   const int s = __ldg(p.kv_len + b), n = p.valid_len ? __ldg(p.valid_len + b) : p.few_tokens;
   return (n < 1 || n > p.few_tokens ? GROK_DEV_BAD_VALID : 0) |
@@ -116,14 +122,15 @@ __device__ __forceinline__ int bad_bits(const DqParams& p, int v) {
 }
 
 // The queries' blocks: total over the batch of ceil(rows / 64), by one warp.
+template <bool kFew>
 __device__ __forceinline__ int count_blocks(const DqParams& p, int lane) {
   int total = 0;
   for (int c = 0; c < p.n_seq; c += 32)
-    total += __reduce_add_sync(0xffffffffu, c + lane < p.n_seq ? blocks_of(p, c + lane) : 0);
+    total += __reduce_add_sync(0xffffffffu, c + lane < p.n_seq ? blocks_of<kFew>(p, c + lane) : 0);
   return total;
 }
 
-template <int kKind, bool kWeights>
+template <int kKind, bool kWeights, bool kFew>
 __global__ void __launch_bounds__(kDqThreads, kDqCtas) kv8_decode_kernel(const DqParams p) {
   extern __shared__ __align__(128) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -140,13 +147,13 @@ __global__ void __launch_bounds__(kDqThreads, kDqCtas) kv8_decode_kernel(const D
   }
   __syncthreads();
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int n_total = kKVHeads * count_blocks(p, lane);
+  const int n_total = kKVHeads * count_blocks<kFew>(p, lane);
   const Deal deal(n_total, p.wave, p.second);
   const int n_first = p.wave / kDqWarps, cta = blockIdx.x;
   const int item = cta < n_first ? warp * n_first + cta : cta * kDqWarps + warp;  // (few blocks: over the SMs first)
   if (item == 0)
     for (int v = lane; v < p.n_seq; v += 32)
-      if (blocks_of(p, v) == 0) report(p.status, bad_bits(p, v));
+      if (blocks_of<kFew>(p, v) == 0) report(p.status, bad_bits<kFew>(p, v));
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   // (item * small passes n_total by less than a wave of shares: no overflow below 2^31)
   const int lo = min(deal.start(item), n_total), hi = min(deal.start(item + 1), n_total);
@@ -194,7 +201,7 @@ __global__ void __launch_bounds__(kDqThreads, kDqCtas) kv8_decode_kernel(const D
       bool found = lane >= cnt;
       int cum = 0;
       for (int c = 0; c < p.n_seq; c += 32) {
-        const int len = c + lane < p.n_seq ? rows_of(p, c + lane) : 0;
+        const int len = c + lane < p.n_seq ? rows_of<kFew>(p, c + lane) : 0;
         const int n = kv8_blocks(len, p.c.max_blocks);
         int incl = n;
 #pragma unroll
@@ -227,7 +234,7 @@ __global__ void __launch_bounds__(kDqThreads, kDqCtas) kv8_decode_kernel(const D
     float my_ks = 0.f, my_vs = 0.f;
     if (lane < cnt) {
       size_t row_of = my_pair;  // of the table
-      if (p.few_tokens) row_of = (size_t)(my_pair / kKVHeads / p.few_tokens) * kKVHeads + my_pair % kKVHeads;
+      if (kFew) row_of = (size_t)(my_pair / kKVHeads / p.few_tokens) * kKVHeads + my_pair % kKVHeads;
       my_id = max(0, kv8_block_id(p.c.table, row_of * p.c.max_blocks + my_blk, p.c.n_blocks, p.status));
       my_ks = __ldg(p.c.k_scale + my_id);
       my_vs = __ldg(p.c.v_scale + my_id);
@@ -430,14 +437,14 @@ __device__ __forceinline__ float warp_sum(float x) {
   return x;
 }
 
-template <int kHeads, int kSplit>
+template <int kHeads, int kSplit, bool kFew>
 __global__ void __launch_bounds__(kHeads * kSplit * 32) kv8_join_kernel(const DqParams p) {
   constexpr int kThreads = kHeads * kSplit * 32;
   constexpr int kBatch = 12;  // partial outputs in flight per warp
   __shared__ float4 s_o[kHeads * kSplit][32];
   __shared__ float s_inv[8];
   const int pair = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int blocks = blocks_of(p, pair / kKVHeads);
+  const int blocks = blocks_of<kFew>(p, pair / kKVHeads);
   const bool weights = p.weight_out && (kHeads > 1 || blockIdx.y == kGroup);
   // The first blocks' old weights do not depend on the first kernel.
   const size_t at0 = (size_t)pair * p.c.max_blocks + threadIdx.x;
@@ -592,10 +599,15 @@ grok_status grok::kv8_decode_run(const grok_kv8_cache& cache, const grok_bf16* q
                    second,
                    dev_status};
   const bool i8 = cache.kind == GROK_KV8_INT8;
-  auto kernel = i8 ? (weight_out ? kv8_decode_kernel<GROK_KV8_INT8, true> : kv8_decode_kernel<GROK_KV8_INT8, false>)
-                   : (weight_out ? kv8_decode_kernel<GROK_KV8_E4M3, true> : kv8_decode_kernel<GROK_KV8_E4M3, false>);
-  static bool attr_set[kMaxDevices][4] = {};  // per device and kernel; idempotent: every thread would set the same value
-  bool& set = attr_set[dev][(i8 ? 0 : 2) + (weight_out ? 1 : 0)];
+  const int which = few_tokens ? 2 : weight_out ? 1 : 0;
+  decltype(&kv8_decode_kernel<GROK_KV8_INT8, false, false>) kernels[2][3] = {
+      {kv8_decode_kernel<GROK_KV8_INT8, false, false>, kv8_decode_kernel<GROK_KV8_INT8, true, false>,
+       kv8_decode_kernel<GROK_KV8_INT8, false, true>},
+      {kv8_decode_kernel<GROK_KV8_E4M3, false, false>, kv8_decode_kernel<GROK_KV8_E4M3, true, false>,
+       kv8_decode_kernel<GROK_KV8_E4M3, false, true>}};
+  auto kernel = kernels[i8 ? 0 : 1][which];
+  static bool attr_set[kMaxDevices][2][3] = {};  // per device and kernel; idempotent: every thread would set the same value
+  bool& set = attr_set[dev][i8 ? 0 : 1][which];
   if (!set) {
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kDqSmem);
     if (e != cudaSuccess) return fail(cuda_status(e), "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
@@ -625,7 +637,9 @@ grok_status grok::kv8_decode_run(const grok_kv8_cache& cache, const grok_bf16* q
   cfg.gridDim = few ? dim3(pairs, kGroup + (weight_out ? 1 : 0)) : dim3(pairs);
   cfg.blockDim = dim3(few ? 256 : kGroup * 32);
   cfg.dynamicSmemBytes = 0;
-  e = cudaLaunchKernelEx(&cfg, few ? kv8_join_kernel<1, 8> : kv8_join_kernel<kGroup, 1>, p);
+  auto join = few_tokens ? (few ? kv8_join_kernel<1, 8, true> : kv8_join_kernel<kGroup, 1, true>)
+                         : (few ? kv8_join_kernel<1, 8, false> : kv8_join_kernel<kGroup, 1, false>);
+  e = cudaLaunchKernelEx(&cfg, join, p);
   if (e != cudaSuccess) return fail(cuda_status(e), "kv8_join launch: %s", cudaGetErrorString(e));
   return check_launch("kv8_join");
 }
