@@ -54,11 +54,10 @@ grok_status linear_int8_small(const grok_bf16* x, const int8_t* w8, const float*
 // Checks of an 8-bit cache's description (kv8_append.cu).
 grok_status kv8_check(const grok_kv8_cache* c, const char* who);
 
-// Attention over an 8-bit cache with a query of its own for each token (kv8_decode.cu).
+// Attention over an 8-bit cache, a pass over the codes for one token or a few (kv8_decode.cu).
 // few_tokens 0: one token per sequence, which sees len[b] rows. T: T tokens per
-// sequence behind len[b] rows, q_rot and out [B,T,48,128]. ws: kv8_decode_bytes for
-// B * max(1, few_tokens) sequences.
-size_t kv8_decode_bytes(int n_seq, int max_blocks, bool weights, int sms);
+// sequence behind len[b] rows, q_rot and out [B,T,48,128]. ws: kv8_decode_bytes.
+size_t kv8_decode_bytes(int B, int few_tokens, int max_blocks, bool weights, int sms);
 grok_status kv8_decode_run(const grok_kv8_cache& cache, const grok_bf16* q_rot, const int32_t* len,
                            const int32_t* valid_len, int few_tokens, char* ws, grok_bf16* out, const float* weight_in,
                            float* weight_out, int sms, int32_t* dev_status, cudaStream_t stream);

@@ -14,7 +14,7 @@
 // and writes one partial result (m, l, O) per pair that it touches; a second
 // kernel, launched as a dependent, joins a pair's partials. Which blocks make a
 // partial follows from the lengths alone, so the bits do too. Calls of a few tokens
-// run here as well, every token a query with a length of its own (few_tokens).
+// run here as well (kFew).
 //
 // Measured (graph replays, one GB300): 32 sequences of up to 8192 rows (274 MB of
 // codes) 52.1 us, 5.26 TB/s, 0.78 of the copy rate; 16 of up to 65536 (1.14 GB) 179 us,
@@ -33,6 +33,13 @@
 // block, so a thread reads operands as 16-byte words and the order of the
 // contracted index is chosen to fit them: thread t of a row's four holds
 // features (keys) 16 t .. 16 t + 15.
+// kFew: four tokens of a sequence are 24 columns, three tiles without waste, over
+// one pass: their codes are loaded and converted once. A column has the keys that
+// its token sees. Two more tiles' outputs and scores leave registers for four warps
+// per CTA (255 each) and put the queries in shared memory. Four tokens of 8
+// sequences behind 8000 rows 41.6 us (72 as four single ones), 32 tokens behind
+// 16000 rows 66 us; without four tokens to fill it a pass costs more than a single
+// token's (1 token, 300 rows: 9.8 us against 6.3).
 // P is rounded once to fp16 (2^-11 relative) against a running reference that may
 // lag the maximum by 2^8; l, the weights and O stay in fp32.
 #include <algorithm>
@@ -49,6 +56,14 @@ constexpr int kDqThreads = kDqWarps * 32;
 constexpr int kDqRing = kDqBufs * kKv8Bytes;
 constexpr int kDqSmem = kDqWarps * kDqRing + kDqWarps * kDqBufs * 8 + 16;
 static_assert(kDqCtas * (kDqSmem + 1024) <= 233472, "shared memory per SM");
+constexpr int kDqTok = 4;  // tokens that share a pass over the codes in a call of few tokens: 24 columns, three tiles of 8
+constexpr int kDqFewCols = kDqTok * kGroup;
+constexpr int kDqFewQ = 8 * (kDqFewCols / 8) * 32 * 8;  // a warp's queries as operands, in shared memory
+constexpr int kDqFewWarps = 4;  // two warps on a scheduler, up to 255 registers each
+constexpr int kDqFewThreads = kDqFewWarps * 32;
+constexpr int kDqFewSmem = kDqFewWarps * (kDqRing + kDqFewQ) + kDqFewWarps * kDqBufs * 8 + 16;
+static_assert(kDqCtas * (kDqFewSmem + 1024) <= 233472, "shared memory per SM");
+constexpr float kDqNone = -1.0e4f;  // reference of a column that has seen no key
 constexpr int kDqLong = 24;  // blocks per worker from which a second wave of small shares pays
 constexpr float kDqLag = 8.f;  // log2 units a weight may exceed the reference by
 
@@ -57,8 +72,8 @@ struct DqParams {
   const uint4* q;
   const int32_t* kv_len;     // rows that a query sees; kFew: rows before the call's tokens
   const int32_t* valid_len;  // kFew: valid tokens of a sequence, or null (all)
-  int few_tokens;  // kFew: tokens per sequence, each a query of its own
-  int n_seq;       // queries: B, or B * T
+  int few_tokens;  // kFew: tokens per sequence
+  int n_seq;       // what a pair is one KV head of: sequences, or (kFew) groups of kDqTok tokens of a sequence
   float* part_o;    // [slot][6][128]
   float2* part_ml;  // [slot][6]: reference (log2), sum
   int2* pair_parts; // [B * 8]: a pair's first slot and number of slots
@@ -95,16 +110,19 @@ struct Deal {
 
 __device__ __forceinline__ uint32_t word_of(const uint4& x, int w) { return w == 0 ? x.x : w == 1 ? x.y : w == 2 ? x.z : x.w; }
 
-// Rows that query v sees: 0 when its sequence's integers are bad. kFew: token i of a
-// sequence sees those before the call and the valid ones up to itself. (A template:
-// the choice at run time costs a call over 300 rows 0.3 of its 6.2 us.)
+__host__ __device__ __forceinline__ int groups_of(int tokens) { return (tokens + kDqTok - 1) / kDqTok; }
+
+// Rows that v's queries see: 0 when its sequence's integers are bad. kFew: those of
+// the group's last token (token i sees the rows before the call and the valid
+// tokens' up to its own). (A template: the choice at run time costs a call over
+// 300 rows 0.3 of its 6.2 us.)
 template <bool kFew>
 __device__ __forceinline__ int rows_of(const DqParams& p, int v) {
   if (!kFew) return __ldg(p.kv_len + v);
-  const int b = v / p.few_tokens, i = v % p.few_tokens;
+  const int groups = groups_of(p.few_tokens), b = v / groups, first = v % groups * kDqTok;
   const int s = __ldg(p.kv_len + b), n = p.valid_len ? __ldg(p.valid_len + b) : p.few_tokens;
   if (s < 0 || n < 1 || n > p.few_tokens || (long long)s + n > (long long)p.c.max_blocks * kKv8Block) return 0;
-  return s + min(i + 1, n);
+  return s + min(first + kDqTok, n);
 }
 template <bool kFew>
 __device__ __forceinline__ int blocks_of(const DqParams& p, int v) {
@@ -115,7 +133,7 @@ __device__ __forceinline__ int blocks_of(const DqParams& p, int v) {
 template <bool kFew>
 __device__ __forceinline__ int bad_bits(const DqParams& p, int v) {
   if (!kFew) return GROK_DEV_BAD_KV_LEN;
-  const int b = v / p.few_tokens;
+  const int b = v / groups_of(p.few_tokens);
   const int s = __ldg(p.kv_len + b), n = p.valid_len ? __ldg(p.valid_len + b) : p.few_tokens;
   return (n < 1 || n > p.few_tokens ? GROK_DEV_BAD_VALID : 0) |
          (s < 0 || (long long)s + max(n, 0) > (long long)p.c.max_blocks * kKv8Block ? GROK_DEV_BAD_KV_LEN : 0);
@@ -131,12 +149,16 @@ __device__ __forceinline__ int count_blocks(const DqParams& p, int lane) {
 }
 
 template <int kKind, bool kWeights, bool kFew>
-__global__ void __launch_bounds__(kDqThreads, kDqCtas) kv8_decode_kernel(const DqParams p) {
+__global__ void __launch_bounds__(kFew ? kDqFewThreads : kDqThreads, kDqCtas) kv8_decode_kernel(const DqParams p) {
+  constexpr int kWarps = kFew ? kDqFewWarps : kDqWarps;
+  constexpr int kTiles = kFew ? kDqFewCols / 8 : 1;  // of 8 columns: a column is a query head of a token
+  constexpr int kCols = kFew ? kDqFewCols : kGroup;
   extern __shared__ __align__(128) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int row = lane >> 2, t = lane & 3;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kDqWarps * kDqRing);
-  int* abort_flag = reinterpret_cast<int*>(bars + kDqBufs * kDqWarps);
+  constexpr int kData = kWarps * (kDqRing + (kFew ? kDqFewQ : 0));
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kData);
+  int* abort_flag = reinterpret_cast<int*>(bars + kDqBufs * kWarps);
   volatile int* abort = abort_flag;
   bars += kDqBufs * warp;
   uint8_t* ring = smem + warp * kDqRing;
@@ -149,8 +171,8 @@ __global__ void __launch_bounds__(kDqThreads, kDqCtas) kv8_decode_kernel(const D
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int n_total = kKVHeads * count_blocks<kFew>(p, lane);
   const Deal deal(n_total, p.wave, p.second);
-  const int n_first = p.wave / kDqWarps, cta = blockIdx.x;
-  const int item = cta < n_first ? warp * n_first + cta : cta * kDqWarps + warp;  // (few blocks: over the SMs first)
+  const int n_first = p.wave / kWarps, cta = blockIdx.x;
+  const int item = cta < n_first ? warp * n_first + cta : cta * kWarps + warp;  // (few blocks: over the SMs first)
   if (item == 0)
     for (int v = lane; v < p.n_seq; v += 32)
       if (blocks_of<kFew>(p, v) == 0) report(p.status, bad_bits<kFew>(p, v));
@@ -159,9 +181,11 @@ __global__ void __launch_bounds__(kDqThreads, kDqCtas) kv8_decode_kernel(const D
   const int lo = min(deal.start(item), n_total), hi = min(deal.start(item + 1), n_total);
   if (lo >= hi) return;
 
-  uint32_t qb[8][2];
-  float q_scale0 = 0.f, q_scale1 = 0.f;  // of heads 2 t, 2 t + 1
-  float o[8][4], m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
+  uint32_t qb[8][2];  // (kFew: in shared memory)
+  uint2* sq = reinterpret_cast<uint2*>(smem + kWarps * kDqRing + warp * kDqFewQ) + lane;
+  // of columns 8 nt + 2 t, 8 nt + 2 t + 1
+  float q_scale[kTiles][2], o[kTiles][8][4], m[kTiles][2], l[kTiles][2];
+  int seen = 0;  // kFew: tokens of the group up to the last valid one
   int pair = -1;
   int buf = 0, next_buf = 0;         // buffers of the next piece to read and to load (a piece: a block's K or V)
   uint32_t phase = 0;                // of buffer `buf`
@@ -170,24 +194,28 @@ __global__ void __launch_bounds__(kDqThreads, kDqCtas) kv8_decode_kernel(const D
 
   // One partial result: this item's share of a pair.
   auto flush = [&]() {
+    const size_t slot = (size_t)item + pair;
 #pragma unroll
-    for (int d = 4; d < 32; d *= 2) {
-      l0 += __shfl_xor_sync(0xffffffffu, l0, d);
-      l1 += __shfl_xor_sync(0xffffffffu, l1, d);
-    }
-    if (t < kGroup / 2) {
-      const size_t slot = (size_t)item + pair;
-      float* po = p.part_o + (slot * kGroup + 2 * t) * kD + row;
+    for (int nt = 0; nt < kTiles; ++nt) {
 #pragma unroll
-      for (int mt = 0; mt < 8; ++mt) {
-        po[16 * mt] = o[mt][0];
-        po[16 * mt + kD] = o[mt][1];
-        po[16 * mt + 8] = o[mt][2];
-        po[16 * mt + 8 + kD] = o[mt][3];
+      for (int d = 4; d < 32; d *= 2) {
+        l[nt][0] += __shfl_xor_sync(0xffffffffu, l[nt][0], d);
+        l[nt][1] += __shfl_xor_sync(0xffffffffu, l[nt][1], d);
       }
-      if (row == 0) {
-        p.part_ml[slot * kGroup + 2 * t] = make_float2(m0, l0);
-        p.part_ml[slot * kGroup + 2 * t + 1] = make_float2(m1, l1);
+      if (kFew || t < kGroup / 2) {
+        const int c = 8 * nt + 2 * t;
+        float* po = p.part_o + (slot * kCols + c) * kD + row;
+#pragma unroll
+        for (int mt = 0; mt < 8; ++mt) {
+          po[16 * mt] = o[nt][mt][0];
+          po[16 * mt + kD] = o[nt][mt][1];
+          po[16 * mt + 8] = o[nt][mt][2];
+          po[16 * mt + 8 + kD] = o[nt][mt][3];
+        }
+        if (row == 0) {
+          p.part_ml[slot * kCols + c] = make_float2(m[nt][0], l[nt][0]);
+          p.part_ml[slot * kCols + c + 1] = make_float2(m[nt][1], l[nt][1]);
+        }
       }
     }
   };
@@ -222,7 +250,7 @@ __global__ void __launch_bounds__(kDqThreads, kDqCtas) kv8_decode_kernel(const D
           const int in = rest - kKVHeads * (si - sn);
           my_pair = (c + s) * kKVHeads + in / sn;
           my_blk = in % sn;
-          my_keys = min(kKv8Block, sl - my_blk * kKv8Block);
+          my_keys = min(2 * kKv8Block, sl - my_blk * kKv8Block);  // (up to the last row)
           found = true;
           if (my_blk == 0) p.pair_parts[my_pair] = make_int2(item + my_pair, deal.item_of(idx + sn - 1) - item + 1);
         }
@@ -234,10 +262,12 @@ __global__ void __launch_bounds__(kDqThreads, kDqCtas) kv8_decode_kernel(const D
     float my_ks = 0.f, my_vs = 0.f;
     if (lane < cnt) {
       size_t row_of = my_pair;  // of the table
-      if (kFew) row_of = (size_t)(my_pair / kKVHeads / p.few_tokens) * kKVHeads + my_pair % kKVHeads;
+      if (kFew) row_of = (size_t)(my_pair / kKVHeads / groups_of(p.few_tokens)) * kKVHeads + my_pair % kKVHeads;
       my_id = max(0, kv8_block_id(p.c.table, row_of * p.c.max_blocks + my_blk, p.c.n_blocks, p.status));
       my_ks = __ldg(p.c.k_scale + my_id);
       my_vs = __ldg(p.c.v_scale + my_id);
+      // (a token that does not see the block meets its V scale: what is not finite shows in the logits)
+      if (kFew && my_vs != my_vs) my_ks = my_vs, my_vs = 0.f;
     }
     int loaded = 0;  // pieces of this batch
     auto load = [&]() {
@@ -275,46 +305,73 @@ __global__ void __launch_bounds__(kDqThreads, kDqCtas) kv8_decode_kernel(const D
       if (jp != pair) {  // the next pair: its partial starts empty, its six queries come in
         if (pair >= 0) flush();
         pair = jp;
-        m0 = m1 = -INFINITY;
-        l0 = l1 = 0.f;
-#pragma unroll
-        for (int mt = 0; mt < 8; ++mt) o[mt][0] = o[mt][1] = o[mt][2] = o[mt][3] = 0.f;
-        uint4 x[4];
-        uint32_t top = 0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          x[i] = make_uint4(0, 0, 0, 0);
-          if (row < kGroup) x[i] = __ldg(p.q + ((size_t)pair * kGroup + row) * 16 + (i >> 1) * 8 + 2 * t + (i & 1));
-          top = __vmaxu2(top, __vmaxu2(__vmaxu2(x[i].x & 0x7FFF7FFFu, x[i].y & 0x7FFF7FFFu),
-                                       __vmaxu2(x[i].z & 0x7FFF7FFFu, x[i].w & 0x7FFF7FFFu)));
+        int b = 0, first = 0;
+        if (kFew) {
+          const int groups = groups_of(p.few_tokens), v = pair / kKVHeads;
+          b = v / groups, first = v % groups * kDqTok;
+          seen = min(kDqTok, (p.valid_len ? __ldg(p.valid_len + b) : p.few_tokens) - first);
         }
-        top = max(top & 0xFFFFu, top >> 16);
-        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        // q / 2^e with the largest element in [1, 2): what falls below fp16's normal range is off by 2^-25 at most
-        const uint32_t e = min(max(top >> 7, 1u), 253u);
-        const float down = __uint_as_float((254u - e) << 23), up = __uint_as_float(e << 23);
+        uint4 xs[kTiles][4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+        for (int nt = 0; nt < kTiles; ++nt) {  // the query row of this lane's column
+          const int c = 8 * nt + row, tok = first + c / kGroup;
+          const bool live = kFew ? tok < p.few_tokens : row < kGroup;
+          const size_t at =
+              kFew ? (((size_t)b * p.few_tokens + tok) * kKVHeads + pair % kKVHeads) * kGroup + c % kGroup
+                   : (size_t)pair * kGroup + row;
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const int u = (i >> 1) * 4 + (i & 1) * 2 + (c >> 1);  // product of the 16 features 64 (i >> 1) + 16 t + ..
-            qb[u][c & 1] = pack_f16x2(bf16lo_to_f32(w[c]) * down, bf16hi_to_f32(w[c]) * down);
+          for (int i = 0; i < 4; ++i) {
+            xs[nt][i] = make_uint4(0, 0, 0, 0);
+            if (live) xs[nt][i] = __ldg(p.q + at * 16 + (i >> 1) * 8 + 2 * t + (i & 1));
           }
         }
-        q_scale0 = __shfl_sync(0xffffffffu, up, 8 * t) * (2.f * kY * kLog2e);
-        q_scale1 = __shfl_sync(0xffffffffu, up, 8 * t + 4) * (2.f * kY * kLog2e);
+#pragma unroll
+        for (int nt = 0; nt < kTiles; ++nt) {
+          m[nt][0] = m[nt][1] = kDqNone;
+          l[nt][0] = l[nt][1] = 0.f;
+#pragma unroll
+          for (int mt = 0; mt < 8; ++mt) o[nt][mt][0] = o[nt][mt][1] = o[nt][mt][2] = o[nt][mt][3] = 0.f;
+          const uint4 (&x)[4] = xs[nt];
+          uint32_t top = 0;
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            top = __vmaxu2(top, __vmaxu2(__vmaxu2(x[i].x & 0x7FFF7FFFu, x[i].y & 0x7FFF7FFFu),
+                                         __vmaxu2(x[i].z & 0x7FFF7FFFu, x[i].w & 0x7FFF7FFFu)));
+          top = max(top & 0xFFFFu, top >> 16);
+          top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+          top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+          // q / 2^e with the largest element in [1, 2): what falls below fp16's normal range is off by 2^-25 at most
+          const uint32_t e = min(max(top >> 7, 1u), 253u);
+          const float down = __uint_as_float((254u - e) << 23), up = __uint_as_float(e << 23);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+            for (int c4 = 0; c4 < 4; c4 += 2) {
+              const int u = (i >> 1) * 4 + (i & 1) * 2 + (c4 >> 1);  // product of the 16 features 64 (i >> 1) + 16 t + ..
+              const uint32_t y0 = pack_f16x2(bf16lo_to_f32(w[c4]) * down, bf16hi_to_f32(w[c4]) * down);
+              const uint32_t y1 = pack_f16x2(bf16lo_to_f32(w[c4 + 1]) * down, bf16hi_to_f32(w[c4 + 1]) * down);
+              if (kFew) {
+                sq[(nt * 8 + u) * 32] = make_uint2(y0, y1);  // (read by this lane alone)
+              } else {
+                qb[u][0] = y0, qb[u][1] = y1;
+              }
+            }
+          }
+          q_scale[nt][0] = __shfl_sync(0xffffffffu, up, 8 * t) * (2.f * kY * kLog2e);
+          q_scale[nt][1] = __shfl_sync(0xffffffffu, up, 8 * t + 4) * (2.f * kY * kLog2e);
+        }
       }
       const float ks = __shfl_sync(0xffffffffu, my_ks, j), vs = __shfl_sync(0xffffffffu, my_vs, j);
       const int keys = __shfl_sync(0xffffffffu, my_keys, j), blk = __shfl_sync(0xffffffffu, my_blk, j);
 
       if (!wait()) break;
       const uint8_t* k_buf = ring + buf * kKv8Bytes;
-      float s[4][4];
+      float s[kTiles][4][4];
 #pragma unroll
       for (int st = 0; st < 4; ++st) {
-        s[st][0] = s[st][1] = s[st][2] = s[st][3] = 0.f;
+#pragma unroll
+        for (int nt = 0; nt < kTiles; ++nt) s[nt][st][0] = s[nt][st][1] = s[nt][st][2] = s[nt][st][3] = 0.f;
         // row r of the tile is key 16 (r >> 1) + 4 st + (r & 1), row r + 8 two keys on: the order P^T is read in below
         const uint8_t* k0 = k_buf + (16 * (row >> 1) + 4 * st + (row & 1)) * 64 + 16 * t;
 #pragma unroll
@@ -326,57 +383,72 @@ __global__ void __launch_bounds__(kDqThreads, kDqCtas) kv8_decode_kernel(const D
             uint32_t a0, a1, a2, a3;
             kv8_to_half<kKind>(word_of(a, w), a0, a2);
             kv8_to_half<kKind>(word_of(b, w), a1, a3);
-            mma_f16_16816(s[st], a0, a1, a2, a3, qb[4 * h + w][0], qb[4 * h + w][1]);
+#pragma unroll
+            for (int nt = 0; nt < kTiles; ++nt) {
+              const uint2 q = kFew ? sq[(nt * 8 + 4 * h + w) * 32] : make_uint2(qb[4 * h + w][0], qb[4 * h + w][1]);
+              mma_f16_16816(s[nt][st], a0, a1, a2, a3, q.x, q.y);
+            }
           }
         }
       }
       release();
 
-      // z = log2 of the weight against the fixed reference 30: -2 kT / (1 + e^(2 x / 30))
-      const float f0 = ks * q_scale0, f1 = ks * q_scale1;
-      float top0 = -INFINITY, top1 = -INFINITY;
+      uint32_t pb[kTiles][4][2];
 #pragma unroll
-      for (int st = 0; st < 4; ++st)
+      for (int nt = 0; nt < kTiles; ++nt) {
+        float (&z)[4][4] = s[nt];
+        // z = log2 of the weight against the fixed reference 30: -2 kT / (1 + e^(2 x / 30))
+        const float f0 = ks * q_scale[nt][0], f1 = ks * q_scale[nt][1];
+        // keys seen: a group's earlier tokens see fewer than its last
+        const int keys0 = kFew ? keys - max(0, seen - 1 - (8 * nt + 2 * t) / kGroup) : keys;
+        const int keys1 = kFew ? keys - max(0, seen - 1 - (8 * nt + 2 * t + 1) / kGroup) : keys;
+        float top0 = -INFINITY, top1 = -INFINITY;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          float z = (-2.f * kT) * rcp_approx(1.f + ex2_approx(s[st][e] * (e & 1 ? f1 : f0)));
-          if (keys < kKv8Block && 16 * (row >> 1) + 4 * st + (row & 1) + (e & 2) >= keys) z = -INFINITY;
-          s[st][e] = z;
-          if (e & 1) top1 = fmaxf(top1, z); else top0 = fmaxf(top0, z);
-        }
+        for (int st = 0; st < 4; ++st)
 #pragma unroll
-      for (int d = 4; d < 32; d *= 2) {
-        top0 = fmaxf(top0, __shfl_xor_sync(0xffffffffu, top0, d));
-        top1 = fmaxf(top1, __shfl_xor_sync(0xffffffffu, top1, d));
-      }
-      if (__any_sync(0xffffffffu, top0 > m0 + kDqLag || top1 > m1 + kDqLag)) {
-        const float n0 = fmaxf(m0, top0), n1 = fmaxf(m1, top1);
-        const float c0 = m0 == -INFINITY ? 0.f : ex2_approx(m0 - n0), c1 = m1 == -INFINITY ? 0.f : ex2_approx(m1 - n1);
-        m0 = n0, m1 = n1;
-        l0 *= c0, l1 *= c1;
-#pragma unroll
-        for (int mt = 0; mt < 8; ++mt) o[mt][0] *= c0, o[mt][1] *= c1, o[mt][2] *= c0, o[mt][3] *= c1;
-      }
-      uint32_t pb[4][2];
-      float b0 = 0.f, b1 = 0.f;
-#pragma unroll
-      for (int st = 0; st < 4; ++st) {
-        const float p0 = ex2_approx(s[st][0] - m0), p1 = ex2_approx(s[st][1] - m1);
-        const float p2 = ex2_approx(s[st][2] - m0), p3 = ex2_approx(s[st][3] - m1);
-        b0 += p0 + p2, b1 += p1 + p3;
-        pb[st][0] = movmatrix_trans(pack_f16x2(p0, p1));
-        pb[st][1] = movmatrix_trans(pack_f16x2(p2, p3));
-      }
-      l0 += b0, l1 += b1;
-      if (kWeights) {
+          for (int e = 0; e < 4; ++e) {
+            float x = (-2.f * kT) * rcp_approx(1.f + ex2_approx(z[st][e] * (e & 1 ? f1 : f0)));
+            if (keys < kKv8Block + (kFew ? kDqTok - 1 : 0) &&
+                16 * (row >> 1) + 4 * st + (row & 1) + (e & 2) >= (e & 1 ? keys1 : keys0))
+              x = -INFINITY;
+            z[st][e] = x;
+            if (e & 1) top1 = fmaxf(top1, x); else top0 = fmaxf(top0, x);
+          }
 #pragma unroll
         for (int d = 4; d < 32; d *= 2) {
-          b0 += __shfl_xor_sync(0xffffffffu, b0, d);
-          b1 += __shfl_xor_sync(0xffffffffu, b1, d);
+          top0 = fmaxf(top0, __shfl_xor_sync(0xffffffffu, top0, d));
+          top1 = fmaxf(top1, __shfl_xor_sync(0xffffffffu, top1, d));
         }
-        if (row == 0 && t < kGroup / 2)
-          *reinterpret_cast<float2*>(p.block_w + ((size_t)pair * p.c.max_blocks + blk) * 8 + 2 * t) =
-              make_float2(b0 * ex2_approx(m0), b1 * ex2_approx(m1));
+        float &m0 = m[nt][0], &m1 = m[nt][1];
+        if (__any_sync(0xffffffffu, top0 > m0 + kDqLag || top1 > m1 + kDqLag)) {
+          const float n0 = fmaxf(m0, top0), n1 = fmaxf(m1, top1);
+          const float c0 = ex2_approx(m0 - n0), c1 = ex2_approx(m1 - n1);
+          m0 = n0, m1 = n1;
+          l[nt][0] *= c0, l[nt][1] *= c1;
+#pragma unroll
+          for (int mt = 0; mt < 8; ++mt)
+            o[nt][mt][0] *= c0, o[nt][mt][1] *= c1, o[nt][mt][2] *= c0, o[nt][mt][3] *= c1;
+        }
+        float b0 = 0.f, b1 = 0.f;
+#pragma unroll
+        for (int st = 0; st < 4; ++st) {
+          const float p0 = ex2_approx(z[st][0] - m0), p1 = ex2_approx(z[st][1] - m1);
+          const float p2 = ex2_approx(z[st][2] - m0), p3 = ex2_approx(z[st][3] - m1);
+          b0 += p0 + p2, b1 += p1 + p3;
+          pb[nt][st][0] = movmatrix_trans(pack_f16x2(p0, p1));
+          pb[nt][st][1] = movmatrix_trans(pack_f16x2(p2, p3));
+        }
+        l[nt][0] += b0, l[nt][1] += b1;
+        if (kWeights) {
+#pragma unroll
+          for (int d = 4; d < 32; d *= 2) {
+            b0 += __shfl_xor_sync(0xffffffffu, b0, d);
+            b1 += __shfl_xor_sync(0xffffffffu, b1, d);
+          }
+          if (row == 0 && t < kGroup / 2)
+            *reinterpret_cast<float2*>(p.block_w + ((size_t)pair * p.c.max_blocks + blk) * 8 + 2 * t) =
+                make_float2(b0 * ex2_approx(m0), b1 * ex2_approx(m1));
+        }
       }
 
       if (!wait()) break;
@@ -394,16 +466,21 @@ __global__ void __launch_bounds__(kDqThreads, kDqCtas) kv8_decode_kernel(const D
             reinterpret_cast<uint32_t*>(&b)[st] &= mask;
           }
         }
-        float acc[4] = {0.f, 0.f, 0.f, 0.f};
+        float acc[kTiles][4];
+#pragma unroll
+        for (int nt = 0; nt < kTiles; ++nt) acc[nt][0] = acc[nt][1] = acc[nt][2] = acc[nt][3] = 0.f;
 #pragma unroll
         for (int st = 0; st < 4; ++st) {
           uint32_t a0, a1, a2, a3;
           kv8_to_half<kKind>(word_of(a, st), a0, a2);
           kv8_to_half<kKind>(word_of(b, st), a1, a3);
-          mma_f16_16816(acc, a0, a1, a2, a3, pb[st][0], pb[st][1]);
+#pragma unroll
+          for (int nt = 0; nt < kTiles; ++nt) mma_f16_16816(acc[nt], a0, a1, a2, a3, pb[nt][st][0], pb[nt][st][1]);
         }
 #pragma unroll
-        for (int e = 0; e < 4; ++e) o[mt][e] = fmaf(acc[e], vs, o[mt][e]);
+        for (int nt = 0; nt < kTiles; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[nt][mt][e] = fmaf(acc[nt][e], vs, o[nt][mt][e]);
       }
       release();
     }
@@ -443,18 +520,28 @@ __global__ void __launch_bounds__(kHeads * kSplit * 32) kv8_join_kernel(const Dq
   constexpr int kBatch = 12;  // partial outputs in flight per warp
   __shared__ float4 s_o[kHeads * kSplit][32];
   __shared__ float s_inv[8];
+  constexpr int kCols = kFew ? kDqFewCols : kGroup;
   const int pair = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // The column of head 0: kFew has its tokens' heads along y.
+  const int col0 = kFew ? blockIdx.y / (kGroup / kHeads) * kGroup : 0;
+  const int head0 = kHeads == 1 ? (kFew ? blockIdx.y % kGroup : blockIdx.y) : 0;
   const int blocks = blocks_of<kFew>(p, pair / kKVHeads);
   const bool weights = p.weight_out && (kHeads > 1 || blockIdx.y == kGroup);
+  int few_b = 0, few_tok = 0;
+  if (kFew) {
+    const int groups = groups_of(p.few_tokens), v = pair / kKVHeads;
+    few_b = v / groups, few_tok = v % groups * kDqTok + col0 / kGroup;
+  }
   // The first blocks' old weights do not depend on the first kernel.
   const size_t at0 = (size_t)pair * p.c.max_blocks + threadIdx.x;
   float w_in = 0.f;
   if (weights && p.weight_in && threadIdx.x < p.c.max_blocks) w_in = p.weight_in[at0];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (blocks == 0) return;                // reported by the first kernel
+  if (kFew && few_tok >= p.few_tokens) return;
   const int2 parts = p.pair_parts[pair];  // first slot, number
   const int n_parts = parts.y;
-  const float2* ml = p.part_ml + (size_t)parts.x * kGroup;
+  const float2* ml = p.part_ml + (size_t)parts.x * kCols + col0;
   float4 wa = make_float4(0.f, 0.f, 0.f, 0.f);
   float2 wb = make_float2(0.f, 0.f);
   if (weights && threadIdx.x < blocks) {
@@ -462,11 +549,11 @@ __global__ void __launch_bounds__(kHeads * kSplit * 32) kv8_join_kernel(const Dq
     wb = *reinterpret_cast<const float2*>(p.block_w + at0 * 8 + 4);
   }
 
-  if (kHeads > 1 || blockIdx.y < kGroup) {
+  if (kFew || kHeads > 1 || blockIdx.y < kGroup) {
     // Everything is loaded before anything is used: the partials' sums, a lane to each, and this warp's first outputs.
-    const int head = kHeads == 1 ? blockIdx.y : warp / kSplit, sub = warp % kSplit;
-    const float* po = p.part_o + ((size_t)parts.x * kGroup + head) * kD + 4 * lane;
-    const float2 mine = lane < n_parts ? ml[lane * kGroup + head] : make_float2(-INFINITY, 0.f);
+    const int head = kHeads == 1 ? head0 : warp / kSplit, sub = warp % kSplit;
+    const float* po = p.part_o + ((size_t)parts.x * kCols + col0 + head) * kD + 4 * lane;
+    const float2 mine = lane < n_parts ? ml[lane * kCols + head] : make_float2(-INFINITY, 0.f);
     float4 v[kBatch];
     float vm[kBatch];
 #pragma unroll
@@ -475,16 +562,16 @@ __global__ void __launch_bounds__(kHeads * kSplit * 32) kv8_join_kernel(const Dq
       v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
       vm[u] = -INFINITY;
       if (k < n_parts) {
-        v[u] = *reinterpret_cast<const float4*>(po + (size_t)k * (kGroup * kD));
-        vm[u] = ml[k * kGroup + head].x;
+        v[u] = *reinterpret_cast<const float4*>(po + (size_t)k * (kCols * kD));
+        vm[u] = ml[k * kCols + head].x;
       }
     }
     float m = mine.x;
-    for (int k = lane + 32; k < n_parts; k += 32) m = fmaxf(m, ml[k * kGroup + head].x);
+    for (int k = lane + 32; k < n_parts; k += 32) m = fmaxf(m, ml[k * kCols + head].x);
     m = warp_max(m);
     float l = mine.y * ex2_approx(mine.x - m);
     for (int k = lane + 32; k < n_parts; k += 32) {
-      const float2 x = ml[k * kGroup + head];
+      const float2 x = ml[k * kCols + head];
       l = fmaf(x.y, ex2_approx(x.x - m), l);
     }
     l = warp_sum(l);
@@ -499,8 +586,8 @@ __global__ void __launch_bounds__(kHeads * kSplit * 32) kv8_join_kernel(const Dq
     }
 #pragma unroll 8
     for (int k = sub + kBatch * kSplit; k < n_parts; k += kSplit) {
-      const float4 x = *reinterpret_cast<const float4*>(po + (size_t)k * (kGroup * kD));
-      const float f = ex2_approx(ml[k * kGroup + head].x - m);
+      const float4 x = *reinterpret_cast<const float4*>(po + (size_t)k * (kCols * kD));
+      const float f = ex2_approx(ml[k * kCols + head].x - m);
       acc.x = fmaf(x.x, f, acc.x);
       acc.y = fmaf(x.y, f, acc.y);
       acc.z = fmaf(x.z, f, acc.z);
@@ -519,7 +606,10 @@ __global__ void __launch_bounds__(kHeads * kSplit * 32) kv8_join_kernel(const Dq
     }
     if (sub == 0) {
       const float inv = 1.f / l;
-      p.out[((size_t)pair * kGroup + head) * (kD / 4) + lane] =
+      size_t at = (size_t)pair * kGroup + head;
+      if (kFew)
+        at = (((size_t)few_b * p.few_tokens + few_tok) * kKVHeads + pair % kKVHeads) * kGroup + head;
+      p.out[at * (kD / 4) + lane] =
           make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
       if (kHeads > 1 && lane == 0) s_inv[head] = 1.f / (l * ex2_approx(m));  // on the fixed reference 30
     }
@@ -556,18 +646,19 @@ using namespace grok;
 namespace {
 
 size_t up256(size_t n) { return (n + 255) & ~size_t(255); }
-int wave_of(int sms) { return sms * kDqCtas * kDqWarps; }  // workers resident at a time
+int wave_of(int sms, int warps = kDqWarps) { return sms * kDqCtas * warps; }  // workers resident at a time
 // A share touches a run of pairs, so (share, pair) runs through fewer than shares + pairs values of their sum.
 size_t part_slots(int B, int sms) { return size_t(2) * wave_of(sms) + size_t(B) * kKVHeads; }
-size_t part_o_bytes(int B, int sms) { return part_slots(B, sms) * kGroup * kD * sizeof(float); }
-size_t part_ml_bytes(int B, int sms) { return up256(part_slots(B, sms) * kGroup * sizeof(float2)); }
+size_t part_o_bytes(int B, int sms, int cols) { return part_slots(B, sms) * cols * kD * sizeof(float); }
+size_t part_ml_bytes(int B, int sms, int cols) { return up256(part_slots(B, sms) * cols * sizeof(float2)); }
 size_t pairs_bytes(int B) { return up256(size_t(B) * kKVHeads * sizeof(int2)); }
 size_t block_w_bytes(int B, int max_blocks) { return size_t(B) * kKVHeads * max_blocks * 8 * sizeof(float); }
 
 }  // namespace
 
-size_t grok::kv8_decode_bytes(int n_seq, int max_blocks, bool weights, int sms) {
-  return part_o_bytes(n_seq, sms) + part_ml_bytes(n_seq, sms) + pairs_bytes(n_seq) +
+size_t grok::kv8_decode_bytes(int B, int few_tokens, int max_blocks, bool weights, int sms) {
+  const int n_seq = few_tokens ? B * groups_of(few_tokens) : B, cols = few_tokens ? kDqFewCols : kGroup;
+  return part_o_bytes(n_seq, sms, cols) + part_ml_bytes(n_seq, sms, cols) + pairs_bytes(n_seq) +
          (weights ? block_w_bytes(n_seq, max_blocks) : 0);
 }
 
@@ -578,9 +669,9 @@ grok_status grok::kv8_decode_run(const grok_kv8_cache& cache, const grok_bf16* q
   int dev = 0;
   grok_status st = device_index(&dev);
   if (st != GROK_OK) return st;
-  const int n_seq = cache.B * std::max(1, few_tokens);
-  const size_t o_bytes = part_o_bytes(n_seq, sms), ml_bytes = part_ml_bytes(n_seq, sms);
-  const int wave = wave_of(sms);
+  const int n_seq = few_tokens ? cache.B * groups_of(few_tokens) : cache.B, cols = few_tokens ? kDqFewCols : kGroup;
+  const size_t o_bytes = part_o_bytes(n_seq, sms, cols), ml_bytes = part_ml_bytes(n_seq, sms, cols);
+  const int warps = few_tokens ? kDqFewWarps : kDqWarps, wave = wave_of(sms, warps);
   const int second = (long long)n_seq * kKVHeads * cache.max_blocks >= (long long)kDqLong * wave ? wave : 0;
   const DqParams p{cache,
                    reinterpret_cast<const uint4*>(q_rot),
@@ -607,17 +698,18 @@ grok_status grok::kv8_decode_run(const grok_kv8_cache& cache, const grok_bf16* q
        kv8_decode_kernel<GROK_KV8_E4M3, false, true>}};
   auto kernel = kernels[i8 ? 0 : 1][which];
   static bool attr_set[kMaxDevices][2][3] = {};  // per device and kernel; idempotent: every thread would set the same value
+  const int smem = few_tokens ? kDqFewSmem : kDqSmem;
   bool& set = attr_set[dev][i8 ? 0 : 1][which];
   if (!set) {
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kDqSmem);
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return fail(cuda_status(e), "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
     set = true;
   }
   // Both kernels are launched as dependents of the one before them: each begins with a wait for all of it.
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((p.wave + p.second) / kDqWarps);
-  cfg.blockDim = dim3(kDqThreads);
-  cfg.dynamicSmemBytes = kDqSmem;
+  cfg.gridDim = dim3((p.wave + p.second) / warps);
+  cfg.blockDim = dim3(32 * warps);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -633,8 +725,9 @@ grok_status grok::kv8_decode_run(const grok_kv8_cache& cache, const grok_bf16* q
   // 21.9; of 300 rows 1 6.9 against 6.9, 8 9.0 against 7.6, 16 11.0 against 8.3.
   // (With or without weights the same join adds the outputs, in the same order.)
   const int pairs = n_seq * kKVHeads;
-  const bool few = pairs * (kGroup + 1) <= 2 * sms;
-  cfg.gridDim = few ? dim3(pairs, kGroup + (weight_out ? 1 : 0)) : dim3(pairs);
+  const int toks = few_tokens ? kDqTok : 1;  // (a group's tokens are joined apart)
+  const bool few = pairs * toks * (kGroup + 1) <= 2 * sms;
+  cfg.gridDim = dim3(pairs, few ? toks * kGroup + (weight_out ? 1 : 0) : toks);
   cfg.blockDim = dim3(few ? 256 : kGroup * 32);
   cfg.dynamicSmemBytes = 0;
   auto join = few_tokens ? (few ? kv8_join_kernel<1, 8, true> : kv8_join_kernel<kGroup, 1, true>)
@@ -652,7 +745,7 @@ extern "C" grok_status grok_kv8_decode_workspace(int B, int max_blocks, int weig
   int sms = 0;
   grok_status st = device_sm_count(&sms);
   if (st != GROK_OK) return st;
-  *bytes = kv8_decode_bytes(B, max_blocks, weights != 0, sms);
+  *bytes = kv8_decode_bytes(B, 0, max_blocks, weights != 0, sms);
   return GROK_OK;
 }
 
@@ -669,7 +762,7 @@ extern "C" grok_status grok_kv8_decode(const grok_kv8_cache* cache, const grok_b
     return fail(GROK_ERR_INVALID_ARG, "grok_kv8_decode: workspace must be 256-byte aligned");
   int sms = 0;
   if ((st = device_sm_count(&sms)) != GROK_OK) return st;
-  const size_t need = kv8_decode_bytes(cache->B, cache->max_blocks, weight_out != nullptr, sms);
+  const size_t need = kv8_decode_bytes(cache->B, 0, cache->max_blocks, weight_out != nullptr, sms);
   if (workspace_bytes < need)
     return fail(GROK_ERR_INVALID_ARG, "grok_kv8_decode: workspace of %zu bytes is smaller than the %zu needed",
                 workspace_bytes, need);

@@ -165,13 +165,13 @@ namespace {
 
 size_t up256(size_t n) { return (n + 255) & ~size_t(255); }
 
-// Up to here every token runs as a query of its own over the codes (kv8_decode.cu): no copies of the cache, its codes
-// read (mostly from L2) once per token, and the split over the key range that single tokens have. Above, the copies
-// cost less than the tokens' reads. Measured, us, own queries against copies: 1 sequence behind 16000 rows 13 against
-// 79 for 1 token, 39 against 79 for 8, 53 against 78 for 12, 71 against 79 for 16; 8 behind 8000 137 against 257 for 8,
-// 256 against 257 for 16; 32 behind 4000 276 against 519 for 8, 534 against 520 for 16; 256 behind 1000 763 against
-// 1019 for 8, 1269 against 1020 for 12.
-constexpr int kFewTokens = 8;
+// Calls of up to this many tokens run on the codes (kv8_decode.cu, four tokens to a pass): no copies of the cache, and
+// the split over the key range that single tokens have. Above, the copies cost less than the passes. Measured, us, codes
+// against copies: 1 sequence behind 300 rows 10 against 17 for 4 tokens, 11.5 against 18 for 32; 1 behind 16000 21
+// against 78 for 4, 66 against 78 for 32, 85 against 78 for 48; 8 behind 8000 41 against 256 for 4, 226 against 257 for
+// 32, 326 against 257 for 48; 32 behind 4000 239 against 518 for 16, 457 against 521 for 32; 32 behind 300 43 against 74
+// for 16, 88 against 80 for 32; 256 behind 1000 658 against 1024 for 16, 1387 against 1097 for 32.
+int few_tokens(int B) { return B <= 8 ? 32 : 20; }
 
 // Workspace: fallback count and list, K scales, output factors, the copies of K and V, the split's area.
 struct Layout {
@@ -189,7 +189,7 @@ Layout layout(int B, int max_blocks, int sms) {
   w.v_copy = w.k_copy + copy;
   w.split = w.v_copy + copy;
   w.bytes = w.split + (split_allowed(w.rows) ? split_area_bytes(sms) : 0);
-  w.bytes = std::max(w.bytes, kv8_decode_bytes(B * kFewTokens, max_blocks, false, sms));
+  w.bytes = std::max(w.bytes, kv8_decode_bytes(B, few_tokens(B), max_blocks, false, sms));
   return w;
 }
 
@@ -235,7 +235,7 @@ extern "C" grok_status grok_kv8_prefill(const grok_kv8_cache* cache, const grok_
   if (workspace_bytes < w.bytes)
     return fail(GROK_ERR_INVALID_ARG, "grok_kv8_prefill: workspace of %zu bytes is smaller than the %zu needed",
                 workspace_bytes, w.bytes);
-  if (T <= kFewTokens)
+  if (T <= few_tokens(B))
     return kv8_decode_run(*cache, q_rot, cache_len, valid_len, T, static_cast<char*>(workspace), out, nullptr, nullptr, sms,
                           dev_status, static_cast<cudaStream_t>(stream));
   char* ws = static_cast<char*>(workspace);

@@ -535,8 +535,10 @@ PREFILLS = {
     "split_unequal": ([2000, 64, 900], [300, 500, 7], 500),
     "split_causal": ([700], [1400], 1400),
     # the longest call that runs as single tokens, and the shortest that does not
-    "last_few": ([2500, 63, 120], [8, 4, 7], 8),
-    "first_many": ([2500, 63, 120], [9, 4, 7], 9),
+    "last_few": ([2500, 63, 120], [32, 4, 17], 32),
+    "first_many": ([2500, 63, 120], [33, 4, 17], 33),
+    "last_few_of_nine": (list(range(40, 400, 40)), [20, 1, 2, 3, 4, 5, 17, 19, 20], 20),
+    "first_many_of_nine": (list(range(40, 400, 40)), [21, 1, 2, 3, 4, 5, 17, 19, 20], 21),
     "few_over_many_shares": ([9000, 60, 0, 7000], [5, 7, 1, 2], 7),
     "few_over_many_sequences": (list(range(0, 320, 5)), [1 + i % 3 for i in range(64)], 3),
 }
@@ -571,15 +573,40 @@ def test_prefill_of_one_token_is_the_decode():
 
 
 def test_prefill_of_few_tokens_is_that_of_many():
-    """The same valid tokens in calls of 8 and of 9 tokens, which take different kernels."""
+    """The same valid tokens in calls of 32 and of 33 tokens, which take different kernels."""
     rng = np.random.default_rng(48)
-    cache, host = filled(rng, [700, 64, 12, 300], "e4m3", 11, seed=38)
-    q = _bf16(rng.standard_normal((4, 9, 48, 128)) * 3).to(DEV)
-    lens, valid = [692, 60, 4, 293], [8, 4, 8, 7]
-    a, sa = run_prefill(cache, q[:, :8].contiguous(), lens, valid, 8)
-    b, sb = run_prefill(cache, q, lens, valid, 9)
+    cache, host = filled(rng, [700, 64, 32, 300], "e4m3", 11, seed=38)
+    q = _bf16(rng.standard_normal((4, 33, 48, 128)) * 3).to(DEV)
+    lens, valid = [668, 60, 0, 269], [32, 4, 32, 31]
+    a, sa = run_prefill(cache, q[:, :32].contiguous(), lens, valid, 32)
+    b, sb = run_prefill(cache, q, lens, valid, 33)
     assert sa == sb == 0
-    assert_close(_bits(a), _bits(b[:, :8]), "kv8 prefill of 8 tokens against 9")
+    assert_close(_bits(a), _bits(b[:, :32]), "kv8 prefill of 32 tokens against 33")
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("where", ["k", "v"])
+def test_prefill_of_few_tokens_non_finite_block_reaches_its_tokens_alone(kind, where):
+    """Tokens 0 and 1 end the first block; token 3 makes the second one's scale a NaN, which tokens 2 to 5 see."""
+    tab, T = tables(256), 6
+    results = []
+    for broken in (False, True):
+        rng = np.random.default_rng(51)
+        cache, _ = filled(rng, [62, 62], kind, 3, seed=41, tab=tab)
+        q, k, v = rows(rng, 2, T)
+        if broken:
+            (k if where == "k" else v)[0, 3, 5, 17] = float("inf")
+        q_rot = torch.empty_like(q, device=DEV)
+        G.kv8_append(cache, q.to(DEV), k.to(DEV), v.to(DEV), _ints([62, 62]), _ints([62, 62]), None, *tab, q_rot)
+        got, status = run_prefill(cache, q_rot, [62, 62], None, T)
+        assert status == 0
+        results.append(got.float())
+    good, bad = results
+    head = slice(30, 36)
+    assert torch.isnan(bad[0, 2:, head]).all() and torch.equal(bad[0, :2], good[0, :2])
+    keep = [*range(30), *range(36, 48)]
+    assert torch.equal(bad[0][:, keep], good[0][:, keep]) and torch.equal(bad[1], good[1])
+    assert torch.isfinite(good).all()
 
 
 def test_prefill_of_few_tokens_bad_integers():
@@ -698,21 +725,22 @@ def test_prefill_split_items_of_good_and_bad_sequences():
     assert status == G.DEV_BAD_KV_LEN and (got == 7.0).all()
 
 
-def test_prefill_bad_integers_leave_the_outputs():
+@pytest.mark.parametrize("T", [28, 40])  # on the codes, over the copies
+def test_prefill_bad_integers_leave_the_outputs(T):
     rng = np.random.default_rng(45)
     cache, host = filled(rng, [128] * 3, "int8", 2, seed=35)
-    q = _bf16(rng.standard_normal((3, 28, 48, 128))).to(DEV)
-    good, _ = run_prefill(cache, q, [100] * 3, [28] * 3, 28)
-    for lens, valid, bit in (([100, -1, 100], [28] * 3, G.DEV_BAD_KV_LEN), ([100, 101, 100], [28] * 3, G.DEV_BAD_KV_LEN),
-                             ([100] * 3, [28, 0, 28], G.DEV_BAD_VALID), ([100] * 3, [28, 29, 28], G.DEV_BAD_VALID | G.DEV_BAD_KV_LEN)):
-        got, status = run_prefill(cache, q, lens, valid, 28)
+    q = _bf16(rng.standard_normal((3, T, 48, 128))).to(DEV)
+    good, _ = run_prefill(cache, q, [128 - T] * 3, [T] * 3, T)
+    for lens, valid, bit in (([128 - T, -1, 128 - T], [T] * 3, G.DEV_BAD_KV_LEN), ([128 - T, 129 - T, 128 - T], [T] * 3, G.DEV_BAD_KV_LEN),
+                             ([128 - T] * 3, [T, 0, T], G.DEV_BAD_VALID), ([128 - T] * 3, [T, T + 1, T], G.DEV_BAD_VALID | G.DEV_BAD_KV_LEN)):
+        got, status = run_prefill(cache, q, lens, valid, T)
         assert status == bit
         assert (got[1] == 7.0).all() and torch.equal(got[[0, 2]], good[[0, 2]])
     # padding tokens past the capacity are no error
-    got, status = run_prefill(cache, q, [110] * 3, [18, 1, 10], 28)
+    got, status = run_prefill(cache, q, [110] * 3, [18, 1, 10], T)
     assert status == 0
     cache.table[1, 7, 1] = cache.n_blocks
-    got, status = run_prefill(cache, q, [100] * 3, [28] * 3, 28)
+    got, status = run_prefill(cache, q, [128 - T] * 3, [T] * 3, T)
     assert status == G.DEV_BAD_PAGE and torch.equal(got[[0, 2]], good[[0, 2]])
 
 
