@@ -731,8 +731,10 @@ def test_prefill_bad_integers_leave_the_outputs(T):
     cache, host = filled(rng, [128] * 3, "int8", 2, seed=35)
     q = _bf16(rng.standard_normal((3, T, 48, 128))).to(DEV)
     good, _ = run_prefill(cache, q, [128 - T] * 3, [T] * 3, T)
-    for lens, valid, bit in (([128 - T, -1, 128 - T], [T] * 3, G.DEV_BAD_KV_LEN), ([128 - T, 129 - T, 128 - T], [T] * 3, G.DEV_BAD_KV_LEN),
-                             ([128 - T] * 3, [T, 0, T], G.DEV_BAD_VALID), ([128 - T] * 3, [T, T + 1, T], G.DEV_BAD_VALID | G.DEV_BAD_KV_LEN)):
+    for lens, valid, bit in (([128 - T, -1, 128 - T], [T] * 3, G.DEV_BAD_KV_LEN),
+                             ([128 - T, 129 - T, 128 - T], [T] * 3, G.DEV_BAD_KV_LEN),
+                             ([128 - T] * 3, [T, 0, T], G.DEV_BAD_VALID),
+                             ([128 - T] * 3, [T, T + 1, T], G.DEV_BAD_VALID | G.DEV_BAD_KV_LEN)):
         got, status = run_prefill(cache, q, lens, valid, T)
         assert status == bit
         assert (got[1] == 7.0).all() and torch.equal(got[[0, 2]], good[[0, 2]])
