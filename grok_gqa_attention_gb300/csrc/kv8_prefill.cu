@@ -143,6 +143,7 @@ __global__ void __launch_bounds__(kUnThreads) kv8_unpack_kernel(const UnParams p
 
 // The fallback pass multiplies bf16: when an item is listed, the copy of V is rounded to bf16 in its place.
 __global__ void __launch_bounds__(256) kv8_v_to_bf16_kernel(const int32_t* fb_count, uint4* v, long long n) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the fp16 passes, which list the items
   if (*fb_count == 0) return;
   for (long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += (long long)gridDim.x * blockDim.x) {

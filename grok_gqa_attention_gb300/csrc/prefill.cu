@@ -553,7 +553,11 @@ __global__ void __launch_bounds__(kPfThreads, 1)
   // (8-bit cache: the whole-item pass is a dependent of the kernel that makes the copies, and each pass of the one
   // before it. Its producer waits before the first K tile, its softmax warps before the first scale; the set-up and
   // the first Q tile need nothing of theirs.)
+  // (The pass over whole items lets the next kernel in early, which waits for the whole of it. Not the split pass: the
+  // kernel that adds the parts would crowd on the few SMs that are free then.)
+  if (kQ8 && !kList && !kSplit) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (!kQ8 || kList) asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (kList && *reinterpret_cast<const volatile int32_t*>(p.item_count) == 0) return;  // the usual case
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sQ = smem;
   uint8_t* sK = smem + kQBytes;                           // K ring
