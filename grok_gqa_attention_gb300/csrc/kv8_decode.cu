@@ -524,7 +524,7 @@ __global__ void __launch_bounds__(kHeads * kSplit * 32) kv8_join_kernel(const Dq
   const int pair = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // The column of head 0: kFew has its tokens' heads along y.
   const int col0 = kFew ? blockIdx.y / (kGroup / kHeads) * kGroup : 0;
-  const int head0 = kHeads == 1 ? (kFew ? blockIdx.y % kGroup : blockIdx.y) : 0;
+  const int head0 = (kFew ? blockIdx.y % (kGroup / kHeads) : kHeads == 1 ? blockIdx.y : 0) * kHeads;
   const int blocks = blocks_of<kFew>(p, pair / kKVHeads);
   const bool weights = p.weight_out && (kHeads > 1 || blockIdx.y == kGroup);
   int few_b = 0, few_tok = 0;
@@ -551,7 +551,7 @@ __global__ void __launch_bounds__(kHeads * kSplit * 32) kv8_join_kernel(const Dq
 
   if (kFew || kHeads > 1 || blockIdx.y < kGroup) {
     // Everything is loaded before anything is used: the partials' sums, a lane to each, and this warp's first outputs.
-    const int head = kHeads == 1 ? head0 : warp / kSplit, sub = warp % kSplit;
+    const int head = head0 + warp / kSplit, sub = warp % kSplit;
     const float* po = p.part_o + ((size_t)parts.x * kCols + col0 + head) * kD + 4 * lane;
     const float2 mine = lane < n_parts ? ml[lane * kCols + head] : make_float2(-INFINITY, 0.f);
     float4 v[kBatch];
@@ -727,11 +727,17 @@ grok_status grok::kv8_decode_run(const grok_kv8_cache& cache, const grok_bf16* q
   const int pairs = n_seq * kKVHeads;
   const int toks = few_tokens ? kDqTok : 1;  // (a group's tokens are joined apart)
   const bool few = pairs * toks * (kGroup + 1) <= 2 * sms;
-  cfg.gridDim = dim3(pairs, few ? toks * kGroup + (weight_out ? 1 : 0) : toks);
-  cfg.blockDim = dim3(few ? 256 : kGroup * 32);
+  auto join = few ? kv8_join_kernel<1, 8, false> : kv8_join_kernel<kGroup, 1, false>;
+  int split = few ? kGroup : 1, threads = few ? 256 : kGroup * 32;  // CTAs per pair and token
+  if (few_tokens) {
+    join = few ? kv8_join_kernel<1, 8, true> : kv8_join_kernel<kGroup, 1, true>;
+    // Between the two, two warps per head, three CTAs on an SM: 1 sequence behind 16000 rows, 8 / 12 tokens 28.1 / 34.7
+    // against 29.6 / 36.1 with a warp per head; 4 behind 3000, 2 tokens 16.5 against 18.1, 16 tokens 35.1 against 33.3.
+    if (!few && pairs * toks * 2 <= 3 * sms) join = kv8_join_kernel<3, 2, true>, split = 2;
+  }
+  cfg.gridDim = dim3(pairs, toks * split + (weight_out && few ? 1 : 0));
+  cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = 0;
-  auto join = few_tokens ? (few ? kv8_join_kernel<1, 8, true> : kv8_join_kernel<kGroup, 1, true>)
-                         : (few ? kv8_join_kernel<1, 8, false> : kv8_join_kernel<kGroup, 1, false>);
   e = cudaLaunchKernelEx(&cfg, join, p);
   if (e != cudaSuccess) return fail(cuda_status(e), "kv8_join launch: %s", cudaGetErrorString(e));
   return check_launch("kv8_join");
