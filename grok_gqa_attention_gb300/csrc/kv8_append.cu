@@ -221,8 +221,9 @@ __device__ void append_block(const ApParams& p, int b, int g, int j, int len, in
 }
 
 // kHeads: query heads loaded at a time. Three leave room for a fourth CTA on an SM
-// (8192 tokens: 47.9 -> 44.6 us); six are quicker where few CTAs run (one token for
-// one sequence: 4.3 us against 4.5).
+// (8192 tokens: 47.9 -> 44.6 us; one token of 64 sequences 8.2 -> 7.0); six are
+// quicker where three CTAs per SM take the whole call (one token of one sequence:
+// 4.3 us against 4.5; 104 of 11 11.2 against 12.0; 2048 of one 14.9 against 15.8).
 template <int kKind, int kHeads>
 __global__ void __launch_bounds__(kApThreads, kHeads == kGroup ? 3 : 4) kv8_append_kernel(const ApParams p) {
   __shared__ uint32_t red[kApThreads / 32][2];
@@ -333,7 +334,8 @@ extern "C" grok_status grok_kv8_append(const grok_kv8_cache* cache, const grok_b
                    dev_status};
   // T tokens behind up to 63 open rows touch at most (T + 126) / 64 blocks
   const dim3 grid((T + 2 * kKv8Block - 2) / kKv8Block, kKVHeads, cache->B);
-  const bool few = T < kKv8Block;
+  // CTAs with tokens, about: three on an SM at once with six heads, four with three
+  const bool few = (long long)cache->B * ((T + kKv8Block - 1) / kKv8Block) * kKVHeads <= 3 * sms;
   auto kernel = cache->kind == GROK_KV8_INT8
                     ? (few ? kv8_append_kernel<GROK_KV8_INT8, kGroup> : kv8_append_kernel<GROK_KV8_INT8, kGroup / 2>)
                     : (few ? kv8_append_kernel<GROK_KV8_E4M3, kGroup> : kv8_append_kernel<GROK_KV8_E4M3, kGroup / 2>);
