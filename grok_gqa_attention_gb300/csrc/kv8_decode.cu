@@ -56,7 +56,8 @@ constexpr int kDqThreads = kDqWarps * 32;
 constexpr int kDqRing = kDqBufs * kKv8Bytes;
 constexpr int kDqSmem = kDqWarps * kDqRing + kDqWarps * kDqBufs * 8 + 16;
 static_assert(kDqCtas * (kDqSmem + 1024) <= 233472, "shared memory per SM");
-constexpr int kDqTok = 4;  // tokens that share a pass over the codes in a call of few tokens: 24 columns, three tiles of 8
+// A call of few tokens: this many share a pass over the codes, 24 columns, three tiles of 8.
+constexpr int kDqTok = 4;
 constexpr int kDqFewCols = kDqTok * kGroup;
 constexpr int kDqFewQ = 8 * (kDqFewCols / 8) * 32 * 8;  // a warp's queries as operands, in shared memory
 constexpr int kDqFewWarps = 4;  // two warps on a scheduler, up to 255 registers each
@@ -74,10 +75,10 @@ struct DqParams {
   const int32_t* valid_len;  // kFew: valid tokens of a sequence, or null (all)
   int few_tokens;  // kFew: tokens per sequence
   int n_seq;       // what a pair is one KV head of: sequences, or (kFew) groups of kDqTok tokens of a sequence
-  float* part_o;    // [slot][6][128]
+  float* part_o;    // [slot][6][128] (kFew: 24 for 6)
   float2* part_ml;  // [slot][6]: reference (log2), sum
-  int2* pair_parts; // [B * 8]: a pair's first slot and number of slots
-  float* block_w;   // [B * 8][max_blocks][8]: a block's weights per head on the fixed reference 30
+  int2* pair_parts; // [n_seq * 8]: a pair's first slot and number of slots
+  float* block_w;   // [n_seq * 8][max_blocks][8]: a block's weights per head on the fixed reference 30
   uint2* out;
   const float* weight_in;
   float* weight_out;
@@ -108,7 +109,9 @@ struct Deal {
   }
 };
 
-__device__ __forceinline__ uint32_t word_of(const uint4& x, int w) { return w == 0 ? x.x : w == 1 ? x.y : w == 2 ? x.z : x.w; }
+__device__ __forceinline__ uint32_t word_of(const uint4& x, int w) {
+  return w == 0 ? x.x : w == 1 ? x.y : w == 2 ? x.z : x.w;
+}
 
 __host__ __device__ __forceinline__ int groups_of(int tokens) { return (tokens + kDqTok - 1) / kDqTok; }
 
@@ -697,7 +700,8 @@ grok_status grok::kv8_decode_run(const grok_kv8_cache& cache, const grok_bf16* q
       {kv8_decode_kernel<GROK_KV8_E4M3, false, false>, kv8_decode_kernel<GROK_KV8_E4M3, true, false>,
        kv8_decode_kernel<GROK_KV8_E4M3, false, true>}};
   auto kernel = kernels[i8 ? 0 : 1][which];
-  static bool attr_set[kMaxDevices][2][3] = {};  // per device and kernel; idempotent: every thread would set the same value
+  // Per device and kernel; idempotent: every thread would set the same value.
+  static bool attr_set[kMaxDevices][2][3] = {};
   const int smem = few_tokens ? kDqFewSmem : kDqSmem;
   bool& set = attr_set[dev][i8 ? 0 : 1][which];
   if (!set) {
