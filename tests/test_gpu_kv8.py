@@ -436,10 +436,10 @@ def test_decode_longest_cache(kind, rows_):
 
 
 @pytest.mark.parametrize("kind", KINDS)
-def test_prefill_behind_the_longest_cache(kind):
-    """Few tokens behind 65000 rows: items in eight parts, kernels over 510 key tiles."""
+@pytest.mark.parametrize("T,start", [(3, 65000), (32, 65504), (40, 65000)])
+def test_prefill_behind_the_longest_cache(kind, T, start):
+    """Tokens behind 65000 rows: passes over the codes to the last row; items in parts, kernels over 510 key tiles."""
     cache = random_cache(1, 1024, kind, 52)
-    T, start = 3, 65000
     q = (torch.randn(1, T, 48, 128, generator=torch.Generator(DEV).manual_seed(10), device=DEV) * 3).bfloat16()
     got, status = run_prefill(cache, q, [start], [T], T)
     assert status == 0
@@ -448,7 +448,7 @@ def test_prefill_behind_the_longest_cache(kind):
         K, V = cache_values(cache, 0, h, start + T)
         for r in range(6):
             want.append(kv8.attend(q[0, :, 6 * h + r].double().cpu().numpy(), K, V, start + np.arange(T))[0])
-    assert_close(_bits(got[0]), bf16.from_f64(np.stack(want, 1)), f"kv8 prefill behind 65000 rows {kind}")
+    assert_close(_bits(got[0]), bf16.from_f64(np.stack(want, 1)), f"kv8 prefill of {T} behind {start} rows {kind}")
 
 
 def test_calls_on_two_streams_at_once():
