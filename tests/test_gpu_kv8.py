@@ -585,6 +585,31 @@ def test_prefill_of_few_tokens_is_that_of_many():
 
 
 @pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("scale", [1e-6, 0.02, 8.0, "unequal"])
+def test_prefill_of_few_tokens_flat_and_peaked_logits(kind, scale):
+    """Seven tokens over a block's end: all weights alike, logits beyond the cap, queries of unequal magnitudes."""
+    lens, T = [517, 66], 7
+    rng = np.random.default_rng(52)
+    cache, host = filled(rng, lens, kind, 9, seed=42, scale=3.0 if scale == "unequal" else scale)
+    size = 2.0 ** rng.integers(-40, 4, (2, T, 48, 1)) if scale == "unequal" else scale
+    q = _bf16(rng.standard_normal((2, T, 48, 128)) * size).to(DEV)
+    got, status = run_prefill(cache, q, [n - T for n in lens], None, T)
+    assert status == 0
+    x = bf16.to_f64(_bits(q))
+    out, scale_v = np.zeros((2, T, 48, 128)), np.zeros((2, T, 48, 128))
+    s_abs = 0.0
+    for b, n in enumerate(lens):
+        for g in range(8):
+            K, V = kv8.held(host.k[b][:n, g], kind), kv8.held(host.v[b][:n, g], kind)
+            for h in range(6 * g, 6 * g + 6):
+                o, w = kv8.attend(x[b, :, h], K, V, n - T + np.arange(T))
+                out[b, :, h], scale_v[b, :, h] = o, w @ np.abs(V)
+                s_abs = max(s_abs, (np.abs(x[b, :, h]) @ np.abs(K).T).max() / 128 ** 0.5)
+    flat = lambda a: a.reshape(2 * T, 48, 128)  # noqa: E731
+    check_decode(flat(got), flat(out), flat(scale_v), s_abs, 517, np.ones(2 * T, bool))
+
+
+@pytest.mark.parametrize("kind", KINDS)
 @pytest.mark.parametrize("where", ["k", "v"])
 def test_prefill_of_few_tokens_non_finite_block_reaches_its_tokens_alone(kind, where):
     """Tokens 0 and 1 end the first block; token 3 makes the second one's scale a NaN, which tokens 2 to 5 see."""
