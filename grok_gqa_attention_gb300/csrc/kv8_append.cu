@@ -221,7 +221,7 @@ __device__ void append_block(const ApParams& p, int b, int g, int j, int len, in
 }
 
 // kHeads: query heads loaded at a time. Three leave room for a fourth CTA on an SM
-// (8192 tokens: 47.9 -> 44.6 us; one token of 64 sequences 8.2 -> 7.0); six are
+// (8192 tokens: 47.9 -> 44.6 us; eight of 64 sequences 10.3 -> 9.0); six are
 // quicker where three CTAs per SM take the whole call (one token of one sequence:
 // 4.3 us against 4.5; 104 of 11 11.2 against 12.0; 2048 of one 14.9 against 15.8).
 template <int kKind, int kHeads>
@@ -276,6 +276,160 @@ __global__ void __launch_bounds__(kApThreads, kHeads == kGroup ? 3 : 4) kv8_appe
   if (j == 0 && tail) {
     __syncthreads();
     append_block<kKind>(p, b, g, last, len, n, start, red);
+  }
+}
+
+// One token of many sequences: a CTA per sequence, a warp per KV head, where the
+// kernel above has a CTA of 256 threads for a few dozen live ones and runs them in
+// rounds. Where a token raises its block's scale (in a block of r random rows with
+// probability 1 / r for K and for V), the CTA's threads share the old rows of all such
+// heads. Steps of random rows, us, this kernel against the one above: 32 sequences
+// 7.1 to 8.1 against 5.9 to 7.0, 64 8.3 to 9.8 against 8.6 to 9.3, 128 8.6 to 10.7
+// against 14.5, 256 10.7 to 13.0 against 25.
+constexpr int kApMany = 64;  // sequences from which it is used
+
+template <int kKind>
+__global__ void __launch_bounds__(kApThreads, 4) kv8_append_one_kernel(const ApParams p) {
+  constexpr int kHeadsQ = kGroup * 8;  // (head, chunk) pairs of a KV head's queries
+  __shared__ uint32_t s_top[2][kKVHeads];  // largest magnitudes of the blocks that are written again; 0: none
+  __shared__ int s_id[kKVHeads], s_list[2][kKVHeads];
+  const int b = blockIdx.x, tid = threadIdx.x, g = tid >> 5, lane = tid & 31, c = lane & 7;
+  const int start = __ldg(p.start_pos + b), len = __ldg(p.cache_len + b);
+  const int n = p.valid_len ? __ldg(p.valid_len + b) : 1;
+  int bad = 0;
+  if (start < 0 || start >= p.tab_n) bad |= GROK_DEV_BAD_START;
+  if (n != 1) bad |= GROK_DEV_BAD_VALID;
+  if (len < 0 || (long long)len + max(n, 0) > (long long)p.c.max_blocks * kKv8Block) bad |= GROK_DEV_BAD_KV_LEN;
+  if (bad) {
+    if (tid == 0) report(p.status, bad);
+    return;
+  }
+  const int row = len % kKv8Block;
+  const size_t head = (size_t)b * kKVHeads + g;
+  const int id = kv8_block_id(p.c.table, head * p.c.max_blocks + len / kKv8Block, p.c.n_blocks,
+                              lane == 0 ? p.status : nullptr);
+  uint4 x1[2], x2[2], kx[2] = {}, vx = make_uint4(0, 0, 0, 0);
+#pragma unroll
+  for (int u = 0; u < 2; ++u)
+    if (lane + 32 * u < kHeadsQ) {
+      const size_t at = (head * kGroup + (lane + 32 * u) / 8) * 16 + c;
+      x1[u] = __ldg(p.q + at);
+      x2[u] = __ldg(p.q + at + 8);
+    }
+  if (lane < 8) {  // the key: pairs 8 c .. 8 c + 7; the value, next lanes: features 8 (lane - 8) ..
+    kx[0] = __ldg(p.k + head * 16 + c);
+    kx[1] = __ldg(p.k + head * 16 + c + 8);
+  } else if (lane < 24) {
+    vx = __ldg(p.v + head * 16 + lane - 8);
+  }
+  float tc[8], ts[8];
+  load_cs(p, start, c, tc, ts);
+  const float k_was = row > 0 && id >= 0 ? p.c.k_scale[id] : 0.f, v_was = row > 0 && id >= 0 ? p.c.v_scale[id] : 0.f;
+#pragma unroll
+  for (int u = 0; u < 2; ++u)
+    if (lane + 32 * u < kHeadsQ) {
+      const size_t at = (head * kGroup + (lane + 32 * u) / 8) * 16 + c;
+      uint4 y1, y2;
+      rotate8(x1[u], x2[u], tc, ts, y1, y2);
+      p.q_rot[at] = y1;
+      p.q_rot[at + 8] = y2;
+    }
+  if (lane < 8) rotate8(kx[0], kx[1], tc, ts, kx[0], kx[1]);
+  uint32_t km = absmax4(absmax4(0u, kx[0]), kx[1]), vm = absmax4(0u, vx);
+  km = __reduce_max_sync(0xffffffffu, max(km & 0xFFFFu, km >> 16));
+  vm = __reduce_max_sync(0xffffffffu, max(vm & 0xFFFFu, vm >> 16));
+  float ks = scale_of<kKind>(km), vs = scale_of<kKind>(vm);
+  // (as in append_block)
+  const bool k_all = row == 0 || !(ks <= k_was), v_all = row == 0 || !(vs <= v_was);
+  const bool again = row > 0 && id >= 0 && (k_all || v_all);
+  if (lane == 0) {
+    s_top[0][g] = again && k_all ? max(km, 1u) : 0u;
+    s_top[1][g] = again && v_all ? max(vm, 1u) : 0u;
+    s_id[g] = id;
+  }
+  const bool any = __syncthreads_or(again);
+  const uint4* open_k = reinterpret_cast<const uint4*>(p.c.open_k) + (size_t)b * kKVHeads * (kKv8Block * 16);
+  const uint4* open_v = reinterpret_cast<const uint4*>(p.c.open_v) + (size_t)b * kKVHeads * (kKv8Block * 16);
+  int again_n[2] = {0, 0};  // heads whose K, V blocks are written again, listed
+  if (any) {
+#pragma unroll
+    for (int kv = 0; kv < 2; ++kv) {
+      const uint32_t set = __ballot_sync(0xffffffffu, lane < kKVHeads && s_top[kv][lane & 7] != 0);
+      again_n[kv] = __popc(set);  // (every warp writes the same list)
+      if ((set >> lane) & 1) s_list[kv][__popc(set & ((1u << lane) - 1))] = lane;
+    }
+    __syncthreads();  // (the flags are read before they grow)
+    // the old rows' largest magnitudes: (head, row, chunk) over the threads
+#pragma unroll
+    for (int kv = 0; kv < 2; ++kv) {
+      const uint4* old = kv ? open_v : open_k;
+#pragma unroll 2
+      for (int e = tid; e < again_n[kv] * 8 * row; e += kApThreads) {
+        const int h = s_list[kv][(e >> 3) / row];
+        const size_t at = ((size_t)h * kKv8Block + (e >> 3) % row) * 16 + (e & 7);
+        const uint32_t m = absmax4(absmax4(0u, old[at]), old[at + 8]);
+        atomicMax(&s_top[kv][h], max(m & 0xFFFFu, m >> 16));
+      }
+    }
+    __syncthreads();
+    if (again && k_all) ks = scale_of<kKind>(s_top[0][g]);
+    if (again && v_all) vs = scale_of<kKind>(s_top[1][g]);
+  }
+  if (id >= 0) {  // the new row
+    if (!k_all) ks = k_was;
+    if (!v_all) vs = v_was;
+    const float k_inv = ks > 0.f ? __fdiv_rn(1.f, ks) : 0.f, v_inv = vs > 0.f ? __fdiv_rn(1.f, vs) : 0.f;
+    if (lane == 0) {
+      if (k_all) p.c.k_scale[id] = ks;
+      if (v_all) p.c.v_scale[id] = vs;
+    }
+    const bool open = row + 1 < kKv8Block;
+    uint4* my_k = reinterpret_cast<uint4*>(p.c.open_k) + (head * kKv8Block + row) * 16;
+    uint4* my_v = reinterpret_cast<uint4*>(p.c.open_v) + (head * kKv8Block + row) * 16;
+    if (lane < 8) {
+      uint8_t* dst = static_cast<uint8_t*>(p.c.k_pool) + (size_t)id * kKv8Bytes + row * 64 + 8 * c;
+      *reinterpret_cast<uint2*>(dst) = codes8<kKind>(kx[0], k_inv);
+      *reinterpret_cast<uint2*>(dst + kKv8Bytes / 2) = codes8<kKind>(kx[1], k_inv);
+      if (open) my_k[c] = kx[0], my_k[c + 8] = kx[1];
+    } else if (lane < 24) {
+      uint8_t* dst = static_cast<uint8_t*>(p.c.v_pool) + (size_t)id * kKv8Bytes + (lane - 8) * 8 * kKv8Block + row;
+      const uint2 w = codes8<kKind>(vx, v_inv);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) dst[e * kKv8Block] = uint8_t((e < 4 ? w.x : w.y) >> (8 * (e & 3)));
+      if (open) my_v[lane - 8] = vx;
+    }
+  }
+  if (!any) return;
+  // the old rows' codes on the new scales
+#pragma unroll 2
+  for (int e = tid; e < again_n[0] * 8 * row; e += kApThreads) {
+    const int h = s_list[0][(e >> 3) / row], r = (e >> 3) % row, ch = e & 7;
+    const float scale = scale_of<kKind>(s_top[0][h]), inv = scale > 0.f ? __fdiv_rn(1.f, scale) : 0.f;
+    const size_t at = ((size_t)h * kKv8Block + r) * 16 + ch;
+    uint8_t* dst = static_cast<uint8_t*>(p.c.k_pool) + (size_t)s_id[h] * kKv8Bytes + r * 64 + 8 * ch;
+    *reinterpret_cast<uint2*>(dst) = codes8<kKind>(open_k[at], inv);
+    *reinterpret_cast<uint2*>(dst + kKv8Bytes / 2) = codes8<kKind>(open_k[at + 8], inv);
+  }
+  const int quads = (row + 3) / 4;  // four rows of a feature make one word of the feature's 64 bytes
+  for (int e = tid; e < again_n[1] * 16 * quads; e += kApThreads) {
+    const int h = s_list[1][(e >> 4) / quads], r0 = (e >> 4) % quads * 4, ch = e & 15;
+    const float scale = scale_of<kKind>(s_top[1][h]), inv = scale > 0.f ? __fdiv_rn(1.f, scale) : 0.f;
+    uint4 x[4];
+#pragma unroll
+    for (int m = 0; m < 4; ++m)
+      x[m] = r0 + m < row ? open_v[((size_t)h * kKv8Block + r0 + m) * 16 + ch] : make_uint4(0, 0, 0, 0);
+    uint8_t* dst = static_cast<uint8_t*>(p.c.v_pool) + (size_t)s_id[h] * kKv8Bytes + ch * 8 * kKv8Block + r0;
+#pragma unroll
+    for (int f = 0; f < 8; ++f, dst += kKv8Block) {
+      const uint32_t w = codes4<kKind>(bf16_at(x[0], f), bf16_at(x[1], f), bf16_at(x[2], f), bf16_at(x[3], f), inv);
+      if (r0 + 4 <= row) {
+        *reinterpret_cast<uint32_t*>(dst) = w;
+      } else {
+#pragma unroll
+        for (int m = 0; m < 3; ++m)
+          if (r0 + m < row) dst[m] = uint8_t(w >> (8 * m));
+      }
+    }
   }
 }
 
@@ -334,6 +488,12 @@ extern "C" grok_status grok_kv8_append(const grok_kv8_cache* cache, const grok_b
                    dev_status};
   // T tokens behind up to 63 open rows touch at most (T + 126) / 64 blocks
   const dim3 grid((T + 2 * kKv8Block - 2) / kKv8Block, kKVHeads, cache->B);
+  if (T == 1 && cache->B >= kApMany) {
+    auto one =
+        cache->kind == GROK_KV8_INT8 ? kv8_append_one_kernel<GROK_KV8_INT8> : kv8_append_one_kernel<GROK_KV8_E4M3>;
+    one<<<cache->B, kApThreads, 0, static_cast<cudaStream_t>(stream)>>>(p);
+    return check_launch("kv8_append_one");
+  }
   // CTAs with tokens, about: three on an SM at once with six heads, four with three
   const bool few = (long long)cache->B * ((T + kKv8Block - 1) / kKv8Block) * kKVHeads <= 3 * sms;
   auto kernel = cache->kind == GROK_KV8_INT8
