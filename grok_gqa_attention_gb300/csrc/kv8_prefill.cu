@@ -168,11 +168,20 @@ size_t up256(size_t n) { return (n + 255) & ~size_t(255); }
 
 // Calls of up to this many tokens run on the codes (kv8_decode.cu, four tokens to a pass): no copies of the cache, and
 // the split over the key range that single tokens have. Above, the copies cost less than the passes. Measured, us, codes
-// against copies: 1 sequence behind 300 rows 10 against 17 for 4 tokens, 11.5 against 18 for 32; 1 behind 16000 21
-// against 78 for 4, 66 against 78 for 32, 85 against 78 for 48; 8 behind 8000 41 against 256 for 4, 226 against 257 for
-// 32, 326 against 257 for 48; 32 behind 4000 239 against 518 for 16, 457 against 521 for 32; 32 behind 300 43 against 74
-// for 16, 88 against 80 for 32; 256 behind 1000 658 against 1024 for 16, 1387 against 1097 for 32.
-int few_tokens(int B) { return B <= 8 ? 32 : 20; }
+// against copies:
+//   1 sequence behind 16000 rows: 4 tokens 21 against 78, 32 66 against 78, 48 85 against 78
+//   8 behind 8000: 4 41 against 256, 32 226 against 257, 48 326 against 257
+//   32 behind 4000: 16 239 against 518; 256 behind 1000: 16 658 against 1024; 64 behind 100: 16 62 against 68, 20 82
+//   against 68; 32 behind 300: 16 43 against 74, 32 88 against 80
+//   small caches of one or two sequences, where the copies' four launches are most of the time: 1 behind 300, 4 10
+//   against 17, 96 15 against 19, 128 20 against 20; 1 behind 2000, 96 34 against 35; 2 behind 1000, 48 23 against 30
+//   caches of one key tile, which need two launches: 8 sequences behind 20 rows, 12 12 against 14, 20 15 against 14.5;
+//   1 behind 20, 4 10.2 against 9.1
+int few_tokens(int B, int max_blocks) {
+  if (max_blocks * kKv8Block <= kPfKeys) return 12;
+  if (B <= 2 && B * max_blocks <= 36) return 96 / B;
+  return B <= 8 ? 32 : 16;
+}
 
 // Workspace: fallback count and list, K scales, output factors, the copies of K and V, the split's area.
 struct Layout {
@@ -190,7 +199,7 @@ Layout layout(int B, int max_blocks, int sms) {
   w.v_copy = w.k_copy + copy;
   w.split = w.v_copy + copy;
   w.bytes = w.split + (split_allowed(w.rows) ? split_area_bytes(sms) : 0);
-  w.bytes = std::max(w.bytes, kv8_decode_bytes(B, few_tokens(B), max_blocks, false, sms));
+  w.bytes = std::max(w.bytes, kv8_decode_bytes(B, few_tokens(B, max_blocks), max_blocks, false, sms));
   return w;
 }
 
@@ -236,7 +245,7 @@ extern "C" grok_status grok_kv8_prefill(const grok_kv8_cache* cache, const grok_
   if (workspace_bytes < w.bytes)
     return fail(GROK_ERR_INVALID_ARG, "grok_kv8_prefill: workspace of %zu bytes is smaller than the %zu needed",
                 workspace_bytes, w.bytes);
-  if (T <= few_tokens(B))
+  if (T <= few_tokens(B, max_blocks))
     return kv8_decode_run(*cache, q_rot, cache_len, valid_len, T, static_cast<char*>(workspace), out, nullptr, nullptr, sms,
                           dev_status, static_cast<cudaStream_t>(stream));
   char* ws = static_cast<char*>(workspace);

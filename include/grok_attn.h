@@ -649,10 +649,11 @@ grok_status grok_kv8_decode(const grok_kv8_cache* cache, const grok_bf16* q_rot,
  * valid_len[b] outside [1, T] sets GROK_DEV_BAD_VALID, cache_len[b] < 0 or
  * cache_len[b] + valid_len[b] > max_blocks * 64 GROK_DEV_BAD_KV_LEN; the sequence's
  * outputs are left as they were.
- * T <= 20, or B <= 8 and T <= 32: as grok_kv8_decode, from the codes. More: the rows are first copied to the workspace, K codes as bf16 (exact), V as fp16
- * on a common scale per sequence and head (2^-11 relative for values down to
- * 2^-28 of the head's largest); softmax weights are rounded to fp16 as in
- * grok_attn_prefill_ws. Items whose weights leave fp16's range are recomputed with
+ * Short calls (up to 12 to 96 tokens, by B and max_blocks) run as grok_kv8_decode,
+ * from the codes. For others the rows are first copied to the workspace, K codes as
+ * bf16 (exact), V as fp16 on a common scale per sequence and head (2^-11 relative for
+ * values down to 2^-28 of the head's largest); softmax weights are rounded to fp16 as
+ * in grok_attn_prefill_ws. Items whose weights leave fp16's range are recomputed with
  * bf16 hi + lo weights and V rounded to bf16.
  *   workspace: device memory, 256-byte aligned, of at least
  *   grok_kv8_prefill_workspace(B, max_blocks) bytes for the current device (4 KB

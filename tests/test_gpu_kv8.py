@@ -585,8 +585,12 @@ PREFILLS = {
     # the longest call that runs as single tokens, and the shortest that does not
     "last_few": ([2500, 63, 120], [32, 4, 17], 32),
     "first_many": ([2500, 63, 120], [33, 4, 17], 33),
-    "last_few_of_nine": (list(range(40, 400, 40)), [20, 1, 2, 3, 4, 5, 17, 19, 20], 20),
-    "first_many_of_nine": (list(range(40, 400, 40)), [21, 1, 2, 3, 4, 5, 17, 19, 20], 21),
+    "last_few_of_nine": (list(range(40, 400, 40)), [16, 1, 2, 3, 4, 5, 11, 15, 16], 16),
+    "first_many_of_nine": (list(range(40, 400, 40)), [17, 1, 2, 3, 4, 5, 11, 15, 16], 17),
+    "last_few_of_one": ([700], [95], 96),
+    "first_many_of_one": ([700], [96], 97),
+    "last_few_of_one_tile": ([100, 1], [12, 5], 12),
+    "first_many_of_one_tile": ([100, 1], [13, 5], 13),
     "few_over_many_shares": ([9000, 60, 0, 7000], [5, 7, 1, 2], 7),
     "few_over_many_sequences": (list(range(0, 320, 5)), [1 + i % 3 for i in range(64)], 3),
 }
@@ -798,7 +802,7 @@ def test_prefill_split_items_of_good_and_bad_sequences():
     assert status == G.DEV_BAD_KV_LEN and (got == 7.0).all()
 
 
-@pytest.mark.parametrize("T", [28, 40])  # on the codes, over the copies
+@pytest.mark.parametrize("T", [28, 40])
 def test_prefill_bad_integers_leave_the_outputs(T):
     rng = np.random.default_rng(45)
     cache, host = filled(rng, [128] * 3, "int8", 2, seed=35)
