@@ -57,14 +57,27 @@
 // 16 keys instead of two, with V read as fp16 from a copy in the caller's
 // workspace (both operands of a kind::f16 product have one type). fp16's
 // exponent range cannot hold weights relative to the fixed reference 30, so
-// each row takes its own reference from its item's first key tile: the two
-// warps of a quadrant exchange their 64-key maxima once per item, and
-// m = 30 log2(e) tanh(y_max) + 8 (log2 units) puts the row's largest weight of
-// that tile at 2^-8. Later tiles whose logits rise above it by up to 2^24
-// (about 16.6 on the capped-logit scale) still fit fp16; a row whose weight sum
-// reaches 65504 (or any non-finite sum) puts its item on a fallback list in the
-// workspace, and so does every item of a sequence whose V does not fit fp16.
-// The bf16 mode of this kernel then recomputes exactly the listed items.
+// each row takes its own reference, from the largest logit y_max of a sample of
+// its keys: the item's first key tile and, from 16 tiles on, about one in 32 of the
+// others. (Their Q K^T comes ahead of the first tile's, for the maximum alone;
+// they are staged in the V ring, which is idle then.) The two warps of a quadrant
+// exchange their maxima once per item.
+//   m = 30 log2(e) tanh(y_max) - log2(n) + 15 (log2 units), n the row's keys
+// rounded up to a power of two, 128 at least, puts the sample's largest weight at
+// n 2^-15. A weight below fp16's normal range (2^-14) is off by 2^-25 at most, so
+// n of them are off by n 2^-25, which is 2^-10 of the row's sum at most: a row whose
+// sum is thousands of small weights beside a few large ones keeps them. (With the
+// first tile's largest weight at 2^-8 for every n, outputs of such rows are off by up
+// to 2 % of V with 8192 keys and 20 % with 65536.) Keys whose weights rise above
+// the sample's by more than 2^31 / n (2^18 for 8192 keys, 12.5 on the capped-logit
+// scale) overflow fp16. An infinite weight makes the outputs non-finite: such a
+// row puts its item on a fallback list in the workspace, and so does every item of a
+// sequence whose V does not fit fp16. The bf16 mode of this kernel then recomputes
+// exactly the listed items. Why a sample of that size: of normal logits with
+// deviation 6 to 9, up to 3 rows in 10^4 rise that far above 128 of their 8192 keys,
+// which lists one item in ten and takes 788 us where 649 are enough; above 384 of
+// them 3 in 10^7 do. The samples cost 1 % of 8192 tokens and 4 % of a chunk of 256
+// behind 6144 rows; bf16 weights throughout would cost 16 and 22 %.
 //
 // Split pass (kSplit, fp16 mode): when a call has fewer than two items per SM,
 // the items of the ragged last round run in a second launch, each shared among
@@ -91,7 +104,8 @@ constexpr int kQBytes = 2 * 2 * kBox;       // two heads, two 64-wide halves of 
 constexpr int kTileBytes = 2 * kBox;        // one K or V tile: two 64-wide halves of d
 constexpr int kPfData = kQBytes + 2 * kPfStages * kTileBytes;
 constexpr int kPfSeqCache = 512;  // sequences whose start / valid length are staged in shared memory
-constexpr float kPfHeadroom = 8.0f;  // fp16 mode: log2 gap between a row's reference and its first-tile maximum
+constexpr int kPfSampleTiles = 32;  // fp16 mode: a row's reference looks at one key tile in about this many, and the first
+constexpr int kPfLossBits = 15;     // fp16 mode: of n keys, the sample's largest weight is n 2^-15
 
 struct PfBars {
   uint64_t q_full, q_empty;
@@ -100,11 +114,11 @@ struct PfBars {
   uint64_t mma_done;
   uint64_t lsum_ready[2];  // both halves of a slot posted their partial row sums
   uint64_t epi_done[2];    // the slot's eight epilogue warps' output stores have read their staging
-  uint64_t xbar[2][4];     // fp16 mode: [slot][quad] both warps of a quadrant posted their first-tile maxima
+  uint64_t xbar[2][4];     // fp16 mode: [slot][quad] both warps of a quadrant posted their maxima
   uint64_t split_in[2];    // key-range split: the slot's eight epilogue warps wrote their unit's part
   uint64_t split_out[2];   // key-range split: the unit is counted (split_last is set)
   int split_last[2];       // key-range split: this unit is its item's last to finish (it adds the parts)
-  int split_over[2];       // key-range split: some row of this unit reached fp16's range
+  int split_over[2];       // key-range split: some row of this unit left fp16's range
   float xmax[2][4][2][32];   // [slot][quad][half][lane]
   float lsum[2][2][2][128];  // [item parity][slot][half][row]
   int seq_start[kPfSeqCache], seq_valid[kPfSeqCache], seq_vflag[kPfSeqCache];
@@ -149,6 +163,8 @@ struct PfItem {
   int kv_end;   // keys [0, kv_end) are visible to some row of the tile
   int n_kv;     // key tiles to visit from j0 (0: skip the unit)
   int n_sub;    // 64-key halves of those tiles that hold a visible key
+  int n_pk;     // fp16 mode: sampled key tiles besides the first
+  int pk_last;  // the last tile of the unit that every row sees whole
   int bad;      // GROK_DEV_* bits when the sequence's integers are invalid
   bool redirect;  // fp16 mode: the sequence's V does not fit fp16; the fallback pass computes the item
 };
@@ -194,6 +210,8 @@ __device__ __forceinline__ PfItem pf_item(const PfParams& p, const PfBars* bars,
   }
   it.bad = 0;
   it.redirect = false;
+  it.n_pk = 0;
+  it.pk_last = 0;
   if (kQ8) {  // (padding tokens are not in the cache)
     if (it.s < 0 || (long long)it.s + max(it.n, 0) > p.Tmax) it.bad |= GROK_DEV_BAD_KV_LEN;
   } else if (it.s < 0 || (long long)it.s + p.T > p.Tmax) {
@@ -232,8 +250,16 @@ __device__ __forceinline__ PfItem pf_item(const PfParams& p, const PfBars* bars,
     it.n_sub = min(2 * j1, it.n_sub) - 2 * j0;
     it.n_kv = j1 - j0;
   }
+  if (kF16) {
+    it.n_pk = (it.n_kv + kPfSampleTiles / 2) / kPfSampleTiles;
+    // (16 tiles and more, of which at most the last two are not seen whole by the item's first row)
+    it.pk_last = min((min(it.s + it.qt * kPfRows, it.s + it.n - 1) + 1) / kPfKeys - 1 - it.j0, it.n_kv - 1);
+  }
   return it;
 }
+
+// fp16 mode: the k-th sampled tile (k < n_pk), counted from the unit's first: evenly over tiles 1 .. pk_last.
+__device__ __forceinline__ int pf_sample_tile(int k, int n_pk, int pk_last) { return (k + 1) * pk_last / n_pk; }
 
 // Append an item to the fallback list (duplicates are harmless: the fallback
 // pass would compute the same bits twice).
@@ -443,6 +469,71 @@ __device__ __forceinline__ float pf_rowmax_half(uint32_t trow, int half, int rel
   return mx;
 }
 
+// The same, in the form that the warp's rows allow; over the 8-bit cache times the K scale of the half's block.
+template <bool kQ8>
+__device__ __forceinline__ float pf_sample_max(uint32_t trow, int half, int rel, float ks) {
+  const float m = __all_sync(0xffffffffu, rel >= 64 * half + 63) ? pf_rowmax_half<false>(trow, half, rel)
+                                                                 : pf_rowmax_half<true>(trow, half, rel);
+  return kQ8 && m != -INFINITY ? m * ks : m;
+}
+
+// fp16 mode: this row's reference (log2 units), from the sampled tiles and the unit's first tile; infinity when a bounded
+// wait gave up (of the whole warp, then). Every tile's two halves are read by the two warps of the quadrant, which exchange
+// their maxima. sub_cnt, xch_cnt: phases of s_full and xbar so far; lim: the row's last visible key.
+template <bool kSplit, bool kQ8>
+static __device__ __forceinline__ float pf_reference(const PfParams& p, PfBars* bars, int n_pk, int pk_last, int n_kv,
+                                                  int n_sub, int slot, int half, int quad, int lane, uint32_t trow,
+                                                  int lim, const float* k_scale, int sub_cnt, int xch_cnt) {
+  volatile int* abort = &bars->abort;
+  float mx = -INFINITY;  // largest raw logit
+  float ks = kQ8 ? __ldg(k_scale + 2 * (n_pk > 0 ? pf_sample_tile(0, n_pk, pk_last) : 0) + half) : 1.f;
+#pragma unroll 1
+  for (int k = 0; k <= n_pk; ++k, ++sub_cnt) {
+    const int j = k < n_pk ? pf_sample_tile(k, n_pk, pk_last) : 0;
+    const int next = k + 1 < n_pk ? pf_sample_tile(k + 1, n_pk, pk_last) : 0;
+    const float ks_next = kQ8 ? __ldg(k_scale + 2 * next + half) : 1.f;
+    if (!__all_sync(0xffffffffu, mbar_wait(&bars->s_full[slot][half], sub_cnt & 1, abort, p.status))) return INFINITY;
+    tc_fence_after();
+    mx = fmaxf(mx, pf_sample_max<kQ8>(trow, half, lim - j * kPfKeys, ks));
+    ks = ks_next;
+    if (k < n_pk) {
+      tc_fence_before();
+      mbar_arrive(&bars->p_full[slot][half]);  // S is read
+    }
+  }
+  if (n_sub >= 2) {
+    bars->xmax[slot][quad][half][lane] = mx;
+    mbar_arrive(&bars->xbar[slot][quad]);
+    if (!__all_sync(0xffffffffu, mbar_wait(&bars->xbar[slot][quad], xch_cnt & 1, abort, p.status))) return INFINITY;
+    mx = fmaxf(mx, bars->xmax[slot][quad][half ^ 1][lane]);
+  }
+  // Key 0 is visible to every row, so mx is finite, except in a split unit after an item's first: rows with no visible
+  // key in it (all their weights zero) keep a finite reference through the clamp.
+  const int keys = min(max(lim + 1, kPfKeys), n_kv * kPfKeys);  // of the row in this unit, about
+  return kT * tanh_approx((kSplit ? fmaxf(mx, -1.0e30f) : mx) * kY) + float(kPfLossBits - (32 - __clz(keys - 1)));
+}
+
+// Out of line for whole items: its registers stay out of the softmax loop's (8192 tokens: 651 us, 683 with the call
+// inlined). Inlined for the shorter units of the split pass, where the call costs more than that gives (4 x 256 tokens
+// behind 6144 rows of an 8-bit cache, both passes out of line: 193 us, both inlined: 191).
+template <bool kQ8>
+static __device__ __noinline__ float pf_reference_whole(const PfParams& p, PfBars* bars, int n_pk, int pk_last, int n_kv,
+                                                        int n_sub, int slot, int half, int quad, int lane,
+                                                        uint32_t trow, int lim, const float* k_scale, int sub_cnt,
+                                                        int xch_cnt) {
+  return pf_reference<false, kQ8>(p, bars, n_pk, pk_last, n_kv, n_sub, slot, half, quad, lane, trow, lim, k_scale, sub_cnt,
+                                  xch_cnt);
+}
+
+// fp16 mode: a weight of the row left fp16's range. A weight beyond it is at least 65504, as then the row sum is, and is
+// infinite in P, which makes every output of the row infinite or NaN (o: any one of them). A NaN sum comes from NaN
+// logits, which the bf16 pass treats as it should; over the 8-bit cache it is a block without finite values, which
+// another pass would not mend.
+template <bool kQ8>
+__device__ __forceinline__ bool pf_over(float lt, uint32_t o) {
+  return (lt >= 65504.0f && !(fabsf(__uint_as_float(o)) < INFINITY)) || (!kQ8 && lt != lt);
+}
+
 // Split-pass epilogue of one epilogue warp (slot, half, quad) for a unit whose
 // item is shared among `parts` units: the unit's unnormalised O (the warp's 32
 // rows x 64 features) and, from half 0, the rows' sums and references go to
@@ -453,16 +544,18 @@ __device__ __forceinline__ float pf_rowmax_half(uint32_t trow, int half, int rel
 // gave up. Out of line: its registers stay out of the softmax loop's.
 static __device__ __noinline__ int pf_split_epilogue(const PfParams& p, PfBars* bars, volatile int* abort, int unit,
                                               int item, int parts, int slot, int half, int quad, int lane,
-                                              uint32_t trow, float lt, float mref, float o_scale, bool over,
-                                              uint8_t* stage, uint32_t parity) {
+                                              uint32_t trow, float lt, float mref, float o_scale, uint8_t* stage,
+                                              uint32_t parity) {
   const int r = quad * 32 + lane;
   const size_t su = size_t(unit) * 2 + slot;
   float4* po = p.part_o + (su * 2 + half) * (16 * kPfRows) + r;
+  bool over = false;  // of the warp's rows
 #pragma unroll
   for (int cc = 0; cc < 2; ++cc) {
     uint32_t ov[32];
     tmem_ld32(trow + 128 + half * 64 + cc * 32, ov);
     tmem_wait_ld_dep(ov);
+    if (cc == 0) over = __any_sync(0xffffffffu, pf_over<false>(lt, ov[0]));
 #pragma unroll
     for (int q = 0; q < 8; ++q)
       po[(cc * 8 + q) * kPfRows] = make_float4(__uint_as_float(ov[4 * q]), __uint_as_float(ov[4 * q + 1]),
@@ -617,7 +710,20 @@ __global__ void __launch_bounds__(kPfThreads, 1)
   if (warp == 0) {
     // ------------------------------------------------------------ TMA producer
     if (lane == 0) {
-      int kv_it = 0, q_it = 0;
+      uint32_t k_it = 0, v_it = 0, q_it = 0;  // tiles loaded into the K and V rings, Q tiles
+      // key tile t of the unit into a ring (sampled tiles take the V ring, which is idle until the first tile's P is
+      // there); krow, kb: where it lies
+      auto load_k = [&](const PfItem& it, int t, uint8_t* ring, uint64_t* full, uint64_t* empty, uint32_t& n, int& krow,
+                        int& kb) {
+        const uint32_t st = n % kPfStages;
+        if (!mbar_wait(&empty[st], ((n / kPfStages) & 1) ^ 1, abort, p.status)) return false;
+        kv_coord(p.pm, it.b, (it.j0 + t) * kPfKeys, krow, kb, p.status);  // a tile is one page when paged
+        mbar_arrive_expect_tx(&full[st], kTileBytes);
+        tma_load_4d(ring + st * kTileBytes, &tm_k, &full[st], 0, it.g, krow, kb);
+        tma_load_4d(ring + st * kTileBytes + kBox, &tm_k, &full[st], 64, it.g, krow, kb);
+        ++n;
+        return true;
+      };
       for (int rd = 0, item; (item = pf_item_index<kList>(p, rd)) >= 0; ++rd) {
         const PfItem it = pf_item<kF16, kSplit, kQ8>(p, bars, item);
         if (it.n_kv == 0) continue;
@@ -631,19 +737,17 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         ++q_it;
         if (kQ8 && !kList && q_it == 1) asm volatile("griddepcontrol.wait;" ::: "memory");
         bool ok = true;
-        for (int j = 0; j < it.n_kv; ++j, ++kv_it) {
-          const int st = kv_it % kPfStages;
-          const uint32_t par = ((kv_it / kPfStages) & 1) ^ 1;
-          if (!mbar_wait(&bars->k_empty[st], par, abort, p.status)) {
-            ok = false;
-            break;
-          }
-          int krow, kb;
-          kv_coord(p.pm, it.b, (it.j0 + j) * kPfKeys, krow, kb, p.status);  // a tile is one page when paged
-          mbar_arrive_expect_tx(&bars->k_full[st], kTileBytes);
-          tma_load_4d(sK + st * kTileBytes, &tm_k, &bars->k_full[st], 0, it.g, krow, kb);
-          tma_load_4d(sK + st * kTileBytes + kBox, &tm_k, &bars->k_full[st], 64, it.g, krow, kb);
-          if (!mbar_wait(&bars->v_empty[st], par, abort, p.status)) {
+        int krow = 0, kb = 0;
+        // (A ring has one free stage while the item before is in its epilogue: the first key tile goes ahead of the
+        // second sample.)
+        for (int k = 0; kF16 && ok && k < it.n_pk; ++k)
+          ok = load_k(it, pf_sample_tile(k, it.n_pk, it.pk_last), sV, bars->v_full, bars->v_empty, v_it, krow, kb) &&
+               (k > 0 || load_k(it, 0, sK, bars->k_full, bars->k_empty, k_it, krow, kb));
+        for (int j = 0; ok && j < it.n_kv; ++j, ++v_it) {
+          const uint32_t st = v_it % kPfStages;
+          if (((!kF16 || j > 0 || it.n_pk == 0) &&
+               !load_k(it, j, sK, bars->k_full, bars->k_empty, k_it, krow, kb)) ||
+              !mbar_wait(&bars->v_empty[st], ((v_it / kPfStages) & 1) ^ 1, abort, p.status)) {
             ok = false;
             break;
           }
@@ -658,10 +762,10 @@ __global__ void __launch_bounds__(kPfThreads, 1)
       }
       // Drain: copies still in flight (only after an abort) land before the CTA exits.
       volatile int never = 0;
-      for (int t = max(0, kv_it - kPfStages); t < kv_it; ++t) {
+      for (uint32_t t = k_it - min(k_it, uint32_t(kPfStages)); t < k_it; ++t)
         mbar_wait(&bars->k_full[t % kPfStages], (t / kPfStages) & 1, &never, p.status);
+      for (uint32_t t = v_it - min(v_it, uint32_t(kPfStages)); t < v_it; ++t)
         mbar_wait(&bars->v_full[t % kPfStages], (t / kPfStages) & 1, &never, p.status);
-      }
       if (q_it > 0) mbar_wait(&bars->q_full, (q_it - 1) & 1, &never, p.status);
     }
   } else if (warp == 1 || warp == 18) {
@@ -674,16 +778,37 @@ __global__ void __launch_bounds__(kPfThreads, 1)
     const uint64_t qd = make_sdesc_sw128(smem_u32(sQ), 16, 1024) + slot * kQSlotDesc;
     const uint64_t kd = make_sdesc_sw128(smem_u32(sK), 16, 1024);
     const uint64_t vd = make_sdesc_sw128(smem_u32(sV), kBox, 1024);
-    int kv_it = 0, q_it = 0, item_it = 0;
-    int pc0 = 0, pc1 = 0;  // P hand-overs consumed per half (p_full parity)
+    const uint64_t pd = make_sdesc_sw128(smem_u32(sV), 16, 1024);  // a sampled K tile in the V ring
+    uint32_t k_it = 0, v_it = 0, q_it = 0, item_it = 0;  // tiles of the K and V rings before this item
+    uint32_t pc0 = 0, pc1 = 0;  // P hand-overs consumed per half (p_full parity)
     bool ok = true;
     for (int rd = 0, item; ok && (item = pf_item_index<kList>(p, rd)) >= 0; ++rd) {
       const PfItem it = pf_item<kF16, kSplit, kQ8>(p, bars, item);
       if (it.n_kv == 0) continue;
       if (!__all_sync(0xffffffffu, mbar_wait(&bars->q_full, q_it & 1, abort, p.status))) break;
+      // The sampled tiles' logits, which the softmax warps read for their maximum and hand back as they do P.
+      for (int k = 0; kF16 && k < it.n_pk; ++k, ++v_it) {
+        const uint32_t st = v_it % kPfStages;
+        ok = __all_sync(0xffffffffu, mbar_wait(&bars->v_full[st], (v_it / kPfStages) & 1, abort, p.status));
+        if (!ok) break;
+        tc_fence_after();
+        if (leader) {
+          pf_issue_qk(s_tm, qd, pd + st * kStageDesc);
+          umma_commit(&bars->s_full[slot][0]);
+          umma_commit(&bars->s_full[slot][1]);
+          umma_commit(&bars->v_empty[st]);
+        }
+        __syncwarp();
+        ok = __all_sync(0xffffffffu, mbar_wait(&bars->p_full[slot][0], pc0 & 1, abort, p.status) &&
+                                         mbar_wait(&bars->p_full[slot][1], pc1 & 1, abort, p.status));
+        if (!ok) break;
+        ++pc0;
+        ++pc1;
+      }
+      if (!ok) break;
       {
-        const int st = kv_it % kPfStages;
-        if (!__all_sync(0xffffffffu, mbar_wait(&bars->k_full[st], (kv_it / kPfStages) & 1, abort, p.status))) break;
+        const uint32_t st = k_it % kPfStages;
+        if (!__all_sync(0xffffffffu, mbar_wait(&bars->k_full[st], (k_it / kPfStages) & 1, abort, p.status))) break;
         tc_fence_after();
         if (leader) {
           if (it.n_sub >= 2)
@@ -699,31 +824,31 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         }
         __syncwarp();
         // The first tile's other inputs, waited while that product runs.
-        const bool w = mbar_wait(&bars->v_full[st], (kv_it / kPfStages) & 1, abort, p.status) &&
-                       (it.n_sub <= 2 || mbar_wait(&bars->k_full[(kv_it + 1) % kPfStages], ((kv_it + 1) / kPfStages) & 1, abort, p.status)) &&
+        const bool w = mbar_wait(&bars->v_full[v_it % kPfStages], (v_it / kPfStages) & 1, abort, p.status) &&
+                       (it.n_sub <= 2 || mbar_wait(&bars->k_full[(k_it + 1) % kPfStages], ((k_it + 1) / kPfStages) & 1, abort, p.status)) &&
                        mbar_wait(&bars->o_empty[slot], (item_it & 1) ^ 1, abort, p.status);
         if (!__all_sync(0xffffffffu, w)) break;
       }
       for (int u = 0; u < it.n_sub; ++u) {
         const int h = u & 1, j = u >> 1;
-        const int cur = kv_it + j;
-        const int st = cur % kPfStages, stn = (cur + 1) % kPfStages;
+        const uint32_t vst = (v_it + j) % kPfStages, vstn = (v_it + j + 1) % kPfStages;  // V of this tile and the next
+        const uint32_t kst = (k_it + j) % kPfStages, kstn = (k_it + j + 1) % kPfStages;
         const bool qk_next = u + 2 < it.n_sub;
         const bool tile_end = h == 1 || u == it.n_sub - 1;
         // V of tile j and K of tile j + 1 were waited for earlier (item start or
         // the middle of the previous tile's second step); only P is waited here.
-        if (!__all_sync(0xffffffffu, mbar_wait(&bars->p_full[slot][h], uint32_t(h ? pc1 : pc0) & 1, abort, p.status))) {
+        if (!__all_sync(0xffffffffu, mbar_wait(&bars->p_full[slot][h], (h ? pc1 : pc0) & 1, abort, p.status))) {
           ok = false;
           break;
         }
         if (h) ++pc1; else ++pc0;
         tc_fence_after();
-        if (leader) pf_issue_pv_half<kF16>(o_tm, s_tm, vd + st * kStageDesc, h, u > 0);
+        if (leader) pf_issue_pv_half<kF16>(o_tm, s_tm, vd + vst * kStageDesc, h, u > 0);
         __syncwarp();
         if (h == 1 && u + 1 < it.n_sub) {
           // inputs of the next tile's steps: its V and the K after it
-          const bool w = mbar_wait(&bars->v_full[stn], ((cur + 1) / kPfStages) & 1, abort, p.status) &&
-                         (u + 3 >= it.n_sub || mbar_wait(&bars->k_full[st], ((cur + 2) / kPfStages) & 1, abort, p.status));
+          const bool w = mbar_wait(&bars->v_full[vstn], ((v_it + j + 1) / kPfStages) & 1, abort, p.status) &&
+                         (u + 3 >= it.n_sub || mbar_wait(&bars->k_full[kst], ((k_it + j + 2) / kPfStages) & 1, abort, p.status));
           if (!__all_sync(0xffffffffu, w)) {
             ok = false;
             break;
@@ -732,21 +857,22 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         }
         if (leader) {
           if (qk_next) {
-            pf_issue_qk_half(s_tm + 64 * h, qd, kd + stn * kStageDesc + uint64_t((8192 * h) >> 4));
+            pf_issue_qk_half(s_tm + 64 * h, qd, kd + kstn * kStageDesc + uint64_t((8192 * h) >> 4));
             umma_commit(&bars->s_full[slot][h]);
             // The item's last Q K^T: the producer may load the next item's Q
             // while the remaining P V products and the epilogue run.
             if (u + 3 == it.n_sub) umma_commit(&bars->q_empty);
           }
           if (tile_end && j + 1 < it.n_kv) {  // not the item's last tile
-            umma_commit(&bars->v_empty[st]);
-            if (j + 2 < it.n_kv) umma_commit(&bars->k_empty[stn]);
+            umma_commit(&bars->v_empty[vst]);
+            if (j + 2 < it.n_kv) umma_commit(&bars->k_empty[kstn]);
           }
           if (u == it.n_sub - 1) umma_commit(&bars->o_full[slot]);
         }
         __syncwarp();
       }
-      kv_it += it.n_kv;
+      k_it += it.n_kv;
+      v_it += it.n_kv;
       ++q_it;
       ++item_it;
     }
@@ -762,7 +888,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
     const int quad = warp & 3;                 // TMEM lane quadrant of this warp
     const int r = quad * 32 + lane;            // query row within the tile
     const uint32_t trow = tmem + (uint32_t(quad * 32) << 16) + slot * 256;
-    int tile_cnt = 0, item_it = 0, sub_cnt = 0, xch_cnt = 0, split_cnt = 0;
+    int tile_cnt = 0, pk_cnt = 0, item_it = 0, sub_cnt = 0, xch_cnt = 0, split_cnt = 0;  // (tiles, sampled tiles so far)
     if (kQ8 && !kList) asm volatile("griddepcontrol.wait;" ::: "memory");
     for (int rd = 0, item; (item = pf_item_index<kList>(p, rd)) >= 0; ++rd) {
       const PfItem it = pf_item<kF16, kSplit, kQ8>(p, bars, item);
@@ -780,6 +906,16 @@ __global__ void __launch_bounds__(kPfThreads, 1)
       float l0 = 0.f, l1 = 0.f;
       float mref = kT;  // bf16 mode: the fixed reference logit 30 (30 log2(e) in log2 units)
       bool ok = true;
+      if (kF16 && half < it.n_sub) {
+        mref = kSplit ? pf_reference<true, kQ8>(p, bars, it.n_pk, it.pk_last, it.n_kv, it.n_sub, slot, half, quad, lane,
+                                                trow, lim, k_scale, sub_cnt, xch_cnt)
+                      : pf_reference_whole<kQ8>(p, bars, it.n_pk, it.pk_last, it.n_kv, it.n_sub, slot, half, quad, lane,
+                                                trow, lim, k_scale, sub_cnt, xch_cnt);
+        if (mref == INFINITY) break;
+        sub_cnt += it.n_pk;
+        xch_cnt += it.n_sub >= 2;
+      }
+      pk_cnt += it.n_pk;
       for (int u = half; u < it.n_sub; u += 2) {
         const int j = u >> 1;
         const float ks = kQ8 ? __ldg(k_scale + u) : 1.f;  // (block 2 j + half: arrives while the products run)
@@ -796,26 +932,6 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         const bool unmasked = __all_sync(0xffffffffu, rel >= 64 * half + 63);
         // (a block that holds a NaN has a NaN scale; the exp2 polynomial may lose it)
         if (kQ8 && rel >= 64 * half) l0 = fmaf(ks, 0.f, l0);
-        if (kF16 && j == 0) {
-          // fp16 mode: the row's reference from the unit's first tile (both halves)
-          float mx = unmasked ? pf_rowmax_half<false>(trow, half, rel) : pf_rowmax_half<true>(trow, half, rel);
-          if (kQ8 && mx != -INFINITY) mx *= ks;
-          if (it.n_sub >= 2) {
-            bars->xmax[slot][quad][half][lane] = mx;
-            mbar_arrive(&bars->xbar[slot][quad]);
-            const bool w = mbar_wait(&bars->xbar[slot][quad], xch_cnt & 1, abort, p.status);
-            ++xch_cnt;
-            if (!__all_sync(0xffffffffu, w)) {
-              ok = false;
-              break;
-            }
-            mx = fmaxf(mx, bars->xmax[slot][quad][half ^ 1][lane]);
-          }
-          // Key 0 is visible to every row, so mx is finite, except in a split
-          // unit after an item's first: rows with no visible key in it (all
-          // their weights zero) keep a finite reference through the clamp.
-          mref = kT * tanh_approx((kSplit ? fmaxf(mx, -1.0e30f) : mx) * kY) + kPfHeadroom;
-        }
         if (unmasked)
           pf_softmax_half<false, kF16, kQ8>(trow, half, rel, mref, ks, l0, l1);
         else
@@ -866,23 +982,21 @@ __global__ void __launch_bounds__(kPfThreads, 1)
       tc_fence_after();
       const float lt = bars->lsum[item_it & 1][slot][0][r] + bars->lsum[item_it & 1][slot][1][r];
       const int h = it.g * kGroup + it.hp * 2 + slot;
-      const int st_last = (tile_cnt - 1) % kPfStages;
-      uint8_t* stage = (slot == 0 ? sK : sV) + st_last * kTileBytes + half * kBox;
+      const int k_last = (tile_cnt - 1) % kPfStages, v_last = (tile_cnt + pk_cnt - 1) % kPfStages;
+      uint8_t* stage = (slot == 0 ? sK + k_last * kTileBytes : sV + v_last * kTileBytes) + half * kBox;
       bool store = true;  // this warp's output rows are staged
       const float o_scale = kQ8 ? __ldg(p.o_scale + it.b * kKVHeads + it.g) : 1.f;
-      // (8-bit cache: a NaN sum is a block without finite values, which another pass would not mend)
-      const bool over = kQ8 ? lt >= 65504.0f : !(lt < 65504.0f);
       if (!kSplit || it.parts == 1) {
-        // fp16 mode: a weight sum that reached fp16's range means some weight may
-        // have overflowed: the fallback pass recomputes the item (a half-0 warp
-        // of each quadrant reports; duplicates are harmless)
-        if (kF16 && half == 0 && __any_sync(0xffffffffu, over) && lane == 0) pf_fallback(p, it.item);
         const float inv_l = (kQ8 ? o_scale : 1.0f) / lt;
 #pragma unroll
         for (int cc = 0; cc < 2; ++cc) {
           uint32_t ov[32];
           tmem_ld32(trow + 128 + half * 64 + cc * 32, ov);
           tmem_wait_ld_dep(ov);
+          // fp16 mode: the fallback pass recomputes the item of a row that overflowed
+          // (a half-0 warp of each quadrant reports; duplicates are harmless)
+          if (kF16 && cc == 0 && half == 0 && __any_sync(0xffffffffu, pf_over<kQ8>(lt, ov[0])) && lane == 0)
+            pf_fallback(p, it.item);
           uint32_t pk[16];
 #pragma unroll
           for (int e = 0; e < 16; ++e)
@@ -900,11 +1014,13 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         // the unit's part; a kernel of its own adds the parts (prefill_join_kernel)
         const size_t su = size_t(item) * 2 + slot;
         float4* po = p.part_o + (su * 2 + half) * (16 * kPfRows) + r;
+        bool over = false;
 #pragma unroll
         for (int cc = 0; cc < 2; ++cc) {
           uint32_t ov[32];
           tmem_ld32(trow + 128 + half * 64 + cc * 32, ov);
           tmem_wait_ld_dep(ov);
+          if (cc == 0) over = __any_sync(0xffffffffu, pf_over<true>(lt, ov[0]));
 #pragma unroll
           for (int q = 0; q < 8; ++q)
             po[(cc * 8 + q) * kPfRows] = make_float4(__uint_as_float(ov[4 * q]), __uint_as_float(ov[4 * q + 1]),
@@ -913,15 +1029,14 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         if (half == 0) p.part_lm[su * kPfRows + r] = make_float2(lt, mref);
         tc_fence_before();
         mbar_arrive(&bars->o_empty[slot]);
-        if (__any_sync(0xffffffffu, over) && half == 0 && lane == 0 &&
+        if (over && half == 0 && lane == 0 &&
             atomicExch(p.part_cnt + (it.item - p.item_base) * 2, 1) == 0)
           pf_fallback(p, it.item);  // once per item
         store = false;
       } else {
         const int res =
             pf_split_epilogue(p, bars, abort, item, it.item - p.item_base, it.parts, slot, half, quad, lane, trow, lt,
-                              mref, o_scale, __any_sync(0xffffffffu, over), stage,
-                              uint32_t(split_cnt & 1));
+                              mref, o_scale, stage, uint32_t(split_cnt & 1));
         ++split_cnt;
         if (!__all_sync(0xffffffffu, res >= 0)) break;
         store = res > 0;
@@ -941,8 +1056,8 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         // one hand-back from each slot).
         if (half == 0 && quad == 2) {
           if (mbar_wait(&bars->epi_done[slot], item_it & 1, abort, p.status)) {
-            mbar_arrive(&bars->k_empty[st_last]);
-            mbar_arrive(&bars->v_empty[st_last]);
+            mbar_arrive(&bars->k_empty[k_last]);
+            mbar_arrive(&bars->v_empty[v_last]);
           }
         }
       }

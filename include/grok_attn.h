@@ -191,12 +191,15 @@ grok_status grok_attn_prefill(const grok_bf16* q_rot, const grok_bf16* cache_k, 
  * grok_attn_prefill; ch. 4 §4.5.3 casts the softmax weights to the value dtype
  * before the weighted sum, which this call does in fp16 instead of bf16, so
  * each P V product runs once instead of twice). Each row's weights are taken
- * relative to a reference set from its first key tile (its largest weight
- * there is 2^-8) and rounded once to fp16; V is read from an fp16 copy that
+ * relative to a reference set from a sample of its keys and rounded once to fp16:
+ * 2^-11 relative for weights down to 2^-14, an absolute 2^-25 below, where the
+ * sample's largest weight is n 2^-15, n the row's keys rounded up to a power of
+ * two (128 at least). All small weights of a row together are off by 2^-10 of its
+ * sum at most. V is read from an fp16 copy that
  * the call first writes into `workspace` (rows [0, start_pos[b] + T) of each
  * sequence rounded to nearest fp16, then zeros to the next multiple of 128).
- * Items (128 query rows x 2 heads) whose weights could leave fp16's range (a
- * row's weight sum reaching 65504), and every item of a sequence holding a
+ * Items (128 query rows x 2 heads) with a weight beyond fp16's range (2^31 / n
+ * times the sample's largest), and every item of a sequence holding a
  * finite |v| >= 65520, are listed in the workspace and recomputed by a second
  * pass with bf16 weights from the bf16 cache, so every finite input is
  * handled; results then equal grok_attn_prefill's for those items.
@@ -652,9 +655,10 @@ grok_status grok_kv8_decode(const grok_kv8_cache* cache, const grok_bf16* q_rot,
  * Short calls (up to 12 to 96 tokens, by B and max_blocks) run as grok_kv8_decode,
  * from the codes. For others the rows are first copied to the workspace, K codes as
  * bf16 (exact), V as fp16 on a common scale per sequence and head (2^-11 relative for
- * values down to 2^-28 of the head's largest); softmax weights are rounded to fp16 as
- * in grok_attn_prefill_ws. Items whose weights leave fp16's range are recomputed with
- * bf16 hi + lo weights and V rounded to bf16.
+ * values down to 2^-28 of the head's largest, an absolute 2^-39 of it or less below);
+ * softmax weights are rounded to fp16 as in grok_attn_prefill_ws, small ones
+ * included. Items with a weight beyond fp16's range are recomputed with bf16 hi + lo
+ * weights and V rounded to bf16 (2^-8).
  *   workspace: device memory, 256-byte aligned, of at least
  *   grok_kv8_prefill_workspace(B, max_blocks) bytes for the current device (4 KB
  *   per row of the cache and sequence or, where it is more, 0.5 MB per sequence, and
