@@ -40,8 +40,10 @@
 // sequences behind 8000 rows 41.6 us (72 as four single ones), 32 tokens behind
 // 16000 rows 66 us; without four tokens to fill it a pass costs more than a single
 // token's (1 token, 300 rows: 9.8 us against 6.3).
-// P is rounded once to fp16 (2^-11 relative) against a running reference that may
-// lag the maximum by 2^8; l, the weights and O stay in fp32.
+// P is rounded once to fp16 against a running reference: the maximum puts P at 2^7
+// and may outgrow that by 2^8 before the reference follows it. A weight is off by
+// 2^-11 of itself, or where it is below 2^-21 of the largest by 2^-32 of that (2^-16
+// for 65536 of them). l, the weights and O stay in fp32.
 #include <algorithm>
 
 #include "host.cuh"
@@ -66,7 +68,8 @@ constexpr int kDqFewSmem = kDqFewWarps * (kDqRing + kDqFewQ) + kDqFewWarps * kDq
 static_assert(kDqCtas * (kDqFewSmem + 1024) <= 233472, "shared memory per SM");
 constexpr float kDqNone = -1.0e4f;  // reference of a column that has seen no key
 constexpr int kDqLong = 24;  // blocks per worker from which a second wave of small shares pays
-constexpr float kDqLag = 8.f;  // log2 units a weight may exceed the reference by
+constexpr float kDqTop = 7.f;  // log2 of the weight of the maximum that sets the reference
+constexpr float kDqLag = 15.f;  // log2 units that a weight may reach before the reference follows
 
 struct DqParams {
   grok_kv8_cache c;
@@ -424,7 +427,7 @@ __global__ void __launch_bounds__(kFew ? kDqFewThreads : kDqThreads, kDqCtas) kv
         }
         float &m0 = m[nt][0], &m1 = m[nt][1];
         if (__any_sync(0xffffffffu, top0 > m0 + kDqLag || top1 > m1 + kDqLag)) {
-          const float n0 = fmaxf(m0, top0), n1 = fmaxf(m1, top1);
+          const float n0 = fmaxf(m0, top0 - kDqTop), n1 = fmaxf(m1, top1 - kDqTop);
           const float c0 = ex2_approx(m0 - n0), c1 = ex2_approx(m1 - n1);
           m0 = n0, m1 = n1;
           l[nt][0] *= c0, l[nt][1] *= c1;

@@ -625,6 +625,8 @@ grok_status grok_kv8_append(const grok_kv8_cache* cache, const grok_bf16* q, con
  * over the 8-bit cache, in one call. The blocks of all sequences are dealt out
  * evenly to the GPU's warps, whatever the lengths; a sequence's bits depend on
  * the lengths in its batch through the places where its sums are split.
+ * Softmax weights are rounded to fp16 (2^-11 relative; weights below 2^-21 of the
+ * largest 2^-32 of that), sums, outputs' partial sums and block weights are fp32.
  *   q_rot, out [B,48,128]; kv_len [B] int32 in [1, max_blocks * 64] (else
  *   GROK_DEV_BAD_KV_LEN, and the sequence's outputs are left as they were).
  *   weight_out [B,8,max_blocks] fp32 or NULL: weight_out = weight_in + the

@@ -215,3 +215,46 @@ def test_prefill_ws(shape, paged, tail):
     K, V = k.double().numpy(), v.double().numpy()
     for g in (0, 7):
         check(got[0, rows, 6 * g:6 * g + 6], x[rows, 6 * g:6 * g + 6], K, V, start + rows, f"{shape} {tail}", 2.0 ** -11)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_kv8_decode_of_many_long_caches_keeps_the_smallest_weights(kind):
+    """256 sequences, so that a warp reads a head's whole range: one key 17.4 nats above 65535 equal ones, each 2^-25.1
+    of it, together 0.18 % of the sum. The 128 outputs' mean difference from the rounded exact ones shows what a bf16
+    step hides: without the small weights it is about -1.8e-3. The weights' own errors (tanh and exp2 at 3 * 87 * 2^-20,
+    a 128-term fp32 logit) move the large key's share by less than 2e-6; ten outputs next to a midpoint that round the
+    other way are 10 * 2^-8 / 128 = 3e-4."""
+    B, n = 256, 65536
+    rng = np.random.default_rng(9)
+    c = np.full(n, SINK - 17.4)
+    c[0] = SINK
+    x = raw(c) / (128 * MULT)
+    vp = 1.0 + rng.standard_normal((n, 128)) * 0.25
+    vp[0] = -1.0 + rng.standard_normal(128) * 0.25
+    top = kv8.TOP[kind]
+
+    def codes(y):
+        s = torch.from_numpy(np.abs(y).max((1, 2)) / top).float()
+        z = torch.from_numpy(y).float() / s[:, None, None]
+        return (torch.round(z).to(torch.int8) if kind == "int8" else z.to(torch.float8_e4m3fn)), s
+
+    xb = np.repeat(x.reshape(-1, 64, 1), 128, 2)
+    xb[0, 1:] = xb[1, 0]
+    kc, ks = codes(xb)
+    vc, vs = codes(vp.reshape(-1, 64, 128))
+    k1 = kc.view(torch.uint8).view(-1, 64, 2, 64).transpose(1, 2).contiguous().to(DEV)
+    v1 = vc.view(torch.uint8).transpose(1, 2).contiguous().to(DEV)
+    open_ = torch.zeros(B, 8, 64, 128, dtype=torch.bfloat16, device=DEV)
+    table = torch.arange(1024, dtype=torch.int32, device=DEV).expand(B, 8, 1024).contiguous()  # all share the blocks
+    cache = G.Kv8Cache(k1.view(DT[kind]), v1.view(DT[kind]), ks.to(DEV), vs.to(DEV), table, open_, open_.clone())
+    q = torch.ones(B, 48, 128, dtype=torch.bfloat16, device=DEV)  # (all heads alike)
+    out = torch.full_like(q, 7.0)
+    lens = torch.full((B,), n, dtype=torch.int32, device=DEV)
+    G.kv8_decode(cache, q, lens, G.alloc_kv8_decode_workspace(cache, False), out)
+    K = (kc.double() * ks.double()[:, None, None]).reshape(-1, 128).numpy()
+    V = (vc.double() * vs.double()[:, None, None]).reshape(-1, 128).numpy()
+    qx = bf16.to_f64(q[0].cpu().contiguous().view(torch.int16).numpy().view(np.uint16))
+    o, w = kv8.attend(qx, K, V)
+    assert 1.2e-3 < 1 - w[:, 0].min() < 2.5e-3
+    delta = (out.float().cpu().numpy().astype(np.float64) - bf16.to_f64(bf16.from_f64(o))[None]).mean()
+    assert abs(delta) < 3e-4, float(delta)
