@@ -45,6 +45,7 @@
 // 2^-11 of itself, or where it is below 2^-21 of the largest by 2^-32 of that (2^-16
 // for 65536 of them). l, the weights and O stay in fp32.
 #include <algorithm>
+#include <cfloat>
 
 #include "host.cuh"
 #include "kv8.cuh"
@@ -404,7 +405,10 @@ __global__ void __launch_bounds__(kFew ? kDqFewThreads : kDqThreads, kDqCtas) kv
       for (int nt = 0; nt < kTiles; ++nt) {
         float (&z)[4][4] = s[nt];
         // z = log2 of the weight against the fixed reference 30: -2 kT / (1 + e^(2 x / 30))
-        const float f0 = ks * q_scale[nt][0], f1 = ks * q_scale[nt][1];
+        // (a product beyond fp32 counts as its largest number: a score of zero stays zero, others are at the cap all the
+        // same; a NaN scale stays NaN)
+        float f0 = ks * q_scale[nt][0], f1 = ks * q_scale[nt][1];
+        f0 = f0 > FLT_MAX ? FLT_MAX : f0, f1 = f1 > FLT_MAX ? FLT_MAX : f1;
         // keys seen: a group's earlier tokens see fewer than its last
         const int keys0 = kFew ? keys - max(0, seen - 1 - (8 * nt + 2 * t) / kGroup) : keys;
         const int keys1 = kFew ? keys - max(0, seen - 1 - (8 * nt + 2 * t + 1) / kGroup) : keys;
