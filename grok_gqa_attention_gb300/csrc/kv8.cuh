@@ -19,7 +19,7 @@ __device__ __forceinline__ int kv8_blocks(int len, int max_blocks) {
 
 // A table entry; -1, reported, when it lies outside the pool.
 __device__ __forceinline__ int kv8_block_id(const int32_t* table, size_t at, int n_blocks, int32_t* status) {
-  const int id = __ldg(table + at);
+  const int id = table[at];
   if (id < 0 || id >= n_blocks) {
     report(status, GROK_DEV_BAD_PAGE);
     return -1;

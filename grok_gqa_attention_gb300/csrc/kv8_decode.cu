@@ -119,15 +119,17 @@ __device__ __forceinline__ uint32_t word_of(const uint4& x, int w) {
 
 __host__ __device__ __forceinline__ int groups_of(int tokens) { return (tokens + kDqTok - 1) / kDqTok; }
 
+// (This kernel starts beside the one before it, which may write any of its inputs: they are loaded behind the wait, and
+// not by the read-only path, which supposes that they stay as they are while the kernel runs.)
 // Rows that v's queries see: 0 when its sequence's integers are bad. kFew: those of
 // the group's last token (token i sees the rows before the call and the valid
 // tokens' up to its own). (A template: the choice at run time costs a call over
 // 300 rows 0.3 of its 6.2 us.)
 template <bool kFew>
 __device__ __forceinline__ int rows_of(const DqParams& p, int v) {
-  if (!kFew) return __ldg(p.kv_len + v);
+  if (!kFew) return p.kv_len[v];
   const int groups = groups_of(p.few_tokens), b = v / groups, first = v % groups * kDqTok;
-  const int s = __ldg(p.kv_len + b), n = p.valid_len ? __ldg(p.valid_len + b) : p.few_tokens;
+  const int s = p.kv_len[b], n = p.valid_len ? p.valid_len[b] : p.few_tokens;
   if (s < 0 || n < 1 || n > p.few_tokens || (long long)s + n > (long long)p.c.max_blocks * kKv8Block) return 0;
   return s + min(first + kDqTok, n);
 }
@@ -141,7 +143,7 @@ template <bool kFew>
 __device__ __forceinline__ int bad_bits(const DqParams& p, int v) {
   if (!kFew) return GROK_DEV_BAD_KV_LEN;
   const int b = v / groups_of(p.few_tokens);
-  const int s = __ldg(p.kv_len + b), n = p.valid_len ? __ldg(p.valid_len + b) : p.few_tokens;
+  const int s = p.kv_len[b], n = p.valid_len ? p.valid_len[b] : p.few_tokens;
   return (n < 1 || n > p.few_tokens ? GROK_DEV_BAD_VALID : 0) |
          (s < 0 || (long long)s + max(n, 0) > (long long)p.c.max_blocks * kKv8Block ? GROK_DEV_BAD_KV_LEN : 0);
 }
@@ -271,8 +273,8 @@ __global__ void __launch_bounds__(kFew ? kDqFewThreads : kDqThreads, kDqCtas) kv
       size_t row_of = my_pair;  // of the table
       if (kFew) row_of = (size_t)(my_pair / kKVHeads / groups_of(p.few_tokens)) * kKVHeads + my_pair % kKVHeads;
       my_id = max(0, kv8_block_id(p.c.table, row_of * p.c.max_blocks + my_blk, p.c.n_blocks, p.status));
-      my_ks = __ldg(p.c.k_scale + my_id);
-      my_vs = __ldg(p.c.v_scale + my_id);
+      my_ks = p.c.k_scale[my_id];
+      my_vs = p.c.v_scale[my_id];
       // (a token that does not see the block meets its V scale: what is not finite shows in the logits)
       if (kFew && my_vs != my_vs) my_ks = my_vs, my_vs = 0.f;
     }
@@ -316,7 +318,7 @@ __global__ void __launch_bounds__(kFew ? kDqFewThreads : kDqThreads, kDqCtas) kv
         if (kFew) {
           const int groups = groups_of(p.few_tokens), v = pair / kKVHeads;
           b = v / groups, first = v % groups * kDqTok;
-          seen = min(kDqTok, (p.valid_len ? __ldg(p.valid_len + b) : p.few_tokens) - first);
+          seen = min(kDqTok, (p.valid_len ? p.valid_len[b] : p.few_tokens) - first);
         }
         uint4 xs[kTiles][4];
 #pragma unroll
@@ -329,7 +331,7 @@ __global__ void __launch_bounds__(kFew ? kDqFewThreads : kDqThreads, kDqCtas) kv
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             xs[nt][i] = make_uint4(0, 0, 0, 0);
-            if (live) xs[nt][i] = __ldg(p.q + at * 16 + (i >> 1) * 8 + 2 * t + (i & 1));
+            if (live) xs[nt][i] = p.q[at * 16 + (i >> 1) * 8 + 2 * t + (i & 1)];
           }
         }
 #pragma unroll
