@@ -141,20 +141,33 @@ __global__ void __launch_bounds__(kUnThreads) kv8_unpack_kernel(const UnParams p
   }
 }
 
-// The fallback pass multiplies bf16: when an item is listed, the copy of V is rounded to bf16 in its place.
-__global__ void __launch_bounds__(256) kv8_v_to_bf16_kernel(const int32_t* fb_count, uint4* v, long long n) {
+// The fallback pass multiplies bf16: when an item is listed, the copy of V is rounded to bf16 in its place, 128 rows
+// of a head at a time, up to the rows that the copies have.
+__global__ void __launch_bounds__(256) kv8_v_to_bf16_kernel(const UnParams p) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the fp16 passes, which list the items
-  if (*fb_count == 0) return;
-  for (long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += (long long)gridDim.x * blockDim.x) {
-    uint4 x = v[i];
-    uint32_t* w = reinterpret_cast<uint32_t*>(&x);
+  if (*p.fb_count == 0) return;
+  const int tiles = p.rows / kPfKeys;
+  const long long n = (long long)p.c.B * kKVHeads * tiles;
+  for (long long e = blockIdx.x; e < n; e += gridDim.x) {
+    const long long head = e / tiles;
+    const int tile = int(e % tiles), b = int(head / kKVHeads);
+    const int s = p.cache_len[b], valid = p.valid_len ? p.valid_len[b] : p.T;
+    if (s < 0 || valid < 1 || valid > p.T || (long long)s + valid > (long long)p.c.max_blocks * kKv8Block) continue;
+    if (tile * kPfKeys >= s + valid) continue;
+    uint4* v = p.v_copy + ((size_t)head * p.rows + (size_t)tile * kPfKeys) * 16;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float2 a = __half22float2(reinterpret_cast<const __half2&>(w[e]));
-      w[e] = pack_bf16x2(a.x, a.y);
+    for (int m = 0; m < kPfKeys * 16 / 256; ++m) {
+      const int i = m * 256 + threadIdx.x;
+      uint4 x = v[i];
+      uint32_t* w = reinterpret_cast<uint32_t*>(&x);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const float2 a = __half22float2(reinterpret_cast<const __half2&>(w[q]));
+        w[q] = pack_bf16x2(a.x, a.y);
+      }
+      v[i] = x;
     }
-    v[i] = x;
   }
 }
 
@@ -307,8 +320,7 @@ extern "C" grok_status grok_kv8_prefill(const grok_kv8_cache* cache, const grok_
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  cudaError_t e = cudaLaunchKernelEx(&cfg, kv8_v_to_bf16_kernel, static_cast<const int32_t*>(fb_count), u.v_copy,
-                                     (long long)B * w.rows * kKVHeads * (kD / 8));
+  cudaError_t e = cudaLaunchKernelEx(&cfg, kv8_v_to_bf16_kernel, u);
   if (e != cudaSuccess) return fail(cuda_status(e), "kv8_v_to_bf16 launch: %s", cudaGetErrorString(e));
   if ((st = check_launch("kv8_v_to_bf16")) != GROK_OK) return st;
   return prefill_q8_passes(a, true, s);

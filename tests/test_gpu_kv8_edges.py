@@ -40,3 +40,51 @@ def test_zero_keys_in_a_block_of_very_large_ones(kind, tokens):
     assert torch.isfinite(got).all()
     # (every logit is 0 or far beyond the cap: none has an error of its own)
     check_decode(got[0], out, scale_v, 0.0, L, np.ones(tokens, bool))
+
+
+def overflowing(kind, B, L, max_blocks, seed, first=0):
+    """A cache whose items from sequence `first` on hold weights beyond fp16's range: a first tile of small logits and a
+    later key at the cap (no rotation: it would keep q . k only at equal positions)."""
+    rng = np.random.default_rng(seed)
+    cache, host = make_cache(B, max_blocks, kind, seed=seed), Host(B)
+    q, k, v = rows(rng, B, L)
+    k[first:] = (k[first:].float() * 0.02).bfloat16()
+    q[first:] = q[first:, L - 100, :1][:, None].expand(-1, L, 48, -1)
+    k[first:, L - 100] = q[first:, L - 100, :1].expand(-1, 8, -1)
+    tab = tables(L)
+    tab = (torch.ones_like(tab[0]), torch.zeros_like(tab[1]))
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    q_rot = torch.zeros_like(q, device=DEV)
+    zero = _ints([0] * B)
+    G.kv8_append(cache, q.to(DEV), k.to(DEV), v.to(DEV), zero, zero, None, *tab, q_rot, status)
+    assert int(status.item()) == 0 and torch.equal(q_rot.cpu(), q)
+    for b in range(B):
+        host.k[b], host.v[b] = _bits(k)[b], _bits(v)[b]
+    return cache, host, q_rot
+
+
+def check_overflowing(host, q_rot, got, kind, picks, heads=(0, 7, 47)):
+    """Half a step of the result, 2^-8; of V 2^-8; a weight's approximate functions 3e-4 and its logit, 128 * 2^-23 of the
+    sum of the magnitudes, in the sum too; fp16 weights 2^-11, and 2^-10 of the sum for all small ones."""
+    x, y = bf16.to_f64(_bits(q_rot)), got.float().cpu().numpy().astype(np.float64)
+    for b in range(len(host.k)):
+        for h in heads:
+            K, V = kv8.held(host.k[b][:, h // 6], kind), kv8.held(host.v[b][:, h // 6], kind)
+            o, w = kv8.attend(x[b, picks, h], K, V, np.array(picks))
+            logit = 128 * 2.0 ** -23 * (np.abs(x[b, picks, h]) @ np.abs(K).T).max() / 128 ** 0.5
+            rel = 2.0 ** -8 + 2.0 ** -11 + 2.0 ** -10 + 2 * (3e-4 + logit)
+            assert (np.abs(y[b, picks, h] - o) <= 2.0 ** -8 * np.abs(o) + rel * (w @ np.abs(V))).all(), (b, h)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_fallback_touches_the_rows_of_the_call_alone(kind):
+    """Two sequences of 300 rows with room for 32768: the workspace behind their copies keeps its bytes."""
+    B, L, max_blocks = 2, 300, 512
+    cache, host, q_rot = overflowing(kind, B, L, max_blocks, 3, first=1)
+    out = torch.empty_like(q_rot)
+    ws = G.alloc_kv8_prefill_workspace(cache)
+    ws.fill_(0xff)  # as fp16 a NaN, which a conversion to bf16 would write as another one
+    G.kv8_prefill(cache, q_rot, _ints([0] * B), None, out, ws)
+    copies = 2 * B * 8 * 384 * 128 * 2  # K and V, rows up to the next 128
+    assert int((ws != 0xff).sum()) <= copies + (1 << 16)
+    check_overflowing(host, q_rot, out, kind, [0, 100, 199, 200, 250, 299])
