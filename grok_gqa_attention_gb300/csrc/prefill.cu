@@ -77,7 +77,8 @@
 // deviation 6 to 9, up to 3 rows in 10^4 rise that far above 128 of their 8192 keys,
 // which lists one item in ten and takes 788 us where 649 are enough; above 384 of
 // them 3 in 10^7 do. The samples cost 1 % of 8192 tokens and 4 % of a chunk of 256
-// behind 6144 rows; bf16 weights throughout would cost 16 and 22 %.
+// behind 6144 rows (and the reference's call 3 to 5 % of short ragged prompts); bf16
+// weights throughout would cost 16 and 22 %.
 //
 // Split pass (kSplit, fp16 mode): when a call has fewer than two items per SM,
 // the items of the ragged last round run in a second launch, each shared among
@@ -164,7 +165,6 @@ struct PfItem {
   int n_kv;     // key tiles to visit from j0 (0: skip the unit)
   int n_sub;    // 64-key halves of those tiles that hold a visible key
   int n_pk;     // fp16 mode: sampled key tiles besides the first
-  int pk_last;  // the last tile of the unit that every row sees whole
   int bad;      // GROK_DEV_* bits when the sequence's integers are invalid
   bool redirect;  // fp16 mode: the sequence's V does not fit fp16; the fallback pass computes the item
 };
@@ -211,7 +211,6 @@ __device__ __forceinline__ PfItem pf_item(const PfParams& p, const PfBars* bars,
   it.bad = 0;
   it.redirect = false;
   it.n_pk = 0;
-  it.pk_last = 0;
   if (kQ8) {  // (padding tokens are not in the cache)
     if (it.s < 0 || (long long)it.s + max(it.n, 0) > p.Tmax) it.bad |= GROK_DEV_BAD_KV_LEN;
   } else if (it.s < 0 || (long long)it.s + p.T > p.Tmax) {
@@ -250,16 +249,13 @@ __device__ __forceinline__ PfItem pf_item(const PfParams& p, const PfBars* bars,
     it.n_sub = min(2 * j1, it.n_sub) - 2 * j0;
     it.n_kv = j1 - j0;
   }
-  if (kF16) {
-    it.n_pk = (it.n_kv + kPfSampleTiles / 2) / kPfSampleTiles;
-    // (16 tiles and more, of which at most the last two are not seen whole by the item's first row)
-    it.pk_last = min((min(it.s + it.qt * kPfRows, it.s + it.n - 1) + 1) / kPfKeys - 1 - it.j0, it.n_kv - 1);
-  }
+  if (kF16) it.n_pk = (unsigned(it.n_kv) + kPfSampleTiles / 2) / kPfSampleTiles;
   return it;
 }
 
-// fp16 mode: the k-th sampled tile (k < n_pk), counted from the unit's first: evenly over tiles 1 .. pk_last.
-__device__ __forceinline__ int pf_sample_tile(int k, int n_pk, int pk_last) { return (k + 1) * pk_last / n_pk; }
+// fp16 mode: the k-th sampled tile (k < n_pk), counted from the unit's first. At most the last two tiles of a unit are not
+// seen whole by the item's first row; the last sample is the third tile from the end, or lies before it.
+__device__ __forceinline__ int pf_sample_tile(int k) { return k * kPfSampleTiles + kPfSampleTiles / 2 - 3; }
 
 // Append an item to the fallback list (duplicates are harmless: the fallback
 // pass would compute the same bits twice).
@@ -481,20 +477,19 @@ __device__ __forceinline__ float pf_sample_max(uint32_t trow, int half, int rel,
 // wait gave up (of the whole warp, then). Every tile's two halves are read by the two warps of the quadrant, which exchange
 // their maxima. sub_cnt, xch_cnt: phases of s_full and xbar so far; lim: the row's last visible key.
 template <bool kSplit, bool kQ8>
-static __device__ __forceinline__ float pf_reference(const PfParams& p, PfBars* bars, int n_pk, int pk_last, int n_kv,
+static __device__ __forceinline__ float pf_reference(const PfParams& p, PfBars* bars, int n_pk, int n_kv,
                                                   int n_sub, int slot, int half, int quad, int lane, uint32_t trow,
                                                   int lim, const float* k_scale, int sub_cnt, int xch_cnt) {
   volatile int* abort = &bars->abort;
   float mx = -INFINITY;  // largest raw logit
-  float ks = kQ8 ? ld_chained(k_scale + 2 * (n_pk > 0 ? pf_sample_tile(0, n_pk, pk_last) : 0) + half) : 1.f;
+  auto tile = [&](int k) { return k < n_pk ? pf_sample_tile(k) : 0; };  // (the first tile comes last)
+  float ks = kQ8 ? ld_chained(k_scale + 2 * tile(0) + half) : 1.f;
 #pragma unroll 1
   for (int k = 0; k <= n_pk; ++k, ++sub_cnt) {
-    const int j = k < n_pk ? pf_sample_tile(k, n_pk, pk_last) : 0;
-    const int next = k + 1 < n_pk ? pf_sample_tile(k + 1, n_pk, pk_last) : 0;
-    const float ks_next = kQ8 ? ld_chained(k_scale + 2 * next + half) : 1.f;
+    const float ks_next = kQ8 ? ld_chained(k_scale + 2 * tile(k + 1) + half) : 1.f;
     if (!__all_sync(0xffffffffu, mbar_wait(&bars->s_full[slot][half], sub_cnt & 1, abort, p.status))) return INFINITY;
     tc_fence_after();
-    mx = fmaxf(mx, pf_sample_max<kQ8>(trow, half, lim - j * kPfKeys, ks));
+    mx = fmaxf(mx, pf_sample_max<kQ8>(trow, half, lim - tile(k) * kPfKeys, ks));
     ks = ks_next;
     if (k < n_pk) {
       tc_fence_before();
@@ -517,11 +512,11 @@ static __device__ __forceinline__ float pf_reference(const PfParams& p, PfBars* 
 // inlined). Inlined for the shorter units of the split pass, where the call costs more than that gives (4 x 256 tokens
 // behind 6144 rows of an 8-bit cache, both passes out of line: 193 us, both inlined: 191).
 template <bool kQ8>
-static __device__ __noinline__ float pf_reference_whole(const PfParams& p, PfBars* bars, int n_pk, int pk_last, int n_kv,
+static __device__ __noinline__ float pf_reference_whole(const PfParams& p, PfBars* bars, int n_pk, int n_kv,
                                                         int n_sub, int slot, int half, int quad, int lane,
                                                         uint32_t trow, int lim, const float* k_scale, int sub_cnt,
                                                         int xch_cnt) {
-  return pf_reference<false, kQ8>(p, bars, n_pk, pk_last, n_kv, n_sub, slot, half, quad, lane, trow, lim, k_scale, sub_cnt,
+  return pf_reference<false, kQ8>(p, bars, n_pk, n_kv, n_sub, slot, half, quad, lane, trow, lim, k_scale, sub_cnt,
                                   xch_cnt);
 }
 
@@ -743,7 +738,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         // (A ring has one free stage while the item before is in its epilogue: the first key tile goes ahead of the
         // second sample.)
         for (int k = 0; kF16 && ok && k < it.n_pk; ++k)
-          ok = load_k(it, pf_sample_tile(k, it.n_pk, it.pk_last), sV, bars->v_full, bars->v_empty, v_it, krow, kb) &&
+          ok = load_k(it, pf_sample_tile(k), sV, bars->v_full, bars->v_empty, v_it, krow, kb) &&
                (k > 0 || load_k(it, 0, sK, bars->k_full, bars->k_empty, k_it, krow, kb));
         for (int j = 0; ok && j < it.n_kv; ++j, ++v_it) {
           const uint32_t st = v_it % kPfStages;
@@ -909,9 +904,9 @@ __global__ void __launch_bounds__(kPfThreads, 1)
       float mref = kT;  // bf16 mode: the fixed reference logit 30 (30 log2(e) in log2 units)
       bool ok = true;
       if (kF16 && half < it.n_sub) {
-        mref = kSplit ? pf_reference<true, kQ8>(p, bars, it.n_pk, it.pk_last, it.n_kv, it.n_sub, slot, half, quad, lane,
+        mref = kSplit ? pf_reference<true, kQ8>(p, bars, it.n_pk, it.n_kv, it.n_sub, slot, half, quad, lane,
                                                 trow, lim, k_scale, sub_cnt, xch_cnt)
-                      : pf_reference_whole<kQ8>(p, bars, it.n_pk, it.pk_last, it.n_kv, it.n_sub, slot, half, quad, lane,
+                      : pf_reference_whole<kQ8>(p, bars, it.n_pk, it.n_kv, it.n_sub, slot, half, quad, lane,
                                                 trow, lim, k_scale, sub_cnt, xch_cnt);
         if (mref == INFINITY) break;
         sub_cnt += it.n_pk;
