@@ -123,6 +123,7 @@ struct PfBars {
   float xmax[2][4][2][32];   // [slot][quad][half][lane]
   float lsum[2][2][2][128];  // [item parity][slot][half][row]
   int seq_start[kPfSeqCache], seq_valid[kPfSeqCache], seq_vflag[kPfSeqCache];
+  int listed;  // fp16 mode: the item that this CTA put on the fallback list last, plus one
   uint32_t tmem_base;
   int abort;
 };
@@ -257,8 +258,9 @@ __device__ __forceinline__ PfItem pf_item(const PfParams& p, const PfBars* bars,
 // seen whole by the item's first row; the last sample is the third tile from the end, or lies before it.
 __device__ __forceinline__ int pf_sample_tile(int k) { return k * kPfSampleTiles + kPfSampleTiles / 2 - 3; }
 
-// Append an item to the fallback list (duplicates are harmless: the fallback
-// pass would compute the same bits twice).
+// Append an item to the fallback list (duplicates, as units of the split pass
+// over the bf16 cache make them, are harmless: the fallback pass computes the same
+// bits twice).
 __device__ __forceinline__ void pf_fallback(const PfParams& p, int item) {
   const int k = atomicAdd(p.fb_count, 1);
   if (k < p.fb_cap) p.fb_list[k] = item;
@@ -681,6 +683,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
     }
     mbar_init(&bars->mma_done, 2);
     bars->abort = 0;
+    bars->listed = 0;
     fence_barrier_init();
   }
   // Every role reads each item's sequence integers; stage them once.
@@ -990,9 +993,10 @@ __global__ void __launch_bounds__(kPfThreads, 1)
           uint32_t ov[32];
           tmem_ld32(trow + 128 + half * 64 + cc * 32, ov);
           tmem_wait_ld_dep(ov);
-          // fp16 mode: the fallback pass recomputes the item of a row that overflowed
-          // (a half-0 warp of each quadrant reports; duplicates are harmless)
-          if (kF16 && cc == 0 && half == 0 && __any_sync(0xffffffffu, pf_over<kQ8>(lt, ov[0])) && lane == 0)
+          // fp16 mode: the fallback pass recomputes the item of a row that overflowed. Up to eight warps see one (a
+          // half-0 warp of each quadrant and slot); the first lists it, as all do before the next item's O is complete.
+          if (kF16 && cc == 0 && half == 0 && __any_sync(0xffffffffu, pf_over<kQ8>(lt, ov[0])) && lane == 0 &&
+              atomicExch(&bars->listed, it.item + 1) != it.item + 1)
             pf_fallback(p, it.item);
           uint32_t pk[16];
 #pragma unroll

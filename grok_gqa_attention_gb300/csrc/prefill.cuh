@@ -32,9 +32,9 @@ inline size_t split_area_bytes(int sms) {
   return split_cnt_bytes(sms) + split_lm_bytes(sms) + size_t(sms) * 2 * 2 * 16 * kPfRows * sizeof(float4);
 }
 inline int ws_fb_cap(int B, int Tmax) {
-  // items of the largest call (T = Tmax); each may be listed by up to 8
-  // quadrant warps of the fp16 pass (split items: once per slot by each of up
-  // to 4 units) plus once for its sequence's V
+  // items of the largest call (T = Tmax); an item is listed once, or once for each
+  // slot by each of up to 4 units (split items of a bf16 cache), plus once for its
+  // sequence's V
   return 9 * ((Tmax + kPfRows - 1) / kPfRows) * B * GROK_N_KV_HEADS * 3;
 }
 

@@ -88,3 +88,19 @@ def test_fallback_touches_the_rows_of_the_call_alone(kind):
     copies = 2 * B * 8 * 384 * 128 * 2  # K and V, rows up to the next 128
     assert int((ws != 0xff).sum()) <= copies + (1 << 16)
     check_overflowing(host, q_rot, out, kind, [0, 100, 199, 200, 250, 299])
+
+
+def test_fallback_lists_an_item_once():
+    """The items of rows 128 to 299 of every sequence overflow (key 200 is at the cap): each is computed again once. The
+    workspace begins with their number (prefill_ws: behind a flag for each sequence)."""
+    B, L = 4, 300
+    cache, host, q_rot = overflowing("int8", B, L, 8, 4)
+    out, ws = torch.empty_like(q_rot), G.alloc_kv8_prefill_workspace(cache)
+    zero = _ints([0] * B)
+    G.kv8_prefill(cache, q_rot, zero, None, out, ws)
+    assert int(ws.view(torch.int32)[0]) == B * 2 * 24
+    check_overflowing(host, q_rot, out, "int8", [0, 199, 200, 299])
+    ck, cv = (torch.from_numpy(np.stack(x).view(np.int16)).view(torch.bfloat16).to(DEV) for x in (host.k, host.v))
+    ws = G.alloc_prefill_workspace(B, L)
+    G.prefill_ws(q_rot, ck, cv, zero, None, out, ws)
+    assert int(ws.view(torch.int32)[B]) == B * 2 * 24
