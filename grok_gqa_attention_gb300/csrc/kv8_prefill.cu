@@ -196,6 +196,10 @@ int few_tokens(int B, int max_blocks) {
   return B <= 8 ? 32 : 16;
 }
 
+// Groups of tokens in such a call: at least as many as B sequences or fewer with any capacity have (96 / 4 for one or
+// two, 8 each for up to eight, 4 each for more), so that a workspace for a cache serves every smaller one too.
+int few_groups(int B) { return std::max({24, 8 * std::min(B, 8), 4 * B}); }
+
 // Workspace: fallback count and list, K scales, output factors, the copies of K and V, the split's area.
 struct Layout {
   int rows;
@@ -212,7 +216,7 @@ Layout layout(int B, int max_blocks, int sms) {
   w.v_copy = w.k_copy + copy;
   w.split = w.v_copy + copy;
   w.bytes = w.split + (split_allowed(w.rows) ? split_area_bytes(sms) : 0);
-  w.bytes = std::max(w.bytes, kv8_decode_bytes(B, few_tokens(B, max_blocks), max_blocks, false, sms));
+  w.bytes = std::max(w.bytes, kv8_decode_bytes(few_groups(B), 1, max_blocks, false, sms));
   return w;
 }
 

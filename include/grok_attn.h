@@ -664,7 +664,8 @@ grok_status grok_kv8_decode(const grok_kv8_cache* cache, const grok_bf16* q_rot,
  *   workspace: device memory, 256-byte aligned, of at least
  *   grok_kv8_prefill_workspace(B, max_blocks) bytes for the current device (4 KB
  *   per row of the cache and sequence or, where it is more, 0.5 MB per sequence, and
- *   about 40 MB; B * max_blocks <= 2^21).
+ *   about 40 MB; B * max_blocks <= 2^21). A workspace for a cache serves every
+ *   one with fewer sequences or blocks.
  *   Calls that overlap on the GPU need separate workspaces; nothing is kept.
  */
 grok_status grok_kv8_prefill_workspace(int B, int max_blocks, size_t* bytes);

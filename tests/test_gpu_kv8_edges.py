@@ -104,3 +104,19 @@ def test_fallback_lists_an_item_once():
     ws = G.alloc_prefill_workspace(B, L)
     G.prefill_ws(q_rot, ck, cv, zero, None, out, ws)
     assert int(ws.view(torch.int32)[B]) == B * 2 * 24
+
+
+def test_a_workspace_serves_every_smaller_cache():
+    """Sizes do not fall with the number of sequences or blocks; a call over 36 blocks in the workspace for 64."""
+    Bs, blocks = [*range(1, 20), 31, 32, 33, 64, 100, 256], [*range(1, 41), 64, 100, 128, 511, 512, 1024]
+    for size in (G.kv8_prefill_workspace, G.kv8_decode_workspace):
+        n = np.array([[size(B, m) for m in blocks] for B in Bs])
+        assert (np.diff(n, axis=0) >= 0).all() and (np.diff(n, axis=1) >= 0).all(), size.__name__
+    rng = np.random.default_rng(5)
+    cache, host = filled(rng, [300], "int8", 36, seed=5)
+    q = _bf16(rng.standard_normal((1, 90, 48, 128))).to(DEV)
+    want, _ = run_prefill(cache, q, [210], None, 90)
+    ws = torch.empty(G.kv8_prefill_workspace(1, 64), dtype=torch.uint8, device=DEV)
+    out = torch.empty_like(q)
+    G.kv8_prefill(cache, q, _ints([210]), None, out, ws)
+    assert torch.equal(out, want)
