@@ -133,7 +133,7 @@ def kv8_append(cache: Kv8Cache, q, k, v, start_pos, cache_len, valid_len, cos_ta
     """RoPE on q and k at positions start_pos[b] + i; tokens i < valid_len[b] become rows cache_len[b] + i.
 
     valid_len may be None (all T tokens). cos_tab, sin_tab [n, 64] as from rope_cos_sin(0, n). The caller advances
-    cache_len and start_pos (see grok_kv8_append).
+    cache_len and start_pos, and sets cache_len back, if at all, to a multiple of 64 (see grok_kv8_append).
     """
     B, T, n, at = cache.B, q.shape[1], cos_tab.shape[0], cache.index
     kv = (B, T, N_KV_HEADS, HEAD_DIM)

@@ -613,6 +613,13 @@ typedef struct {
  * cache_len[b] + valid_len[b] > max_blocks * 64 (GROK_DEV_BAD_KV_LEN), or
  * valid_len[b] is outside [1, T] (GROK_DEV_BAD_VALID). Code rows behind a
  * sequence's last are left as they were.
+ * Rows may be dropped from a multiple of 64 on: a cache_len[b] set back to one
+ * makes the cache of the rows before it and the new ones. It may not be set back to
+ * other rows: the open block's scale would count the dropped rows, and where they
+ * had reached the next block, open_k and open_v hold that one's rows (the call
+ * cannot tell, the codes would be wrong). To drop the end of a block, as after
+ * rejected drafts, set cache_len[b] back to the block's first row and append the
+ * block's rows that stay again.
  */
 grok_status grok_kv8_append(const grok_kv8_cache* cache, const grok_bf16* q, const grok_bf16* k, const grok_bf16* v,
                             const int32_t* start_pos, const int32_t* cache_len, const int32_t* valid_len, int T,

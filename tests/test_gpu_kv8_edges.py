@@ -120,3 +120,35 @@ def test_a_workspace_serves_every_smaller_cache():
     out = torch.empty_like(q)
     G.kv8_prefill(cache, q, _ints([210]), None, out, ws)
     assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("many", [False, True])
+def test_rows_taken_back_to_a_blocks_start(kind, many):
+    """Lengths set back to a multiple of 64, from inside the block and from a later one: the next rows make the cache that
+    they alone would have made, with scales that the dropped rows, larger ones, had raised. (64 and more sequences: single
+    tokens by their own kernel.)"""
+    rng = np.random.default_rng(8)
+    B, tab = (65, tables(400)) if many else (3, tables(400))
+    cache, host = make_cache(B, 5, kind, seed=8), Host(B)
+    append(cache, host, *rows(rng, B, 100), [0] * B, [100] * B, tab)
+    q, k, v = rows(rng, B, 130)
+    append(cache, host, q, (k.float() * 50).bfloat16(), (v.float() * 50).bfloat16(), [100] * B, [130] * B, tab)
+    for b in range(B):  # 230 rows: back to 64, to 192 or to nothing
+        keep = (64, 192, 0)[b % 3]
+        host.k[b], host.v[b] = host.k[b][:keep], host.v[b][:keep]
+    for T in (1, 1, 40, 1, 30) if not many else (1, 1, 1):
+        append(cache, host, *rows(rng, B, T), [len(x) for x in host.k], [T] * B, tab)
+    for b in range(B if not many else 4):
+        L = len(host.k[b])
+        for g in range(8):
+            for pool, scale, held_rows in ((cache.k_pool, cache.k_scale, host.k[b]), (cache.v_pool, cache.v_scale, host.v[b])):
+                for i, (codes, s) in enumerate(kv8.blocks(held_rows[:, g], kind)):
+                    at = int(cache.table[b, g, i])
+                    got = pool[at].view(torch.uint8).cpu().numpy()
+                    got = np.concatenate([got[0], got[1]], 1) if pool is cache.k_pool else got.T
+                    assert np.float32(scale[at].item()) == s and np.array_equal(got[:len(codes)], codes), (b, g, i)
+    lens = [len(x) for x in host.k]
+    q = _bf16(rng.standard_normal((B, 48, 128)) * 3).to(DEV)
+    out, _, status = run_decode(cache, q, lens, weights=False)
+    assert status == 0 and torch.isfinite(out).all()
