@@ -541,8 +541,7 @@ __device__ __forceinline__ bool pf_over(float lt, uint32_t o) {
 // gave up. Out of line: its registers stay out of the softmax loop's.
 static __device__ __noinline__ int pf_split_epilogue(const PfParams& p, PfBars* bars, volatile int* abort, int unit,
                                               int item, int parts, int slot, int half, int quad, int lane,
-                                              uint32_t trow, float lt, float mref, float o_scale, uint8_t* stage,
-                                              uint32_t parity) {
+                                              uint32_t trow, float lt, float mref, uint8_t* stage, uint32_t parity) {
   const int r = quad * 32 + lane;
   const size_t su = size_t(unit) * 2 + slot;
   float4* po = p.part_o + (su * 2 + half) * (16 * kPfRows) + r;
@@ -601,7 +600,7 @@ static __device__ __noinline__ int pf_split_epilogue(const PfParams& p, PfBars* 
       fk[k] = ex2_approx(lm[k].y - mx);
       lsum = fmaf(lm[k].x, fk[k], lsum);
     }
-  const float inv_l = o_scale / lsum;
+  const float inv_l = 1.0f / lsum;
 #pragma unroll 2
   for (int c = 0; c < 8; ++c) {  // 16-byte chunk c of the row's 64 output features (8 bf16)
     float acc[8];
@@ -985,9 +984,8 @@ __global__ void __launch_bounds__(kPfThreads, 1)
       const int k_last = (tile_cnt - 1) % kPfStages, v_last = (tile_cnt + pk_cnt - 1) % kPfStages;
       uint8_t* stage = (slot == 0 ? sK + k_last * kTileBytes : sV + v_last * kTileBytes) + half * kBox;
       bool store = true;  // this warp's output rows are staged
-      const float o_scale = kQ8 ? ld_chained(p.o_scale + it.b * kKVHeads + it.g) : 1.f;
       if (!kSplit || it.parts == 1) {
-        const float inv_l = (kQ8 ? o_scale : 1.0f) / lt;
+        const float inv_l = (kQ8 ? ld_chained(p.o_scale + it.b * kKVHeads + it.g) : 1.0f) / lt;
 #pragma unroll
         for (int cc = 0; cc < 2; ++cc) {
           uint32_t ov[32];
@@ -1037,7 +1035,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
       } else {
         const int res =
             pf_split_epilogue(p, bars, abort, item, it.item - p.item_base, it.parts, slot, half, quad, lane, trow, lt,
-                              mref, o_scale, stage, uint32_t(split_cnt & 1));
+                              mref, stage, uint32_t(split_cnt & 1));
         ++split_cnt;
         if (!__all_sync(0xffffffffu, res >= 0)) break;
         store = res > 0;
