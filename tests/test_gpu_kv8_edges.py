@@ -42,15 +42,17 @@ def test_zero_keys_in_a_block_of_very_large_ones(kind, tokens):
     check_decode(got[0], out, scale_v, 0.0, L, np.ones(tokens, bool))
 
 
-def overflowing(kind, B, L, max_blocks, seed, first=0):
+def overflowing(kind, B, L, max_blocks, seed, first=0, v_of_the_key=None):
     """A cache whose items from sequence `first` on hold weights beyond fp16's range: a first tile of small logits and a
-    later key at the cap (no rotation: it would keep q . k only at equal positions)."""
+    later key at the cap (no rotation: it would keep q . k only at equal positions). v_of_the_key: that key's value."""
     rng = np.random.default_rng(seed)
     cache, host = make_cache(B, max_blocks, kind, seed=seed), Host(B)
     q, k, v = rows(rng, B, L)
     k[first:] = (k[first:].float() * 0.02).bfloat16()
     q[first:] = q[first:, L - 100, :1][:, None].expand(-1, L, 48, -1)
     k[first:, L - 100] = q[first:, L - 100, :1].expand(-1, 8, -1)
+    if v_of_the_key is not None:
+        v[first:, L - 100] = v_of_the_key
     tab = tables(L)
     tab = (torch.ones_like(tab[0]), torch.zeros_like(tab[1]))
     status = torch.zeros(1, dtype=torch.int32, device=DEV)
@@ -88,6 +90,20 @@ def test_fallback_touches_the_rows_of_the_call_alone(kind):
     copies = 2 * B * 8 * 384 * 128 * 2  # K and V, rows up to the next 128
     assert int((ws != 0xff).sum()) <= copies + (1 << 16)
     check_overflowing(host, q_rot, out, kind, [0, 100, 199, 200, 250, 299])
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_fallback_where_the_large_keys_value_is_zero(kind):
+    """An infinite weight is seen in the outputs also where it meets zeros."""
+    cache, host, q_rot = overflowing(kind, 2, 300, 8, 6, v_of_the_key=0.0)
+    got, status = run_prefill(cache, q_rot, [0, 0], None, 300)
+    assert status == 0 and torch.isfinite(got).all()
+    check_overflowing(host, q_rot, got, kind, [0, 100, 199, 200, 250, 299])
+    ck, cv = (torch.from_numpy(np.stack(x).view(np.int16)).view(torch.bfloat16).to(DEV) for x in (host.k, host.v))
+    out, want = torch.empty_like(q_rot), torch.empty_like(q_rot)
+    G.prefill_ws(q_rot, ck, cv, _ints([0, 0]), None, out, G.alloc_prefill_workspace(2, 300))
+    G.prefill(q_rot, ck, cv, _ints([0, 0]), None, want)
+    assert torch.equal(out[:, 200:], want[:, 200:])
 
 
 def test_fallback_lists_an_item_once():
@@ -152,3 +168,24 @@ def test_rows_taken_back_to_a_blocks_start(kind, many):
     q = _bf16(rng.standard_normal((B, 48, 128)) * 3).to(DEV)
     out, _, status = run_decode(cache, q, lens, weights=False)
     assert status == 0 and torch.isfinite(out).all()
+
+
+@pytest.mark.parametrize("T,start", [(2200, 0), (200, 2300)])
+def test_non_finite_blocks_among_the_sampled_keys(T, start):
+    """Rows 1664 to 1791 are a key tile that rows' references look at ahead of the rest (whole items, and parts of items):
+    a block of it without finite values is NaN for the rows that see it, and nothing to the others."""
+    rng = np.random.default_rng(9)
+    L = start + T
+    cache, _ = filled(rng, [L], "int8", 40, seed=9)
+    q = _bf16(rng.standard_normal((1, T, 48, 128)) * 3).to(DEV)
+    good, status = run_prefill(cache, q, [start], None, T)
+    assert status == 0 and torch.isfinite(good).all()
+    for scale in (cache.k_scale, cache.v_scale):
+        at = cache.table[0, 2, 27].long()
+        saved = scale[at].clone()
+        scale[at] = float("nan")
+        got, _ = run_prefill(cache, q, [start], None, T)
+        scale[at] = saved
+        want = torch.zeros(1, T, 48, dtype=torch.bool, device=DEV)
+        want[0, max(0, 64 * 27 - start):, 12:18] = True
+        assert torch.equal(torch.isnan(got).all(-1), want) and torch.equal(got[~want], good[~want])
