@@ -58,13 +58,12 @@
 // workspace (both operands of a kind::f16 product have one type). fp16's
 // exponent range cannot hold weights relative to the fixed reference 30, so
 // each row takes its own reference, from the largest logit y_max of a sample of
-// its keys: the item's first key tile and, from 16 tiles on, about one in 32 of the
+// its keys: the item's first key tile and, from 12 tiles on, about one in 24 of the
 // others. (Their Q K^T comes ahead of the first tile's, for the maximum alone;
 // they are staged in the V ring, which is idle then.) The two warps of a quadrant
 // exchange their maxima once per item.
-//   m = 30 log2(e) tanh(y_max) - log2(n) + 15 (log2 units), n the row's keys
-// rounded up to a power of two, 128 at least, puts the sample's largest weight at
-// n 2^-15. A weight below fp16's normal range (2^-14) is off by 2^-25 at most, so
+//   m = 30 log2(e) tanh(y_max) - log2(n) + 15 (log2 units), n the row's keys, 128 at
+// least, puts the sample's largest weight at n 2^-15. A weight below fp16's normal range (2^-14) is off by 2^-25 at most, so
 // n of them are off by n 2^-25, which is 2^-10 of the row's sum at most: a row whose
 // sum is thousands of small weights beside a few large ones keeps them. (With the
 // first tile's largest weight at 2^-8 for every n, outputs of such rows are off by up
@@ -75,8 +74,8 @@
 // sequence whose V does not fit fp16. The bf16 mode of this kernel then recomputes
 // exactly the listed items. Why a sample of that size: of normal logits with
 // deviation 6 to 9, up to 3 rows in 10^4 rise that far above 128 of their 8192 keys,
-// which lists one item in ten and takes 788 us where 649 are enough; above 384 of
-// them 3 in 10^7 do. The samples cost 1 % of 8192 tokens and 4 % of a chunk of 256
+// which lists one item in ten and takes 788 us where 649 are enough; above 512 of
+// them 5 in 10^8 do. The samples cost 1 % of 8192 tokens and 3 % of a chunk of 256
 // behind 6144 rows (and the reference's call 3 to 5 % of short ragged prompts); bf16
 // weights throughout would cost 16 and 22 %.
 //
@@ -105,8 +104,8 @@ constexpr int kQBytes = 2 * 2 * kBox;       // two heads, two 64-wide halves of 
 constexpr int kTileBytes = 2 * kBox;        // one K or V tile: two 64-wide halves of d
 constexpr int kPfData = kQBytes + 2 * kPfStages * kTileBytes;
 constexpr int kPfSeqCache = 512;  // sequences whose start / valid length are staged in shared memory
-constexpr int kPfSampleTiles = 32;  // fp16 mode: a row's reference looks at one key tile in about this many, and the first
-constexpr int kPfLossBits = 15;     // fp16 mode: of n keys, the sample's largest weight is n 2^-15
+constexpr int kPfSampleTiles = 24;  // fp16 mode: a row's reference looks at one key tile in about this many, and the first
+constexpr float kPfLossBits = 15.f;  // fp16 mode: of n keys, the sample's largest weight is n 2^-15
 
 struct PfBars {
   uint64_t q_full, q_empty;
@@ -507,7 +506,7 @@ static __device__ __forceinline__ float pf_reference(const PfParams& p, PfBars* 
   // Key 0 is visible to every row, so mx is finite, except in a split unit after an item's first: rows with no visible
   // key in it (all their weights zero) keep a finite reference through the clamp.
   const int keys = min(max(lim + 1, kPfKeys), n_kv * kPfKeys);  // of the row in this unit, about
-  return kT * tanh_approx((kSplit ? fmaxf(mx, -1.0e30f) : mx) * kY) + float(kPfLossBits - (32 - __clz(keys - 1)));
+  return kT * tanh_approx((kSplit ? fmaxf(mx, -1.0e30f) : mx) * kY) + (kPfLossBits - __log2f(float(keys)));
 }
 
 // Out of line for whole items: its registers stay out of the softmax loop's (8192 tokens: 651 us, 683 with the call

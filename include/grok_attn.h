@@ -193,10 +193,9 @@ grok_status grok_attn_prefill(const grok_bf16* q_rot, const grok_bf16* cache_k, 
  * each P V product runs once instead of twice). Each row's weights are taken
  * relative to a reference set from a sample of its keys and rounded once to fp16:
  * 2^-11 relative for weights down to 2^-14, an absolute 2^-25 below, where the
- * sample's largest weight is n 2^-15, n the row's keys rounded up to a power of
- * two (128 at least). All small weights of a row together are off by 2^-10 of its
- * sum at most. V is read from an fp16 copy that
- * the call first writes into `workspace` (rows [0, start_pos[b] + T) of each
+ * sample's largest weight is n 2^-15, n the row's keys (128 at least). All small
+ * weights of a row together are off by 2^-10 of its sum at most. V is read from an
+ * fp16 copy that the call first writes into `workspace` (rows [0, start_pos[b] + T) of each
  * sequence rounded to nearest fp16, then zeros to the next multiple of 128).
  * Items (128 query rows x 2 heads) with a weight beyond fp16's range (2^31 / n
  * times the sample's largest), and every item of a sequence holding a
