@@ -80,15 +80,6 @@ __device__ __forceinline__ void kv_coord(const PageMap& pm, int b, int key, int&
 }
 
 // ----------------------------------------------------------------------------
-// A load of what an earlier kernel of a chain of programmatic dependents writes:
-// it stays behind the thread's griddepcontrol.wait, and is no read-only load.
-__device__ __forceinline__ float ld_chained(const float* p) {
-  float v;
-  asm volatile("ld.global.f32 %0, [%1];" : "=f"(v) : "l"(p));
-  return v;
-}
-
-// ----------------------------------------------------------------------------
 // shared-memory addresses, mbarrier
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));

@@ -169,6 +169,14 @@ struct PfItem {
   bool redirect;  // fp16 mode: the sequence's V does not fit fp16; the fallback pass computes the item
 };
 
+// A load of what an earlier kernel of a chain of programmatic dependents writes:
+// it stays behind the thread's griddepcontrol.wait, and is no read-only load.
+__device__ __forceinline__ float ld_chained(const float* p) {
+  float v;
+  asm volatile("ld.global.f32 %0, [%1];" : "=f"(v) : "l"(p));
+  return v;
+}
+
 // The item a CTA takes in round rd (-1 when there is none): rounds of gridDim.x
 // items, odd rounds in reverse CTA order, so the heavy items of one round and
 // the light items of the next land on the same CTA.

@@ -691,6 +691,9 @@ grok_status grok_kv8_prefill(const grok_kv8_cache* cache, const grok_bf16* q_rot
  * owner of a shared pool finds their numbers behind the last block in use (where
  * an evicted block is another sequence's too, the caller puts a free one in its
  * place before rows are appended there).
+ * The weights come from grok_kv8_decode; grok_kv8_prefill gives none, so the blocks
+ * of a prompt have what the tokens after it gave them: decode some before evicting
+ * (or keep the prompt's start by `sink`).
  * kv_len_out[b] = keep * 64 + kv_len[b] % 64, or kv_len[b] where nc <= keep.
  *   table, table_out [B,8,max_blocks] int32, weight, weight_out
  *   [B,8,max_blocks] fp32, kv_len, kv_len_out [B] int32. table_out may be table and

@@ -189,3 +189,21 @@ def test_non_finite_blocks_among_the_sampled_keys(T, start):
         want = torch.zeros(1, T, 48, dtype=torch.bool, device=DEV)
         want[0, max(0, 64 * 27 - start):, 12:18] = True
         assert torch.equal(torch.isnan(got).all(-1), want) and torch.equal(got[~want], good[~want])
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_outputs_of_flat_peaked_and_unequal_logits_are_finite(kind, monkeypatch):
+    """The cases of those tests again: a comparison with a NaN is false, so their bound alone lets one pass."""
+    from tests import test_gpu_kv8 as T
+
+    def strict(got, out, scale_v, s_abs, L, live):
+        assert torch.isfinite(got[torch.from_numpy(live).to(got.device)]).all()
+        check_decode(got, out, scale_v, s_abs, L, live)
+
+    monkeypatch.setattr(T, "check_decode", strict)
+    for scale in (1e-6, 0.02, 8.0):
+        T.test_decode_flat_and_peaked_logits(kind, scale)
+        T.test_prefill_of_few_tokens_flat_and_peaked_logits(kind, scale)
+    T.test_prefill_of_few_tokens_flat_and_peaked_logits(kind, "unequal")
+    T.test_decode_unequal_query_heads()
+    T.test_decode_bad_lengths_leave_the_outputs()
