@@ -14,7 +14,7 @@
 // the new rows are written.
 //
 // Memory-bound: per token 16 KB of q, k, v read, 12 KB of q_rot and 2 KB of codes
-// written. Measured (graph replays, one GB300): 8192 tokens (257 MB) 44.8 us,
+// written. Measured (graph replays, one GB300): 8192 tokens (257 MB) 44.5 us,
 // 5.7 TB/s, 0.85 of the copy rate (1032 CTAs are 1.7 rounds of the resident ones);
 // 8 ragged sequences of up to 2048 (467 MB) 73.0 us, 0.95; one token 4.1 us.
 #include "host.cuh"

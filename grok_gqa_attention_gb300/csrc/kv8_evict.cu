@@ -9,7 +9,7 @@
 //
 // Bound by that search (71 % of the issue slots are busy). 2048 rows of 1024: 41 us with a thread per
 // entry (32 barriers of 1024 threads), 14.0 us with a warp per row (13 warps on an
-// SM do not hide it), 12.5 us with four; reading and writing 34 MB takes 5 us.
+// SM do not hide it), 13.2 us with four; reading and writing 34 MB takes 5 us.
 #include "host.cuh"
 #include "kv8.cuh"
 
