@@ -9,8 +9,8 @@
 //
 // Tensor-bound for all but short calls: the copies cost 1 byte read, 2 written
 // and 2 read per code. Measured (graph replays, one GB300): 8192 tokens in an empty
-// cache 672 us, 1227 TFLOP/s, 0.63 of the library GEMM's rate, of which the copies
-// are 12 us; 4 x 256 tokens behind 6144 rows 183 us, 26 of them the copies (52 MB of
+// cache 670 us, 1231 TFLOP/s, 0.63 of the library GEMM's rate, of which the copies
+// are 12 us; 4 x 256 tokens behind 6144 rows 181 us, 26 of them the copies (52 MB of
 // codes read, 105 MB written, 6 TB/s); 128 tokens behind 8192 rows 51 us.
 #include "host.cuh"
 #include "kv8.cuh"

@@ -63,9 +63,10 @@
 // they are staged in the V ring, which is idle then.) The two warps of a quadrant
 // exchange their maxima once per item.
 //   m = 30 log2(e) tanh(y_max) - log2(n) + 15 (log2 units), n the row's keys, 128 at
-// least, puts the sample's largest weight at n 2^-15. A weight below fp16's normal range (2^-14) is off by 2^-25 at most, so
-// n of them are off by n 2^-25, which is 2^-10 of the row's sum at most: a row whose
-// sum is thousands of small weights beside a few large ones keeps them. (With the
+// least, puts the sample's largest weight at n 2^-15. A weight below fp16's normal
+// range (2^-14) is off by 2^-25 at most, so n of them are off by n 2^-25, which is
+// 2^-10 of the row's sum at most: a row whose sum is thousands of small weights
+// beside a few large ones keeps them. (With the
 // first tile's largest weight at 2^-8 for every n, outputs of such rows are off by up
 // to 2 % of V with 8192 keys and 20 % with 65536.) Keys whose weights rise above
 // the sample's by more than 2^31 / n (2^18 for 8192 keys, 12.5 on the capped-logit
@@ -76,7 +77,7 @@
 // deviation 6 to 9, up to 3 rows in 10^4 rise that far above 128 of their 8192 keys,
 // which lists one item in ten and takes 788 us where 649 are enough; above 512 of
 // them 5 in 10^8 do. The samples cost 1 % of 8192 tokens and 3 % of a chunk of 256
-// behind 6144 rows (and the reference's call 3 to 5 % of short ragged prompts); bf16
+// behind 6144 rows (and the reference's call 2 to 4 % of short ragged prompts); bf16
 // weights throughout would cost 16 and 22 %.
 //
 // Split pass (kSplit, fp16 mode): when a call has fewer than two items per SM,
@@ -717,19 +718,6 @@ __global__ void __launch_bounds__(kPfThreads, 1)
     // ------------------------------------------------------------ TMA producer
     if (lane == 0) {
       uint32_t k_it = 0, v_it = 0, q_it = 0;  // tiles loaded into the K and V rings, Q tiles
-      // key tile t of the unit into a ring (sampled tiles take the V ring, which is idle until the first tile's P is
-      // there); krow, kb: where it lies
-      auto load_k = [&](const PfItem& it, int t, uint8_t* ring, uint64_t* full, uint64_t* empty, uint32_t& n, int& krow,
-                        int& kb) {
-        const uint32_t st = n % kPfStages;
-        if (!mbar_wait(&empty[st], ((n / kPfStages) & 1) ^ 1, abort, p.status)) return false;
-        kv_coord(p.pm, it.b, (it.j0 + t) * kPfKeys, krow, kb, p.status);  // a tile is one page when paged
-        mbar_arrive_expect_tx(&full[st], kTileBytes);
-        tma_load_4d(ring + st * kTileBytes, &tm_k, &full[st], 0, it.g, krow, kb);
-        tma_load_4d(ring + st * kTileBytes + kBox, &tm_k, &full[st], 64, it.g, krow, kb);
-        ++n;
-        return true;
-      };
       for (int rd = 0, item; (item = pf_item_index<kList>(p, rd)) >= 0; ++rd) {
         const PfItem it = pf_item<kF16, kSplit, kQ8>(p, bars, item);
         if (it.n_kv == 0) continue;
@@ -743,17 +731,31 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         ++q_it;
         if (kQ8 && !kList && q_it == 1) asm volatile("griddepcontrol.wait;" ::: "memory");
         bool ok = true;
-        int krow = 0, kb = 0;
-        // (A ring has one free stage while the item before is in its epilogue: the first key tile goes ahead of the
-        // second sample.)
-        for (int k = 0; kF16 && ok && k < it.n_pk; ++k)
-          ok = load_k(it, pf_sample_tile(k), sV, bars->v_full, bars->v_empty, v_it, krow, kb) &&
-               (k > 0 || load_k(it, 0, sK, bars->k_full, bars->k_empty, k_it, krow, kb));
-        for (int j = 0; ok && j < it.n_kv; ++j, ++v_it) {
-          const uint32_t st = v_it % kPfStages;
-          if (((!kF16 || j > 0 || it.n_pk == 0) &&
-               !load_k(it, j, sK, bars->k_full, bars->k_empty, k_it, krow, kb)) ||
-              !mbar_wait(&bars->v_empty[st], ((v_it / kPfStages) & 1) ^ 1, abort, p.status)) {
+        // The sampled key tiles (j < 0), in the V ring, which is idle until the first tile's P is there; then the K and V
+        // tiles of the unit.
+        for (int j = kF16 ? -it.n_pk : 0; j < it.n_kv; ++j) {
+          const bool sample = kF16 && j < 0;
+          const uint32_t n = sample ? v_it : k_it;
+          uint32_t st = n % kPfStages;
+          uint64_t* full = (sample ? bars->v_full : bars->k_full) + st;
+          uint8_t* dst = (sample ? sV : sK) + st * kTileBytes;
+          if (!mbar_wait((sample ? bars->v_empty : bars->k_empty) + st, ((n / kPfStages) & 1) ^ 1, abort, p.status)) {
+            ok = false;
+            break;
+          }
+          int krow, kb;
+          const int tile = it.j0 + (sample ? pf_sample_tile(j + it.n_pk) : j);
+          kv_coord(p.pm, it.b, tile * kPfKeys, krow, kb, p.status);  // a tile is one page when paged
+          mbar_arrive_expect_tx(full, kTileBytes);
+          tma_load_4d(dst, &tm_k, full, 0, it.g, krow, kb);
+          tma_load_4d(dst + kBox, &tm_k, full, 64, it.g, krow, kb);
+          if (sample) {
+            ++v_it;
+            continue;
+          }
+          ++k_it;
+          st = v_it % kPfStages;
+          if (!mbar_wait(&bars->v_empty[st], ((v_it / kPfStages) & 1) ^ 1, abort, p.status)) {
             ok = false;
             break;
           }
@@ -763,6 +765,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
           mbar_arrive_expect_tx(&bars->v_full[st], kTileBytes);
           tma_load_4d(sV + st * kTileBytes, &tm_v, &bars->v_full[st], 0, it.g, vrow, vb);
           tma_load_4d(sV + st * kTileBytes + kBox, &tm_v, &bars->v_full[st], 64, it.g, vrow, vb);
+          ++v_it;
         }
         if (!ok) break;
       }
@@ -792,19 +795,31 @@ __global__ void __launch_bounds__(kPfThreads, 1)
       const PfItem it = pf_item<kF16, kSplit, kQ8>(p, bars, item);
       if (it.n_kv == 0) continue;
       if (!__all_sync(0xffffffffu, mbar_wait(&bars->q_full, q_it & 1, abort, p.status))) break;
-      // The sampled tiles' logits, which the softmax warps read for their maximum and hand back as they do P.
-      for (int k = 0; kF16 && k < it.n_pk; ++k, ++v_it) {
-        const uint32_t st = v_it % kPfStages;
-        ok = __all_sync(0xffffffffu, mbar_wait(&bars->v_full[st], (v_it / kPfStages) & 1, abort, p.status));
+      // The logits of the sampled tiles (k < n_pk), which the softmax warps read for their maximum and hand back as they do
+      // P, then the first tile's.
+      for (int k = 0;; ++k) {
+        const bool sample = kF16 && k < it.n_pk;
+        const uint32_t n = sample ? v_it : k_it, st = n % kPfStages;
+        ok = __all_sync(0xffffffffu, mbar_wait((sample ? bars->v_full : bars->k_full) + st, (n / kPfStages) & 1, abort,
+                                               p.status));
         if (!ok) break;
         tc_fence_after();
         if (leader) {
-          pf_issue_qk(s_tm, qd, pd + st * kStageDesc);
+          const uint64_t d = (sample ? pd : kd) + st * kStageDesc;
+          if (it.n_sub >= 2)
+            pf_issue_qk(s_tm, qd, d);
+          else
+            pf_issue_qk_half(s_tm, qd, d);
           umma_commit(&bars->s_full[slot][0]);
-          umma_commit(&bars->s_full[slot][1]);
-          umma_commit(&bars->v_empty[st]);
+          if (it.n_sub >= 2) umma_commit(&bars->s_full[slot][1]);
+          // (the last tile's K and V stages are handed back by the epilogue, which
+          // stages the output in them)
+          if (sample || it.n_kv > 1) umma_commit((sample ? bars->v_empty : bars->k_empty) + st);
+          if (it.n_sub <= 2) umma_commit(&bars->q_empty);  // Q is read by no later product
         }
         __syncwarp();
+        if (!sample) break;
+        ++v_it;
         ok = __all_sync(0xffffffffu, mbar_wait(&bars->p_full[slot][0], pc0 & 1, abort, p.status) &&
                                          mbar_wait(&bars->p_full[slot][1], pc1 & 1, abort, p.status));
         if (!ok) break;
@@ -813,22 +828,6 @@ __global__ void __launch_bounds__(kPfThreads, 1)
       }
       if (!ok) break;
       {
-        const uint32_t st = k_it % kPfStages;
-        if (!__all_sync(0xffffffffu, mbar_wait(&bars->k_full[st], (k_it / kPfStages) & 1, abort, p.status))) break;
-        tc_fence_after();
-        if (leader) {
-          if (it.n_sub >= 2)
-            pf_issue_qk(s_tm, qd, kd + st * kStageDesc);
-          else
-            pf_issue_qk_half(s_tm, qd, kd + st * kStageDesc);
-          umma_commit(&bars->s_full[slot][0]);
-          if (it.n_sub >= 2) umma_commit(&bars->s_full[slot][1]);
-          // (the last tile's K and V stages are handed back by the epilogue, which
-          // stages the output in them)
-          if (it.n_kv > 1) umma_commit(&bars->k_empty[st]);
-          if (it.n_sub <= 2) umma_commit(&bars->q_empty);  // Q is read by no later product
-        }
-        __syncwarp();
         // The first tile's other inputs, waited while that product runs.
         const bool w = mbar_wait(&bars->v_full[v_it % kPfStages], (v_it / kPfStages) & 1, abort, p.status) &&
                        (it.n_sub <= 2 || mbar_wait(&bars->k_full[(k_it + 1) % kPfStages], ((k_it + 1) / kPfStages) & 1, abort, p.status)) &&
