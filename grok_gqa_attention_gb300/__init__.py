@@ -25,8 +25,12 @@ DEV_BAD_VALID = 0x2
 DEV_BAD_KV_LEN = 0x4
 DEV_TIMEOUT = 0x8
 DEV_BAD_PAGE = 0x10
+DEV_BAD_BLOCK = 0x20
+DEV_BAD_GROUP = 0x40
 
 PAGE_TOKENS = 128
+
+SPARSE_BLOCK = 64
 
 KV8_BLOCK = 64
 KV8_INT8 = 0
@@ -74,6 +78,12 @@ EXPORTS = (
     "grok_attn_prefill_ws_paged",
     "grok_attn_decode_paged",
     "grok_qkv_rope_append_paged",
+    "grok_kv_bounds_paged",
+    "grok_attn_select_paged",
+    "grok_attn_decode_sparse_workspace",
+    "grok_attn_decode_sparse_paged",
+    "grok_attn_decode_shared_workspace",
+    "grok_attn_decode_shared_paged",
     "grok_kv_insert_slot",
     "grok_attn_decode_step_workspace",
     "grok_attn_decode_step",
@@ -167,6 +177,18 @@ def load() -> ctypes.CDLL:
     lib.grok_attn_decode_paged.argtypes = [P, P, P, I, P, I, P, I, P, S, P, P]
     lib.grok_qkv_rope_append_paged.restype = I
     lib.grok_qkv_rope_append_paged.argtypes = [P, P, P, I, I, P, P, P, I, P, I, P, S, P, P]
+    lib.grok_kv_bounds_paged.restype = I
+    lib.grok_kv_bounds_paged.argtypes = [P, I, P, I, P, P, I, I, P, P, P, P]
+    lib.grok_attn_select_paged.restype = I
+    lib.grok_attn_select_paged.argtypes = [P, P, P, I, P, I, P, I, I, I, I, P, P, P, P]
+    lib.grok_attn_decode_sparse_workspace.restype = I
+    lib.grok_attn_decode_sparse_workspace.argtypes = [I, I, ctypes.POINTER(S)]
+    lib.grok_attn_decode_sparse_paged.restype = I
+    lib.grok_attn_decode_sparse_paged.argtypes = [P, P, P, I, P, I, P, P, I, I, P, S, P, P, P]
+    lib.grok_attn_decode_shared_workspace.restype = I
+    lib.grok_attn_decode_shared_workspace.argtypes = [I, I, I, ctypes.POINTER(S)]
+    lib.grok_attn_decode_shared_paged.restype = I
+    lib.grok_attn_decode_shared_paged.argtypes = [P, P, P, I, P, I, P, I, P, P, I, P, S, P, P, P]
     lib.grok_kv_insert_slot.restype = I
     lib.grok_kv_insert_slot.argtypes = [P, P, I, I, I, P, P, I, I, P, I, P]
     lib.grok_attn_decode_step_workspace.restype = I
@@ -699,3 +721,6 @@ def decode_step_chained(q, k, v, start_pos, cache_k, cache_v, workspace, out, de
 
 from .kv8 import (Kv8Cache, alloc_kv8_cache, alloc_kv8_decode_workspace, alloc_kv8_prefill_workspace,  # noqa: E402,F401
                   kv8_append, kv8_decode, kv8_decode_workspace, kv8_evict, kv8_prefill, kv8_prefill_workspace)
+from .sparse import (alloc_decode_shared_workspace, alloc_decode_sparse_workspace, alloc_kv_bounds,  # noqa: E402,F401
+                     decode_shared_paged, decode_shared_workspace, decode_sparse_paged, decode_sparse_workspace,
+                     kv_bounds_paged, select_blocks_paged)

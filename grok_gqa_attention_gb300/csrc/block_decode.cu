@@ -1,0 +1,571 @@
+// Decode over blocks of a paged cache: a list of blocks per KV head, or a sequence's
+// rows behind a prefix that it shares.
+//
+// Code-reading guide ch. 4 §4.4.1, §4.5.2-§4.5.4: out = sum_j w_j v_j / sum_j w_j,
+// w_j = exp(30 tanh(q . k_j / (30 sqrt(128))) - 30). Every capped logit is below 30,
+// so weights need no running maximum and partial sums simply add.
+//
+// Memory-bound: 32 KB of keys and values per block of 64 tokens and KV head are read
+// once. The blocks of all (sequence, KV head) pairs, in order, are dealt out to the
+// CTAs in equal contiguous shares whatever the lengths. A producer warp finds the
+// blocks (32 at a time, one a lane) and streams them through a ring of three stages
+// by TMA, with the pair's six queries beside its first block; four warps take 16 keys
+// of each block. On mma.sync (bf16 operands, fp32 accumulators):
+//   S^T [16 keys x 8 heads] = K q^T, O^T [128 x 8] += V^T P^T
+// (6 of 8 columns used; rows of heads would use 6 of 16). P is split into two bf16
+// halves, so a weight is off by 2^-16. S^T leaves the accumulators as P^T needs it but
+// for an 8 x 8 transpose per register. A warp writes its partial sums where its share
+// of a pair ends, and no barrier joins the warps; a second kernel, launched as a
+// dependent, adds a pair's partial sums in their order.
+#include "block_decode.cuh"
+
+namespace grok {
+
+constexpr int kBkThreads = (kBkWarps + 1) * 32;
+constexpr int kBkStages = 3;
+constexpr int kBkBox = kBlk * 128;           // [64 rows][64 bf16]
+constexpr int kBkQ = kGroup * kD * 2;        // a pair's queries
+constexpr int kBkStage = 4 * kBkBox;         // K halves, V halves
+constexpr int kBkPlan = 1024;                // entries of the table of block counts
+constexpr int kBkCtas = 2;                   // CTAs resident on an SM
+
+struct BkShared {
+  uint64_t full[kBkStages], empty[kBkStages];
+  int2 token[kBkStages];  // pair and visible keys of the block in a stage; pair -1: the end
+  int cum[kBkPlan + 1];   // blocks per KV head of the sequences before each entry's
+  int warp_sum[kBkWarps + 1];
+  int abort;
+};
+constexpr int kBkSmem = 1024 + kBkStages * (kBkStage + kBkQ) + int(sizeof(BkShared));
+static_assert(kBkCtas * (kBkSmem + 1024) <= 233472, "shared memory per SM");
+
+struct BkParams {
+  const uint8_t* q;
+  PageMap pm;
+  const int32_t* kv_len;
+  int B;
+  const int32_t* sel;
+  int budget;
+  Groups groups;
+  BlockParts parts;
+  int4* prefix_pair;  // entries of sequences without a prefix are cleared here
+  int32_t* status;
+};
+
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(smem_u32(dst)),
+      "l"(src), "r"(bytes), "r"(smem_u32(bar))
+      : "memory");
+}
+__device__ __forceinline__ uint32_t movmatrix_trans(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
+// Blocks that sequence b reads per KV head; -1 when its length is bad. share: its pages in common (not kList).
+template <bool kList>
+__device__ __forceinline__ int bk_blocks(const BkParams& p, int b, bool groups, int& share) {
+  const int cap = p.pm.max_pages * GROK_PAGE_TOKENS, len = p.kv_len[b];
+  share = !kList && groups ? seq_pages(p.groups, b) : 0;
+  if (len < 1 || len > cap || len < share * GROK_PAGE_TOKENS) return -1;
+  const int n = (len + kBlk - 1) / kBlk - share * kBlkPerPage;
+  return kList ? min(n, p.budget) : n;
+}
+
+template <bool kList>
+__global__ void __launch_bounds__(kBkThreads, kBkCtas)
+    block_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                        const BkParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sq = smem + kBkStages * kBkStage;
+  BkShared* sh = reinterpret_cast<BkShared*>(sq + kBkStages * kBkQ);
+  volatile int* abort = &sh->abort;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  // The kernel that joins the partial results may be scheduled as soon as every CTA has started.
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (tid == 0) {
+    for (int s = 0; s < kBkStages; ++s) {
+      mbar_init(&sh->full[s], 1);
+      mbar_init(&sh->empty[s], kBkWarps);
+    }
+    sh->abort = 0;
+    fence_barrier_init();
+    prefetch_tmap(&tm_k);
+    prefetch_tmap(&tm_v);
+  }
+
+  // The plan: blocks per KV head before each sequence (or each `step` sequences, where there are many).
+  const bool groups = !kList && groups_ok(p.groups, p.B, p.pm.max_pages);
+  if (!kList && !groups && blockIdx.x == 0 && tid == 0) report(p.status, GROK_DEV_BAD_GROUP);
+  const int step = (p.B + kBkPlan - 1) / kBkPlan, entries = (p.B + step - 1) / step;
+  {
+    const int per = (entries + kBkThreads - 1) / kBkThreads;  // contiguous entries per thread
+    const int e0 = min(tid * per, entries), e1 = min(e0 + per, entries);
+    int mine = 0;
+    for (int b = e0 * step; b < min(e1 * step, p.B); ++b) {
+      int share;
+      const int n = bk_blocks<kList>(p, b, groups, share);
+      if (blockIdx.x == 0) {
+        if (n < 0) report(p.status, GROK_DEV_BAD_KV_LEN);
+        if (n <= 0)
+          for (int g = 0; g < kKVHeads; ++g) p.parts.pair[b * kKVHeads + g] = make_int2(0, n);
+        if (!kList && share == 0)
+          for (int g = 0; g < kKVHeads; ++g) p.prefix_pair[b * kKVHeads + g] = make_int4(0, 0, 0, 0);
+      }
+      mine += max(n, 0);
+    }
+    int incl = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) {
+      const int up = __shfl_up_sync(0xffffffffu, incl, d);
+      if (lane >= d) incl += up;
+    }
+    if (lane == 31) sh->warp_sum[warp] = incl;
+    __syncthreads();
+    int at = incl - mine;
+    for (int w = 0; w < warp; ++w) at += sh->warp_sum[w];
+    for (int e = e0; e < e1; ++e) {
+      sh->cum[e] = at;
+      for (int b = e * step; b < min((e + 1) * step, p.B); ++b) {
+        int share;
+        at += max(bk_blocks<kList>(p, b, groups, share), 0);
+      }
+    }
+    if (e1 == entries && e0 < e1) sh->cum[entries] = at;
+  }
+  __syncthreads();
+  const int total = kKVHeads * sh->cum[entries];
+  const int share_of = max(1, (total + int(gridDim.x) - 1) / int(gridDim.x));  // blocks per CTA
+  const int cta = blockIdx.x;
+  const int lo = min((long long)cta * share_of, (long long)total), hi = min(lo + share_of, total);
+  if (lo < hi) {
+    if (warp == kBkWarps) {
+      // ------------------------------------------------------------ producer
+      int it = 0;          // tokens so far
+      int cur = -1;        // the pair of the last block looked at
+      bool sent = true;    // a token of that pair is out
+      bool ok = true;
+      // A stage for the next token; false when a bounded wait gave up.
+      auto acquire = [&]() {
+        ok = __all_sync(0xffffffffu, it < kBkStages || mbar_wait(&sh->empty[it % kBkStages],
+                                                                 ((it / kBkStages) & 1) ^ 1, abort, p.status));
+        return ok;
+      };
+      auto send_empty = [&](int pair) {  // a token without a block
+        if (!acquire()) return;
+        if (lane == 0) {
+          sh->token[it % kBkStages] = make_int2(pair, 0);
+          mbar_arrive(&sh->full[it % kBkStages]);
+        }
+        ++it;
+      };
+      for (int base = lo; base < hi && ok; base += 32) {
+        const int cnt = min(32, hi - base), idx = base + lane;
+        int my_pair = 0, my_row = -1, my_keys = 0;  // (row of the pools; -1: no block here)
+        if (lane < cnt) {
+          int e = 0;
+          for (int d = kBkPlan / 2; d; d /= 2)
+            if (e + d < entries && kKVHeads * sh->cum[e + d] <= idx) e += d;
+          int rest = idx - kKVHeads * sh->cum[e], b = e * step, share, n;
+          while (n = max(bk_blocks<kList>(p, b, groups, share), 0), rest >= kKVHeads * n) {
+            rest -= kKVHeads * n;
+            ++b;
+          }
+          const int g = rest / n, k = rest % n;
+          my_pair = b * kKVHeads + g;
+          if (k == 0) {  // the pair's parts: one of each CTA from this one on that takes some of its blocks
+            const int last = (idx + n - 1) / share_of;
+            p.parts.pair[my_pair] = make_int2(cta + my_pair, last - cta + 1);
+          }
+          const int len = p.kv_len[b], blocks = (len + kBlk - 1) / kBlk;
+          int blk = share * kBlkPerPage + k;
+          if (kList) blk = p.sel[(size_t)my_pair * p.budget + k];
+          if (blk >= blocks) {
+            report(p.status, GROK_DEV_BAD_BLOCK);
+          } else if (blk >= 0) {
+            my_row = max(0, blk_page(p.pm, b, blk, p.status)) * GROK_PAGE_TOKENS + blk % kBlkPerPage * kBlk;
+            my_keys = min(kBlk, len - blk * kBlk);
+          }
+        }
+        for (int j = 0; j < cnt && ok; ++j) {
+          const int pair = __shfl_sync(0xffffffffu, my_pair, j), row = __shfl_sync(0xffffffffu, my_row, j);
+          const int keys = __shfl_sync(0xffffffffu, my_keys, j);
+          if (pair != cur) {
+            if (!sent) send_empty(cur);  // nothing of the last pair's list here: its part is zero
+            cur = pair;
+            sent = false;
+          }
+          if (row < 0 || !ok || !acquire()) continue;
+          if (lane == 0) {
+            const int st = it % kBkStages, g = pair % kKVHeads;
+            uint8_t* dst = smem + st * kBkStage;
+            sh->token[st] = make_int2(pair, keys);
+            mbar_arrive_expect_tx(&sh->full[st], kBkStage + (sent ? 0 : kBkQ));
+            if (!sent) bulk_load(sq + st * kBkQ, p.q + (size_t)pair * kBkQ, kBkQ, &sh->full[st]);
+            tma_load_4d(dst, &tm_k, &sh->full[st], 0, g, row, 0);
+            tma_load_4d(dst + kBkBox, &tm_k, &sh->full[st], 64, g, row, 0);
+            tma_load_4d(dst + 2 * kBkBox, &tm_v, &sh->full[st], 0, g, row, 0);
+            tma_load_4d(dst + 3 * kBkBox, &tm_v, &sh->full[st], 64, g, row, 0);
+          }
+          sent = true;
+          ++it;
+        }
+      }
+      if (ok && !sent) send_empty(cur);
+      if (ok) send_empty(-1);
+      // Copies in flight (only after an abort) land before the CTA exits.
+      volatile int never = 0;
+      if (lane == 0)
+        for (int t = max(0, it - kBkStages); t < it; ++t)
+          mbar_wait(&sh->full[t % kBkStages], (t / kBkStages) & 1, &never, p.status);
+    } else {
+      // ------------------------------------------------------------ 16 keys of each block
+      const int row = lane >> 2, t = lane & 3, mi = lane >> 3, mr = lane & 7;
+      const uint32_t sbase = smem_u32(smem);
+      uint32_t qb[8][2];
+      float o[8][4], l0 = 0.f, l1 = 0.f;  // columns 2 t, 2 t + 1
+      int cur = -1;
+      for (int it = 0;; ++it) {
+        const int st = it % kBkStages;
+        if (!__all_sync(0xffffffffu, mbar_wait(&sh->full[st], (it / kBkStages) & 1, abort, p.status))) break;
+        const int2 tok = sh->token[st];
+        if (tok.x != cur) {
+          if (cur >= 0) {  // the partial sums of this CTA's share of the pair
+            const size_t slot = ((size_t)cta + cur) * kBkWarps + warp;
+#pragma unroll
+            for (int d = 4; d < 32; d *= 2) {
+              l0 += __shfl_xor_sync(0xffffffffu, l0, d);
+              l1 += __shfl_xor_sync(0xffffffffu, l1, d);
+            }
+#pragma unroll
+            for (int mt = 0; mt < 8; ++mt)
+              p.parts.o[slot * kBkPartO + mt * 32 + lane] = make_float4(o[mt][0], o[mt][1], o[mt][2], o[mt][3]);
+            if (row == 0) *reinterpret_cast<float2*>(p.parts.l + slot * 8 + 2 * t) = make_float2(l0, l1);
+          }
+          cur = tok.x;
+          if (cur < 0) break;
+          l0 = l1 = 0.f;
+#pragma unroll
+          for (int mt = 0; mt < 8; ++mt) o[mt][0] = o[mt][1] = o[mt][2] = o[mt][3] = 0.f;
+          const uint32_t* qs = reinterpret_cast<const uint32_t*>(sq + st * kBkQ) + row * (kD / 2) + t;
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk) {
+            qb[kk][0] = row < kGroup && tok.y > 0 ? qs[kk * 8] : 0u;
+            qb[kk][1] = row < kGroup && tok.y > 0 ? qs[kk * 8 + 4] : 0u;
+          }
+        }
+        const int key0 = warp * 16;
+        if (key0 < tok.y) {
+          const uint32_t kb = sbase + st * kBkStage, vb = kb + 2 * kBkBox;
+          float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk) {
+            uint32_t a[4];
+            ldsm_x4(kb + (kk >> 2) * kBkBox + sw128_offset(key0 + (mi & 1) * 8 + mr, (kk & 3) * 16 + (mi >> 1) * 8),
+                    a[0], a[1], a[2], a[3]);
+            mma_bf16_16816(s[kk & 1], a, qb[kk][0], qb[kk][1]);
+          }
+          const bool in0 = key0 + row < tok.y, in1 = key0 + 8 + row < tok.y;
+          const float w0 = in0 ? capped_weight_precise(s[0][0] + s[1][0]) : 0.f;
+          const float w1 = in0 ? capped_weight_precise(s[0][1] + s[1][1]) : 0.f;
+          const float w2 = in1 ? capped_weight_precise(s[0][2] + s[1][2]) : 0.f;
+          const float w3 = in1 ? capped_weight_precise(s[0][3] + s[1][3]) : 0.f;
+          l0 += w0 + w2;
+          l1 += w1 + w3;
+          uint32_t h0, h1, e0, e1;
+          split_bf16x2(w0, w1, h0, e0);
+          split_bf16x2(w2, w3, h1, e1);
+          h0 = movmatrix_trans(h0);
+          h1 = movmatrix_trans(h1);
+          e0 = movmatrix_trans(e0);
+          e1 = movmatrix_trans(e1);
+          const bool tail = key0 + 16 > tok.y;  // rows behind the last may hold anything
+          uint32_t m0 = 0xFFFFFFFFu, m1 = 0xFFFFFFFFu;
+          if (tail) {
+            const int k0 = key0 + 2 * t;
+            m0 = (k0 < tok.y ? 0x0000FFFFu : 0u) | (k0 + 1 < tok.y ? 0xFFFF0000u : 0u);
+            m1 = (k0 + 8 < tok.y ? 0x0000FFFFu : 0u) | (k0 + 9 < tok.y ? 0xFFFF0000u : 0u);
+          }
+#pragma unroll
+          for (int mt = 0; mt < 8; ++mt) {
+            uint32_t a[4];
+            ldsm_x4_t(vb + (mt >> 2) * kBkBox + sw128_offset(key0 + (mi >> 1) * 8 + mr, (mt & 3) * 16 + (mi & 1) * 8),
+                      a[0], a[1], a[2], a[3]);
+            if (tail) {
+              a[0] &= m0;
+              a[1] &= m0;
+              a[2] &= m1;
+              a[3] &= m1;
+            }
+            mma_bf16_16816(o[mt], a, h0, h1);
+            mma_bf16_16816(o[mt], a, e0, e1);
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh->empty[st]);
+      }
+    }
+  }
+  // Started as the dependent of the prefix kernel, this one ends behind it, so that the kernel that waits for this one
+  // finds both results (a no-op otherwise).
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+// ----------------------------------------------------------------------------
+// out = (sum of the partial O) / (sum of the partial l) of one (sequence, KV head).
+// Four teams of 256 threads take one warp's parts each, in order.
+constexpr int kJnTeams = kBkWarps;
+constexpr int kJnThreads = kJnTeams * kBkPartO;
+
+template <bool kPrefix>
+__global__ void __launch_bounds__(kJnThreads) block_join_kernel(const BlockParts parts, const PrefixParts prefix,
+                                                                const PageMap pm, uint2* __restrict__ out,
+                                                                int32_t* status) {
+  __shared__ float4 so[kJnTeams][kBkPartO];
+  __shared__ float sl[kJnTeams][8];
+  __shared__ float acc[kGroup][kD + 4];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int g = blockIdx.x, b = blockIdx.y, pair = b * kKVHeads + g;
+  const int tid = threadIdx.x, team = tid / kBkPartO, at = tid % kBkPartO;
+  const int2 mine = parts.pair[pair];
+  if (mine.y < 0) return;  // (the whole CTA)
+  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+  float l = 0.f;
+  const size_t s0 = (size_t)mine.x * kBkWarps + team;
+#pragma unroll 8
+  for (int i = 0; i < mine.y; ++i) {
+    const size_t s = s0 + (size_t)i * kBkWarps;
+    const float4 x = parts.o[s * kBkPartO + at];
+    v.x += x.x;
+    v.y += x.y;
+    v.z += x.z;
+    v.w += x.w;
+    if (at < 8) l += parts.l[s * 8 + at];
+  }
+  so[team][at] = v;
+  if (at < 8) sl[team][at] = l;
+  // The prefix's parts: thread (head, feature quad).
+  float4 pv = make_float4(0.f, 0.f, 0.f, 0.f);
+  float pl = 0.f;
+  const int h = tid % kGroup, quad = tid / kGroup;
+  const int4 pre = kPrefix ? prefix.pair[pair] : make_int4(0, 0, 0, 0);
+  if (kPrefix && quad >= kD / 4 && g == 0) {  // the other threads: does the table agree with the one that was read?
+    const int seq = pre.w & 0xFFFF;
+    for (int i = tid - kGroup * kD / 4; i < int(uint32_t(pre.w) >> 16); i += kJnThreads - kGroup * kD / 4)
+      if (pm.table[(size_t)b * pm.max_pages + i] != pm.table[(size_t)seq * pm.max_pages + i])
+        report(status, GROK_DEV_BAD_GROUP);
+  }
+  if (kPrefix && quad < kD / 4) {
+    const int r = pre.z + h;
+#pragma unroll 4
+    for (int i = 0; i < pre.y; ++i) {
+      const size_t s = (size_t)pre.x + i;
+      const float4 x = prefix.o[(s * (kD / 4) + quad) * kPxRows + r];
+      pv.x += x.x;
+      pv.y += x.y;
+      pv.z += x.z;
+      pv.w += x.w;
+      pl += prefix.l[(s * 2) * kPxRows + r] + prefix.l[(s * 2 + 1) * kPxRows + r];
+    }
+  }
+  __syncthreads();
+  if (team == 0) {
+#pragma unroll
+    for (int w = 1; w < kJnTeams; ++w) {
+      const float4 x = so[w][at];
+      v.x += x.x;
+      v.y += x.y;
+      v.z += x.z;
+      v.w += x.w;
+    }
+    // accumulator layout: features 16 mt + row (+ 8) of heads 2 t, 2 t + 1
+    const int d = at / 32 * 16 + at % 32 / 4, c = at % 4 * 2;
+    if (c < kGroup) {
+      acc[c][d] = v.x;
+      acc[c + 1][d] = v.y;
+      acc[c][d + 8] = v.z;
+      acc[c + 1][d + 8] = v.w;
+    }
+  }
+  __syncthreads();
+  if (quad < kD / 4) {
+    float sum = pl;
+#pragma unroll
+    for (int w = 0; w < kJnTeams; ++w) sum += sl[w][h];
+    const float inv = sum == 0.f ? 0.f : 1.0f / sum;  // (a list without a block: zeros)
+    const float* x = &acc[h][quad * 4];
+    out[((size_t)pair * kGroup + h) * (kD / 4) + quad] =
+        make_uint2(pack_bf16x2((x[0] + pv.x) * inv, (x[1] + pv.y) * inv),
+                   pack_bf16x2((x[2] + pv.z) * inv, (x[3] + pv.w) * inv));
+  }
+}
+
+// ----------------------------------------------------------------------------
+static size_t up256(size_t n) { return (n + 255) & ~size_t(255); }
+static size_t bk_slots(int B, int sms) { return (size_t)B * kKVHeads + (size_t)kBkCtas * sms; }
+static BlockParts block_parts(char* ws, int B, int sms) {
+  const size_t slots = bk_slots(B, sms) * kBkWarps;
+  BlockParts p;
+  p.o = reinterpret_cast<float4*>(ws);
+  ws += up256(slots * kBkPartO * sizeof(float4));
+  p.l = reinterpret_cast<float*>(ws);
+  ws += up256(slots * 8 * sizeof(float));
+  p.pair = reinterpret_cast<int2*>(ws);
+  return p;
+}
+size_t block_parts_bytes(int B, int sms) {
+  const size_t slots = bk_slots(B, sms) * kBkWarps;
+  return up256(slots * kBkPartO * sizeof(float4)) + up256(slots * 8 * sizeof(float)) +
+         up256((size_t)B * kKVHeads * sizeof(int2));
+}
+
+// Query tiles of the prefix kernel: sum of ceil(n_i / 21) over groups of two sequences at least.
+static size_t px_slots(int B, int n_groups, int sms) {
+  const size_t tiles = min(B / 2, B / kPxSeqs + n_groups);
+  return tiles * kKVHeads + sms;
+}
+PrefixParts prefix_parts(char* ws, int B, int n_groups, int sms) {
+  const size_t slots = px_slots(B, n_groups, sms);
+  PrefixParts p;
+  p.o = reinterpret_cast<float4*>(ws);
+  ws += slots * kPxRows * kD * 4;
+  p.l = reinterpret_cast<float*>(ws);
+  ws += slots * 2 * kPxRows * 4;
+  p.pair = reinterpret_cast<int4*>(ws);
+  return p;
+}
+size_t prefix_parts_bytes(int B, int n_groups, int sms) {
+  return px_slots(B, n_groups, sms) * kPxRows * (kD * 4 + 8) + up256((size_t)B * kKVHeads * sizeof(int4));
+}
+
+template <bool kList>
+static grok_status bk_launch(const BlockArgs& a, const BkParams& p, int sms) {
+  CUtensorMap tk, tv;
+  const uint64_t rows = uint64_t(a.pm.n_pages) * GROK_PAGE_TOKENS;
+  const uint64_t dims[4] = {kD, kKVHeads, rows, 1};
+  const uint64_t strides[3] = {kD * 2, uint64_t(kKVHeads) * kD * 2, rows * kKVHeads * kD * 2};
+  const uint32_t box[4] = {64, 1, kBlk, 1};
+  grok_status st;
+  if ((st = encode_tmap_bf16_4d(&tk, a.k_pool, dims, strides, box)) != GROK_OK) return st;
+  if ((st = encode_tmap_bf16_4d(&tv, a.v_pool, dims, strides, box)) != GROK_OK) return st;
+  static bool attr_set[kMaxDevices] = {};  // per device; idempotent: every thread would set the same value
+  int dev = 0;
+  if ((st = device_index(&dev)) != GROK_OK) return st;
+  cudaError_t e;
+  if (!attr_set[dev]) {
+    e = cudaFuncSetAttribute(block_decode_kernel<kList>, cudaFuncAttributeMaxDynamicSharedMemorySize, kBkSmem);
+    if (e != cudaSuccess) return fail(cuda_status(e), "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
+    attr_set[dev] = true;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  cfg.gridDim = dim3(kBkCtas * sms);
+  cfg.blockDim = dim3(kBkThreads);
+  cfg.dynamicSmemBytes = kBkSmem;
+  cfg.stream = a.stream;
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = kList ? 0 : 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, block_decode_kernel<kList>, tk, tv, p);
+  if (e != cudaSuccess) return fail(cuda_status(e), "block decode launch: %s", cudaGetErrorString(e));
+  return check_launch("block decode");
+}
+
+grok_status block_decode_run(const BlockArgs& a, char* ws, const PrefixParts* prefix, int sms) {
+  BkParams p;
+  p.q = reinterpret_cast<const uint8_t*>(a.q_rot);
+  p.pm = a.pm;
+  p.kv_len = a.kv_len;
+  p.B = a.B;
+  p.sel = a.sel;
+  p.budget = a.budget;
+  p.groups = a.groups;
+  p.parts = block_parts(ws, a.B, sms);
+  p.prefix_pair = prefix ? prefix->pair : nullptr;
+  p.status = a.status;
+  grok_status st = a.sel ? bk_launch<true>(a, p, sms) : bk_launch<false>(a, p, sms);
+  if (st != GROK_OK) return st;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  cfg.gridDim = dim3(kKVHeads, a.B);
+  cfg.blockDim = dim3(kJnThreads);
+  cfg.stream = a.stream;
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  uint2* out = reinterpret_cast<uint2*>(a.out);
+  const cudaError_t e =
+      prefix ? cudaLaunchKernelEx(&cfg, block_join_kernel<true>, p.parts, *prefix, a.pm, out, a.status)
+             : cudaLaunchKernelEx(&cfg, block_join_kernel<false>, p.parts, PrefixParts{}, a.pm, out, a.status);
+  if (e != cudaSuccess) return fail(cuda_status(e), "block join launch: %s", cudaGetErrorString(e));
+  return check_launch("block join");
+}
+
+grok_status page_args(int n_pages, int max_pages, int B, const char* who) {
+  if (n_pages < 1 || max_pages < 1 || (long long)n_pages * GROK_PAGE_TOKENS > (1LL << 31) - 1 ||
+      (long long)max_pages * GROK_PAGE_TOKENS > GROK_MAX_POSITION || B < 1 || B > 65535)
+    return fail(GROK_ERR_INVALID_ARG,
+                "%s: need 1 <= n_pages < 2^24, 1 <= max_pages <= %d, 1 <= B <= 65535 (n_pages=%d max_pages=%d B=%d)", who,
+                GROK_MAX_POSITION / GROK_PAGE_TOKENS, n_pages, max_pages, B);
+  return GROK_OK;
+}
+
+}  // namespace grok
+
+using namespace grok;
+
+extern "C" grok_status grok_attn_decode_sparse_workspace(int B, int budget, size_t* bytes) {
+  if (!bytes) return fail(GROK_ERR_INVALID_ARG, "grok_attn_decode_sparse_workspace: null pointer");
+  if (B < 1 || B > 65535 || budget < 1 || budget > kBlkMax)
+    return fail(GROK_ERR_INVALID_ARG,
+                "grok_attn_decode_sparse_workspace: need 1 <= B <= 65535, 1 <= budget <= %d (B=%d budget=%d)", kBlkMax, B,
+                budget);
+  int sms = 0;
+  const grok_status st = device_sm_count(&sms);
+  if (st != GROK_OK) return st;
+  *bytes = block_parts_bytes(B, sms);
+  return GROK_OK;
+}
+
+extern "C" grok_status grok_attn_decode_sparse_paged(const grok_bf16* q_rot, const grok_bf16* k_pool,
+                                                     const grok_bf16* v_pool, int n_pages, const int32_t* block_table,
+                                                     int max_pages, const int32_t* kv_len, const int32_t* sel,
+                                                     int budget, int B, void* workspace, size_t workspace_bytes,
+                                                     grok_bf16* out, int32_t* dev_status, void* stream) {
+  const char* who = "grok_attn_decode_sparse_paged";
+  if (!q_rot || !k_pool || !v_pool || !block_table || !kv_len || !sel || !workspace || !out)
+    return fail(GROK_ERR_INVALID_ARG, "%s: null pointer", who);
+  if (!aligned16(q_rot) || !aligned16(k_pool) || !aligned16(v_pool) || !aligned16(out))
+    return fail(GROK_ERR_INVALID_ARG, "%s: bf16 tensors must be 16-byte aligned", who);
+  if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
+    return fail(GROK_ERR_INVALID_ARG, "%s: workspace must be 256-byte aligned", who);
+  grok_status st = page_args(n_pages, max_pages, B, who);
+  if (st != GROK_OK) return st;
+  if (budget < 1 || budget > kBlkMax)
+    return fail(GROK_ERR_INVALID_ARG, "%s: need 1 <= budget <= %d (budget=%d)", who, kBlkMax, budget);
+  int sms = 0;
+  if ((st = device_sm_count(&sms)) != GROK_OK) return st;
+  const size_t need = block_parts_bytes(B, sms);
+  if (workspace_bytes < need)
+    return fail(GROK_ERR_INVALID_ARG, "%s: workspace of %zu bytes is smaller than the %zu needed", who, workspace_bytes,
+                need);
+  BlockArgs a = {};
+  a.q_rot = q_rot;
+  a.k_pool = k_pool;
+  a.v_pool = v_pool;
+  a.pm = PageMap{block_table, max_pages, n_pages};
+  a.kv_len = kv_len;
+  a.B = B;
+  a.sel = sel;
+  a.budget = budget;
+  a.out = out;
+  a.status = dev_status;
+  a.stream = static_cast<cudaStream_t>(stream);
+  return block_decode_run(a, static_cast<char*>(workspace), nullptr, sms);
+}

@@ -1,0 +1,87 @@
+// Attention of one token per sequence over 64-token blocks of a paged cache
+// (block_decode.cu), used over a list of blocks per KV head (grok_attn_decode_sparse_paged)
+// and over the rows behind a shared prefix (grok_attn_decode_shared_paged).
+#pragma once
+
+#include "blocks.cuh"
+#include "host.cuh"
+
+namespace grok {
+
+constexpr int kGroupsMax = 1024;  // groups of sequences with a common prefix
+constexpr int kPxSeqs = 21;       // sequences per query tile of the prefix kernel: 126 of its 128 rows
+
+// Sequences [start[i], start[i + 1]) have their first pages[i] pages in common.
+struct Groups {
+  const int32_t* start;
+  const int32_t* pages;
+  int n;
+};
+
+// Whether the groups are usable: starts in order within [0, B], pages within [0, max_pages]. The whole CTA calls this.
+__device__ __forceinline__ bool groups_ok(const Groups& gr, int B, int max_pages) {
+  bool bad = false;
+  for (int i = threadIdx.x; i < gr.n; i += blockDim.x) {
+    const int a = gr.start[i], z = gr.start[i + 1], pg = gr.pages[i];
+    bad |= a < 0 || z < a || z > B || pg < 0 || pg > max_pages;
+  }
+  return !__syncthreads_or(bad);
+}
+
+// Pages that a group's sequences are given in common: a group of one has nothing to share.
+__device__ __forceinline__ int group_pages(const Groups& gr, int i) {
+  return gr.start[i + 1] - gr.start[i] < 2 ? 0 : gr.pages[i];
+}
+// Those of sequence b (the groups are usable).
+__device__ __forceinline__ int seq_pages(const Groups& gr, int b) {
+  int lo = 0, hi = gr.n;  // start[lo] <= b < start[hi], where there is such a group
+  if (b < gr.start[0] || b >= gr.start[gr.n]) return 0;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (gr.start[mid] <= b) lo = mid; else hi = mid;
+  }
+  return group_pages(gr, lo);
+}
+
+// Partial results of the block kernel, per (part, warp): the sums O in the layout of the products' accumulators
+// (float4 [8 tiles of 16 features][32 lanes]) and the weights' sums of 8 columns (6 heads, 2 unused).
+constexpr int kBkWarps = 4;
+constexpr int kBkPartO = 8 * 32;  // float4s
+struct BlockParts {
+  float4* o;
+  float* l;
+  int2* pair;  // [B * 8]: first part and number of parts; number -1: the sequence is skipped
+};
+// Partial results of the prefix kernel, per part: O as float4 [32 feature quads][128 rows], and two sums per row.
+constexpr int kPxRows = 128;
+struct PrefixParts {
+  float4* o;
+  float* l;
+  int4* pair;  // [B * 8]: first part, number of parts, the sequence's first row, pages << 16 | the sequence whose table is read
+};
+
+struct BlockArgs {
+  const grok_bf16* q_rot;
+  const grok_bf16* k_pool;
+  const grok_bf16* v_pool;
+  PageMap pm;
+  const int32_t* kv_len;
+  int B;
+  const int32_t* sel;  // nullptr: the rows behind the groups' prefixes
+  int budget;
+  Groups groups;
+  grok_bf16* out;
+  int32_t* status;
+  cudaStream_t stream;
+};
+
+size_t block_parts_bytes(int B, int sms);
+size_t prefix_parts_bytes(int B, int n_groups, int sms);
+// The block kernel, then the kernel that joins its partial results (and, where prefix is given, the prefix kernel's,
+// which was launched before on the stream).
+grok_status block_decode_run(const BlockArgs& a, char* ws, const PrefixParts* prefix, int sms);
+PrefixParts prefix_parts(char* ws, int B, int n_groups, int sms);
+
+grok_status page_args(int n_pages, int max_pages, int B, const char* who);
+
+}  // namespace grok

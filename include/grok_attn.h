@@ -28,6 +28,9 @@
  *   runtime             grok_prefill_pipe_create / _submit / _wait / _destroy
  *   paged cache         grok_rope_kv_append_paged, grok_attn_prefill_paged, grok_attn_prefill_ws_paged,
  *                       grok_attn_decode_paged, grok_qkv_rope_append_paged
+ *   parts of the cache  grok_kv_bounds_paged, grok_attn_select_paged,
+ *                       grok_attn_decode_sparse_paged, grok_attn_decode_sparse_workspace,
+ *                       grok_attn_decode_shared_paged, grok_attn_decode_shared_workspace
  *   continuous batching grok_kv_insert_slot
  *   8-bit cache         grok_kv8_append, grok_kv8_decode(_workspace), grok_kv8_prefill(_workspace),
  *                       grok_kv8_evict
@@ -102,9 +105,14 @@ typedef enum {
 #define GROK_DEV_BAD_KV_LEN 0x4  /* kv_len[b] outside [1, Tmax] */
 #define GROK_DEV_TIMEOUT 0x8     /* a bounded wait inside a kernel gave up */
 #define GROK_DEV_BAD_PAGE 0x10   /* a block-table entry the paged calls need lies outside [0, n_pages) */
+#define GROK_DEV_BAD_BLOCK 0x20  /* a listed block lies behind the sequence's last row */
+#define GROK_DEV_BAD_GROUP 0x40  /* groups out of order or range, or sequences of a group with unequal table entries */
 
 /* Tokens per page of the paged KV cache (one prefill key tile). */
 #define GROK_PAGE_TOKENS 128
+
+/* Tokens per block of the calls that read part of a paged cache (two blocks to a page). */
+#define GROK_SPARSE_BLOCK 64
 
 /* The 8-bit KV cache: tokens per block, and the element types of its codes. */
 #define GROK_KV8_BLOCK 64
@@ -524,6 +532,95 @@ grok_status grok_qkv_rope_append_paged(const grok_bf16* x, const grok_bf16* w, c
                                        int T, grok_bf16* q_rot, grok_bf16* k_pool, grok_bf16* v_pool, int n_pages,
                                        const int32_t* block_table, int max_pages, void* workspace, size_t ws_bytes,
                                        int32_t* dev_status, void* stream);
+
+/*
+ * Decode that reads part of a paged cache. A decode step is bound by the rows that
+ * it reads (ch. 4 §4.4.1: all of them); these calls leave out rows that hardly
+ * count, and read rows that several sequences have in common once. They work on the
+ * pools and block tables of the paged calls above. (A contiguous cache whose Tmax is
+ * a multiple of 128 is a pool of B * Tmax / 128 pages with the table 0, 1, 2, ...)
+ * A block is GROK_SPARSE_BLOCK = 64 tokens, half a page; block i of a sequence holds
+ * its rows [64 i, 64 i + 64). 1 <= B <= 65535, max_pages * 128 <= GROK_MAX_POSITION,
+ * n_pages * 128 < 2^31.
+ *
+ * grok_kv_bounds_paged: bounds of the keys of every block that rows [start_pos[b],
+ *   start_pos[b] + valid_len[b]) of sequence b touch, from the block's rows up to the last
+ *   of them; call it after each append, with the append's start_pos and T.
+ *   codes int8 [n_pages, 2, 8, 2, 128] (block of the page, KV head, upper and lower
+ *   bound, feature), scale fp32 [n_pages, 2, 8]. With a = max |k| over the block's rows
+ *   of the head, scale = 2^e, e the least integer with a <= 127 * 2^e, kept within
+ *   [-32, 16]; upper = ceil(max k / 2^e), lower = floor(min k / 2^e), kept within
+ *   [-127, 127]; a NaN counts as the infinity of its sign. Other blocks' entries are left as
+ *   they were. Nothing but the rows counts: rows may be dropped and written again, so
+ *   long as the blocks that change are given to this call.
+ *   start_pos [B], valid_len [B] int32 or NULL (= T). start_pos[b] < 0 or start_pos[b] + T >
+ *   max_pages * 128 sets GROK_DEV_BAD_START, valid_len[b] outside [1, T] GROK_DEV_BAD_VALID:
+ *   the sequence is skipped. A bad table entry sets GROK_DEV_BAD_PAGE, its block is skipped.
+ *
+ * grok_attn_select_paged: the blocks that each KV head of each sequence should read.
+ *   A query head in 8 bits in the same way (rounded to nearest, ties to even): q = c *
+ *   2^f. score [B, 8, 2 * max_pages] fp32 is for each block of the sequence the largest over the
+ *   head's six query heads of 2^(e + f) * sum over features of max(c * upper, c * lower),
+ *   which no q . k of the block exceeds, but for q's rounding. Scores are exact, so the
+ *   choice does not depend on the order of sums. sel [B, 8, budget] int32: the first
+ *   `sink` and the last `recent` blocks of the sequence, then those with the largest scores
+ *   (the lower index first among equals), `budget` in all or as many as there are, in
+ *   ascending order; -1 behind them. Scores behind the sequence's last block are left as they
+ *   were. 1 <= budget <= 1024, sink, recent >= 0, sink + recent <= budget.
+ *   q_rot [B,48,128]; kv_len [B] int32 in [1, max_pages * 128], else GROK_DEV_BAD_KV_LEN
+ *   and the sequence's outputs are left as they were.
+ *
+ * grok_attn_decode_sparse_paged: grok_attn_decode_paged and grok_attn_combine over
+ *   the rows below kv_len[b] of the blocks in sel [B, 8, budget] alone, in one call. Of a list
+ *   the first min(budget, ceil(kv_len[b] / 64)) entries count; negative ones are passed
+ *   over; an entry listed twice counts twice; one behind the sequence's last block sets
+ *   GROK_DEV_BAD_BLOCK and is passed over. A head whose list holds no block gets zeros.
+ *   kv_len[b] outside [1, max_pages * 128] sets GROK_DEV_BAD_KV_LEN, and the sequence's
+ *   outputs are left as they were.
+ *   q_rot, out [B,48,128]; workspace: device memory, 256-byte aligned, of at least
+ *   grok_attn_decode_sparse_workspace(B, budget) bytes for the current device.
+ *
+ * grok_attn_decode_shared_paged: grok_attn_decode_paged and grok_attn_combine over
+ *   rows [0, kv_len[b]), in one call, for a batch whose sequences share prefixes: sequences
+ *   [group_start[i], group_start[i + 1]), i < n_groups, have the first shared_pages[i]
+ *   entries of their block tables in common. Those rows are read once for up to 21
+ *   sequences (on the tensor cores), the rows behind them once for each.
+ *   group_start [n_groups + 1], shared_pages [n_groups] int32 (device), 1 <= n_groups <=
+ *   1024. Sequences in no group are decoded by themselves. Where group_start is not
+ *   ascending within [0, B], or a shared_pages[i] lies outside [0, max_pages],
+ *   GROK_DEV_BAD_GROUP is set and every sequence is decoded by itself. Sequences of a group
+ *   whose tables differ in those entries set it too; their outputs are meaningless.
+ *   kv_len[b] outside [1, max_pages * 128], or below the group's shared rows, sets
+ *   GROK_DEV_BAD_KV_LEN, and the sequence's outputs are left as they were. (It may equal
+ *   them: the sequence has no rows of its own then.)
+ *   q_rot, out [B,48,128]; workspace: device memory, 256-byte aligned, of at least
+ *   grok_attn_decode_shared_workspace(B, max_pages, n_groups) bytes for the current device.
+ *
+ * Sums are split where the shares of the GPU's SMs end, which the lengths in the batch
+ * decide: the same call gives the same bits, and a sequence in another batch may
+ * differ in the last place. Weights keep 2^-16 relative in the decode over blocks; over a
+ * shared prefix they carry the special-function unit's tanh, 4e-4 relative at most.
+ * Calls that overlap on the GPU need separate workspaces; nothing is kept in one.
+ * Bad table entries: GROK_DEV_BAD_PAGE, page 0 in their place, as above.
+ */
+grok_status grok_kv_bounds_paged(const grok_bf16* k_pool, int n_pages, const int32_t* block_table, int max_pages,
+                                 const int32_t* start_pos, const int32_t* valid_len, int B, int T, int8_t* codes,
+                                 float* scale, int32_t* dev_status, void* stream);
+grok_status grok_attn_select_paged(const grok_bf16* q_rot, const int8_t* codes, const float* scale, int n_pages,
+                                   const int32_t* block_table, int max_pages, const int32_t* kv_len, int B, int budget,
+                                   int sink, int recent, float* score, int32_t* sel, int32_t* dev_status, void* stream);
+grok_status grok_attn_decode_sparse_workspace(int B, int budget, size_t* bytes);
+grok_status grok_attn_decode_sparse_paged(const grok_bf16* q_rot, const grok_bf16* k_pool, const grok_bf16* v_pool,
+                                          int n_pages, const int32_t* block_table, int max_pages,
+                                          const int32_t* kv_len, const int32_t* sel, int budget, int B,
+                                          void* workspace, size_t workspace_bytes, grok_bf16* out,
+                                          int32_t* dev_status, void* stream);
+grok_status grok_attn_decode_shared_workspace(int B, int max_pages, int n_groups, size_t* bytes);
+grok_status grok_attn_decode_shared_paged(const grok_bf16* q_rot, const grok_bf16* k_pool, const grok_bf16* v_pool,
+                                          int n_pages, const int32_t* block_table, int max_pages,
+                                          const int32_t* kv_len, int B, const int32_t* group_start,
+                                          const int32_t* shared_pages, int n_groups, void* workspace,
+                                          size_t workspace_bytes, grok_bf16* out, int32_t* dev_status, void* stream);
 
 /*
  * Continuous-batching slot insertion (code-reading guide ch. 6 §6.6.1: every
