@@ -17,27 +17,36 @@
 // for an 8 x 8 transpose per register. A warp writes its partial sums where its share
 // of a pair ends, and no barrier joins the warps; a second kernel, launched as a
 // dependent, adds a pair's partial sums in their order.
+#include <algorithm>
+
 #include "block_decode.cuh"
 
 namespace grok {
 
 constexpr int kBkThreads = (kBkWarps + 1) * 32;
-constexpr int kBkStages = 3;
 constexpr int kBkBox = kBlk * 128;           // [64 rows][64 bf16]
+constexpr int kBkTile = 2 * kBkBox;          // the K or the V of a block
+// Tiles of the ring, K and V of the blocks in turn. Over lists two CTAs share an SM; over the rows behind prefixes one runs
+// beside a CTA of the prefix kernel.
+__host__ __device__ constexpr int bk_ring(bool list) { return list ? 5 : 4; }
 constexpr int kBkQ = kGroup * kD * 2;        // a pair's queries
-constexpr int kBkStage = 4 * kBkBox;         // K halves, V halves
-constexpr int kBkPlan = 1024;                // entries of the table of block counts
+constexpr int kBkPlan = 512;                 // entries of the table of block counts
 constexpr int kBkCtas = 2;                   // CTAs resident on an SM
 
+template <int kRing>
 struct BkShared {
-  uint64_t full[kBkStages], empty[kBkStages];
-  int2 token[kBkStages];  // pair and visible keys of the block in a stage; pair -1: the end
+  float4 sum_o[kBkWarps - 1][kBkPartO];  // partial sums of warps 1 to 3 for warp 0
+  float2 sum_l[kBkWarps - 1][4];
+  uint64_t full[kRing], empty[kRing], sum_full, sum_empty;
+  int2 token[kRing];      // pair and visible keys of the block whose K is in a place of the ring; pair -1: the end
   int cum[kBkPlan + 1];   // blocks per KV head of the sequences before each entry's
   int warp_sum[kBkWarps + 1];
   int abort;
 };
-constexpr int kBkSmem = 1024 + kBkStages * (kBkStage + kBkQ) + int(sizeof(BkShared));
-static_assert(kBkCtas * (kBkSmem + 1024) <= 233472, "shared memory per SM");
+template <bool kList>
+constexpr int kBkSmem = 1024 + bk_ring(kList) * (kBkTile + kBkQ) + int(sizeof(BkShared<bk_ring(kList)>));
+static_assert(kBkCtas * (kBkSmem<true> + 1024) <= 233472, "shared memory per SM");
+static_assert(kBkSmem<false> + 1024 + kPxSmemMax + 1024 <= 233472, "shared memory beside the prefix kernel");
 
 struct BkParams {
   const uint8_t* q;
@@ -74,24 +83,28 @@ __device__ __forceinline__ int bk_blocks(const BkParams& p, int b, bool groups, 
   return kList ? min(n, p.budget) : n;
 }
 
+// (Registers: 112 a thread at most behind prefixes, for the same reason as in the prefix kernel.)
 template <bool kList>
-__global__ void __launch_bounds__(kBkThreads, kBkCtas)
+__global__ void __launch_bounds__(kList ? kBkThreads : 576, kList ? kBkCtas : 1)
     block_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                         const BkParams p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t* sq = smem + kBkStages * kBkStage;
-  BkShared* sh = reinterpret_cast<BkShared*>(sq + kBkStages * kBkQ);
+  constexpr int kBkRing = bk_ring(kList);
+  uint8_t* sq = smem + kBkRing * kBkTile;
+  BkShared<kBkRing>* sh = reinterpret_cast<BkShared<kBkRing>*>(sq + kBkRing * kBkQ);
   volatile int* abort = &sh->abort;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
   // The kernel that joins the partial results may be scheduled as soon as every CTA has started.
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (tid == 0) {
-    for (int s = 0; s < kBkStages; ++s) {
+    for (int s = 0; s < kBkRing; ++s) {
       mbar_init(&sh->full[s], 1);
       mbar_init(&sh->empty[s], kBkWarps);
     }
+    mbar_init(&sh->sum_full, kBkWarps - 1);
+    mbar_init(&sh->sum_empty, 1);
     sh->abort = 0;
     fence_barrier_init();
     prefetch_tmap(&tm_k);
@@ -145,23 +158,25 @@ __global__ void __launch_bounds__(kBkThreads, kBkCtas)
   if (lo < hi) {
     if (warp == kBkWarps) {
       // ------------------------------------------------------------ producer
-      int it = 0;          // tokens so far
+      int st = 0, turn = 1, loads = 0;  // the ring's next place, the parity that frees it, places taken so far
       int cur = -1;        // the pair of the last block looked at
       bool sent = true;    // a token of that pair is out
       bool ok = true;
-      // A stage for the next token; false when a bounded wait gave up.
-      auto acquire = [&]() {
-        ok = __all_sync(0xffffffffu, it < kBkStages || mbar_wait(&sh->empty[it % kBkStages],
-                                                                 ((it / kBkStages) & 1) ^ 1, abort, p.status));
+      auto acquire = [&]() {  // (false when a bounded wait gave up)
+        ok = ok && __all_sync(0xffffffffu, mbar_wait(&sh->empty[st], turn, abort, p.status));
         return ok;
+      };
+      auto next = [&]() {
+        ++loads;
+        if (++st == kBkRing) st = 0, turn ^= 1;
       };
       auto send_empty = [&](int pair) {  // a token without a block
         if (!acquire()) return;
         if (lane == 0) {
-          sh->token[it % kBkStages] = make_int2(pair, 0);
-          mbar_arrive(&sh->full[it % kBkStages]);
+          sh->token[st] = make_int2(pair, 0);
+          mbar_arrive(&sh->full[st]);
         }
-        ++it;
+        next();
       };
       for (int base = lo; base < hi && ok; base += 32) {
         const int cnt = min(32, hi - base), idx = base + lane;
@@ -199,20 +214,22 @@ __global__ void __launch_bounds__(kBkThreads, kBkCtas)
             cur = pair;
             sent = false;
           }
-          if (row < 0 || !ok || !acquire()) continue;
+          if (row < 0 || !acquire()) continue;
+          const int g = pair % kKVHeads;
           if (lane == 0) {
-            const int st = it % kBkStages, g = pair % kKVHeads;
-            uint8_t* dst = smem + st * kBkStage;
             sh->token[st] = make_int2(pair, keys);
-            mbar_arrive_expect_tx(&sh->full[st], kBkStage + (sent ? 0 : kBkQ));
+            mbar_arrive_expect_tx(&sh->full[st], kBkTile + (sent ? 0 : kBkQ));
             if (!sent) bulk_load(sq + st * kBkQ, p.q + (size_t)pair * kBkQ, kBkQ, &sh->full[st]);
-            tma_load_4d(dst, &tm_k, &sh->full[st], 0, g, row, 0);
-            tma_load_4d(dst + kBkBox, &tm_k, &sh->full[st], 64, g, row, 0);
-            tma_load_4d(dst + 2 * kBkBox, &tm_v, &sh->full[st], 0, g, row, 0);
-            tma_load_4d(dst + 3 * kBkBox, &tm_v, &sh->full[st], 64, g, row, 0);
+            tma_load_4d(smem + st * kBkTile, &tm_k, &sh->full[st], 0, row, 0, g);
           }
           sent = true;
-          ++it;
+          next();
+          if (!acquire()) continue;
+          if (lane == 0) {
+            mbar_arrive_expect_tx(&sh->full[st], kBkTile);
+            tma_load_4d(smem + st * kBkTile, &tm_v, &sh->full[st], 0, row, 0, g);
+          }
+          next();
         }
       }
       if (ok && !sent) send_empty(cur);
@@ -220,31 +237,68 @@ __global__ void __launch_bounds__(kBkThreads, kBkCtas)
       // Copies in flight (only after an abort) land before the CTA exits.
       volatile int never = 0;
       if (lane == 0)
-        for (int t = max(0, it - kBkStages); t < it; ++t)
-          mbar_wait(&sh->full[t % kBkStages], (t / kBkStages) & 1, &never, p.status);
+        for (int t = max(0, loads - kBkRing); t < loads; ++t)
+          mbar_wait(&sh->full[t % kBkRing], (t / kBkRing) & 1, &never, p.status);
     } else {
       // ------------------------------------------------------------ 16 keys of each block
       const int row = lane >> 2, t = lane & 3, mi = lane >> 3, mr = lane & 7;
       const uint32_t sbase = smem_u32(smem);
       uint32_t qb[8][2];
       float o[8][4], l0 = 0.f, l1 = 0.f;  // columns 2 t, 2 t + 1
-      int cur = -1;
-      for (int it = 0;; ++it) {
-        const int st = it % kBkStages;
-        if (!__all_sync(0xffffffffu, mbar_wait(&sh->full[st], (it / kBkStages) & 1, abort, p.status))) break;
+      int cur = -1, st = 0, turn = 0, sums = 0;
+      auto release = [&]() {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh->empty[st]);
+        if (++st == kBkRing) st = 0, turn ^= 1;
+      };
+      while (true) {
+        if (!__all_sync(0xffffffffu, mbar_wait(&sh->full[st], turn, abort, p.status))) break;
         const int2 tok = sh->token[st];
         if (tok.x != cur) {
-          if (cur >= 0) {  // the partial sums of this CTA's share of the pair
-            const size_t slot = ((size_t)cta + cur) * kBkWarps + warp;
+          if (cur >= 0) {  // the sums of this CTA's share of the pair: warp 0 adds the other warps' and writes them
 #pragma unroll
             for (int d = 4; d < 32; d *= 2) {
               l0 += __shfl_xor_sync(0xffffffffu, l0, d);
               l1 += __shfl_xor_sync(0xffffffffu, l1, d);
             }
+            const bool mine = warp == 0;
+            if (!__all_sync(0xffffffffu, mbar_wait(mine ? &sh->sum_full : &sh->sum_empty, (sums & 1) ^ (mine ? 0 : 1),
+                                                   abort, p.status)))
+              break;
+            ++sums;
+            if (!mine) {
 #pragma unroll
-            for (int mt = 0; mt < 8; ++mt)
-              p.parts.o[slot * kBkPartO + mt * 32 + lane] = make_float4(o[mt][0], o[mt][1], o[mt][2], o[mt][3]);
-            if (row == 0) *reinterpret_cast<float2*>(p.parts.l + slot * 8 + 2 * t) = make_float2(l0, l1);
+              for (int mt = 0; mt < 8; ++mt)
+                sh->sum_o[warp - 1][mt * 32 + lane] = make_float4(o[mt][0], o[mt][1], o[mt][2], o[mt][3]);
+              if (row == 0) sh->sum_l[warp - 1][t] = make_float2(l0, l1);
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&sh->sum_full);
+            } else {
+              const size_t slot = (size_t)cta + cur;
+#pragma unroll
+              for (int mt = 0; mt < 8; ++mt) {
+                float4 v = make_float4(o[mt][0], o[mt][1], o[mt][2], o[mt][3]);
+#pragma unroll
+                for (int w = 0; w < kBkWarps - 1; ++w) {
+                  const float4 x = sh->sum_o[w][mt * 32 + lane];
+                  v.x += x.x;
+                  v.y += x.y;
+                  v.z += x.z;
+                  v.w += x.w;
+                }
+                p.parts.o[slot * kBkPartO + mt * 32 + lane] = v;
+              }
+              if (row == 0) {
+#pragma unroll
+                for (int w = 0; w < kBkWarps - 1; ++w) {
+                  l0 += sh->sum_l[w][t].x;
+                  l1 += sh->sum_l[w][t].y;
+                }
+                *reinterpret_cast<float2*>(p.parts.l + slot * 8 + 2 * t) = make_float2(l0, l1);
+              }
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&sh->sum_empty);
+            }
           }
           cur = tok.x;
           if (cur < 0) break;
@@ -258,9 +312,15 @@ __global__ void __launch_bounds__(kBkThreads, kBkCtas)
             qb[kk][1] = row < kGroup && tok.y > 0 ? qs[kk * 8 + 4] : 0u;
           }
         }
+        if (tok.y == 0) {  // (no block)
+          release();
+          continue;
+        }
         const int key0 = warp * 16;
-        if (key0 < tok.y) {
-          const uint32_t kb = sbase + st * kBkStage, vb = kb + 2 * kBkBox;
+        const bool live = key0 < tok.y, tail = key0 + 16 > tok.y;
+        uint32_t h0 = 0u, h1 = 0u, e0 = 0u, e1 = 0u;
+        if (live) {
+          const uint32_t kb = sbase + st * kBkTile;
           float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk) {
@@ -276,16 +336,19 @@ __global__ void __launch_bounds__(kBkThreads, kBkCtas)
           const float w3 = in1 ? capped_weight_precise(s[0][3] + s[1][3]) : 0.f;
           l0 += w0 + w2;
           l1 += w1 + w3;
-          uint32_t h0, h1, e0, e1;
           split_bf16x2(w0, w1, h0, e0);
           split_bf16x2(w2, w3, h1, e1);
           h0 = movmatrix_trans(h0);
           h1 = movmatrix_trans(h1);
           e0 = movmatrix_trans(e0);
           e1 = movmatrix_trans(e1);
-          const bool tail = key0 + 16 > tok.y;  // rows behind the last may hold anything
+        }
+        release();
+        if (!__all_sync(0xffffffffu, mbar_wait(&sh->full[st], turn, abort, p.status))) break;
+        if (live) {
+          const uint32_t vb = sbase + st * kBkTile;
           uint32_t m0 = 0xFFFFFFFFu, m1 = 0xFFFFFFFFu;
-          if (tail) {
+          if (tail) {  // rows behind the last may hold anything
             const int k0 = key0 + 2 * t;
             m0 = (k0 < tok.y ? 0x0000FFFFu : 0u) | (k0 + 1 < tok.y ? 0xFFFF0000u : 0u);
             m1 = (k0 + 8 < tok.y ? 0x0000FFFFu : 0u) | (k0 + 9 < tok.y ? 0xFFFF0000u : 0u);
@@ -305,8 +368,7 @@ __global__ void __launch_bounds__(kBkThreads, kBkCtas)
             mma_bf16_16816(o[mt], a, e0, e1);
           }
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sh->empty[st]);
+        release();
       }
     }
   }
@@ -316,29 +378,27 @@ __global__ void __launch_bounds__(kBkThreads, kBkCtas)
 }
 
 // ----------------------------------------------------------------------------
-// out = (sum of the partial O) / (sum of the partial l) of one (sequence, KV head).
-// Four teams of 256 threads take one warp's parts each, in order.
-constexpr int kJnTeams = kBkWarps;
-constexpr int kJnThreads = kJnTeams * kBkPartO;
-
-template <bool kPrefix>
-__global__ void __launch_bounds__(kJnThreads) block_join_kernel(const BlockParts parts, const PrefixParts prefix,
-                                                                const PageMap pm, uint2* __restrict__ out,
-                                                                int32_t* status) {
-  __shared__ float4 so[kJnTeams][kBkPartO];
-  __shared__ float sl[kJnTeams][8];
+// out = (sum of the partial O) / (sum of the partial l) of one (sequence, KV head). Each team of 256 threads adds every
+// kTeams-th part: four teams where there are few CTAs and many parts each, one where there are many CTAs.
+template <bool kPrefix, int kTeams>
+__global__ void __launch_bounds__(kTeams* kBkPartO)
+    block_join_kernel(const BlockParts parts, const PrefixParts prefix, const PageMap pm, uint2* __restrict__ out,
+                      int32_t* status) {
+  __shared__ float4 so[kTeams][kBkPartO];
+  __shared__ float sl[kTeams][8];
   __shared__ float acc[kGroup][kD + 4];
+  constexpr int kThreads = kTeams * kBkPartO;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int g = blockIdx.x, b = blockIdx.y, pair = b * kKVHeads + g;
   const int tid = threadIdx.x, team = tid / kBkPartO, at = tid % kBkPartO;
   const int2 mine = parts.pair[pair];
+  const int4 pre = kPrefix ? prefix.pair[pair] : make_int4(0, 0, 0, 0);
   if (mine.y < 0) return;  // (the whole CTA)
   float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
   float l = 0.f;
-  const size_t s0 = (size_t)mine.x * kBkWarps + team;
-#pragma unroll 8
-  for (int i = 0; i < mine.y; ++i) {
-    const size_t s = s0 + (size_t)i * kBkWarps;
+#pragma unroll 4
+  for (int i = team; i < mine.y; i += kTeams) {
+    const size_t s = (size_t)mine.x + i;
     const float4 x = parts.o[s * kBkPartO + at];
     v.x += x.x;
     v.y += x.y;
@@ -346,19 +406,10 @@ __global__ void __launch_bounds__(kJnThreads) block_join_kernel(const BlockParts
     v.w += x.w;
     if (at < 8) l += parts.l[s * 8 + at];
   }
-  so[team][at] = v;
-  if (at < 8) sl[team][at] = l;
-  // The prefix's parts: thread (head, feature quad).
+  // The prefix's parts: thread (head, feature quad). The other threads: does the table agree with the one that was read?
   float4 pv = make_float4(0.f, 0.f, 0.f, 0.f);
   float pl = 0.f;
   const int h = tid % kGroup, quad = tid / kGroup;
-  const int4 pre = kPrefix ? prefix.pair[pair] : make_int4(0, 0, 0, 0);
-  if (kPrefix && quad >= kD / 4 && g == 0) {  // the other threads: does the table agree with the one that was read?
-    const int seq = pre.w & 0xFFFF;
-    for (int i = tid - kGroup * kD / 4; i < int(uint32_t(pre.w) >> 16); i += kJnThreads - kGroup * kD / 4)
-      if (pm.table[(size_t)b * pm.max_pages + i] != pm.table[(size_t)seq * pm.max_pages + i])
-        report(status, GROK_DEV_BAD_GROUP);
-  }
   if (kPrefix && quad < kD / 4) {
     const int r = pre.z + h;
 #pragma unroll 4
@@ -369,13 +420,23 @@ __global__ void __launch_bounds__(kJnThreads) block_join_kernel(const BlockParts
       pv.y += x.y;
       pv.z += x.z;
       pv.w += x.w;
-      pl += prefix.l[(s * 2) * kPxRows + r] + prefix.l[(s * 2 + 1) * kPxRows + r];
+#pragma unroll
+      for (int w = 0; w < kPxSums; ++w) pl += prefix.l[(s * kPxSums + w) * kPxRows + r];
     }
+  } else if (kPrefix && g == 0) {
+    const int seq = pre.w & 0xFFFF;
+    for (int i = tid - kGroup * kD / 4; i < int(uint32_t(pre.w) >> 16); i += kThreads - kGroup * kD / 4)
+      if (pm.table[(size_t)b * pm.max_pages + i] != pm.table[(size_t)seq * pm.max_pages + i])
+        report(status, GROK_DEV_BAD_GROUP);
   }
-  __syncthreads();
+  if (at < 8) sl[team][at] = l;
+  if (kTeams > 1) {
+    so[team][at] = v;
+    __syncthreads();
+  }
   if (team == 0) {
 #pragma unroll
-    for (int w = 1; w < kJnTeams; ++w) {
+    for (int w = 1; w < kTeams; ++w) {
       const float4 x = so[w][at];
       v.x += x.x;
       v.y += x.y;
@@ -395,7 +456,7 @@ __global__ void __launch_bounds__(kJnThreads) block_join_kernel(const BlockParts
   if (quad < kD / 4) {
     float sum = pl;
 #pragma unroll
-    for (int w = 0; w < kJnTeams; ++w) sum += sl[w][h];
+    for (int w = 0; w < kTeams; ++w) sum += sl[w][h];
     const float inv = sum == 0.f ? 0.f : 1.0f / sum;  // (a list without a block: zeros)
     const float* x = &acc[h][quad * 4];
     out[((size_t)pair * kGroup + h) * (kD / 4) + quad] =
@@ -408,7 +469,7 @@ __global__ void __launch_bounds__(kJnThreads) block_join_kernel(const BlockParts
 static size_t up256(size_t n) { return (n + 255) & ~size_t(255); }
 static size_t bk_slots(int B, int sms) { return (size_t)B * kKVHeads + (size_t)kBkCtas * sms; }
 static BlockParts block_parts(char* ws, int B, int sms) {
-  const size_t slots = bk_slots(B, sms) * kBkWarps;
+  const size_t slots = bk_slots(B, sms);
   BlockParts p;
   p.o = reinterpret_cast<float4*>(ws);
   ws += up256(slots * kBkPartO * sizeof(float4));
@@ -418,14 +479,14 @@ static BlockParts block_parts(char* ws, int B, int sms) {
   return p;
 }
 size_t block_parts_bytes(int B, int sms) {
-  const size_t slots = bk_slots(B, sms) * kBkWarps;
+  const size_t slots = bk_slots(B, sms);
   return up256(slots * kBkPartO * sizeof(float4)) + up256(slots * 8 * sizeof(float)) +
          up256((size_t)B * kKVHeads * sizeof(int2));
 }
 
-// Query tiles of the prefix kernel: sum of ceil(n_i / 21) over groups of two sequences at least.
+// Query tiles of the prefix kernel: the sum of ceil(n_i / 21) over groups of two sequences at least.
 static size_t px_slots(int B, int n_groups, int sms) {
-  const size_t tiles = min(B / 2, B / kPxSeqs + n_groups);
+  const size_t tiles = std::min(B / 2, B / kPxSeqs + n_groups);
   return tiles * kKVHeads + sms;
 }
 PrefixParts prefix_parts(char* ws, int B, int n_groups, int sms) {
@@ -434,30 +495,36 @@ PrefixParts prefix_parts(char* ws, int B, int n_groups, int sms) {
   p.o = reinterpret_cast<float4*>(ws);
   ws += slots * kPxRows * kD * 4;
   p.l = reinterpret_cast<float*>(ws);
-  ws += slots * 2 * kPxRows * 4;
+  ws += slots * kPxSums * kPxRows * 4;
   p.pair = reinterpret_cast<int4*>(ws);
   return p;
 }
 size_t prefix_parts_bytes(int B, int n_groups, int sms) {
-  return px_slots(B, n_groups, sms) * kPxRows * (kD * 4 + 8) + up256((size_t)B * kKVHeads * sizeof(int4));
+  return px_slots(B, n_groups, sms) * kPxRows * (kD + kPxSums) * 4 + up256((size_t)B * kKVHeads * sizeof(int4));
+}
+
+grok_status encode_pool(CUtensorMap* map, const grok_bf16* pool, int n_pages) {
+  const uint64_t dims[4] = {kD / 2, uint64_t(n_pages) * GROK_PAGE_TOKENS, 2, kKVHeads};
+  const uint64_t strides[3] = {uint64_t(kKVHeads) * kD * 2, kD, kD * 2};
+  const uint32_t box[4] = {kD / 2, kBlk, 2, 1};
+  return encode_tmap_bf16_4d(map, pool, dims, strides, box);
 }
 
 template <bool kList>
 static grok_status bk_launch(const BlockArgs& a, const BkParams& p, int sms) {
   CUtensorMap tk, tv;
-  const uint64_t rows = uint64_t(a.pm.n_pages) * GROK_PAGE_TOKENS;
-  const uint64_t dims[4] = {kD, kKVHeads, rows, 1};
-  const uint64_t strides[3] = {kD * 2, uint64_t(kKVHeads) * kD * 2, rows * kKVHeads * kD * 2};
-  const uint32_t box[4] = {64, 1, kBlk, 1};
   grok_status st;
-  if ((st = encode_tmap_bf16_4d(&tk, a.k_pool, dims, strides, box)) != GROK_OK) return st;
-  if ((st = encode_tmap_bf16_4d(&tv, a.v_pool, dims, strides, box)) != GROK_OK) return st;
+  if ((st = encode_pool(&tk, a.k_pool, a.pm.n_pages)) != GROK_OK) return st;
+  if ((st = encode_pool(&tv, a.v_pool, a.pm.n_pages)) != GROK_OK) return st;
   static bool attr_set[kMaxDevices] = {};  // per device; idempotent: every thread would set the same value
   int dev = 0;
   if ((st = device_index(&dev)) != GROK_OK) return st;
   cudaError_t e;
   if (!attr_set[dev]) {
-    e = cudaFuncSetAttribute(block_decode_kernel<kList>, cudaFuncAttributeMaxDynamicSharedMemorySize, kBkSmem);
+    e = cudaFuncSetAttribute(block_decode_kernel<kList>, cudaFuncAttributeMaxDynamicSharedMemorySize, kBkSmem<kList>);
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(block_decode_kernel<kList>, cudaFuncAttributePreferredSharedMemoryCarveout,
+                               cudaSharedmemCarveoutMaxShared);
     if (e != cudaSuccess) return fail(cuda_status(e), "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
     attr_set[dev] = true;
   }
@@ -465,7 +532,7 @@ static grok_status bk_launch(const BlockArgs& a, const BkParams& p, int sms) {
   cudaLaunchAttribute attr[1];
   cfg.gridDim = dim3(kBkCtas * sms);
   cfg.blockDim = dim3(kBkThreads);
-  cfg.dynamicSmemBytes = kBkSmem;
+  cfg.dynamicSmemBytes = kBkSmem<kList>;
   cfg.stream = a.stream;
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = kList ? 0 : 1;
@@ -492,17 +559,18 @@ grok_status block_decode_run(const BlockArgs& a, char* ws, const PrefixParts* pr
   if (st != GROK_OK) return st;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
+  const int teams = a.B * kKVHeads <= sms ? 4 : 1;
   cfg.gridDim = dim3(kKVHeads, a.B);
-  cfg.blockDim = dim3(kJnThreads);
+  cfg.blockDim = dim3(teams * kBkPartO);
   cfg.stream = a.stream;
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  uint2* out = reinterpret_cast<uint2*>(a.out);
-  const cudaError_t e =
-      prefix ? cudaLaunchKernelEx(&cfg, block_join_kernel<true>, p.parts, *prefix, a.pm, out, a.status)
-             : cudaLaunchKernelEx(&cfg, block_join_kernel<false>, p.parts, PrefixParts{}, a.pm, out, a.status);
+  auto kernel = prefix ? (teams == 4 ? block_join_kernel<true, 4> : block_join_kernel<true, 1>)
+                       : (teams == 4 ? block_join_kernel<false, 4> : block_join_kernel<false, 1>);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, p.parts, prefix ? *prefix : PrefixParts{}, a.pm,
+                                           reinterpret_cast<uint2*>(a.out), a.status);
   if (e != cudaSuccess) return fail(cuda_status(e), "block join launch: %s", cudaGetErrorString(e));
   return check_launch("block join");
 }

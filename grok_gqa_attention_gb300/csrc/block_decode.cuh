@@ -8,7 +8,7 @@
 
 namespace grok {
 
-constexpr int kGroupsMax = 1024;  // groups of sequences with a common prefix
+constexpr int kGroupsMax = 256;   // groups of sequences with a common prefix
 constexpr int kPxSeqs = 21;       // sequences per query tile of the prefix kernel: 126 of its 128 rows
 
 // Sequences [start[i], start[i + 1]) have their first pages[i] pages in common.
@@ -43,7 +43,7 @@ __device__ __forceinline__ int seq_pages(const Groups& gr, int b) {
   return group_pages(gr, lo);
 }
 
-// Partial results of the block kernel, per (part, warp): the sums O in the layout of the products' accumulators
+// Partial results of the block kernel, per part: the sums O in the layout of the products' accumulators
 // (float4 [8 tiles of 16 features][32 lanes]) and the weights' sums of 8 columns (6 heads, 2 unused).
 constexpr int kBkWarps = 4;
 constexpr int kBkPartO = 8 * 32;  // float4s
@@ -52,12 +52,15 @@ struct BlockParts {
   float* l;
   int2* pair;  // [B * 8]: first part and number of parts; number -1: the sequence is skipped
 };
-// Partial results of the prefix kernel, per part: O as float4 [32 feature quads][128 rows], and two sums per row.
+// Partial results of the prefix kernel, per part: O as float4 [32 feature quads][128 rows], and four sums per row.
 constexpr int kPxRows = 128;
+constexpr int kPxSums = 4;
+constexpr int kPxSmemMax = 134 * 1024;  // of the prefix kernel's CTA
 struct PrefixParts {
   float4* o;
   float* l;
-  int4* pair;  // [B * 8]: first part, number of parts, the sequence's first row, pages << 16 | the sequence whose table is read
+  // [B * 8]: first part, number of parts, the sequence's first row, pages << 16 | the sequence whose table is read
+  int4* pair;
 };
 
 struct BlockArgs {
@@ -81,6 +84,10 @@ size_t prefix_parts_bytes(int B, int n_groups, int sms);
 // which was launched before on the stream).
 grok_status block_decode_run(const BlockArgs& a, char* ws, const PrefixParts* prefix, int sms);
 PrefixParts prefix_parts(char* ws, int B, int n_groups, int sms);
+
+// Tensor map of a pool as (64 features, row, half of the features, KV head): one copy brings the 64 rows of a block of
+// one head, as two tiles of [64 rows][64 bf16].
+grok_status encode_pool(CUtensorMap* map, const grok_bf16* pool, int n_pages);
 
 grok_status page_args(int n_pages, int max_pages, int B, const char* who);
 

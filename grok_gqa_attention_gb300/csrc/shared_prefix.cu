@@ -11,36 +11,42 @@
 // Work: (group, KV head, query tile, 64-key tile) in this order, dealt out to one CTA per
 // SM in equal contiguous shares; a share that leaves a (group, KV head, query tile) writes
 // a part of its unnormalised O and row sums. Per key tile
-//   S = Q K^T (128 x 64, 64 TMEM columns of one of four buffers), P over S in place as two
-//   bf16 halves that sum to P to 2^-16, O += P_hi V + P_lo V.
-// Warps: 0 TMA, 1 MMA, 2-5 and 6-9 the softmax of even and of odd key tiles. Products of
-// the next tiles are issued ahead of the softmax of this one.
+//   S = Q K^T (128 x 64, one of five buffers of 64 TMEM columns; Q is in TMEM too), P over S
+//   in place as two bf16 halves that sum to P to 2^-16, O += P_hi V + P_lo V.
+// Warps: 0 TMA, 1 the issue of S, 18 that of P V, 2-17 the softmax, four warps to a key
+// tile. S runs up to five tiles ahead of P V.
 #include "block_decode.cuh"
 
 namespace grok {
 
-constexpr int kPxThreads = 320;
-constexpr int kPxStages = 3;
-constexpr int kPxAhead = 2;                 // S products issued ahead of P V
-static_assert(kPxAhead < kPxStages && kPxAhead < 4, "stages and S buffers");
-constexpr int kPxQBox = kPxRows * 128;      // [128 rows][64 bf16]: one half of the features
-constexpr int kPxBox = kBlk * 128;          // the same of a key tile
+constexpr int kPxTeams = kPxSums;           // of four softmax warps, a key tile each in turn
+constexpr int kPxThreads = 32 * (3 + 4 * kPxTeams);
+// Registers: the launch bound is above the launch, for at most 80 a thread, which leaves room beside this CTA for one of
+// the kernel over the sequences' own rows.
+constexpr int kPxBound = 768;
+constexpr int kPxBox = kBlk * 128;          // [64 rows][64 bf16]: one half of the features of a key tile
 constexpr int kPxTile = 2 * kPxBox;
-constexpr int kPxQLoad = 2 * kPxSeqs * kGroup * 128;
+constexpr int kPxStages = 4;                // of the K ring and of the V ring
+// TMEM columns: O, Q, and the S (then P) of key tiles in turn
+constexpr int kPxBufs = 5;
+constexpr uint32_t kPxO = 0, kPxQ = kD, kPxS = kPxQ + kD / 2;
+static_assert(kPxS + kPxBufs * kBlk <= 512, "TMEM columns");
 
 struct PxShared {
   uint64_t q_full, q_empty, o_full, o_empty, done;
-  uint64_t kv_full[kPxStages], kv_empty[kPxStages];
-  uint64_t s_full[4], p_full[4];
+  uint64_t k_full[kPxStages], k_empty[kPxStages], v_full[kPxStages], v_empty[kPxStages];
+  uint64_t s_full[kPxBufs], p_full[kPxBufs], s_empty[kPxBufs];
   int units[kGroupsMax + 1];  // key tiles before each group's
   int items[kGroupsMax + 1];  // (KV head, query tile) pairs before each group's
   int warp_units[kPxThreads / 32], warp_items[kPxThreads / 32];
   uint32_t tmem;
   int abort;
 };
-constexpr int kPxSmem = 1024 + 2 * kPxQBox + kPxStages * 2 * kPxTile + int(sizeof(PxShared));
+constexpr int kPxSmem = 1024 + kPxStages * 2 * kPxTile + int(sizeof(PxShared));
+static_assert(kPxSmem <= kPxSmemMax, "shared memory");
 
 struct PxParams {
+  const uint4* q;
   Groups groups;
   PageMap pm;
   int B;
@@ -50,11 +56,10 @@ struct PxParams {
 
 // A share's run of key tiles of one (group, KV head, query tile).
 struct PxRun {
-  int group, g, mt;  // group, KV head, query tile
-  int item;          // number of the (group, KV head, query tile)
-  int k0, n;         // first key tile and number of them
-  int first, last;   // units: the item's first one and the one behind its last
-  int seq0, seqs;    // sequences of the query tile
+  int g, item;      // KV head; number of the (group, KV head, query tile)
+  int k0, n, keys;  // first key tile, number of them, of the item
+  int base;         // the item's first unit
+  int seq0, seqs;   // sequences of the query tile
 };
 
 __device__ __forceinline__ PxRun px_run(const PxParams& p, const PxShared* sh, int unit, int hi) {
@@ -64,28 +69,42 @@ __device__ __forceinline__ PxRun px_run(const PxParams& p, const PxShared* sh, i
     const int mid = (lo + up) >> 1;
     if (sh->units[mid] <= unit) lo = mid; else up = mid;
   }
-  r.group = lo;
   const int a = p.groups.start[lo], n = p.groups.start[lo + 1] - a;
-  const int tiles = (n + kPxSeqs - 1) / kPxSeqs, keys = p.groups.pages[lo] * kBlkPerPage;
-  const int in = unit - sh->units[lo], it = in / keys;
+  const int tiles = (n + kPxSeqs - 1) / kPxSeqs;
+  r.keys = p.groups.pages[lo] * kBlkPerPage;
+  const int in = unit - sh->units[lo], it = in / r.keys;
   r.g = it / tiles;
-  r.mt = it % tiles;
   r.item = sh->items[lo] + it;
-  r.k0 = in % keys;
-  r.n = min(keys - r.k0, hi - unit);
-  r.first = unit - r.k0;
-  r.last = r.first + keys;
-  r.seq0 = a + r.mt * kPxSeqs;
+  r.k0 = in % r.keys;
+  r.n = min(r.keys - r.k0, hi - unit);
+  r.base = unit - r.k0;
+  r.seq0 = a + it % tiles * kPxSeqs;
   r.seqs = min(kPxSeqs, a + n - r.seq0);
   return r;
 }
 
-// Weights of 32 logits of a row: 2^(kT tanh(y) - kT) as bf16 halves hi and lo, their sum added to l. tanh runs on the
+// 32 lanes x 16 columns, waited for; and the store of 8.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
+      "[%16];\n\ttcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+
+// Weights of 16 logits of a row: 2^(kT tanh(y) - kT) as bf16 halves hi and lo, their sum added to l. tanh runs on the
 // special-function unit, exp2 there for half of the columns and as a polynomial on the FMA pipe for the others.
-__device__ __forceinline__ void px_weights(const uint32_t (&s)[32], uint64_t& l, uint32_t (&hi)[16], uint32_t (&lo)[16]) {
+__device__ __forceinline__ void px_weights(const uint32_t (&s)[16], uint64_t& l, uint32_t (&hi)[8], uint32_t (&lo)[8]) {
   const uint64_t y2 = f2_pack(kY, kY), t2 = f2_pack(kT, kT), m2 = f2_pack(-kT, -kT), z2 = f2_pack(0.f, 0.f);
 #pragma unroll
-  for (int e = 0; e < 16; ++e) {
+  for (int e = 0; e < 8; ++e) {
     float y0, y1, w0, w1;
     f2_unpack(f2_mul(f2_pack(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1])), y2), y0, y1);
     const uint64_t t = f2_pack(tanh_approx(y0), tanh_approx(y1));
@@ -108,36 +127,37 @@ __device__ __forceinline__ void px_weights(const uint32_t (&s)[32], uint64_t& l,
   }
 }
 
-__global__ void __launch_bounds__(kPxThreads, 1)
-    prefix_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-                  const __grid_constant__ CUtensorMap tm_v, const PxParams p) {
+__global__ void __launch_bounds__(kPxBound, 1)
+    prefix_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, const PxParams p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t* sQ = smem;
-  uint8_t* sKV = smem + 2 * kPxQBox;  // stages: K halves, V halves
-  PxShared* sh = reinterpret_cast<PxShared*>(sKV + kPxStages * 2 * kPxTile);
+  uint8_t* sK = smem;
+  uint8_t* sV = sK + kPxStages * kPxTile;
+  PxShared* sh = reinterpret_cast<PxShared*>(sV + kPxStages * kPxTile);
   volatile int* abort = &sh->abort;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
   // The kernel over the sequences' own rows starts beside this one.
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (tid == 0) {
-    mbar_init(&sh->q_full, 1);
+    mbar_init(&sh->q_full, kPxTeams * 128);
     mbar_init(&sh->q_empty, 1);
     mbar_init(&sh->o_full, 1);
-    mbar_init(&sh->o_empty, 256);
-    mbar_init(&sh->done, 1);
-    for (int s = 0; s < kPxStages; ++s) {
-      mbar_init(&sh->kv_full[s], 1);
-      mbar_init(&sh->kv_empty[s], 1);
+    mbar_init(&sh->o_empty, kPxTeams * 128);
+    mbar_init(&sh->done, 2);
+    for (int i = 0; i < kPxStages; ++i) {
+      mbar_init(&sh->k_full[i], 1);
+      mbar_init(&sh->k_empty[i], 1);
+      mbar_init(&sh->v_full[i], 1);
+      mbar_init(&sh->v_empty[i], 1);
     }
-    for (int s = 0; s < 4; ++s) {
-      mbar_init(&sh->s_full[s], 1);
-      mbar_init(&sh->p_full[s], 128);
+    for (int i = 0; i < kPxBufs; ++i) {
+      mbar_init(&sh->s_full[i], 1);
+      mbar_init(&sh->p_full[i], 128);
+      mbar_init(&sh->s_empty[i], 1);
     }
     sh->abort = 0;
     fence_barrier_init();
-    prefetch_tmap(&tm_q);
     prefetch_tmap(&tm_k);
     prefetch_tmap(&tm_v);
   }
@@ -150,7 +170,8 @@ __global__ void __launch_bounds__(kPxThreads, 1)
     const int i0 = min(tid * per, n_groups), i1 = min(i0 + per, n_groups);
     auto of = [&](int i, int& items) {
       const int pages = group_pages(p.groups, i);
-      items = pages == 0 ? 0 : (p.groups.start[i + 1] - p.groups.start[i] + kPxSeqs - 1) / kPxSeqs * kKVHeads;
+      const int tiles = pages == 0 ? 0 : (p.groups.start[i + 1] - p.groups.start[i] + kPxSeqs - 1) / kPxSeqs;
+      items = tiles * kKVHeads;
       return items * pages * kBlkPerPage;
     };
     int units = 0, items = 0;
@@ -185,184 +206,221 @@ __global__ void __launch_bounds__(kPxThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = sh->tmem, o_tm = tmem + 256;
+  const uint32_t tmem = sh->tmem;
   const int total = n_groups ? sh->units[n_groups] : 0;
   const int share = max(1, (total + int(gridDim.x) - 1) / int(gridDim.x));
-  const int u0 = int(min((long long)blockIdx.x * share, (long long)total)), u1 = min(u0 + share, total);
+  const int u0 = int(min((long long)blockIdx.x * share, (long long)total)), u1 = min(u0 + share, total), n_tiles = u1 - u0;
 
-  if (u0 < u1) {
+  if (n_tiles > 0) {
     if (warp == 0) {
       // ------------------------------------------------------------ TMA producer
-      int t = 0, runs = 0, q_loads = 0;
+      for (int u = u0; u < u1;) {  // the items' parts: one of each CTA from the first on that takes some of it
+        const PxRun run = px_run(p, sh, u, u1);
+        if (run.k0 == 0 && lane < run.seqs)
+          p.parts.pair[(size_t)(run.seq0 + lane) * kKVHeads + run.g] =
+              make_int4(int(blockIdx.x) + run.item, (run.base + run.keys - 1) / share - int(blockIdx.x) + 1,
+                        lane * kGroup, int(uint32_t(run.keys / kBlkPerPage) << 16 | uint32_t(run.seq0)));
+        u += run.n;
+      }
+      // The tiles' places are looked up 32 at a time, one a lane, so that a tile costs this warp few instructions: it shares
+      // its scheduler with softmax warps. (With 100 or 150 to a tile, as a lookup in the loop or two ring positions polled in
+      // turn take, the loads bound the kernel at 800 clocks each: 256 sequences behind 16384 rows 145 us.)
+      int st = 0, loads = 0;
+      uint32_t turn = 1;
       bool ok = true;
-      for (int u = u0; u < u1 && ok; ++runs) {
-        const PxRun r = px_run(p, sh, u, u1);
-        if (r.k0 == 0 && lane < r.seqs) {  // the item's parts: one of each CTA from this one on that takes some of it
-          const int last = (r.last - 1) / share;
-          p.parts.pair[(size_t)(r.seq0 + lane) * kKVHeads + r.g] =
-              make_int4(int(blockIdx.x) + r.item, last - int(blockIdx.x) + 1, lane * kGroup,
-                        int(uint32_t(r.last - r.first) / kBlkPerPage << 16 | uint32_t(r.seq0)));
+      for (int base = 0; base < n_tiles && ok; base += 32) {
+        int my_row = 0, my_g = 0;
+        if (base + lane < n_tiles) {
+          const PxRun run = px_run(p, sh, u0 + base + lane, u1);
+          my_g = run.g;
+          my_row = max(0, blk_page(p.pm, run.seq0, run.k0, p.status)) * GROK_PAGE_TOKENS + run.k0 % kBlkPerPage * kBlk;
         }
-        if (lane == 0) {
-          if (!mbar_wait(&sh->q_empty, (runs & 1) ^ 1, abort, p.status)) {
-            ok = false;
-          } else {
-            mbar_arrive_expect_tx(&sh->q_full, kPxQLoad);
-            ++q_loads;
-            tma_load_4d(sQ, &tm_q, &sh->q_full, 0, r.g * kGroup, r.seq0, 0);
-            tma_load_4d(sQ + kPxQBox, &tm_q, &sh->q_full, 64, r.g * kGroup, r.seq0, 0);
-            for (int k = 0; k < r.n; ++k, ++t) {
-              const int st = t % kPxStages;
-              if (!mbar_wait(&sh->kv_empty[st], ((t / kPxStages) & 1) ^ 1, abort, p.status)) {
-                ok = false;
-                break;
+        const int cnt = min(32, n_tiles - base);
+        for (int j = 0; j < cnt; ++j) {
+          const int row = __shfl_sync(0xffffffffu, my_row, j), g = __shfl_sync(0xffffffffu, my_g, j);
+          if (lane == 0) {
+            ok = mbar_wait(&sh->k_empty[st], turn, abort, p.status);
+            if (ok) {
+              mbar_arrive_expect_tx(&sh->k_full[st], kPxTile);
+              tma_load_4d(sK + st * kPxTile, &tm_k, &sh->k_full[st], 0, row, 0, g);
+              ok = mbar_wait(&sh->v_empty[st], turn, abort, p.status);
+              if (ok) {
+                mbar_arrive_expect_tx(&sh->v_full[st], kPxTile);
+                tma_load_4d(sV + st * kPxTile, &tm_v, &sh->v_full[st], 0, row, 0, g);
               }
-              const int blk = r.k0 + k;
-              const int row = max(0, blk_page(p.pm, r.seq0, blk, p.status)) * GROK_PAGE_TOKENS + blk % kBlkPerPage * kBlk;
-              uint8_t* dst = sKV + st * 2 * kPxTile;
-              mbar_arrive_expect_tx(&sh->kv_full[st], 2 * kPxTile);
-              tma_load_4d(dst, &tm_k, &sh->kv_full[st], 0, r.g, row, 0);
-              tma_load_4d(dst + kPxBox, &tm_k, &sh->kv_full[st], 64, r.g, row, 0);
-              tma_load_4d(dst + kPxTile, &tm_v, &sh->kv_full[st], 0, r.g, row, 0);
-              tma_load_4d(dst + kPxTile + kPxBox, &tm_v, &sh->kv_full[st], 64, r.g, row, 0);
+              loads += ok ? 2 : 1;
             }
           }
+          ok = __shfl_sync(0xffffffffu, int(ok), 0);
+          if (!ok) break;
+          if (++st == kPxStages) st = 0, turn ^= 1;
         }
-        ok = __all_sync(0xffffffffu, ok);
-        u += r.n;
       }
       // Copies in flight (only after an abort) land before the CTA exits.
       if (lane == 0) {
         volatile int never = 0;
-        for (int i = max(0, t - kPxStages); i < t; ++i)
-          mbar_wait(&sh->kv_full[i % kPxStages], (i / kPxStages) & 1, &never, p.status);
-        if (q_loads > 0) mbar_wait(&sh->q_full, (q_loads - 1) & 1, &never, p.status);
+        const int k_loads = (loads + 1) / 2, v_loads = loads / 2;
+        for (int i = max(0, k_loads - kPxStages); i < k_loads; ++i)
+          mbar_wait(&sh->k_full[i % kPxStages], (i / kPxStages) & 1, &never, p.status);
+        for (int i = max(0, v_loads - kPxStages); i < v_loads; ++i)
+          mbar_wait(&sh->v_full[i % kPxStages], (i / kPxStages) & 1, &never, p.status);
       }
     } else if (warp == 1) {
-      // ------------------------------------------------------------ MMA issuer
-      // (converged through the waits; one fixed lane issues the products and commits)
+      // ------------------------------------------------------------ S = Q K^T
+      // (The issuing warps run converged through the waits; one fixed lane issues the products and commits.)
       const bool leader = elect_one();
-      const uint64_t qd = make_sdesc_sw128(smem_u32(sQ), 16, 1024);
-      const uint64_t kd = make_sdesc_sw128(smem_u32(sKV), 16, 1024);
-      const uint64_t vd = make_sdesc_sw128(smem_u32(sKV + kPxTile), kPxBox, 1024);
-      constexpr uint32_t idesc_s = make_idesc_bf16(kPxRows, kBlk, 0), idesc_o = make_idesc_bf16(kPxRows, kD, 1);
-      const int n = u1 - u0;
-      PxRun rs = px_run(p, sh, u0, u1), ro = rs;
-      int ts = 0, s_end = rs.n, s_runs = 0;       // next S product, the end of its run, its run's number
-      int o_first = 0, o_end = ro.n, o_runs = 0;  // run of the next P V
-      bool ok = true;
-      for (int t = 0; t < n && ok; ++t) {
-        while (ts < n && ts <= t + kPxAhead) {
-          if (ts == s_end) {
-            rs = px_run(p, sh, u0 + ts, u1);
-            s_end += rs.n;
-            ++s_runs;
-          }
-          const int st = ts % kPxStages;
-          bool w = mbar_wait(&sh->kv_full[st], (ts / kPxStages) & 1, abort, p.status);
-          if (ts == s_end - rs.n) w = w && mbar_wait(&sh->q_full, s_runs & 1, abort, p.status);
-          ok = __all_sync(0xffffffffu, w);
-          if (!ok) break;
-          tc_fence_after();
-          if (leader) {
-#pragma unroll
-            for (int kk = 0; kk < 8; ++kk)
-              umma_ss(tmem + (ts & 3) * 64, qd + uint64_t(((kk >> 2) * kPxQBox + (kk & 3) * 32) >> 4),
-                      kd + uint64_t((st * 2 * kPxTile + (kk >> 2) * kPxBox + (kk & 3) * 32) >> 4), idesc_s, kk > 0);
-            umma_commit(&sh->s_full[ts & 3]);
-            if (ts == s_end - 1) umma_commit(&sh->q_empty);
-          }
-          __syncwarp();
-          ++ts;
+      const uint64_t kd = make_sdesc_sw128(smem_u32(sK), 16, 1024);
+      constexpr uint32_t idesc = make_idesc_bf16(kPxRows, kBlk, 0);
+      int end = 0, runs = -1, st = 0, buf = 0;
+      uint32_t turn = 0, free_turn = 1;
+      for (int t = 0; t < n_tiles; ++t) {
+        bool w = true;
+        if (t == end) {
+          end += px_run(p, sh, u0 + t, u1).n;
+          ++runs;
+          w = mbar_wait(&sh->q_full, runs & 1, abort, p.status);
         }
-        if (!ok) break;
-        if (t == o_end) {
-          ro = px_run(p, sh, u0 + t, u1);
-          o_first = o_end;
-          o_end += ro.n;
-          ++o_runs;
-          ok = __all_sync(0xffffffffu, mbar_wait(&sh->o_empty, (o_runs & 1) ^ 1, abort, p.status));
-          if (!ok) break;
-        }
-        ok = __all_sync(0xffffffffu, mbar_wait(&sh->p_full[t & 3], (t >> 2) & 1, abort, p.status));
-        if (!ok) break;
+        w = w && mbar_wait(&sh->k_full[st], turn, abort, p.status) &&
+            mbar_wait(&sh->s_empty[buf], free_turn, abort, p.status);
+        if (!__all_sync(0xffffffffu, w)) break;
         tc_fence_after();
         if (leader) {
-          const int st = t % kPxStages;
+          const uint64_t k = kd + uint64_t((st * kPxTile) >> 4);
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk) {  // 16 keys each
-            const uint32_t pc = tmem + (t & 3) * 64 + (kk >> 1) * 32 + (kk & 1) * 8;
-            const uint64_t v = vd + uint64_t((st * 2 * kPxTile + kk * 2048) >> 4);
-            umma_ts(o_tm, pc, v, idesc_o, t > o_first || kk > 0);
-            umma_ts(o_tm, pc + 16, v, idesc_o, 1u);
-          }
-          umma_commit(&sh->kv_empty[st]);
-          if (t == o_end - 1) umma_commit(&sh->o_full);
+          for (int kk = 0; kk < 8; ++kk)
+            umma_ts(tmem + kPxS + buf * kBlk, tmem + kPxQ + kk * 8, k + uint64_t(((kk >> 2) * kPxBox + (kk & 3) * 32) >> 4),
+                    idesc, kk > 0);
+          umma_commit(&sh->s_full[buf]);
+          umma_commit(&sh->k_empty[st]);
+          if (t == end - 1) umma_commit(&sh->q_empty);
         }
         __syncwarp();
+        if (++st == kPxStages) st = 0, turn ^= 1;
+        if (++buf == kPxBufs) buf = 0, free_turn ^= 1;
       }
       // No product may still run when TMEM is released.
       if (leader) umma_commit(&sh->done);
       __syncwarp();
       volatile int never = 0;
       mbar_wait(&sh->done, 0, &never, p.status);
+    } else if (warp == kPxThreads / 32 - 1) {
+      // ------------------------------------------------------------ O += P V
+      const bool leader = elect_one();
+      const uint64_t vd = make_sdesc_sw128(smem_u32(sV), kPxBox, 1024);
+      constexpr uint32_t idesc = make_idesc_bf16(kPxRows, kD, 1);
+      int first = 0, end = px_run(p, sh, u0, u1).n, runs = 0, st = 0, buf = 0;
+      uint32_t turn = 0, p_turn = 0;
+      for (int t = 0; t < n_tiles; ++t) {
+        bool w = true;
+        if (t == end) {
+          first = end;
+          end += px_run(p, sh, u0 + t, u1).n;
+          ++runs;
+          w = mbar_wait(&sh->o_empty, (runs & 1) ^ 1, abort, p.status);
+        }
+        w = w && mbar_wait(&sh->v_full[st], turn, abort, p.status) && mbar_wait(&sh->p_full[buf], p_turn, abort, p.status);
+        if (!__all_sync(0xffffffffu, w)) break;
+        tc_fence_after();
+        if (leader) {
+          const uint64_t v = vd + uint64_t((st * kPxTile) >> 4);
+          const uint32_t pc = tmem + kPxS + buf * kBlk;
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk) {  // 16 keys each
+            umma_ts(tmem + kPxO, pc + kk * 16, v + uint64_t((kk * 2048) >> 4), idesc, t > first || kk > 0);
+            umma_ts(tmem + kPxO, pc + kk * 16 + 8, v + uint64_t((kk * 2048) >> 4), idesc, 1u);
+          }
+          umma_commit(&sh->s_empty[buf]);
+          umma_commit(&sh->v_empty[st]);
+          if (t == end - 1) umma_commit(&sh->o_full);
+        }
+        __syncwarp();
+        if (++st == kPxStages) st = 0, turn ^= 1;
+        if (++buf == kPxBufs) buf = 0, p_turn ^= 1;
+      }
+      if (leader) umma_commit(&sh->done);
+      __syncwarp();
+      volatile int never = 0;
+      mbar_wait(&sh->done, 0, &never, p.status);
     } else {
-      // ------------------------------------------------------------ softmax of the key tiles t = team (mod 2), epilogue
-      const int team = warp < 6 ? 0 : 1, quad = warp & 3, r = quad * 32 + lane;
+      // ------------------------------------------------------------ softmax of the key tiles t = team (mod 4), epilogue
+      const int team = (warp - 2) >> 2, quad = warp & 3, r = quad * 32 + lane;
       const uint32_t trow = tmem + (uint32_t(quad * 32) << 16);
-      int t0 = 0, runs = 0;
-      bool ok = true;
-      for (int u = u0; u < u1; ++runs) {
-        const PxRun run = px_run(p, sh, u, u1);
+      // Q of a run into TMEM: this thread's row, features 32 team .. 32 team + 31 (zeros for rows without a query).
+      auto load_q = [&](const PxRun& run) {
+        if (quad * 32 < run.seqs * kGroup) {
+          const bool mine = r < run.seqs * kGroup;
+          const uint4* src = p.q + ((size_t)(run.seq0 + r / kGroup) * kQHeads + run.g * kGroup + r % kGroup) * (kD / 8) + team * 4;
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            const uint4 z = make_uint4(0, 0, 0, 0), x = mine ? src[2 * c] : z, y = mine ? src[2 * c + 1] : z;
+            const uint32_t w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+            tmem_st8(trow + kPxQ + team * 16 + c * 8, w);
+          }
+          tmem_wait_st();
+        }
+        tc_fence_before();
+        mbar_arrive(&sh->q_full);
+      };
+      int t = team, t0 = 0, runs = 0, u = u0;
+      PxRun run = px_run(p, sh, u0, u1);
+      load_q(run);
+      while (true) {
         const int rows = run.seqs * kGroup;
         const bool live = quad * 32 < rows;  // (of the warp; the other warps' P is never looked at)
         uint64_t l = f2_pack(0.f, 0.f);
-        for (int t = t0 + ((t0 ^ team) & 1); t < t0 + run.n; t += 2) {
-          ok = __all_sync(0xffffffffu, mbar_wait(&sh->s_full[t & 3], (t >> 2) & 1, abort, p.status));
+        bool ok = true;
+        t0 += run.n;
+        u += run.n;
+        for (; t < t0; t += kPxTeams) {
+          const int buf = t % kPxBufs;
+          ok = __all_sync(0xffffffffu, mbar_wait(&sh->s_full[buf], (t / kPxBufs) & 1, abort, p.status));
           if (!ok) break;
           tc_fence_after();
           if (live) {
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              uint32_t s[32], hi[16], lo[16];
-              const uint32_t col = trow + (t & 3) * 64 + c * 32;
-              tmem_ld32(col, s);
-              tmem_wait_ld_dep(s);
+            for (int c = 0; c < 4; ++c) {  // P of 16 keys over their S: hi in 8 columns, lo in 8
+              uint32_t s[16], hi[8], lo[8];
+              const uint32_t col = trow + kPxS + buf * kBlk + c * 16;
+              tmem_ld16(col, s);
               px_weights(s, l, hi, lo);
-              tmem_st16(col, hi);
-              tmem_st16(col + 16, lo);
+              tmem_st8(col, hi);
+              tmem_st8(col + 8, lo);
             }
             tmem_wait_st();
           }
           tc_fence_before();
-          mbar_arrive(&sh->p_full[t & 3]);
+          mbar_arrive(&sh->p_full[buf]);
         }
         if (!ok) break;
-        t0 += run.n;
-        u += run.n;
-        ok = __all_sync(0xffffffffu, mbar_wait(&sh->o_full, runs & 1, abort, p.status));
-        if (!ok) break;
-        tc_fence_after();
         const size_t slot = (size_t)blockIdx.x + run.item;
+        if (u < u1) {  // the next run's Q, once this one's is read, ahead of this one's O
+          run = px_run(p, sh, u, u1);
+          if (!__all_sync(0xffffffffu, mbar_wait(&sh->q_empty, runs & 1, abort, p.status))) break;
+          tc_fence_after();
+          load_q(run);
+        }
+        if (!__all_sync(0xffffffffu, mbar_wait(&sh->o_full, runs & 1, abort, p.status))) break;
+        ++runs;
+        tc_fence_after();
         if (live) {
-          float4* po = p.parts.o + (slot * (kD / 4) + team * 16) * kPxRows + r;
+          float4* po = p.parts.o + (slot * (kD / 4) + team * 8) * kPxRows + r;
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            uint32_t o[32];
-            tmem_ld32(trow + 256 + team * 64 + c * 32, o);
-            tmem_wait_ld_dep(o);
+            uint32_t o[16];
+            tmem_ld16(trow + kPxO + team * 32 + c * 16, o);
             if (r < rows)
 #pragma unroll
-              for (int q = 0; q < 8; ++q)
-                po[(c * 8 + q) * kPxRows] = make_float4(__uint_as_float(o[4 * q]), __uint_as_float(o[4 * q + 1]),
+              for (int q = 0; q < 4; ++q)
+                po[(c * 4 + q) * kPxRows] = make_float4(__uint_as_float(o[4 * q]), __uint_as_float(o[4 * q + 1]),
                                                         __uint_as_float(o[4 * q + 2]), __uint_as_float(o[4 * q + 3]));
           }
           float l0, l1;
           f2_unpack(l, l0, l1);
-          if (r < rows) p.parts.l[(slot * 2 + team) * kPxRows + r] = l0 + l1;
+          if (r < rows) p.parts.l[(slot * kPxSums + team) * kPxRows + r] = l0 + l1;
         }
         tc_fence_before();
         mbar_arrive(&sh->o_empty);
+        if (t0 >= n_tiles) break;
       }
     }
   }
@@ -420,38 +478,30 @@ extern "C" grok_status grok_attn_decode_shared_paged(const grok_bf16* q_rot, con
   if (workspace_bytes < need)
     return fail(GROK_ERR_INVALID_ARG, "%s: workspace of %zu bytes is smaller than the %zu needed", who, workspace_bytes,
                 need);
-  CUtensorMap tq, tk, tv;
-  {
-    const uint64_t dims[4] = {kD, kQHeads, uint64_t(B), 1};
-    const uint64_t strides[3] = {kD * 2, uint64_t(kQHeads) * kD * 2, uint64_t(B) * kQHeads * kD * 2};
-    const uint32_t box[4] = {64, kGroup, kPxSeqs, 1};
-    if ((st = encode_tmap_bf16_4d(&tq, q_rot, dims, strides, box)) != GROK_OK) return st;
-  }
-  {
-    const uint64_t rows = uint64_t(n_pages) * GROK_PAGE_TOKENS;
-    const uint64_t dims[4] = {kD, kKVHeads, rows, 1};
-    const uint64_t strides[3] = {kD * 2, uint64_t(kKVHeads) * kD * 2, rows * kKVHeads * kD * 2};
-    const uint32_t box[4] = {64, 1, kBlk, 1};
-    if ((st = encode_tmap_bf16_4d(&tk, k_pool, dims, strides, box)) != GROK_OK) return st;
-    if ((st = encode_tmap_bf16_4d(&tv, v_pool, dims, strides, box)) != GROK_OK) return st;
-  }
+  CUtensorMap tk, tv;
+  if ((st = encode_pool(&tk, k_pool, n_pages)) != GROK_OK) return st;
+  if ((st = encode_pool(&tv, v_pool, n_pages)) != GROK_OK) return st;
   static bool attr_set[kMaxDevices] = {};  // per device; idempotent: every thread would set the same value
   int dev = 0;
   if ((st = device_index(&dev)) != GROK_OK) return st;
   if (!attr_set[dev]) {
     cudaError_t e = cudaFuncSetAttribute(prefix_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kPxSmem);
+    // (the SM's whole shared memory, so that the next kernel's CTAs fit beside this one's)
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(prefix_kernel, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
     if (e != cudaSuccess) return fail(cuda_status(e), "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
     attr_set[dev] = true;
   }
   char* ws = static_cast<char*>(workspace);
   const PrefixParts prefix = prefix_parts(ws + blocks, B, n_groups, sms);
   PxParams p;
+  p.q = reinterpret_cast<const uint4*>(q_rot);
   p.groups = Groups{group_start, shared_pages, n_groups};
   p.pm = PageMap{block_table, max_pages, n_pages};
   p.B = B;
   p.parts = prefix;
   p.status = dev_status;
-  prefix_kernel<<<sms, kPxThreads, kPxSmem, static_cast<cudaStream_t>(stream)>>>(tq, tk, tv, p);
+  prefix_kernel<<<sms, kPxThreads, kPxSmem, static_cast<cudaStream_t>(stream)>>>(tk, tv, p);
   if ((st = check_launch("prefix")) != GROK_OK) return st;
   BlockArgs a = {};
   a.q_rot = q_rot;

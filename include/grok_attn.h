@@ -586,7 +586,7 @@ grok_status grok_qkv_rope_append_paged(const grok_bf16* x, const grok_bf16* w, c
  *   entries of their block tables in common. Those rows are read once for up to 21
  *   sequences (on the tensor cores), the rows behind them once for each.
  *   group_start [n_groups + 1], shared_pages [n_groups] int32 (device), 1 <= n_groups <=
- *   1024. Sequences in no group are decoded by themselves. Where group_start is not
+ *   256. Sequences in no group are decoded by themselves. Where group_start is not
  *   ascending within [0, B], or a shared_pages[i] lies outside [0, max_pages],
  *   GROK_DEV_BAD_GROUP is set and every sequence is decoded by itself. Sequences of a group
  *   whose tables differ in those entries set it too; their outputs are meaningless.

@@ -45,7 +45,7 @@ BAD = {_bounds: [dict(k=None), dict(table=None), dict(start=None), dict(codes=No
                  dict(ws=A + 16), dict(budget=0), dict(budget=1025)],
        _shared: [dict(q=None), dict(k=None), dict(v=None), dict(table=None), dict(length=None), dict(start=None),
                  dict(pages=None), dict(ws=None), dict(out=None), dict(q=A + 2), dict(k=A + 8), dict(v=A + 8),
-                 dict(out=A + 8), dict(ws=A + 16), dict(groups=0), dict(groups=1025)]}
+                 dict(out=A + 8), dict(ws=A + 16), dict(groups=0), dict(groups=257)]}
 
 
 @pytest.mark.parametrize("call,bad", [(c, b) for c, bads in BAD.items() for b in bads + SIZES],
@@ -61,7 +61,7 @@ def test_bad_workspace_questions(lib):
     assert lib.grok_attn_decode_shared_workspace(2, 4, 1, None) == 1
     for B, budget in ((0, 4), (65536, 4), (2, 0), (2, 1025)):
         assert lib.grok_attn_decode_sparse_workspace(B, budget, ctypes.byref(n)) == 1
-    for B, mp, groups in ((0, 4, 1), (65536, 4, 1), (2, 0, 1), (2, 513, 1), (2, 4, 0), (2, 4, 1025)):
+    for B, mp, groups in ((0, 4, 1), (65536, 4, 1), (2, 0, 1), (2, 513, 1), (2, 4, 0), (2, 4, 257)):
         assert lib.grok_attn_decode_shared_workspace(B, mp, groups, ctypes.byref(n)) == 1
 
 
