@@ -32,6 +32,7 @@ __host__ __device__ constexpr int bk_ring(bool list) { return list ? 5 : 4; }
 constexpr int kBkQ = kGroup * kD * 2;        // a pair's queries
 constexpr int kBkPlan = 512;                 // entries of the table of block counts
 constexpr int kBkCtas = 2;                   // CTAs resident on an SM
+constexpr int kBkFew = 8;                    // blocks per CTA up to which half of the CTAs take them (beside a prefix)
 
 template <int kRing>
 struct BkShared {
@@ -40,6 +41,8 @@ struct BkShared {
   uint64_t full[kRing], empty[kRing], sum_full, sum_empty;
   int2 token[kRing];      // pair and visible keys of the block whose K is in a place of the ring; pair -1: the end
   int cum[kBkPlan + 1];   // blocks per KV head of the sequences before each entry's
+  int seq[kBkPlan];       // length | pages left out << 17, where an entry is a sequence
+  GroupTable groups;
   int warp_sum[kBkWarps + 1];
   int abort;
 };
@@ -73,14 +76,10 @@ __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t x) {
   return y;
 }
 
-// Blocks that sequence b reads per KV head; -1 when its length is bad. share: its pages in common (not kList).
-template <bool kList>
-__device__ __forceinline__ int bk_blocks(const BkParams& p, int b, bool groups, int& share) {
-  const int cap = p.pm.max_pages * GROK_PAGE_TOKENS, len = p.kv_len[b];
-  share = !kList && groups ? seq_pages(p.groups, b) : 0;
-  if (len < 1 || len > cap || len < share * GROK_PAGE_TOKENS) return -1;
-  const int n = (len + kBlk - 1) / kBlk - share * kBlkPerPage;
-  return kList ? min(n, p.budget) : n;
+// Blocks that a sequence of `len` rows reads per KV head, `share` of its pages left out; -1 when its length is bad.
+__device__ __forceinline__ int bk_blocks(const BkParams& p, int len, int share) {
+  if (len < 1 || len > p.pm.max_pages * GROK_PAGE_TOKENS || len < share * GROK_PAGE_TOKENS) return -1;
+  return min((len + kBlk - 1) / kBlk - share * kBlkPerPage, p.budget);
 }
 
 // (Registers: 112 a thread at most behind prefixes, for the same reason as in the prefix kernel.)
@@ -112,24 +111,42 @@ __global__ void __launch_bounds__(kList ? kBkThreads : 576, kList ? kBkCtas : 1)
   }
 
   // The plan: blocks per KV head before each sequence (or each `step` sequences, where there are many).
-  const bool groups = !kList && groups_ok(p.groups, p.B, p.pm.max_pages);
-  if (!kList && !groups && blockIdx.x == 0 && tid == 0) report(p.status, GROK_DEV_BAD_GROUP);
   const int step = (p.B + kBkPlan - 1) / kBkPlan, entries = (p.B + step - 1) / step;
+  constexpr int kPer = (kBkPlan + kBkThreads - 1) / kBkThreads;  // contiguous entries per thread
+  const int per = (entries + kBkThreads - 1) / kBkThreads, e0 = tid * per;
+  int len0[kPer];  // (loaded beside the groups)
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) len0[i] = i < per && e0 + i < entries ? p.kv_len[(e0 + i) * step] : 0;
+  int n_groups = 0;
+  if (!kList) {
+    bool fine = true;
+    for (int i = tid; i < p.groups.n; i += kBkThreads) fine &= load_groups(p.groups, p.B, p.pm.max_pages, &sh->groups, i);
+    if (__syncthreads_and(fine))
+      n_groups = p.groups.n;
+    else if (blockIdx.x == 0 && tid == 0)
+      report(p.status, GROK_DEV_BAD_GROUP);
+  }
   {
-    const int per = (entries + kBkThreads - 1) / kBkThreads;  // contiguous entries per thread
-    const int e0 = min(tid * per, entries), e1 = min(e0 + per, entries);
-    int mine = 0;
-    for (int b = e0 * step; b < min(e1 * step, p.B); ++b) {
-      int share;
-      const int n = bk_blocks<kList>(p, b, groups, share);
-      if (blockIdx.x == 0) {
-        if (n < 0) report(p.status, GROK_DEV_BAD_KV_LEN);
-        if (n <= 0)
-          for (int g = 0; g < kKVHeads; ++g) p.parts.pair[b * kKVHeads + g] = make_int2(0, n);
-        if (!kList && share == 0)
-          for (int g = 0; g < kKVHeads; ++g) p.prefix_pair[b * kKVHeads + g] = make_int4(0, 0, 0, 0);
-      }
-      mine += max(n, 0);
+    int n_of[kPer], mine = 0;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      n_of[i] = 0;
+      const int e = e0 + i;
+      if (i < per && e < entries)
+        for (int b = e * step; b < min((e + 1) * step, p.B); ++b) {
+          const int len = b == e * step ? len0[i] : p.kv_len[b], share = n_groups ? sh->groups.of_seq(n_groups, b) : 0;
+          const int n = bk_blocks(p, len, share);
+          if (step == 1) sh->seq[e] = len | share << 17;
+          if (blockIdx.x == 0) {
+            if (n < 0) report(p.status, GROK_DEV_BAD_KV_LEN);
+            if (n <= 0)
+              for (int g = 0; g < kKVHeads; ++g) p.parts.pair[b * kKVHeads + g] = make_int2(0, n);
+            if (!kList && share == 0)
+              for (int g = 0; g < kKVHeads; ++g) p.prefix_pair[b * kKVHeads + g] = make_int4(0, 0, 0, 0);
+          }
+          n_of[i] += max(n, 0);
+        }
+      mine += n_of[i];
     }
     int incl = mine;
 #pragma unroll
@@ -141,18 +158,19 @@ __global__ void __launch_bounds__(kList ? kBkThreads : 576, kList ? kBkCtas : 1)
     __syncthreads();
     int at = incl - mine;
     for (int w = 0; w < warp; ++w) at += sh->warp_sum[w];
-    for (int e = e0; e < e1; ++e) {
-      sh->cum[e] = at;
-      for (int b = e * step; b < min((e + 1) * step, p.B); ++b) {
-        int share;
-        at += max(bk_blocks<kList>(p, b, groups, share), 0);
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+      if (i < per && e0 + i < entries) {
+        sh->cum[e0 + i] = at;
+        at += n_of[i];
+        if (e0 + i == entries - 1) sh->cum[entries] = at;
       }
-    }
-    if (e1 == entries && e0 < e1) sh->cum[entries] = at;
   }
   __syncthreads();
   const int total = kKVHeads * sh->cum[entries];
-  const int share_of = max(1, (total + int(gridDim.x) - 1) / int(gridDim.x));  // blocks per CTA
+  // Beside the prefix kernel an SM has room for one CTA: little work is dealt to the first half of them.
+  const int ctas = !kList && total <= kBkFew * int(gridDim.x) ? int(gridDim.x) / kBkCtas : int(gridDim.x);
+  const int share_of = max(1, (total + ctas - 1) / ctas);  // blocks per CTA
   const int cta = blockIdx.x;
   const int lo = min((long long)cta * share_of, (long long)total), hi = min(lo + share_of, total);
   if (lo < hi) {
@@ -185,8 +203,12 @@ __global__ void __launch_bounds__(kList ? kBkThreads : 576, kList ? kBkCtas : 1)
           int e = 0;
           for (int d = kBkPlan / 2; d; d /= 2)
             if (e + d < entries && kKVHeads * sh->cum[e + d] <= idx) e += d;
-          int rest = idx - kKVHeads * sh->cum[e], b = e * step, share, n;
-          while (n = max(bk_blocks<kList>(p, b, groups, share), 0), rest >= kKVHeads * n) {
+          int rest = idx - kKVHeads * sh->cum[e], b = e * step, len, share, n;
+          while (true) {
+            len = step == 1 ? sh->seq[e] & 0x1FFFF : p.kv_len[b];
+            share = step == 1 ? sh->seq[e] >> 17 : n_groups ? sh->groups.of_seq(n_groups, b) : 0;
+            n = max(bk_blocks(p, len, share), 0);
+            if (step == 1 || rest < kKVHeads * n) break;
             rest -= kKVHeads * n;
             ++b;
           }
@@ -196,7 +218,7 @@ __global__ void __launch_bounds__(kList ? kBkThreads : 576, kList ? kBkCtas : 1)
             const int last = (idx + n - 1) / share_of;
             p.parts.pair[my_pair] = make_int2(cta + my_pair, last - cta + 1);
           }
-          const int len = p.kv_len[b], blocks = (len + kBlk - 1) / kBlk;
+          const int blocks = (len + kBlk - 1) / kBlk;
           int blk = share * kBlkPerPage + k;
           if (kList) blk = p.sel[(size_t)my_pair * p.budget + k];
           if (blk >= blocks) {
@@ -387,7 +409,8 @@ __global__ void __launch_bounds__(kTeams* kBkPartO)
   __shared__ float4 so[kTeams][kBkPartO];
   __shared__ float sl[kTeams][8];
   __shared__ float acc[kGroup][kD + 4];
-  constexpr int kThreads = kTeams * kBkPartO;
+  __shared__ float4 po[kPrefix && kTeams > 1 ? kTeams - 1 : 1][kPrefix && kTeams > 1 ? kGroup * kD / 4 : 1];
+  __shared__ float psum[kTeams][kPxSums][kGroup];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int g = blockIdx.x, b = blockIdx.y, pair = b * kKVHeads + g;
   const int tid = threadIdx.x, team = tid / kBkPartO, at = tid % kBkPartO;
@@ -406,26 +429,29 @@ __global__ void __launch_bounds__(kTeams* kBkPartO)
     v.w += x.w;
     if (at < 8) l += parts.l[s * 8 + at];
   }
-  // The prefix's parts: thread (head, feature quad). The other threads: does the table agree with the one that was read?
+  // The prefix's parts: thread (head, feature quad) of a team. The other threads: does the table agree with the one that
+  // was read?
   float4 pv = make_float4(0.f, 0.f, 0.f, 0.f);
   float pl = 0.f;
-  const int h = tid % kGroup, quad = tid / kGroup;
+  const int h = at % kGroup, quad = at / kGroup;
   if (kPrefix && quad < kD / 4) {
     const int r = pre.z + h;
 #pragma unroll 4
-    for (int i = 0; i < pre.y; ++i) {
+    for (int i = team; i < pre.y; i += kTeams) {
       const size_t s = (size_t)pre.x + i;
       const float4 x = prefix.o[(s * (kD / 4) + quad) * kPxRows + r];
       pv.x += x.x;
       pv.y += x.y;
       pv.z += x.z;
       pv.w += x.w;
-#pragma unroll
-      for (int w = 0; w < kPxSums; ++w) pl += prefix.l[(s * kPxSums + w) * kPxRows + r];
+      if (quad < kPxSums) pl += prefix.l[(s * kPxSums + quad) * kPxRows + r];
     }
+    if (quad < kPxSums) psum[team][quad][h] = pl;
+    if (kTeams > 1 && team > 0) po[team - 1][at] = pv;
   } else if (kPrefix && g == 0) {
+    constexpr int kEach = kBkPartO - kGroup * kD / 4;
     const int seq = pre.w & 0xFFFF;
-    for (int i = tid - kGroup * kD / 4; i < int(uint32_t(pre.w) >> 16); i += kThreads - kGroup * kD / 4)
+    for (int i = team * kEach + at - kGroup * kD / 4; i < int(uint32_t(pre.w) >> 16); i += kTeams * kEach)
       if (pm.table[(size_t)b * pm.max_pages + i] != pm.table[(size_t)seq * pm.max_pages + i])
         report(status, GROK_DEV_BAD_GROUP);
   }
@@ -453,10 +479,24 @@ __global__ void __launch_bounds__(kTeams* kBkPartO)
     }
   }
   __syncthreads();
-  if (quad < kD / 4) {
-    float sum = pl;
+  if (team == 0 && quad < kD / 4) {
+    float sum = 0.f;
 #pragma unroll
     for (int w = 0; w < kTeams; ++w) sum += sl[w][h];
+    if (kPrefix) {
+#pragma unroll
+      for (int w = 0; w < kTeams; ++w) {
+#pragma unroll
+        for (int i = 0; i < kPxSums; ++i) sum += psum[w][i][h];
+        if (w > 0) {
+          const float4 x = po[w - 1][at];
+          pv.x += x.x;
+          pv.y += x.y;
+          pv.z += x.z;
+          pv.w += x.w;
+        }
+      }
+    }
     const float inv = sum == 0.f ? 0.f : 1.0f / sum;  // (a list without a block: zeros)
     const float* x = &acc[h][quad * 4];
     out[((size_t)pair * kGroup + h) * (kD / 4) + quad] =
@@ -550,7 +590,7 @@ grok_status block_decode_run(const BlockArgs& a, char* ws, const PrefixParts* pr
   p.kv_len = a.kv_len;
   p.B = a.B;
   p.sel = a.sel;
-  p.budget = a.budget;
+  p.budget = a.sel ? a.budget : kBlkMax;
   p.groups = a.groups;
   p.parts = block_parts(ws, a.B, sms);
   p.prefix_pair = prefix ? prefix->pair : nullptr;
@@ -559,7 +599,7 @@ grok_status block_decode_run(const BlockArgs& a, char* ws, const PrefixParts* pr
   if (st != GROK_OK) return st;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
-  const int teams = a.B * kKVHeads <= sms ? 4 : 1;
+  const int teams = a.B * kKVHeads <= 2 * sms ? 4 : 1;
   cfg.gridDim = dim3(kKVHeads, a.B);
   cfg.blockDim = dim3(teams * kBkPartO);
   cfg.stream = a.stream;

@@ -18,29 +18,30 @@ struct Groups {
   int n;
 };
 
-// Whether the groups are usable: starts in order within [0, B], pages within [0, max_pages]. The whole CTA calls this.
-__device__ __forceinline__ bool groups_ok(const Groups& gr, int B, int max_pages) {
-  bool bad = false;
-  for (int i = threadIdx.x; i < gr.n; i += blockDim.x) {
-    const int a = gr.start[i], z = gr.start[i + 1], pg = gr.pages[i];
-    bad |= a < 0 || z < a || z > B || pg < 0 || pg > max_pages;
+// The groups in shared memory. One that is not usable, or of one sequence, which has nothing to share, has 0 pages.
+struct GroupTable {
+  int start[kGroupsMax + 1];
+  int pages[kGroupsMax];
+  // Pages that sequence b's group has in common.
+  __device__ __forceinline__ int of_seq(int n, int b) const {
+    if (b < start[0] || b >= start[n]) return 0;
+    int lo = 0, hi = n;  // start[lo] <= b < start[hi]
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (start[mid] <= b) lo = mid; else hi = mid;
+    }
+    return pages[lo];
   }
-  return !__syncthreads_or(bad);
-}
-
-// Pages that a group's sequences are given in common: a group of one has nothing to share.
-__device__ __forceinline__ int group_pages(const Groups& gr, int i) {
-  return gr.start[i + 1] - gr.start[i] < 2 ? 0 : gr.pages[i];
-}
-// Those of sequence b (the groups are usable).
-__device__ __forceinline__ int seq_pages(const Groups& gr, int b) {
-  int lo = 0, hi = gr.n;  // start[lo] <= b < start[hi], where there is such a group
-  if (b < gr.start[0] || b >= gr.start[gr.n]) return 0;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (gr.start[mid] <= b) lo = mid; else hi = mid;
-  }
-  return group_pages(gr, lo);
+};
+// Loads them, by threads 0 to n - 1 of the CTA and without waiting for it; a thread's part of the check that starts
+// ascend within [0, B] and pages lie within [0, max_pages] (where one fails, no group is used).
+__device__ __forceinline__ bool load_groups(const Groups& gr, int B, int max_pages, GroupTable* t, int tid) {
+  if (tid >= gr.n) return true;
+  const int a = gr.start[tid], z = gr.start[tid + 1], pg = gr.pages[tid];
+  t->start[tid] = a;
+  if (tid == gr.n - 1) t->start[gr.n] = z;
+  t->pages[tid] = z - a < 2 ? 0 : pg;
+  return a >= 0 && z >= a && z <= B && pg >= 0 && pg <= max_pages;
 }
 
 // Partial results of the block kernel, per part: the sums O in the layout of the products' accumulators

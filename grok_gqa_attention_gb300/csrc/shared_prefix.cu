@@ -36,6 +36,7 @@ struct PxShared {
   uint64_t q_full, q_empty, o_full, o_empty, done;
   uint64_t k_full[kPxStages], k_empty[kPxStages], v_full[kPxStages], v_empty[kPxStages];
   uint64_t s_full[kPxBufs], p_full[kPxBufs], s_empty[kPxBufs];
+  GroupTable groups;
   int units[kGroupsMax + 1];  // key tiles before each group's
   int items[kGroupsMax + 1];  // (KV head, query tile) pairs before each group's
   int warp_units[kPxThreads / 32], warp_items[kPxThreads / 32];
@@ -60,6 +61,7 @@ struct PxRun {
   int k0, n, keys;  // first key tile, number of them, of the item
   int base;         // the item's first unit
   int seq0, seqs;   // sequences of the query tile
+  int table;        // the sequence whose block table is read: the group's first
 };
 
 __device__ __forceinline__ PxRun px_run(const PxParams& p, const PxShared* sh, int unit, int hi) {
@@ -69,9 +71,10 @@ __device__ __forceinline__ PxRun px_run(const PxParams& p, const PxShared* sh, i
     const int mid = (lo + up) >> 1;
     if (sh->units[mid] <= unit) lo = mid; else up = mid;
   }
-  const int a = p.groups.start[lo], n = p.groups.start[lo + 1] - a;
+  const int a = sh->groups.start[lo], n = sh->groups.start[lo + 1] - a;
   const int tiles = (n + kPxSeqs - 1) / kPxSeqs;
-  r.keys = p.groups.pages[lo] * kBlkPerPage;
+  r.table = a;
+  r.keys = sh->groups.pages[lo] * kBlkPerPage;
   const int in = unit - sh->units[lo], it = in / r.keys;
   r.g = it / tiles;
   r.item = sh->items[lo] + it;
@@ -161,47 +164,35 @@ __global__ void __launch_bounds__(kPxBound, 1)
     prefetch_tmap(&tm_k);
     prefetch_tmap(&tm_v);
   }
-  // The plan: key tiles and items before each group's. (Groups that are not usable are dropped: every sequence is then
-  // decoded by itself, by the other kernel, which reports it.)
-  const bool usable = groups_ok(p.groups, p.B, p.pm.max_pages);
-  const int n_groups = usable ? p.groups.n : 0;
+  // The plan: key tiles and items before each group's, a group a thread. (Groups that are not usable are dropped: every
+  // sequence is then decoded by itself, by the other kernel, which reports it.)
+  const bool fine = load_groups(p.groups, p.B, p.pm.max_pages, &sh->groups, tid);
+  if (warp == 1) {
+    tmem_alloc(&sh->tmem, 512);
+    tmem_relinquish();
+  }
+  const int n_groups = __syncthreads_and(fine) ? p.groups.n : 0;
+  static_assert(kGroupsMax <= kPxThreads, "a group a thread");
   {
-    const int per = (n_groups + kPxThreads - 1) / kPxThreads;
-    const int i0 = min(tid * per, n_groups), i1 = min(i0 + per, n_groups);
-    auto of = [&](int i, int& items) {
-      const int pages = group_pages(p.groups, i);
-      const int tiles = pages == 0 ? 0 : (p.groups.start[i + 1] - p.groups.start[i] + kPxSeqs - 1) / kPxSeqs;
-      items = tiles * kKVHeads;
-      return items * pages * kBlkPerPage;
-    };
-    int units = 0, items = 0;
-    for (int i = i0; i < i1; ++i) {
-      int n;
-      units += of(i, n);
-      items += n;
-    }
+    const int pages = tid < n_groups ? sh->groups.pages[tid] : 0;
+    const int tiles = pages ? (sh->groups.start[tid + 1] - sh->groups.start[tid] + kPxSeqs - 1) / kPxSeqs : 0;
+    const int items = tiles * kKVHeads, units = items * pages * kBlkPerPage;
     int iu = units, ii = items;
 #pragma unroll
     for (int d = 1; d < 32; d *= 2) {
       const int a = __shfl_up_sync(0xffffffffu, iu, d), c = __shfl_up_sync(0xffffffffu, ii, d);
       if (lane >= d) iu += a, ii += c;
     }
-    if (lane == 31) sh->warp_units[warp] = iu, sh->warp_items[warp] = ii;
-    __syncthreads();
-    int u = iu - units, m = ii - items;
-    for (int w = 0; w < warp; ++w) u += sh->warp_units[w], m += sh->warp_items[w];
-    for (int i = i0; i < i1; ++i) {
-      int n;
-      sh->units[i] = u;
-      sh->items[i] = m;
-      u += of(i, n);
-      m += n;
+    if (n_groups > 32) {
+      if (lane == 31) sh->warp_units[warp] = iu, sh->warp_items[warp] = ii;
+      __syncthreads();
+      for (int w = 0; w < warp && w < kGroupsMax / 32; ++w) iu += sh->warp_units[w], ii += sh->warp_items[w];
     }
-    if (i1 == n_groups && i0 < i1) sh->units[n_groups] = u;
-  }
-  if (warp == 1) {
-    tmem_alloc(&sh->tmem, 512);
-    tmem_relinquish();
+    if (tid < n_groups) {
+      sh->units[tid] = iu - units;
+      sh->items[tid] = ii - items;
+      if (tid == n_groups - 1) sh->units[n_groups] = iu;
+    }
   }
   tc_fence_before();
   __syncthreads();
@@ -214,14 +205,6 @@ __global__ void __launch_bounds__(kPxBound, 1)
   if (n_tiles > 0) {
     if (warp == 0) {
       // ------------------------------------------------------------ TMA producer
-      for (int u = u0; u < u1;) {  // the items' parts: one of each CTA from the first on that takes some of it
-        const PxRun run = px_run(p, sh, u, u1);
-        if (run.k0 == 0 && lane < run.seqs)
-          p.parts.pair[(size_t)(run.seq0 + lane) * kKVHeads + run.g] =
-              make_int4(int(blockIdx.x) + run.item, (run.base + run.keys - 1) / share - int(blockIdx.x) + 1,
-                        lane * kGroup, int(uint32_t(run.keys / kBlkPerPage) << 16 | uint32_t(run.seq0)));
-        u += run.n;
-      }
       // The tiles' places are looked up 32 at a time, one a lane, so that a tile costs this warp few instructions: it shares
       // its scheduler with softmax warps. (With 100 or 150 to a tile, as a lookup in the loop or two ring positions polled in
       // turn take, the loads bound the kernel at 800 clocks each: 256 sequences behind 16384 rows 145 us.)
@@ -233,7 +216,7 @@ __global__ void __launch_bounds__(kPxBound, 1)
         if (base + lane < n_tiles) {
           const PxRun run = px_run(p, sh, u0 + base + lane, u1);
           my_g = run.g;
-          my_row = max(0, blk_page(p.pm, run.seq0, run.k0, p.status)) * GROK_PAGE_TOKENS + run.k0 % kBlkPerPage * kBlk;
+          my_row = max(0, blk_page(p.pm, run.table, run.k0, p.status)) * GROK_PAGE_TOKENS + run.k0 % kBlkPerPage * kBlk;
         }
         const int cnt = min(32, n_tiles - base);
         for (int j = 0; j < cnt; ++j) {
@@ -255,6 +238,14 @@ __global__ void __launch_bounds__(kPxBound, 1)
           if (!ok) break;
           if (++st == kPxStages) st = 0, turn ^= 1;
         }
+      }
+      for (int u = u0; u < u1;) {  // the items' parts: one of each CTA from the first on that takes some of it
+        const PxRun run = px_run(p, sh, u, u1);
+        if (run.k0 == 0 && lane < run.seqs)
+          p.parts.pair[(size_t)(run.seq0 + lane) * kKVHeads + run.g] =
+              make_int4(int(blockIdx.x) + run.item, (run.base + run.keys - 1) / share - int(blockIdx.x) + 1,
+                        lane * kGroup, int(uint32_t(run.keys / kBlkPerPage) << 16 | uint32_t(run.table)));
+        u += run.n;
       }
       // Copies in flight (only after an abort) land before the CTA exits.
       if (lane == 0) {
