@@ -100,9 +100,15 @@ __global__ void __launch_bounds__(kBdThreads) kv_bounds_kernel(const uint4* __re
 
 // ----------------------------------------------------------------------------
 // Scores of a sequence's blocks for one KV head, and the choice. A CTA per (KV head,
-// sequence); four threads share a block: two take the upper bounds with the query's
-// positive codes, two the lower bounds with the negative ones.
+// sequence). The products run on tensor-core instructions: 8-bit codes are exact in
+// fp16, and so are sums of whole numbers below 2^24 in fp32:
+//   [16 blocks x 8 heads] += codes [16 x 16] . query codes [16 x 8]  (6 of 8 columns used)
+// over 256 codes of a block, the upper bounds against the query's positive codes and
+// the lower ones against its negative. A lane loads 16-byte words of two blocks; the order
+// of the contracted index is chosen to fit them. A warp has the next 16 blocks' codes
+// under way while it multiplies.
 constexpr int kSlThreads = 256;
+constexpr int kSlWarps = kSlThreads / 32;
 constexpr int kSlPer = kBlkMax / kSlThreads;  // blocks per thread in the choice
 
 struct SlParams {
@@ -117,134 +123,223 @@ struct SlParams {
   int32_t* status;
 };
 
-__global__ void __launch_bounds__(kSlThreads) select_kernel(const SlParams p) {
-  __shared__ uint32_t sq[kGroup][2][kD / 4];  // [head][positive, negative][4 codes]
-  __shared__ float sf[kGroup];
+// D[16 x 8] += A[16 x 16] B[16 x 8], fp16 operands, fp32 sums.
+__device__ __forceinline__ void mma_f16_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                              uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Four codes, first in the low byte, as two pairs of fp16: a byte c with its sign bit flipped is c + 128, behind the byte
+// 0x64 the fp16 number 1024 + (c + 128), from which 1152 is taken.
+__device__ __forceinline__ void codes_to_half(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  const uint32_t u = w ^ 0x80808080u;
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(lo) : "r"(__byte_perm(u, 0x64646464u, 0x4140)), "r"(0x64806480u));
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(hi) : "r"(__byte_perm(u, 0x64646464u, 0x4342)), "r"(0x64806480u));
+}
+
+__device__ __forceinline__ uint32_t word_of(const uint4& x, int w) { return w == 0 ? x.x : w == 1 ? x.y : w == 2 ? x.z : x.w; }
+
+__global__ void __launch_bounds__(kSlThreads, 2) select_kernel(const SlParams p) {
+  __shared__ __align__(16) uint32_t sq[8][kD + 4];  // [head][2 codes in fp16: positive, negative] (rows apart in the banks)
+  __shared__ float sf[8];
+  __shared__ int pages[GROK_MAX_POSITION / GROK_PAGE_TOKENS];
   __shared__ float scores[kBlkMax];
-  __shared__ int sums[2][kSlThreads / 32];
+  __shared__ uint2 sums[kSlWarps];
+  __shared__ uint32_t bins[256];
+  __shared__ uint2 found;
   const int g = blockIdx.x, b = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int cap = p.pm.max_pages * GROK_PAGE_TOKENS, n = blk_count(p.kv_len[b], cap);
-  if (n == 0) {
-    if (g == 0 && tid == 0) report(p.status, GROK_DEV_BAD_KV_LEN);
-    return;
-  }
+  const int cap = p.pm.max_pages * GROK_PAGE_TOKENS;
+  const int len = p.kv_len[b];
+  // (the whole row of the table: entries behind the sequence's last are not looked at)
+  for (int i = tid; i < p.pm.max_pages; i += kSlThreads) pages[i] = p.pm.table[(size_t)b * p.pm.max_pages + i];
   if (warp < kGroup) {  // head `warp` in 8 bits, four features a lane
     const uint2 x = reinterpret_cast<const uint2*>(p.q)[((size_t)b * kQHeads + g * kGroup + warp) * (kD / 4) + lane];
     const uint32_t a = max(max(x.x & 0x7FFFu, (x.x >> 16) & 0x7FFFu), max(x.y & 0x7FFFu, (x.y >> 16) & 0x7FFFu));
     const int f = scale_exponent(__reduce_max_sync(0xffffffffu, a));
     const float inv = pow2(-f), v[4] = {bf16lo_to_f32(x.x), bf16hi_to_f32(x.x), bf16lo_to_f32(x.y), bf16hi_to_f32(x.y)};
-    uint32_t pos = 0, neg = 0;
+    float c[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int c = int(clamp127(rintf(no_nan(v[i]) * inv)));
-      pos |= uint32_t(max(c, 0) & 0xFF) << (8 * i);
-      neg |= uint32_t(min(c, 0) & 0xFF) << (8 * i);
+    for (int i = 0; i < 4; ++i) c[i] = clamp127(rintf(no_nan(v[i]) * inv));
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      sq[warp][2 * lane + i] = pack_f16x2(fmaxf(c[2 * i], 0.f), fmaxf(c[2 * i + 1], 0.f));
+      sq[warp][kD / 2 + 2 * lane + i] = pack_f16x2(fminf(c[2 * i], 0.f), fminf(c[2 * i + 1], 0.f));
     }
-    sq[warp][0][lane] = pos;
-    sq[warp][1][lane] = neg;
     if (lane == 0) sf[warp] = pow2(f);
+  } else {  // columns 6 and 7 are not used
+    if (lane == 0) sf[warp] = 0.f;
+    *reinterpret_cast<uint4*>(&sq[warp][4 * lane]) = make_uint4(0u, 0u, 0u, 0u);
+  }
+  const int n = blk_count(len, cap);
+  if (n == 0) {
+    if (g == 0 && tid == 0) report(p.status, GROK_DEV_BAD_KV_LEN);
+    return;
   }
   __syncthreads();
-  const int part = tid & 3;
-  uint32_t qw[kGroup][16];
+  {
+    const int row = lane >> 2, t = lane & 3;
+    uint32_t qb[16][2];  // k-step: the four codes of word s % 4 of 64-byte group s / 4
 #pragma unroll
-  for (int h = 0; h < kGroup; ++h)
-#pragma unroll
-    for (int w = 0; w < 16; ++w) qw[h][w] = sq[h][part >> 1][(part & 1) * 16 + w];
-  float* out = p.score + ((size_t)b * kKVHeads + g) * (p.pm.max_pages * kBlkPerPage);
-  for (int i0 = 0; i0 < n; i0 += kSlThreads / 4) {
-    const int i = i0 + (tid >> 2), blk = min(i, n - 1);
-    const int pg = max(0, blk_page(p.pm, b, blk, p.status));  // (a bad page: reported, page 0's bounds)
-    const size_t row = ((size_t)pg * kBlkPerPage + blk % kBlkPerPage) * kKVHeads + g;
-    const uint4* src = p.codes + row * (2 * kD / 16) + part * 4;
-    uint4 x[4];
-#pragma unroll
-    for (int c = 0; c < 4; ++c) x[c] = __ldg(src + c);
-    const float sc = __ldg(p.scale + row);
-    int acc[kGroup] = {};
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      const uint32_t w[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-#pragma unroll
-        for (int h = 0; h < kGroup; ++h) acc[h] = __dp4a(int(w[k]), int(qw[h][c * 4 + k]), acc[h]);
+    for (int s = 0; s < 16; ++s) {
+      const uint2 w = *reinterpret_cast<const uint2*>(&sq[row][(s >> 2) * 32 + t * 8 + (s & 3) * 2]);
+      qb[s][0] = w.x;
+      qb[s][1] = w.y;
     }
-    float best = -INFINITY;
+    const float f0 = sf[2 * t], f1 = sf[2 * t + 1];
+    uint4 x[2][4];
+    float sc[2];
+    // Codes and scales of blocks i0 + row and i0 + 8 + row.
+    auto load = [&](int i0) {
 #pragma unroll
-    for (int h = 0; h < kGroup; ++h) {
-      acc[h] += __shfl_xor_sync(0xffffffffu, acc[h], 1);
-      acc[h] += __shfl_xor_sync(0xffffffffu, acc[h], 2);
-      best = fmaxf(best, float(acc[h]) * sf[h]);
+      for (int h = 0; h < 2; ++h) {
+        const int blk = min(i0 + 8 * h + row, n - 1);
+        int pg = pages[blk / kBlkPerPage];
+        if (pg < 0 || pg >= p.pm.n_pages) {  // (page 0's bounds in its place)
+          report(p.status, GROK_DEV_BAD_PAGE);
+          pg = 0;
+        }
+        const size_t at = ((size_t)pg * kBlkPerPage + blk % kBlkPerPage) * kKVHeads + g;
+        const uint4* src = p.codes + at * (2 * kD / 16) + t;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) x[h][c] = __ldg(src + 4 * c);
+        sc[h] = __ldg(p.scale + at);
+      }
+    };
+    float* out = p.score + ((size_t)b * kKVHeads + g) * (p.pm.max_pages * kBlkPerPage);
+    int i0 = warp * 16;
+    if (i0 < n) load(i0);
+    while (i0 < n) {
+      uint4 y[2][4];
+      float ysc[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        ysc[h] = sc[h];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) y[h][c] = x[h][c];
+      }
+      const int next = i0 + kSlWarps * 16;
+      if (next < n) load(next);
+      float d[2][4] = {};
+#pragma unroll
+      for (int s = 0; s < 16; ++s) {
+        uint32_t a[4];
+        codes_to_half(word_of(y[0][s >> 2], s & 3), a[0], a[2]);
+        codes_to_half(word_of(y[1][s >> 2], s & 3), a[1], a[3]);
+        mma_f16_16816(d[s & 1], a[0], a[1], a[2], a[3], qb[s][0], qb[s][1]);
+      }
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        float best = t < kGroup / 2 ? fmaxf((d[0][2 * h] + d[1][2 * h]) * f0, (d[0][2 * h + 1] + d[1][2 * h + 1]) * f1)
+                                    : -INFINITY;
+        best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, 1));
+        best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, 2));
+        const int i = i0 + 8 * h + row;
+        if (t == 0 && i < n) out[i] = scores[i] = best * ysc[h];
+      }
+      i0 = next;
     }
-    if (part == 0 && i < n) out[i] = scores[i] = best * sc;
   }
   __syncthreads();
 
-  // The choice. Keys order as the scores do; blocks that are always chosen come first.
+  // The choice. The first `sink` and the last `recent` blocks are in; the others' keys order as their scores do, and of
+  // them the `want` largest are in: all above `edge`, and of those at it the first ones.
   int32_t* sel = p.sel + ((size_t)b * kKVHeads + g) * p.budget;
-  const int take = min(n, p.budget);
-  uint32_t key[kSlPer];
+  const int take = min(n, p.budget), tail = max(p.sink, n - p.recent);  // (blocks from `tail` on are in)
+  const int want = take - min(n, p.sink) - max(0, n - tail);
+  uint32_t key[kSlPer], top = 0u, low = 0xFFFFFFFFu;
 #pragma unroll
   for (int e = 0; e < kSlPer; ++e) {
     const int i = tid * kSlPer + e;
-    key[e] = 0u;
-    if (i < n) {
+    key[e] = 0u;  // (no score has this key)
+    if (i >= p.sink && i < tail && i < n) {
       const uint32_t x = __float_as_uint(scores[i] + 0.f);
-      key[e] = i < p.sink || i >= n - p.recent ? 0xFFFFFFFFu : x ^ (x >> 31 ? 0xFFFFFFFFu : 0x80000000u);
+      key[e] = x ^ (x >> 31 ? 0xFFFFFFFFu : 0x80000000u);
+      top = max(top, key[e]);
+      low = min(low, key[e]);
     }
   }
-  // The largest `edge` with at least `take` keys at or above it.
-  uint32_t edge = 0;
-  if (n > take) {
-    for (int bit = 31; bit >= 0; --bit) {
-      const uint32_t trial = edge | (1u << bit);
-      int c = 0;
+  uint32_t edge = 0u;
+  if (want == 0) {
+    edge = 0xFFFFFFFFu;
+  } else if (n > take) {
+    // The key of rank `want`, eight bits at a time from the first that any two keys differ in: keys that agree with it so
+    // far are counted by their next eight bits.
+    top = __reduce_max_sync(0xffffffffu, top);
+    low = __reduce_min_sync(0xffffffffu, low);
+    if (lane == 0) sums[warp] = make_uint2(top, low);
+    __syncthreads();
 #pragma unroll
-      for (int e = 0; e < kSlPer; ++e) c += key[e] >= trial;
-      c = __reduce_add_sync(0xffffffffu, c);
-      if (lane == 0) sums[bit & 1][warp] = c;
+    for (int w = 0; w < kSlWarps; ++w) {
+      top = max(top, sums[w].x);
+      low = min(low, sums[w].y);
+    }
+    const int differ = 32 - __clz(top ^ low);
+    int rank = want;
+    edge = differ == 32 ? 0u : top >> differ << differ;
+    for (int bits = differ; bits > 0;) {
+      const int shift = max(0, bits - 8);
+      static_assert(kSlThreads == 256, "a bin a thread");
+      bins[tid] = 0u;
       __syncthreads();
-      int total = 0;
 #pragma unroll
-      for (int w = 0; w < kSlThreads / 32; ++w) total += sums[bit & 1][w];
-      if (total >= take) edge = trial;
-      if (total == take) break;
+      for (int e = 0; e < kSlPer; ++e)
+        if (key[e] && (bits == 32 || (key[e] ^ edge) >> bits == 0)) atomicAdd(&bins[key[e] >> shift & 255u & ((1u << (bits - shift)) - 1u)], 1u);
+      __syncthreads();
+      const uint32_t bin = 255u - tid, mine = bins[bin];  // (the largest first)
+      uint32_t upto = mine;
+#pragma unroll
+      for (int d = 1; d < 32; d *= 2) {
+        const uint32_t up = __shfl_up_sync(0xffffffffu, upto, d);
+        if (lane >= d) upto += up;
+      }
+      if (lane == 31) sums[warp].x = upto;
+      __syncthreads();
+      for (int w = 0; w < warp; ++w) upto += sums[w].x;
+      if (upto >= uint32_t(rank) && upto - mine < uint32_t(rank)) found = make_uint2(bin, (upto - mine) << 16 | mine);
+      __syncthreads();
+      edge |= found.x << shift;
+      rank -= int(found.y >> 16);
+      bits = shift;
+      if (rank == int(found.y & 0xFFFFu)) break;  // all of them are in: those at or above `edge` as it stands
     }
     __syncthreads();
   }
-  // Blocks above the edge, and of those at it the first ones (counts packed: above in the low half).
-  uint32_t mine = 0;
+  // In, and in order: the blocks that are always in count as above the edge (counts packed: above in the low half).
+  uint32_t kind[kSlPer], mine = 0;
 #pragma unroll
-  for (int e = 0; e < kSlPer; ++e)
-    if (tid * kSlPer + e < n) mine += key[e] > edge ? 1u : key[e] == edge ? 0x10000u : 0u;
+  for (int e = 0; e < kSlPer; ++e) {
+    const int i = tid * kSlPer + e;
+    kind[e] = i >= n ? 0u : i < p.sink || i >= tail || key[e] > edge ? 1u : key[e] == edge ? 0x10000u : 0u;
+    mine += kind[e];
+  }
   uint32_t before = mine;
 #pragma unroll
   for (int d = 1; d < 32; d *= 2) {
     const uint32_t up = __shfl_up_sync(0xffffffffu, before, d);
     if (lane >= d) before += up;
   }
-  if (lane == 31) sums[0][warp] = int(before);
+  if (lane == 31) sums[warp].x = before;
   __syncthreads();
   uint32_t all = 0, base = 0;
 #pragma unroll
-  for (int w = 0; w < kSlThreads / 32; ++w) {
-    if (w < warp) base += uint32_t(sums[0][w]);
-    all += uint32_t(sums[0][w]);
+  for (int w = 0; w < kSlWarps; ++w) {
+    if (w < warp) base += sums[w].x;
+    all += sums[w].x;
   }
   before += base - mine;
   const int ties = take - int(all & 0xFFFFu);  // of those at the edge
   int above = int(before & 0xFFFFu), equal = int(before >> 16);
 #pragma unroll
   for (int e = 0; e < kSlPer; ++e) {
-    const int i = tid * kSlPer + e;
-    if (i >= n) break;
     const int at = above + min(equal, ties);
-    if (key[e] > edge) {
-      sel[at] = i;
+    if (kind[e] == 1u) {
+      sel[at] = tid * kSlPer + e;
       ++above;
-    } else if (key[e] == edge) {
-      if (equal < ties) sel[at] = i;
+    } else if (kind[e]) {
+      if (equal < ties) sel[at] = tid * kSlPer + e;
       ++equal;
     }
   }
