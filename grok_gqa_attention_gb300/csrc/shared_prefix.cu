@@ -27,8 +27,12 @@ constexpr int kPxBound = 768;
 constexpr int kPxBox = kBlk * 128;          // [64 rows][64 bf16]: one half of the features of a key tile
 constexpr int kPxTile = 2 * kPxBox;
 constexpr int kPxStages = 4;                // of the K ring and of the V ring
+constexpr int kPxLead = 2;                  // K tiles loaded ahead of the V tile of the same keys
 // TMEM columns: O, Q, and the S (then P) of key tiles in turn
 constexpr int kPxBufs = 5;
+// (K of tile t + kPxLead waits for S of kPxStages tiles before it, and that for P V of kPxBufs tiles before that, whose V
+// has to be loaded by then)
+static_assert(kPxLead < kPxStages + kPxBufs, "the producer's order");
 constexpr uint32_t kPxO = 0, kPxQ = kD, kPxS = kPxQ + kD / 2;
 static_assert(kPxS + kPxBufs * kBlk <= 512, "TMEM columns");
 
@@ -40,6 +44,7 @@ struct PxShared {
   int units[kGroupsMax + 1];  // key tiles before each group's
   int items[kGroupsMax + 1];  // (KV head, query tile) pairs before each group's
   int warp_units[kPxThreads / 32], warp_items[kPxThreads / 32];
+  int2 place[64];  // of the key tiles in turn: row of the pools, KV head
   uint32_t tmem;
   int abort;
 };
@@ -205,39 +210,45 @@ __global__ void __launch_bounds__(kPxBound, 1)
   if (n_tiles > 0) {
     if (warp == 0) {
       // ------------------------------------------------------------ TMA producer
-      // The tiles' places are looked up 32 at a time, one a lane, so that a tile costs this warp few instructions: it shares
-      // its scheduler with softmax warps. (With 100 or 150 to a tile, as a lookup in the loop or two ring positions polled in
-      // turn take, the loads bound the kernel at 800 clocks each: 256 sequences behind 16384 rows 145 us.)
-      int st = 0, loads = 0;
-      uint32_t turn = 1;
+      // K runs kPxLead tiles ahead of V, as S does of P V. The tiles' places are looked up 32 at a time, one a lane, so that a
+      // tile costs this warp few instructions: it shares its scheduler with softmax warps. (With 100 or 150 to a tile, as a
+      // lookup in the loop takes, the loads bound the kernel at 800 clocks each: 256 sequences behind 16384 rows 145 us.)
+      int k_loads = 0, v_loads = 0, k_st = 0, v_st = 0;
+      uint32_t k_turn = 1, v_turn = 1;
       bool ok = true;
-      for (int base = 0; base < n_tiles && ok; base += 32) {
-        int my_row = 0, my_g = 0;
-        if (base + lane < n_tiles) {
-          const PxRun run = px_run(p, sh, u0 + base + lane, u1);
-          my_g = run.g;
-          my_row = max(0, blk_page(p.pm, run.table, run.k0, p.status)) * GROK_PAGE_TOKENS + run.k0 % kBlkPerPage * kBlk;
+      for (int t = 0; t < n_tiles + kPxLead && ok; ++t) {
+        if (t % 32 == 0) {
+          if (t + lane < n_tiles) {
+            const PxRun run = px_run(p, sh, u0 + t + lane, u1);
+            sh->place[(t + lane) % 64] =
+                make_int2(max(0, blk_page(p.pm, run.table, run.k0, p.status)) * GROK_PAGE_TOKENS + run.k0 % kBlkPerPage * kBlk,
+                          run.g);
+          }
+          __syncwarp();
         }
-        const int cnt = min(32, n_tiles - base);
-        for (int j = 0; j < cnt; ++j) {
-          const int row = __shfl_sync(0xffffffffu, my_row, j), g = __shfl_sync(0xffffffffu, my_g, j);
-          if (lane == 0) {
-            ok = mbar_wait(&sh->k_empty[st], turn, abort, p.status);
+        if (lane == 0) {
+          if (t < n_tiles) {
+            ok = mbar_wait(&sh->k_empty[k_st], k_turn, abort, p.status);
             if (ok) {
-              mbar_arrive_expect_tx(&sh->k_full[st], kPxTile);
-              tma_load_4d(sK + st * kPxTile, &tm_k, &sh->k_full[st], 0, row, 0, g);
-              ok = mbar_wait(&sh->v_empty[st], turn, abort, p.status);
-              if (ok) {
-                mbar_arrive_expect_tx(&sh->v_full[st], kPxTile);
-                tma_load_4d(sV + st * kPxTile, &tm_v, &sh->v_full[st], 0, row, 0, g);
-              }
-              loads += ok ? 2 : 1;
+              const int2 at = sh->place[t % 64];
+              mbar_arrive_expect_tx(&sh->k_full[k_st], kPxTile);
+              tma_load_4d(sK + k_st * kPxTile, &tm_k, &sh->k_full[k_st], 0, at.x, 0, at.y);
+              ++k_loads;
+              if (++k_st == kPxStages) k_st = 0, k_turn ^= 1;
             }
           }
-          ok = __shfl_sync(0xffffffffu, int(ok), 0);
-          if (!ok) break;
-          if (++st == kPxStages) st = 0, turn ^= 1;
+          if (ok && t >= kPxLead) {
+            ok = mbar_wait(&sh->v_empty[v_st], v_turn, abort, p.status);
+            if (ok) {
+              const int2 at = sh->place[(t - kPxLead) % 64];
+              mbar_arrive_expect_tx(&sh->v_full[v_st], kPxTile);
+              tma_load_4d(sV + v_st * kPxTile, &tm_v, &sh->v_full[v_st], 0, at.x, 0, at.y);
+              ++v_loads;
+              if (++v_st == kPxStages) v_st = 0, v_turn ^= 1;
+            }
+          }
         }
+        ok = __shfl_sync(0xffffffffu, int(ok), 0);
       }
       for (int u = u0; u < u1;) {  // the items' parts: one of each CTA from the first on that takes some of it
         const PxRun run = px_run(p, sh, u, u1);
@@ -250,7 +261,6 @@ __global__ void __launch_bounds__(kPxBound, 1)
       // Copies in flight (only after an abort) land before the CTA exits.
       if (lane == 0) {
         volatile int never = 0;
-        const int k_loads = (loads + 1) / 2, v_loads = loads / 2;
         for (int i = max(0, k_loads - kPxStages); i < k_loads; ++i)
           mbar_wait(&sh->k_full[i % kPxStages], (i / kPxStages) & 1, &never, p.status);
         for (int i = max(0, v_loads - kPxStages); i < v_loads; ++i)
