@@ -36,8 +36,8 @@ constexpr int kBkFew = 8;                    // blocks per CTA up to which half 
 
 template <int kRing>
 struct BkShared {
-  float4 sum_o[kBkWarps - 1][kBkPartO];  // partial sums of warps 1 to 3 for warp 0
-  float2 sum_l[kBkWarps - 1][4];
+  float4 sum_o[kBkWarps][6 * 32];  // the warps' sums but those of the quarter of the features that each adds itself
+  float2 sum_l[kBkWarps][4];
   uint64_t full[kRing], empty[kRing], sum_full, sum_empty;
   int2 token[kRing];      // pair and visible keys of the block whose K is in a place of the ring; pair -1: the end
   int cum[kBkPlan + 1];   // blocks per KV head of the sequences before each entry's
@@ -102,8 +102,8 @@ __global__ void __launch_bounds__(kList ? kBkThreads : 576, kList ? kBkCtas : 1)
       mbar_init(&sh->full[s], 1);
       mbar_init(&sh->empty[s], kBkWarps);
     }
-    mbar_init(&sh->sum_full, kBkWarps - 1);
-    mbar_init(&sh->sum_empty, 1);
+    mbar_init(&sh->sum_full, kBkWarps);
+    mbar_init(&sh->sum_empty, kBkWarps);
     sh->abort = 0;
     fence_barrier_init();
     prefetch_tmap(&tm_k);
@@ -277,50 +277,53 @@ __global__ void __launch_bounds__(kList ? kBkThreads : 576, kList ? kBkCtas : 1)
         if (!__all_sync(0xffffffffu, mbar_wait(&sh->full[st], turn, abort, p.status))) break;
         const int2 tok = sh->token[st];
         if (tok.x != cur) {
-          if (cur >= 0) {  // the sums of this CTA's share of the pair: warp 0 adds the other warps' and writes them
+          if (cur >= 0) {  // the sums of this CTA's share of the pair: each warp adds and writes a quarter of the features
 #pragma unroll
             for (int d = 4; d < 32; d *= 2) {
               l0 += __shfl_xor_sync(0xffffffffu, l0, d);
               l1 += __shfl_xor_sync(0xffffffffu, l1, d);
             }
-            const bool mine = warp == 0;
-            if (!__all_sync(0xffffffffu, mbar_wait(mine ? &sh->sum_full : &sh->sum_empty, (sums & 1) ^ (mine ? 0 : 1),
-                                                   abort, p.status)))
-              break;
-            ++sums;
-            if (!mine) {
+            const uint32_t odd = sums++ & 1;
+            if (!__all_sync(0xffffffffu, mbar_wait(&sh->sum_empty, odd ^ 1, abort, p.status))) break;
+            float4 own[2];
 #pragma unroll
-              for (int mt = 0; mt < 8; ++mt)
-                sh->sum_o[warp - 1][mt * 32 + lane] = make_float4(o[mt][0], o[mt][1], o[mt][2], o[mt][3]);
-              if (row == 0) sh->sum_l[warp - 1][t] = make_float2(l0, l1);
-              __syncwarp();
-              if (lane == 0) mbar_arrive(&sh->sum_full);
-            } else {
-              const size_t slot = (size_t)cta + cur;
-#pragma unroll
-              for (int mt = 0; mt < 8; ++mt) {
-                float4 v = make_float4(o[mt][0], o[mt][1], o[mt][2], o[mt][3]);
-#pragma unroll
-                for (int w = 0; w < kBkWarps - 1; ++w) {
-                  const float4 x = sh->sum_o[w][mt * 32 + lane];
-                  v.x += x.x;
-                  v.y += x.y;
-                  v.z += x.z;
-                  v.w += x.w;
-                }
-                p.parts.o[slot * kBkPartO + mt * 32 + lane] = v;
-              }
-              if (row == 0) {
-#pragma unroll
-                for (int w = 0; w < kBkWarps - 1; ++w) {
-                  l0 += sh->sum_l[w][t].x;
-                  l1 += sh->sum_l[w][t].y;
-                }
-                *reinterpret_cast<float2*>(p.parts.l + slot * 8 + 2 * t) = make_float2(l0, l1);
-              }
-              __syncwarp();
-              if (lane == 0) mbar_arrive(&sh->sum_empty);
+            for (int mt = 0; mt < 8; ++mt) {
+              const float4 x = make_float4(o[mt][0], o[mt][1], o[mt][2], o[mt][3]);
+              if (mt / 2 == warp)
+                own[mt & 1] = x;
+              else
+                sh->sum_o[warp][(mt - (mt / 2 > warp ? 2 : 0)) * 32 + lane] = x;
             }
+            if (row == 0) sh->sum_l[warp][t] = make_float2(l0, l1);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh->sum_full);
+            if (!__all_sync(0xffffffffu, mbar_wait(&sh->sum_full, odd, abort, p.status))) break;
+            const size_t slot = (size_t)cta + cur;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              float4 v = own[i];
+#pragma unroll
+              for (int j = 1; j < kBkWarps; ++j) {
+                const int w = (warp + j) % kBkWarps;
+                const float4 x = sh->sum_o[w][(2 * warp + i - (warp > w ? 2 : 0)) * 32 + lane];
+                v.x += x.x;
+                v.y += x.y;
+                v.z += x.z;
+                v.w += x.w;
+              }
+              p.parts.o[slot * kBkPartO + (2 * warp + i) * 32 + lane] = v;
+            }
+            if (warp == 0 && lane < 4) {
+              float2 v = sh->sum_l[0][lane];
+#pragma unroll
+              for (int w = 1; w < kBkWarps; ++w) {
+                v.x += sh->sum_l[w][lane].x;
+                v.y += sh->sum_l[w][lane].y;
+              }
+              *reinterpret_cast<float2*>(p.parts.l + slot * 8 + 2 * lane) = v;
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh->sum_empty);
           }
           cur = tok.x;
           if (cur < 0) break;
@@ -395,8 +398,8 @@ __global__ void __launch_bounds__(kList ? kBkThreads : 576, kList ? kBkCtas : 1)
     }
   }
   // Started as the dependent of the prefix kernel, this one ends behind it, so that the kernel that waits for this one
-  // finds both results (a no-op otherwise).
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  // finds both results. (The last CTA alone waits: the others' places beside the prefix kernel are for the CTAs that follow.)
+  if (!kList && blockIdx.x == gridDim.x - 1) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 // ----------------------------------------------------------------------------
