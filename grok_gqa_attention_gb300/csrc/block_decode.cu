@@ -109,7 +109,6 @@ __global__ void __launch_bounds__(kList ? kBkThreads : 576, kList ? kBkCtas : 1)
     prefetch_tmap(&tm_k);
     prefetch_tmap(&tm_v);
   }
-
   // The plan: blocks per KV head before each sequence (or each `step` sequences, where there are many).
   const int step = (p.B + kBkPlan - 1) / kBkPlan, entries = (p.B + step - 1) / step;
   constexpr int kPer = (kBkPlan + kBkThreads - 1) / kBkThreads;  // contiguous entries per thread
@@ -407,7 +406,7 @@ __global__ void __launch_bounds__(kList ? kBkThreads : 576, kList ? kBkCtas : 1)
 // kTeams-th part: four teams where there are few CTAs and many parts each, one where there are many CTAs.
 template <bool kPrefix, int kTeams>
 __global__ void __launch_bounds__(kTeams* kBkPartO)
-    block_join_kernel(const BlockParts parts, const PrefixParts prefix, const PageMap pm, uint2* __restrict__ out,
+    block_join_kernel(const BlockParts parts, const PrefixParts prefix, const PageMap pm, uint2* out,
                       int32_t* status) {
   __shared__ float4 so[kTeams][kBkPartO];
   __shared__ float sl[kTeams][8];
@@ -555,10 +554,7 @@ grok_status encode_pool(CUtensorMap* map, const grok_bf16* pool, int n_pages) {
 
 template <bool kList>
 static grok_status bk_launch(const BlockArgs& a, const BkParams& p, int sms) {
-  CUtensorMap tk, tv;
   grok_status st;
-  if ((st = encode_pool(&tk, a.k_pool, a.pm.n_pages)) != GROK_OK) return st;
-  if ((st = encode_pool(&tv, a.v_pool, a.pm.n_pages)) != GROK_OK) return st;
   static bool attr_set[kMaxDevices] = {};  // per device; idempotent: every thread would set the same value
   int dev = 0;
   if ((st = device_index(&dev)) != GROK_OK) return st;
@@ -571,17 +567,7 @@ static grok_status bk_launch(const BlockArgs& a, const BkParams& p, int sms) {
     if (e != cudaSuccess) return fail(cuda_status(e), "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
     attr_set[dev] = true;
   }
-  cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
-  cfg.gridDim = dim3(kBkCtas * sms);
-  cfg.blockDim = dim3(kBkThreads);
-  cfg.dynamicSmemBytes = kBkSmem<kList>;
-  cfg.stream = a.stream;
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = kList ? 0 : 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, block_decode_kernel<kList>, tk, tv, p);
+  e = launch(!kList, block_decode_kernel<kList>, dim3(kBkCtas * sms), kBkThreads, kBkSmem<kList>, a.stream, a.tm_k, a.tm_v, p);
   if (e != cudaSuccess) return fail(cuda_status(e), "block decode launch: %s", cudaGetErrorString(e));
   return check_launch("block decode");
 }
@@ -600,20 +586,11 @@ grok_status block_decode_run(const BlockArgs& a, char* ws, const PrefixParts* pr
   p.status = a.status;
   grok_status st = a.sel ? bk_launch<true>(a, p, sms) : bk_launch<false>(a, p, sms);
   if (st != GROK_OK) return st;
-  cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
   const int teams = a.B * kKVHeads <= 2 * sms ? 4 : 1;
-  cfg.gridDim = dim3(kKVHeads, a.B);
-  cfg.blockDim = dim3(teams * kBkPartO);
-  cfg.stream = a.stream;
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
   auto kernel = prefix ? (teams == 4 ? block_join_kernel<true, 4> : block_join_kernel<true, 1>)
                        : (teams == 4 ? block_join_kernel<false, 4> : block_join_kernel<false, 1>);
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, p.parts, prefix ? *prefix : PrefixParts{}, a.pm,
-                                           reinterpret_cast<uint2*>(a.out), a.status);
+  const cudaError_t e = launch(true, kernel, dim3(kKVHeads, a.B), teams * kBkPartO, 0, a.stream, p.parts,
+                                       prefix ? *prefix : PrefixParts{}, a.pm, reinterpret_cast<uint2*>(a.out), a.status);
   if (e != cudaSuccess) return fail(cuda_status(e), "block join launch: %s", cudaGetErrorString(e));
   return check_launch("block join");
 }
@@ -667,9 +644,9 @@ extern "C" grok_status grok_attn_decode_sparse_paged(const grok_bf16* q_rot, con
     return fail(GROK_ERR_INVALID_ARG, "%s: workspace of %zu bytes is smaller than the %zu needed", who, workspace_bytes,
                 need);
   BlockArgs a = {};
+  if ((st = encode_pool(&a.tm_k, k_pool, n_pages)) != GROK_OK) return st;
+  if ((st = encode_pool(&a.tm_v, v_pool, n_pages)) != GROK_OK) return st;
   a.q_rot = q_rot;
-  a.k_pool = k_pool;
-  a.v_pool = v_pool;
   a.pm = PageMap{block_table, max_pages, n_pages};
   a.kv_len = kv_len;
   a.B = B;

@@ -3,6 +3,8 @@
 // and over the rows behind a shared prefix (grok_attn_decode_shared_paged).
 #pragma once
 
+#include <utility>
+
 #include "blocks.cuh"
 #include "host.cuh"
 
@@ -66,8 +68,7 @@ struct PrefixParts {
 
 struct BlockArgs {
   const grok_bf16* q_rot;
-  const grok_bf16* k_pool;
-  const grok_bf16* v_pool;
+  CUtensorMap tm_k, tm_v;  // of the pools (encode_pool)
   PageMap pm;
   const int32_t* kv_len;
   int B;
@@ -85,6 +86,23 @@ size_t prefix_parts_bytes(int B, int n_groups, int sms);
 // which was launched before on the stream).
 grok_status block_decode_run(const BlockArgs& a, char* ws, const PrefixParts* prefix, int sms);
 PrefixParts prefix_parts(char* ws, int B, int n_groups, int sms);
+
+// A launch, `beside`: as the programmatic dependent of the kernel before it on the stream, beside which it may start.
+template <typename... Args, typename... Given>
+cudaError_t launch(bool beside, void (*kernel)(Args...), dim3 grid, int threads, int smem, cudaStream_t stream,
+                   Given&&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = beside ? 1 : 0;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, std::forward<Given>(args)...);
+}
 
 // Tensor map of a pool as (64 features, row, half of the features, KV head): one copy brings the 64 rows of a block of
 // one head, as two tiles of [64 rows][64 bf16].

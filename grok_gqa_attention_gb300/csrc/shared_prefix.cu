@@ -172,6 +172,9 @@ __global__ void __launch_bounds__(kPxBound, 1)
   // The plan: key tiles and items before each group's, a group a thread. (Groups that are not usable are dropped: every
   // sequence is then decoded by itself, by the other kernel, which reports it.)
   const bool fine = load_groups(p.groups, p.B, p.pm.max_pages, &sh->groups, tid);
+  if (fine && tid < p.groups.n)  // (the group's table entries come closer meanwhile)
+    for (int i = 0; i < sh->groups.pages[tid]; i += 32)
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(p.pm.table + (size_t)sh->groups.start[tid] * p.pm.max_pages + i));
   if (warp == 1) {
     tmem_alloc(&sh->tmem, 512);
     tmem_relinquish();
@@ -479,9 +482,6 @@ extern "C" grok_status grok_attn_decode_shared_paged(const grok_bf16* q_rot, con
   if (workspace_bytes < need)
     return fail(GROK_ERR_INVALID_ARG, "%s: workspace of %zu bytes is smaller than the %zu needed", who, workspace_bytes,
                 need);
-  CUtensorMap tk, tv;
-  if ((st = encode_pool(&tk, k_pool, n_pages)) != GROK_OK) return st;
-  if ((st = encode_pool(&tv, v_pool, n_pages)) != GROK_OK) return st;
   static bool attr_set[kMaxDevices] = {};  // per device; idempotent: every thread would set the same value
   int dev = 0;
   if ((st = device_index(&dev)) != GROK_OK) return st;
@@ -493,6 +493,9 @@ extern "C" grok_status grok_attn_decode_shared_paged(const grok_bf16* q_rot, con
     if (e != cudaSuccess) return fail(cuda_status(e), "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
     attr_set[dev] = true;
   }
+  BlockArgs a = {};
+  if ((st = encode_pool(&a.tm_k, k_pool, n_pages)) != GROK_OK) return st;
+  if ((st = encode_pool(&a.tm_v, v_pool, n_pages)) != GROK_OK) return st;
   char* ws = static_cast<char*>(workspace);
   const PrefixParts prefix = prefix_parts(ws + blocks, B, n_groups, sms);
   PxParams p;
@@ -502,12 +505,10 @@ extern "C" grok_status grok_attn_decode_shared_paged(const grok_bf16* q_rot, con
   p.B = B;
   p.parts = prefix;
   p.status = dev_status;
-  prefix_kernel<<<sms, kPxThreads, kPxSmem, static_cast<cudaStream_t>(stream)>>>(tk, tv, p);
-  if ((st = check_launch("prefix")) != GROK_OK) return st;
-  BlockArgs a = {};
+  const cudaError_t e = launch(false, prefix_kernel, dim3(sms), kPxThreads, kPxSmem, static_cast<cudaStream_t>(stream),
+                               a.tm_k, a.tm_v, p);
+  if (e != cudaSuccess) return fail(cuda_status(e), "prefix launch: %s", cudaGetErrorString(e));
   a.q_rot = q_rot;
-  a.k_pool = k_pool;
-  a.v_pool = v_pool;
   a.pm = p.pm;
   a.kv_len = kv_len;
   a.B = B;
