@@ -474,6 +474,52 @@ def test_a_batch_as_long_as_it_gets():
     assert ((a - z).abs() <= 2.0 ** -7 * torch.maximum(a.abs(), z.abs()) + 2.0 ** -9 * most).all()
 
 
+def test_long_own_rows():
+    """More blocks of the sequences' own than half of the CTAs are given; compared with the whole decode."""
+    paged, starts = grouped([7, 3], [3, 1], lambda i: 6000 - 517 * i, seed=7)
+    q = queries(10, 22)
+    out, st = run_shared(paged, q, starts, [3, 1])
+    assert st == 0
+    some = [0, 6, 7]
+    want, spread = expected(paged, q, lambda b, g: np.arange(paged.lens[b]) if b in some else [])
+    check(out[some], want[some], spread[some], 2.0 ** -10)
+    k, v, table = paged.dev()
+    ws, full = G.alloc_decode_workspace(10, paged.max_pages * PG, DEV), torch.empty_like(out)
+    G.decode_paged(q.to(DEV), k, v, table, ints(paged.lens), ws)
+    G.combine(ws, ints(paged.lens), full, paged.max_pages * PG)
+    a, z = out.float(), full.float()
+    most = float(paged.v.nan_to_num(0.0).abs().max())
+    assert ((a - z).abs() <= 2.0 ** -7 * torch.maximum(a.abs(), z.abs()) + 2.0 ** -9 * most).all()
+
+
+def test_many_sequences_in_many_groups():
+    """More sequences than the plan's table has entries, as many groups as there may be, some of one sequence, some
+    sequences in none."""
+    rng = np.random.default_rng(5)
+    sizes = [int(x) for x in rng.integers(1, 5, 256)]
+    pages = [int(x) for x in rng.integers(0, 3, 256)]
+    paged, starts = grouped(sizes, pages, lambda i: 1 + i * 37 % 150, seed=8, alone_before=3, alone_after=4)
+    B = len(paged.lens)
+    assert B > 512
+    q = queries(B, 23)
+    out, st = run_shared(paged, q, starts, pages)
+    assert st == 0
+    some = [0, 1, 2, 3, 4, 5, 6, 300, 301, 302, B - 6, B - 5, B - 4, B - 1]
+    want, spread = expected(paged, q, lambda b, g: np.arange(paged.lens[b]) if b in some else [])
+    check(out[some], want[some], spread[some], 2.0 ** -10)
+
+
+def test_results_do_not_change_from_call_to_call():
+    paged, starts = grouped([25, 13], [9, 4], lambda i: 31 * i, seed=9)
+    q = queries(38, 24)
+    first, _ = run_shared(paged, q, starts, [9, 4])
+    sel = lists(paged.lens, 11, seed=10)
+    first_sparse, _ = run_sparse(paged, q, sel)
+    for _ in range(4):
+        assert torch.equal(run_shared(paged, q, starts, [9, 4])[0], first)
+        assert torch.equal(run_sparse(paged, q, sel)[0], first_sparse)
+
+
 # ------------------------------------------------------------------------------------------------------- together
 def append_rows(paged_k, paged_v, table, k, v, q, start):
     q_rot = torch.empty_like(q)
