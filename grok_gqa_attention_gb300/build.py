@@ -1,4 +1,5 @@
-"""Build libgrok_attn.so (the C-ABI library) in-tree for sm_103a with nvcc.
+"""Build libgrok_attn.so (the C-ABI library) in-tree for sm_103a with nvcc, and _binding.so, the Python binding's
+checks of the calls over parts of a cache, with the host compiler.
 
 Each .cu file is compiled in parallel, then linked into one shared library
 next to this file. The CUDA runtime is linked statically; the driver's
@@ -11,6 +12,7 @@ import os
 import platform
 import shutil
 import subprocess
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -18,6 +20,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build", platform.machine())
 LIB = os.path.join(PKG, "libgrok_attn.so")
+BINDING = os.path.join(PKG, "_binding.so")
 SOURCES = ["abi.cu", "rope_append.cu", "prefill.cu", "decode.cu", "selftest.cu", "pipe.cu", "qkv.cu", "slots.cu", "int8_small.cu",
            "kv8_append.cu", "kv8_decode.cu", "kv8_prefill.cu", "kv8_evict.cu",
            "kv_bounds.cu", "block_decode.cu", "shared_prefix.cu"]
@@ -44,12 +47,12 @@ def _inputs() -> list[str]:
 
 
 def up_to_date() -> bool:
-    if not (os.path.exists(LIB) and os.path.exists(_stamp_path())):
+    if not (os.path.exists(LIB) and os.path.exists(BINDING) and os.path.exists(_stamp_path())):
         return False
     with open(_stamp_path()) as f:
         if f.read().strip() != platform.machine():
             return False
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
     return all(os.path.getmtime(p) <= t for p in _inputs())
 
 
@@ -69,8 +72,18 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
             raise RuntimeError(f"nvcc failed on {src}:\n{r.stdout}\n{r.stderr}")
         return obj, r.stdout + r.stderr
 
-    with concurrent.futures.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    def compile_binding() -> None:
+        cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-I", INCLUDE, "-I", sysconfig.get_paths()["include"],
+               os.path.join(CSRC, "binding.cpp"), "-o", BINDING + ".tmp"]
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"g++ failed on binding.cpp:\n{r.stdout}\n{r.stderr}")
+        os.replace(BINDING + ".tmp", BINDING)
+
+    with concurrent.futures.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        binding = ex.submit(compile_binding)
         results = list(ex.map(compile_one, SOURCES))
+        binding.result()
     log = "".join(msg for _, msg in results)
     if verbose or ptxas_info:
         print(log)
@@ -80,6 +93,7 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    os.utime(BINDING)  # (as new as the library: what is built together is up to date together)
     with open(_stamp_path(), "w") as f:
         f.write(platform.machine())
     with open(os.path.join(BUILD, "ptxas.log"), "w") as f:

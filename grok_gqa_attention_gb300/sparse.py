@@ -2,19 +2,44 @@
 
 Bounds of the keys of each 64-token block, the choice of the blocks that a query reads, attention over a list of
 blocks, and attention for a batch whose sequences share prefixes (see grok_kv_bounds_paged in include/grok_attn.h).
-Every call runs on the device of its pools, on that device's current stream unless one is given.
+Every call runs on the device of its pools, on that device's current stream unless one is given. A call's arguments are
+checked by _binding.so where all is as it should be, and by the functions here otherwise, which say what is not.
 """
 from __future__ import annotations
 
 import ctypes
+import importlib.util
+import os
 
 import torch
 
 from . import HEAD_DIM, N_KV_HEADS, N_Q_HEADS, PAGE_TOKENS, SPARSE_BLOCK, _check, load
-from .kv8 import _call, _maybe, _need
+from .kv8 import _call, _maybe, _need, _raw_device, _raw_stream
 
 _BF16, _F32, _I32, _I8, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.int8, torch.uint8
 _PAGE_BLOCKS = PAGE_TOKENS // SPARSE_BLOCK
+
+
+_checked = None
+
+
+def _binding():
+    """The checks in _binding.so, with the library's functions."""
+    global _checked
+    if _checked is None:
+        lib = load()
+        path = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_binding.so")
+        if not os.path.exists(path):
+            raise RuntimeError(f"{path} is missing: build it with grok_gqa_attention_gb300.build.build()")
+        spec = importlib.util.spec_from_file_location("_binding", path)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        calls = (lib.grok_kv_bounds_paged, lib.grok_attn_select_paged, lib.grok_attn_decode_sparse_paged,
+                 lib.grok_attn_decode_shared_paged)
+        module.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in calls), _BF16, _F32, _I32, _I8, _U8, _raw_device,
+                    _raw_stream)
+        _checked = module
+    return _checked
 
 
 def _index(t, name: str) -> int:
@@ -49,6 +74,10 @@ def kv_bounds_paged(k_pool, block_table, start_pos, valid_len, T: int, codes, sc
 
     valid_len may be None (T rows of every sequence). codes, scale as from alloc_kv_bounds(k_pool.shape[0]).
     """
+    status = (_checked or _binding()).kv_bounds_paged(k_pool, block_table, start_pos, valid_len, T, codes, scale, dev_status,
+                                                        stream)
+    if status is not None:
+        return _check(status)
     at, n, B = _index(k_pool, "k_pool"), k_pool.shape[0], start_pos.shape[0]
     table, max_pages = _table(block_table, B, at)
     _call(at, stream, "grok_kv_bounds_paged", _pool(k_pool, "k_pool", n, at), n, table, max_pages,
@@ -63,6 +92,10 @@ def select_blocks_paged(q_rot, codes, scale, block_table, kv_len, sink: int, rec
     """score [B, 8, 2 * max_pages] float32: a bound of q . k over each block; sel [B, 8, budget] int32: the blocks to
     read, ascending, -1 behind them: the first `sink`, the last `recent`, then the largest scores.
     """
+    status = (_checked or _binding()).select_blocks_paged(q_rot, codes, scale, block_table, kv_len, sink, recent, score,
+                                                            sel, dev_status, stream)
+    if status is not None:
+        return _check(status)
     at, n, B = _index(q_rot, "q_rot"), codes.shape[0], q_rot.shape[0]
     if sel.dim() != 3:
         raise ValueError("sel must be [B, 8, budget]")
@@ -93,6 +126,10 @@ def decode_sparse_paged(q_rot, k_pool, v_pool, block_table, kv_len, sel, workspa
     """out [B, 48, 128] = attention of q_rot [B, 48, 128] over the rows below kv_len[b] of the blocks in sel
     [B, 8, budget] (per KV head; negative entries are passed over).
     """
+    status = (_checked or _binding()).decode_sparse_paged(q_rot, k_pool, v_pool, block_table, kv_len, sel, workspace, out,
+                                                            dev_status, stream)
+    if status is not None:
+        return _check(status)
     at, n, B = _index(k_pool, "k_pool"), k_pool.shape[0], q_rot.shape[0]
     if sel.dim() != 3:
         raise ValueError("sel must be [B, 8, budget]")
@@ -125,6 +162,10 @@ def decode_shared_paged(q_rot, k_pool, v_pool, block_table, kv_len, group_start,
     Sequences [group_start[i], group_start[i + 1]) have the first shared_pages[i] entries of block_table in common;
     group_start [n_groups + 1], shared_pages [n_groups] int32.
     """
+    status = (_checked or _binding()).decode_shared_paged(q_rot, k_pool, v_pool, block_table, kv_len, group_start,
+                                                            shared_pages, workspace, out, dev_status, stream)
+    if status is not None:
+        return _check(status)
     at, n, B = _index(k_pool, "k_pool"), k_pool.shape[0], q_rot.shape[0]
     n_groups, nbytes = shared_pages.numel(), workspace.numel()
     table, max_pages = _table(block_table, B, at)
