@@ -32,6 +32,7 @@ __host__ __device__ constexpr int bk_ring(bool list) { return list ? 5 : 4; }
 constexpr int kBkQ = kGroup * kD * 2;        // a pair's queries
 constexpr int kBkPlan = 512;                 // entries of the table of block counts
 constexpr int kBkCtas = 2;                   // CTAs resident on an SM
+constexpr int kBkUneven = 5;                 // blocks an SM may have above its equal share to save the plan and the join
 constexpr int kBkFew = 8;                    // blocks per CTA up to which half of the CTAs take them (beside a prefix)
 
 template <int kRing>
@@ -60,6 +61,7 @@ struct BkParams {
   int budget;
   Groups groups;
   BlockParts parts;
+  grok_bf16* out;     // kPairs
   int4* prefix_pair;  // entries of sequences without a prefix are cleared here
   int32_t* status;
 };
@@ -82,13 +84,17 @@ __device__ __forceinline__ int bk_blocks(const BkParams& p, int len, int share) 
   return min((len + kBlk - 1) / kBlk - share * kBlkPerPage, p.budget);
 }
 
-// (Registers: 112 a thread at most behind prefixes, for the same reason as in the prefix kernel.)
-template <bool kList>
-__global__ void __launch_bounds__(kList ? kBkThreads : 576, kList ? kBkCtas : 1)
+// kOwn: the rows behind prefixes. (Registers: 112 a thread at most, for the same reason as in the prefix kernel.)
+// kLists: lists of blocks, dealt out to the CTAs in equal shares. kPairs: the same for few pairs: a cluster of CTAs takes a
+// pair's list and joins its parts itself, so that there is neither a plan nor a second kernel.
+enum BkMode { kOwn, kLists, kPairs };
+template <int kMode>
+__global__ void __launch_bounds__(kMode != kOwn ? kBkThreads : 576, kMode != kOwn ? kBkCtas : 1)
     block_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                         const BkParams p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  constexpr bool kList = kMode != kOwn, kPair = kMode == kPairs;
   constexpr int kBkRing = bk_ring(kList);
   uint8_t* sq = smem + kBkRing * kBkTile;
   BkShared<kBkRing>* sh = reinterpret_cast<BkShared<kBkRing>*>(sq + kBkRing * kBkQ);
@@ -109,69 +115,89 @@ __global__ void __launch_bounds__(kList ? kBkThreads : 576, kList ? kBkCtas : 1)
     prefetch_tmap(&tm_k);
     prefetch_tmap(&tm_v);
   }
-  // The plan: blocks per KV head before each sequence (or each `step` sequences, where there are many).
-  const int step = (p.B + kBkPlan - 1) / kBkPlan, entries = (p.B + step - 1) / step;
-  constexpr int kPer = (kBkPlan + kBkThreads - 1) / kBkThreads;  // contiguous entries per thread
-  const int per = (entries + kBkThreads - 1) / kBkThreads, e0 = tid * per;
-  int len0[kPer];  // (loaded beside the groups)
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) len0[i] = i < per && e0 + i < entries ? p.kv_len[(e0 + i) * step] : 0;
-  int n_groups = 0;
-  if (!kList) {
-    bool fine = true;
-    for (int i = tid; i < p.groups.n; i += kBkThreads) fine &= load_groups(p.groups, p.B, p.pm.max_pages, &sh->groups, i);
-    if (__syncthreads_and(fine))
-      n_groups = p.groups.n;
-    else if (blockIdx.x == 0 && tid == 0)
-      report(p.status, GROK_DEV_BAD_GROUP);
-  }
-  {
-    int n_of[kPer], mine = 0;
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      n_of[i] = 0;
-      const int e = e0 + i;
-      if (i < per && e < entries)
-        for (int b = e * step; b < min((e + 1) * step, p.B); ++b) {
-          const int len = b == e * step ? len0[i] : p.kv_len[b], share = n_groups ? sh->groups.of_seq(n_groups, b) : 0;
-          const int n = bk_blocks(p, len, share);
-          if (step == 1) sh->seq[e] = len | share << 17;
-          if (blockIdx.x == 0) {
-            if (n < 0) report(p.status, GROK_DEV_BAD_KV_LEN);
-            if (n <= 0)
-              for (int g = 0; g < kKVHeads; ++g) p.parts.pair[b * kKVHeads + g] = make_int2(0, n);
-            if (!kList && share == 0)
-              for (int g = 0; g < kKVHeads; ++g) p.prefix_pair[b * kKVHeads + g] = make_int4(0, 0, 0, 0);
-          }
-          n_of[i] += max(n, 0);
-        }
-      mine += n_of[i];
-    }
-    int incl = mine;
-#pragma unroll
-    for (int d = 1; d < 32; d *= 2) {
-      const int up = __shfl_up_sync(0xffffffffu, incl, d);
-      if (lane >= d) incl += up;
-    }
-    if (lane == 31) sh->warp_sum[warp] = incl;
-    __syncthreads();
-    int at = incl - mine;
-    for (int w = 0; w < warp; ++w) at += sh->warp_sum[w];
-#pragma unroll
-    for (int i = 0; i < kPer; ++i)
-      if (i < per && e0 + i < entries) {
-        sh->cum[e0 + i] = at;
-        at += n_of[i];
-        if (e0 + i == entries - 1) sh->cum[entries] = at;
-      }
-  }
-  __syncthreads();
-  const int total = kKVHeads * sh->cum[entries];
-  // Beside the prefix kernel an SM has room for one CTA: little work is dealt to the first half of them.
-  const int ctas = !kList && total <= kBkFew * int(gridDim.x) ? int(gridDim.x) / kBkCtas : int(gridDim.x);
-  const int share_of = max(1, (total + ctas - 1) / ctas);  // blocks per CTA
   const int cta = blockIdx.x;
-  const int lo = min((long long)cta * share_of, (long long)total), hi = min(lo + share_of, total);
+  int lo, hi, share_of;                    // this CTA's blocks; blocks per CTA
+  int pair0 = 0, len0 = 0, n0 = 0, rank = 0, ctas = 1;  // kPairs: the pair, its sequence's rows, its blocks, the CTA's place
+  int step = 1, entries = 0, n_groups = 0;
+  if (kPair) {
+    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(ctas));
+    pair0 = cta / ctas;
+    rank = cta % ctas;
+    len0 = p.kv_len[pair0 / kKVHeads];
+    n0 = bk_blocks(p, len0, 0);
+    if (n0 < 0) {
+      if (rank == 0 && pair0 % kKVHeads == 0 && tid == 0) report(p.status, GROK_DEV_BAD_KV_LEN);
+      return;  // (the whole cluster)
+    }
+    share_of = (n0 + ctas - 1) / ctas;
+    lo = min(rank * share_of, n0);
+    hi = min(lo + share_of, n0);
+    __syncthreads();
+  } else {
+    // The plan: blocks per KV head before each sequence (or each `step` sequences, where there are many).
+    step = (p.B + kBkPlan - 1) / kBkPlan;
+    entries = (p.B + step - 1) / step;
+    constexpr int kPer = (kBkPlan + kBkThreads - 1) / kBkThreads;  // contiguous entries per thread
+    const int per = (entries + kBkThreads - 1) / kBkThreads, e0 = tid * per;
+    int lens[kPer];  // (loaded beside the groups)
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) lens[i] = i < per && e0 + i < entries ? p.kv_len[(e0 + i) * step] : 0;
+    if (!kList) {
+      bool fine = true;
+      for (int i = tid; i < p.groups.n; i += kBkThreads) fine &= load_groups(p.groups, p.B, p.pm.max_pages, &sh->groups, i);
+      if (__syncthreads_and(fine))
+        n_groups = p.groups.n;
+      else if (blockIdx.x == 0 && tid == 0)
+        report(p.status, GROK_DEV_BAD_GROUP);
+    }
+    {
+      int n_of[kPer], mine = 0;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        n_of[i] = 0;
+        const int e = e0 + i;
+        if (i < per && e < entries)
+          for (int b = e * step; b < min((e + 1) * step, p.B); ++b) {
+            const int len = b == e * step ? lens[i] : p.kv_len[b], share = n_groups ? sh->groups.of_seq(n_groups, b) : 0;
+            const int n = bk_blocks(p, len, share);
+            if (step == 1) sh->seq[e] = len | share << 17;
+            if (blockIdx.x == 0) {
+              if (n < 0) report(p.status, GROK_DEV_BAD_KV_LEN);
+              if (n <= 0)
+                for (int g = 0; g < kKVHeads; ++g) p.parts.pair[b * kKVHeads + g] = make_int2(0, n);
+              if (!kList && share == 0)
+                for (int g = 0; g < kKVHeads; ++g) p.prefix_pair[b * kKVHeads + g] = make_int4(0, 0, 0, 0);
+            }
+            n_of[i] += max(n, 0);
+          }
+        mine += n_of[i];
+      }
+      int incl = mine;
+#pragma unroll
+      for (int d = 1; d < 32; d *= 2) {
+        const int up = __shfl_up_sync(0xffffffffu, incl, d);
+        if (lane >= d) incl += up;
+      }
+      if (lane == 31) sh->warp_sum[warp] = incl;
+      __syncthreads();
+      int at = incl - mine;
+      for (int w = 0; w < warp; ++w) at += sh->warp_sum[w];
+#pragma unroll
+      for (int i = 0; i < kPer; ++i)
+        if (i < per && e0 + i < entries) {
+          sh->cum[e0 + i] = at;
+          at += n_of[i];
+          if (e0 + i == entries - 1) sh->cum[entries] = at;
+        }
+    }
+    __syncthreads();
+    const int total = kKVHeads * sh->cum[entries];
+    // Beside the prefix kernel an SM has room for one CTA: little work is dealt to the first half of them.
+    const int among = !kList && total <= kBkFew * int(gridDim.x) ? int(gridDim.x) / kBkCtas : int(gridDim.x);
+    share_of = max(1, (total + among - 1) / among);
+    lo = int(min((long long)cta * share_of, (long long)total));
+    hi = min(lo + share_of, total);
+  }
   if (lo < hi) {
     if (warp == kBkWarps) {
       // ------------------------------------------------------------ producer
@@ -199,23 +225,28 @@ __global__ void __launch_bounds__(kList ? kBkThreads : 576, kList ? kBkCtas : 1)
         const int cnt = min(32, hi - base), idx = base + lane;
         int my_pair = 0, my_row = -1, my_keys = 0;  // (row of the pools; -1: no block here)
         if (lane < cnt) {
-          int e = 0;
-          for (int d = kBkPlan / 2; d; d /= 2)
-            if (e + d < entries && kKVHeads * sh->cum[e + d] <= idx) e += d;
-          int rest = idx - kKVHeads * sh->cum[e], b = e * step, len, share, n;
-          while (true) {
-            len = step == 1 ? sh->seq[e] & 0x1FFFF : p.kv_len[b];
-            share = step == 1 ? sh->seq[e] >> 17 : n_groups ? sh->groups.of_seq(n_groups, b) : 0;
-            n = max(bk_blocks(p, len, share), 0);
-            if (step == 1 || rest < kKVHeads * n) break;
-            rest -= kKVHeads * n;
-            ++b;
-          }
-          const int g = rest / n, k = rest % n;
-          my_pair = b * kKVHeads + g;
-          if (k == 0) {  // the pair's parts: one of each CTA from this one on that takes some of its blocks
-            const int last = (idx + n - 1) / share_of;
-            p.parts.pair[my_pair] = make_int2(cta + my_pair, last - cta + 1);
+          int b = pair0 / kKVHeads, len = len0, share = 0, k = idx;
+          my_pair = pair0;
+          if (!kPair) {
+            int e = 0, n;
+            for (int d = kBkPlan / 2; d; d /= 2)
+              if (e + d < entries && kKVHeads * sh->cum[e + d] <= idx) e += d;
+            int rest = idx - kKVHeads * sh->cum[e];
+            b = e * step;
+            while (true) {
+              len = step == 1 ? sh->seq[e] & 0x1FFFF : p.kv_len[b];
+              share = step == 1 ? sh->seq[e] >> 17 : n_groups ? sh->groups.of_seq(n_groups, b) : 0;
+              n = max(bk_blocks(p, len, share), 0);
+              if (step == 1 || rest < kKVHeads * n) break;
+              rest -= kKVHeads * n;
+              ++b;
+            }
+            my_pair = b * kKVHeads + rest / n;
+            k = rest % n;
+            if (k == 0) {  // the pair's parts: one of each CTA from this one on that takes some of its blocks
+              const int last = (idx + n - 1) / share_of;
+              p.parts.pair[my_pair] = make_int2(cta + my_pair, last - cta + 1);
+            }
           }
           const int blocks = (len + kBlk - 1) / kBlk;
           int blk = share * kBlkPerPage + k;
@@ -297,7 +328,7 @@ __global__ void __launch_bounds__(kList ? kBkThreads : 576, kList ? kBkCtas : 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(&sh->sum_full);
             if (!__all_sync(0xffffffffu, mbar_wait(&sh->sum_full, odd, abort, p.status))) break;
-            const size_t slot = (size_t)cta + cur;
+            const size_t slot = kPair ? (size_t)cta : (size_t)cta + cur;
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
               float4 v = own[i];
@@ -399,6 +430,40 @@ __global__ void __launch_bounds__(kList ? kBkThreads : 576, kList ? kBkCtas : 1)
   // Started as the dependent of the prefix kernel, this one ends behind it, so that the kernel that waits for this one
   // finds both results. (The last CTA alone waits: the others' places beside the prefix kernel are for the CTAs that follow.)
   if (!kList && blockIdx.x == gridDim.x - 1) asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (kPair) {
+    // The pair's parts are complete: each CTA of the cluster adds a share of the features and writes it.
+    __syncwarp();
+    __threadfence();
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    const int parts = (n0 + share_of - 1) / share_of, each = kBkPartO / ctas;
+    const size_t first = (size_t)pair0 * ctas;
+    for (int i = tid; i < each; i += kBkThreads) {
+      const int at = rank * each + i, c = at % 4 * 2, d = at / 32 * 16 + at % 32 / 4;
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+      float2 l = make_float2(0.f, 0.f);
+#pragma unroll 8
+      for (int r = 0; r < parts; ++r) {
+        const float4 x = __ldcg(p.parts.o + (first + r) * kBkPartO + at);
+        const float2 y = __ldcg(reinterpret_cast<const float2*>(p.parts.l + (first + r) * 8 + c));
+        v.x += x.x;
+        v.y += x.y;
+        v.z += x.z;
+        v.w += x.w;
+        l.x += y.x;
+        l.y += y.y;
+      }
+      if (c < kGroup) {
+        const float i0 = l.x == 0.f ? 0.f : 1.0f / l.x, i1 = l.y == 0.f ? 0.f : 1.0f / l.y;
+        const uint32_t lo0 = pack_bf16x2(v.x * i0, v.z * i0), lo1 = pack_bf16x2(v.y * i1, v.w * i1);
+        grok_bf16* out = p.out + ((size_t)pair0 * kGroup + c) * kD + d;
+        out[0] = grok_bf16(lo0);
+        out[8] = grok_bf16(lo0 >> 16);
+        out[kD] = grok_bf16(lo1);
+        out[kD + 8] = grok_bf16(lo1 >> 16);
+      }
+    }
+  }
 }
 
 // ----------------------------------------------------------------------------
@@ -552,22 +617,25 @@ grok_status encode_pool(CUtensorMap* map, const grok_bf16* pool, int n_pages) {
   return encode_tmap_bf16_4d(map, pool, dims, strides, box);
 }
 
-template <bool kList>
-static grok_status bk_launch(const BlockArgs& a, const BkParams& p, int sms) {
+template <int kMode>
+static grok_status bk_launch(const BlockArgs& a, const BkParams& p, int sms, int ctas) {
+  constexpr int kSmem = kBkSmem<kMode != kOwn>;
   grok_status st;
   static bool attr_set[kMaxDevices] = {};  // per device; idempotent: every thread would set the same value
   int dev = 0;
   if ((st = device_index(&dev)) != GROK_OK) return st;
   cudaError_t e;
   if (!attr_set[dev]) {
-    e = cudaFuncSetAttribute(block_decode_kernel<kList>, cudaFuncAttributeMaxDynamicSharedMemorySize, kBkSmem<kList>);
+    e = cudaFuncSetAttribute(block_decode_kernel<kMode>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(block_decode_kernel<kList>, cudaFuncAttributePreferredSharedMemoryCarveout,
+      e = cudaFuncSetAttribute(block_decode_kernel<kMode>, cudaFuncAttributePreferredSharedMemoryCarveout,
                                cudaSharedmemCarveoutMaxShared);
     if (e != cudaSuccess) return fail(cuda_status(e), "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
     attr_set[dev] = true;
   }
-  e = launch(!kList, block_decode_kernel<kList>, dim3(kBkCtas * sms), kBkThreads, kBkSmem<kList>, a.stream, a.tm_k, a.tm_v, p);
+  const int grid = kMode == kPairs ? a.B * kKVHeads * ctas : kBkCtas * sms;
+  e = launch(kMode == kOwn, kMode == kPairs ? ctas : 1, block_decode_kernel<kMode>, dim3(grid), kBkThreads, kSmem, a.stream,
+             a.tm_k, a.tm_v, p);
   if (e != cudaSuccess) return fail(cuda_status(e), "block decode launch: %s", cudaGetErrorString(e));
   return check_launch("block decode");
 }
@@ -584,12 +652,20 @@ grok_status block_decode_run(const BlockArgs& a, char* ws, const PrefixParts* pr
   p.parts = block_parts(ws, a.B, sms);
   p.prefix_pair = prefix ? prefix->pair : nullptr;
   p.status = a.status;
-  grok_status st = a.sel ? bk_launch<true>(a, p, sms) : bk_launch<false>(a, p, sms);
+  p.out = a.out;
+  if (a.sel && (long long)a.B * kKVHeads <= kBkCtas * sms) {
+    // One wave of clusters holds all pairs. The most blocks that an SM then has, against an equal share of all:
+    int ctas = 8;
+    while (a.B * kKVHeads * ctas > kBkCtas * sms) ctas /= 2;
+    const int most = (a.budget + ctas - 1) / ctas * (a.B * kKVHeads * ctas > sms ? 2 : 1);
+    if (most <= a.B * kKVHeads * a.budget / sms + kBkUneven) return bk_launch<kPairs>(a, p, sms, ctas);
+  }
+  grok_status st = a.sel ? bk_launch<kLists>(a, p, sms, 1) : bk_launch<kOwn>(a, p, sms, 1);
   if (st != GROK_OK) return st;
   const int teams = a.B * kKVHeads <= 2 * sms ? 4 : 1;
   auto kernel = prefix ? (teams == 4 ? block_join_kernel<true, 4> : block_join_kernel<true, 1>)
                        : (teams == 4 ? block_join_kernel<false, 4> : block_join_kernel<false, 1>);
-  const cudaError_t e = launch(true, kernel, dim3(kKVHeads, a.B), teams * kBkPartO, 0, a.stream, p.parts,
+  const cudaError_t e = launch(true, 1, kernel, dim3(kKVHeads, a.B), teams * kBkPartO, 0, a.stream, p.parts,
                                        prefix ? *prefix : PrefixParts{}, a.pm, reinterpret_cast<uint2*>(a.out), a.status);
   if (e != cudaSuccess) return fail(cuda_status(e), "block join launch: %s", cudaGetErrorString(e));
   return check_launch("block join");

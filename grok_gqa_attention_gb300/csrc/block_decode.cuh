@@ -87,20 +87,25 @@ size_t prefix_parts_bytes(int B, int n_groups, int sms);
 grok_status block_decode_run(const BlockArgs& a, char* ws, const PrefixParts* prefix, int sms);
 PrefixParts prefix_parts(char* ws, int B, int n_groups, int sms);
 
-// A launch, `beside`: as the programmatic dependent of the kernel before it on the stream, beside which it may start.
+// A launch in clusters of `cluster` CTAs. `beside`: as the programmatic dependent of the kernel before it on the stream,
+// beside which it may start.
 template <typename... Args, typename... Given>
-cudaError_t launch(bool beside, void (*kernel)(Args...), dim3 grid, int threads, int smem, cudaStream_t stream,
+cudaError_t launch(bool beside, int cluster, void (*kernel)(Args...), dim3 grid, int threads, int smem, cudaStream_t stream,
                    Given&&... args) {
   cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   cfg.gridDim = grid;
   cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = beside ? 1 : 0;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kernel, std::forward<Given>(args)...);
 }
 

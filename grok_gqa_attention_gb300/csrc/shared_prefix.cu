@@ -505,7 +505,7 @@ extern "C" grok_status grok_attn_decode_shared_paged(const grok_bf16* q_rot, con
   p.B = B;
   p.parts = prefix;
   p.status = dev_status;
-  const cudaError_t e = launch(false, prefix_kernel, dim3(sms), kPxThreads, kPxSmem, static_cast<cudaStream_t>(stream),
+  const cudaError_t e = launch(false, 1, prefix_kernel, dim3(sms), kPxThreads, kPxSmem, static_cast<cudaStream_t>(stream),
                                a.tm_k, a.tm_v, p);
   if (e != cudaSuccess) return fail(cuda_status(e), "prefix launch: %s", cudaGetErrorString(e));
   a.q_rot = q_rot;
