@@ -91,6 +91,7 @@ enum BkMode { kOwn, kLists, kPairs };
 template <int kMode>
 __global__ void __launch_bounds__(kMode != kOwn ? kBkThreads : 576, kMode != kOwn ? kBkCtas : 1)
     block_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                        const __grid_constant__ CUtensorMap tm_k16, const __grid_constant__ CUtensorMap tm_v16,
                         const BkParams p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -213,6 +214,20 @@ __global__ void __launch_bounds__(kMode != kOwn ? kBkThreads : 576, kMode != kOw
         ++loads;
         if (++st == kBkRing) st = 0, turn ^= 1;
       };
+      // A block's K or V into the ring, with `more` bytes that come beside it: in one copy, or of a sequence's last block
+      // the rows that there are, 16 at a time (two copies of half of the features each, one a lane).
+      auto load = [&](const CUtensorMap* tm, const CUtensorMap* tm16, int row, int g, int keys, int more) {
+        const int groups = (keys + 15) / 16;
+        if (lane == 0) mbar_arrive_expect_tx(&sh->full[st], groups * 16 * kD * 2 + more);
+        uint8_t* to = smem + st * kBkTile;
+        if (groups == 4) {
+          if (lane == 0) tma_load_4d(to, tm, &sh->full[st], 0, row, 0, g);
+        } else if (lane < 2 * groups) {
+          tma_load_4d(to + (lane & 1) * kBkBox + (lane >> 1) * 16 * 128, tm16, &sh->full[st], 0, row + (lane >> 1) * 16,
+                      lane & 1, g);
+        }
+        next();
+      };
       auto send_empty = [&](int pair) {  // a token without a block
         if (!acquire()) return;
         if (lane == 0) {
@@ -270,18 +285,12 @@ __global__ void __launch_bounds__(kMode != kOwn ? kBkThreads : 576, kMode != kOw
           const int g = pair % kKVHeads;
           if (lane == 0) {
             sh->token[st] = make_int2(pair, keys);
-            mbar_arrive_expect_tx(&sh->full[st], kBkTile + (sent ? 0 : kBkQ));
             if (!sent) bulk_load(sq + st * kBkQ, p.q + (size_t)pair * kBkQ, kBkQ, &sh->full[st]);
-            tma_load_4d(smem + st * kBkTile, &tm_k, &sh->full[st], 0, row, 0, g);
           }
+          load(&tm_k, &tm_k16, row, g, keys, sent ? 0 : kBkQ);
           sent = true;
-          next();
           if (!acquire()) continue;
-          if (lane == 0) {
-            mbar_arrive_expect_tx(&sh->full[st], kBkTile);
-            tma_load_4d(smem + st * kBkTile, &tm_v, &sh->full[st], 0, row, 0, g);
-          }
-          next();
+          load(&tm_v, &tm_v16, row, g, keys, 0);
         }
       }
       if (ok && !sent) send_empty(cur);
@@ -610,11 +619,20 @@ size_t prefix_parts_bytes(int B, int n_groups, int sms) {
   return px_slots(B, n_groups, sms) * kPxRows * (kD + kPxSums) * 4 + up256((size_t)B * kKVHeads * sizeof(int4));
 }
 
-grok_status encode_pool(CUtensorMap* map, const grok_bf16* pool, int n_pages) {
+// A pool as (64 features, row, half of the features, KV head).
+static grok_status encode_pool(CUtensorMap* map, const grok_bf16* pool, int n_pages, bool last) {
   const uint64_t dims[4] = {kD / 2, uint64_t(n_pages) * GROK_PAGE_TOKENS, 2, kKVHeads};
   const uint64_t strides[3] = {uint64_t(kKVHeads) * kD * 2, kD, kD * 2};
-  const uint32_t box[4] = {kD / 2, kBlk, 2, 1};
+  const uint32_t box[4] = {kD / 2, last ? 16u : uint32_t(kBlk), last ? 1u : 2u, 1};
   return encode_tmap_bf16_4d(map, pool, dims, strides, box);
+}
+
+grok_status encode_pools(BlockArgs* a, const grok_bf16* k_pool, const grok_bf16* v_pool, int n_pages) {
+  grok_status st = encode_pool(&a->tm_k, k_pool, n_pages, false);
+  if (st == GROK_OK) st = encode_pool(&a->tm_v, v_pool, n_pages, false);
+  if (st == GROK_OK) st = encode_pool(&a->tm_k16, k_pool, n_pages, true);
+  if (st == GROK_OK) st = encode_pool(&a->tm_v16, v_pool, n_pages, true);
+  return st;
 }
 
 template <int kMode>
@@ -635,7 +653,7 @@ static grok_status bk_launch(const BlockArgs& a, const BkParams& p, int sms, int
   }
   const int grid = kMode == kPairs ? a.B * kKVHeads * ctas : kBkCtas * sms;
   e = launch(kMode == kOwn, kMode == kPairs ? ctas : 1, block_decode_kernel<kMode>, dim3(grid), kBkThreads, kSmem, a.stream,
-             a.tm_k, a.tm_v, p);
+             a.tm_k, a.tm_v, a.tm_k16, a.tm_v16, p);
   if (e != cudaSuccess) return fail(cuda_status(e), "block decode launch: %s", cudaGetErrorString(e));
   return check_launch("block decode");
 }
@@ -720,8 +738,7 @@ extern "C" grok_status grok_attn_decode_sparse_paged(const grok_bf16* q_rot, con
     return fail(GROK_ERR_INVALID_ARG, "%s: workspace of %zu bytes is smaller than the %zu needed", who, workspace_bytes,
                 need);
   BlockArgs a = {};
-  if ((st = encode_pool(&a.tm_k, k_pool, n_pages)) != GROK_OK) return st;
-  if ((st = encode_pool(&a.tm_v, v_pool, n_pages)) != GROK_OK) return st;
+  if ((st = encode_pools(&a, k_pool, v_pool, n_pages)) != GROK_OK) return st;
   a.q_rot = q_rot;
   a.pm = PageMap{block_table, max_pages, n_pages};
   a.kv_len = kv_len;

@@ -68,7 +68,7 @@ struct PrefixParts {
 
 struct BlockArgs {
   const grok_bf16* q_rot;
-  CUtensorMap tm_k, tm_v;  // of the pools (encode_pool)
+  CUtensorMap tm_k, tm_v, tm_k16, tm_v16;  // of the pools (encode_pools)
   PageMap pm;
   const int32_t* kv_len;
   int B;
@@ -109,9 +109,9 @@ cudaError_t launch(bool beside, int cluster, void (*kernel)(Args...), dim3 grid,
   return cudaLaunchKernelEx(&cfg, kernel, std::forward<Given>(args)...);
 }
 
-// Tensor map of a pool as (64 features, row, half of the features, KV head): one copy brings the 64 rows of a block of
-// one head, as two tiles of [64 rows][64 bf16].
-grok_status encode_pool(CUtensorMap* map, const grok_bf16* pool, int n_pages);
+// The tensor maps of the pools. One copy of tm_k or tm_v brings the 64 rows of a block of one head, as two tiles of [64
+// rows][64 bf16], one of tm_k16 or tm_v16 16 rows of half of the features.
+grok_status encode_pools(BlockArgs* a, const grok_bf16* k_pool, const grok_bf16* v_pool, int n_pages);
 
 grok_status page_args(int n_pages, int max_pages, int B, const char* who);
 

@@ -494,8 +494,7 @@ extern "C" grok_status grok_attn_decode_shared_paged(const grok_bf16* q_rot, con
     attr_set[dev] = true;
   }
   BlockArgs a = {};
-  if ((st = encode_pool(&a.tm_k, k_pool, n_pages)) != GROK_OK) return st;
-  if ((st = encode_pool(&a.tm_v, v_pool, n_pages)) != GROK_OK) return st;
+  if ((st = encode_pools(&a, k_pool, v_pool, n_pages)) != GROK_OK) return st;
   char* ws = static_cast<char*>(workspace);
   const PrefixParts prefix = prefix_parts(ws + blocks, B, n_groups, sms);
   PxParams p;
