@@ -244,7 +244,8 @@ __global__ void __launch_bounds__(kMode != kOwn ? kBkThreads : 576, kMode != kOw
         }
         next();
       };
-      for (int base = lo; base < hi && ok; base += 32) {
+      // (The lookups go on after a wait that gave up: every pair's entry is written, and the join reads in bounds.)
+      for (int base = lo; base < hi; base += 32) {
         const int cnt = min(32, hi - base), idx = base + lane;
         int my_pair = 0, my_row = -1, my_keys = 0;  // (row of the pools; -1: no block here)
         if (lane < cnt) {

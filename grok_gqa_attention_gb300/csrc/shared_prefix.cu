@@ -28,6 +28,7 @@
 namespace grok {
 
 constexpr int kPxTeams = kPxSums;           // of four softmax warps, a key tile each in turn
+constexpr int kPxEach = kD / kPxTeams;      // features that a team moves of Q and O
 constexpr int kPxThreads = 32 * (3 + 4 * kPxTeams);
 // Registers: the launch bound is above the launch, for at most 80 a thread, which leaves room beside this CTA for one of
 // the kernel over the sequences' own rows.
@@ -357,16 +358,17 @@ __global__ void __launch_bounds__(kPxBound, 1)
       // ------------------------------------------------------------ softmax of the key tiles t = team (mod 4), epilogue
       const int team = (warp - 2) >> 2, quad = warp & 3, r = quad * 32 + lane;
       const uint32_t trow = tmem + (uint32_t(quad * 32) << 16);
-      // Q of a run into TMEM: this thread's row, features 32 team .. 32 team + 31 (zeros for rows without a query).
+      // Q of a run into TMEM: this thread's row, a team's share of the features (zeros for rows without a query).
       auto load_q = [&](const PxRun& run) {
         if (quad * 32 < run.seqs * kGroup) {
           const bool mine = r < run.seqs * kGroup;
-          const uint4* src = p.q + ((size_t)(run.seq0 + r / kGroup) * kQHeads + run.g * kGroup + r % kGroup) * (kD / 8) + team * 4;
+          const uint4* src = p.q + ((size_t)(run.seq0 + r / kGroup) * kQHeads + run.g * kGroup + r % kGroup) * (kD / 8) +
+                             team * (kPxEach / 8);
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
+          for (int c = 0; c < kPxEach / 16; ++c) {
             const uint4 z = make_uint4(0, 0, 0, 0), x = mine ? src[2 * c] : z, y = mine ? src[2 * c + 1] : z;
             const uint32_t w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
-            tmem_st8(trow + kPxQ + team * 16 + c * 8, w);
+            tmem_st8(trow + kPxQ + team * (kPxEach / 2) + c * 8, w);
           }
           tmem_wait_st();
         }
@@ -415,11 +417,11 @@ __global__ void __launch_bounds__(kPxBound, 1)
         ++runs;
         tc_fence_after();
         if (live) {
-          float4* po = p.parts.o + (slot * (kD / 4) + team * 8) * kPxRows + r;
+          float4* po = p.parts.o + (slot * (kD / 4) + team * (kPxEach / 4)) * kPxRows + r;
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
+          for (int c = 0; c < kPxEach / 16; ++c) {
             uint32_t o[16];
-            tmem_ld16(trow + kPxO + team * 32 + c * 16, o);
+            tmem_ld16(trow + kPxO + team * kPxEach + c * 16, o);
             if (r < rows)
 #pragma unroll
               for (int q = 0; q < 4; ++q)

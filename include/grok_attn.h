@@ -588,8 +588,9 @@ grok_status grok_qkv_rope_append_paged(const grok_bf16* x, const grok_bf16* w, c
  *   group_start [n_groups + 1], shared_pages [n_groups] int32 (device), 1 <= n_groups <=
  *   256. Sequences in no group are decoded by themselves. Where group_start is not
  *   ascending within [0, B], or a shared_pages[i] lies outside [0, max_pages],
- *   GROK_DEV_BAD_GROUP is set and every sequence is decoded by itself. Sequences of a group
- *   whose tables differ in those entries set it too; their outputs are meaningless.
+ *   GROK_DEV_BAD_GROUP is set and every sequence is decoded by itself. A group's first
+ *   sequence's entries are read, whatever its kv_len; sequences of the group whose entries
+ *   are others set the bit too, and their outputs are meaningless.
  *   kv_len[b] outside [1, max_pages * 128], or below the group's shared rows, sets
  *   GROK_DEV_BAD_KV_LEN, and the sequence's outputs are left as they were. (It may equal
  *   them: the sequence has no rows of its own then.)
@@ -600,8 +601,9 @@ grok_status grok_qkv_rope_append_paged(const grok_bf16* x, const grok_bf16* w, c
  * decide: the same call gives the same bits, and a sequence in another batch may
  * differ in the last place. Weights keep 2^-16 relative in the decode over blocks; over a
  * shared prefix they carry the special-function unit's tanh, 4e-4 relative at most.
- * Calls that overlap on the GPU need separate workspaces; nothing is kept in one.
- * Bad table entries: GROK_DEV_BAD_PAGE, page 0 in their place, as above.
+ * Calls that overlap on the GPU need separate workspaces; nothing is kept in one. out may
+ * be q_rot. Bad table entries: GROK_DEV_BAD_PAGE, page 0 in their place, as above. Where
+ * GROK_DEV_TIMEOUT is set the outputs are undefined.
  */
 grok_status grok_kv_bounds_paged(const grok_bf16* k_pool, int n_pages, const int32_t* block_table, int max_pages,
                                  const int32_t* start_pos, const int32_t* valid_len, int B, int T, int8_t* codes,
