@@ -123,6 +123,13 @@ __global__ void __launch_bounds__(kMode != kOwn ? kBkThreads : 576, kMode != kOw
     prefetch_tmap(&tm_k);
     prefetch_tmap(&tm_v);
   }
+  // The lists and the tables come closer while the plan is made, a line a thread of the grid.
+  {
+    const size_t line = (size_t)blockIdx.x * kBkThreads + tid, lines = (size_t)p.B * p.pm.max_pages / 32;
+    if (line < lines) asm volatile("prefetch.global.L2 [%0];" ::"l"(p.pm.table + line * 32));
+    if (kList && line < (size_t)p.B * kKVHeads * p.budget / 32)
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(p.sel + line * 32));
+  }
   const int cta = blockIdx.x;
   int lo, hi, share_of;                    // this CTA's blocks; blocks per CTA
   int pair0 = 0, len0 = 0, n0 = 0, rank = 0, ctas = 1;  // kPairs: the pair, its sequence's rows, its blocks, the CTA's place
