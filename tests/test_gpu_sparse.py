@@ -667,3 +667,54 @@ def test_short_workspaces_and_wrong_shapes_are_refused():
     with pytest.raises(TypeError):
         G.select_blocks_paged(q, *G.alloc_kv_bounds(k.shape[0], DEV), table, ints([200]), 0, 0,
                               torch.zeros(1, 8, 4, device=DEV, dtype=torch.float64), sel)
+
+
+@pytest.mark.parametrize("given", [False, True])
+def test_both_ways_through_the_binding(monkeypatch, given):
+    """The checks in Python, which the extension falls back on, lead to the same calls; with and without a stream."""
+    from grok_gqa_attention_gb300 import sparse as binding
+
+    class Back:  # (an extension that hands everything back)
+        def __getattr__(self, name):
+            return lambda *a: None
+
+    paged, starts = grouped([4], [2], lambda i: 90 * i, seed=31)
+    q, sel = queries(4, 50).to(DEV), ints(lists(paged.lens, 3, seed=11))
+    k, v, table = paged.dev()
+    k.nan_to_num_(0.5)
+    lens, zero = ints(paged.lens), ints([0] * 4)
+    results = []
+    for through in (None, Back()):
+        if through is not None:
+            monkeypatch.setattr(binding, "_checked", through)
+        stream = torch.cuda.Stream() if given else None
+        codes, scale = G.alloc_kv_bounds(k.shape[0], DEV)
+        score, chosen = torch.zeros(4, 8, 2 * paged.max_pages, device=DEV), torch.zeros_like(sel)
+        a, z, st = torch.zeros_like(q), torch.zeros_like(q), status()
+        torch.cuda.synchronize()
+        G.kv_bounds_paged(k, table, zero, lens, max(paged.lens), codes, scale, st, stream)
+        G.select_blocks_paged(q, codes, scale, table, lens, 1, 1, score, chosen, st, stream)
+        G.decode_sparse_paged(q, k, v, table, lens, sel, G.alloc_decode_sparse_workspace(4, 3), a, st, stream)
+        G.decode_shared_paged(q, k, v, table, lens, ints(starts), ints([2]),
+                              G.alloc_decode_shared_workspace(4, paged.max_pages, 1), z, st, stream)
+        torch.cuda.synchronize()
+        assert int(st.item()) == 0
+        results.append((codes, scale, score, chosen, a, z))
+    for x, y in zip(*results):
+        assert torch.equal(x, y) and x.any()
+
+
+def test_tensors_that_are_not_contiguous_are_refused():
+    paged, q = Paged([200], seed=32), queries(1, 51).to(DEV)
+    k, v, table = paged.dev()
+    sel, ws = ints(lists([200], 2, seed=12)), G.alloc_decode_sparse_workspace(1, 2)
+    args = [q, k, v, table, ints([200]), sel, ws, torch.zeros_like(q)]
+    for i in (0, 1, 2, 7):
+        bad = list(args)
+        bad[i] = torch.cat((args[i], args[i]), -1)[..., :128]
+        with pytest.raises(ValueError, match="contiguous"):
+            G.decode_sparse_paged(*bad)
+    with pytest.raises(TypeError):
+        G.decode_sparse_paged(q.half(), *args[1:])
+    with pytest.raises(ValueError):
+        G.decode_sparse_paged(q.cpu(), *args[1:])

@@ -87,3 +87,33 @@ def test_binding_refuses_cpu_tensors():
     for call in calls:
         with pytest.raises(ValueError, match="CUDA tensor"):
             call()
+
+
+def test_the_extension_hands_back_what_it_does_not_take(lib):
+    """Whatever is not a call as it should be comes back as None, without an error left over and without references kept."""
+    import sys
+
+    from grok_gqa_attention_gb300 import sparse
+    m = sparse._binding()
+    q, pool = torch.zeros(2, 48, 128, dtype=torch.bfloat16), torch.zeros(4, 128, 8, 128, dtype=torch.bfloat16)
+    table, one, ws = torch.zeros(2, 2, dtype=torch.int32), torch.ones(2, dtype=torch.int32), torch.zeros(256, dtype=torch.uint8)
+    codes, scale = torch.zeros(4, 2, 8, 2, 128, dtype=torch.int8), torch.zeros(4, 2, 8)
+    sel, score = torch.zeros(2, 8, 2, dtype=torch.int32), torch.zeros(2, 8, 4)
+    calls = {"kv_bounds_paged": (pool, table, one, None, 1, codes, scale, None, None),
+             "select_blocks_paged": (q, codes, scale, table, one, 0, 0, score, sel, None, None),
+             "decode_sparse_paged": (q, pool, pool, table, one, sel, ws, q, None, None),
+             "decode_shared_paged": (q, pool, pool, table, one, one, one[:1], ws, q, None, None)}
+    odd = [None, 3, 2 ** 70, 1.5, "x", [], object(), torch.zeros(3), torch.zeros(2, 2, 2, 2, 2, 2), torch.Size([1]),
+           torch.zeros(2, 48, 128, dtype=torch.bfloat16, device="meta")]
+    kept = [q, pool, table, one, ws, codes, scale, sel, score] + odd[5:]
+    before = [sys.getrefcount(y) for y in kept]
+    for name, args in calls.items():
+        f = getattr(m, name)
+        assert f() is None and f(*args) is None and f(*args, None) is None  # (CPU tensors)
+        for i in range(len(args)):
+            for x in odd:
+                assert f(*args[:i], x, *args[i + 1:]) is None
+    del x  # (the loop's own reference)
+    assert [sys.getrefcount(y) for y in kept] == before
+    with pytest.raises(TypeError):
+        m.bind(1)
