@@ -262,7 +262,7 @@ __global__ void __launch_bounds__(kSlThreads, 2) select_kernel(const SlParams p)
     key[e] = 0u;  // (no score has this key)
     if (i >= p.sink && i < tail && i < n) {
       const uint32_t x = __float_as_uint(scores[i] + 0.f);
-      key[e] = x ^ (x >> 31 ? 0xFFFFFFFFu : 0x80000000u);
+      key[e] = max(1u, x ^ (x >> 31 ? 0xFFFFFFFFu : 0x80000000u));  // (a scale that nobody wrote may be any NaN)
       top = max(top, key[e]);
       low = min(low, key[e]);
     }

@@ -552,7 +552,9 @@ grok_status grok_qkv_rope_append_paged(const grok_bf16* x, const grok_bf16* w, c
  *   [-32, 16]; upper = ceil(max k / 2^e), lower = floor(min k / 2^e), kept within
  *   [-127, 127]; a NaN counts as the infinity of its sign. Other blocks' entries are left as
  *   they were. Nothing but the rows counts: rows may be dropped and written again, so
- *   long as the blocks that change are given to this call.
+ *   long as the blocks that change are given to this call. Sequences of a call that touch a
+ *   block in common (a shared prefix) have the same rows of it; calls that touch the same
+ *   block do not overlap on the GPU.
  *   start_pos [B], valid_len [B] int32 or NULL (= T). start_pos[b] < 0 or start_pos[b] + T >
  *   max_pages * 128 sets GROK_DEV_BAD_START, valid_len[b] outside [1, T] GROK_DEV_BAD_VALID:
  *   the sequence is skipped. A bad table entry sets GROK_DEV_BAD_PAGE, its block is skipped.
@@ -566,7 +568,8 @@ grok_status grok_qkv_rope_append_paged(const grok_bf16* x, const grok_bf16* w, c
  *   `sink` and the last `recent` blocks of the sequence, then those with the largest scores
  *   (the lower index first among equals), `budget` in all or as many as there are, in
  *   ascending order; -1 behind them. Scores behind the sequence's last block are left as they
- *   were. 1 <= budget <= 1024, sink, recent >= 0, sink + recent <= budget.
+ *   were. Where bounds were never written the choice means nothing, but sel holds blocks of
+ *   the sequence, each once. 1 <= budget <= 1024, sink, recent >= 0, sink + recent <= budget.
  *   q_rot [B,48,128]; kv_len [B] int32 in [1, max_pages * 128], else GROK_DEV_BAD_KV_LEN
  *   and the sequence's outputs are left as they were.
  *

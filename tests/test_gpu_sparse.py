@@ -718,3 +718,73 @@ def test_tensors_that_are_not_contiguous_are_refused():
         G.decode_sparse_paged(q.half(), *args[1:])
     with pytest.raises(ValueError):
         G.decode_sparse_paged(q.cpu(), *args[1:])
+
+
+@pytest.mark.parametrize("bits", [0xFFFFFFFF, 0x7FC00000, 0xFF800001, 0x7F800000, 0xFF800000, 0x80000000], ids=hex)
+def test_choice_over_bounds_that_nobody_wrote(bits):
+    """Whatever the scales hold, sel holds blocks of the sequence, ascending and each once, and its neighbours stay."""
+    lens, budget = [3000, 2000], 7
+    paged = Paged(lens, seed=33)
+    codes, scale, _ = run_bounds(paged, [0, 0], lens, 3000)
+    raw = scale.view(torch.int32)
+    raw.view(-1)[::3] = bits - (1 << 32) if bits >> 31 else bits
+    for every in (False, True):
+        if every:
+            raw[:] = raw.view(-1)[0]
+            codes[:] = -128
+        for sink, recent in ((0, 0), (1, 2), (3, 4)):
+            around = torch.full((4, 8, budget), 99, dtype=torch.int32, device=DEV)
+            score = torch.zeros(2, 8, 2 * paged.max_pages, device=DEV)
+            G.select_blocks_paged(queries(2, 7).to(DEV), codes, scale, torch.tensor(paged.table).to(DEV), ints(lens), sink,
+                                  recent, score, around[1:3])
+            got = around.cpu().numpy()
+            assert (got[[0, 3]] == 99).all()
+            for b, n in enumerate(lens):
+                for row in got[1 + b]:
+                    blocks = -(-n // 64)
+                    assert (np.diff(row) > 0).all() and row[0] >= 0 and row[-1] < blocks
+                    assert set(range(sink)) | set(range(blocks - recent, blocks)) <= set(row.tolist())
+
+
+def test_bounds_of_a_prefix_that_many_sequences_share():
+    """All of them may be given to one call, each with the prefix's rows."""
+    paged, _ = grouped([40], [3], lambda i: 1 + 11 * i, seed=34)
+    codes, scale, st = run_bounds(paged, [0] * 40, paged.lens, max(paged.lens))
+    assert st == 0
+    touched = {}
+    for b, n in enumerate(paged.lens):
+        for blk in range(-(-n // 64)):
+            touched[b, blk] = min(64, n - 64 * blk)
+    check_bounds(paged, codes, scale, touched)
+
+
+def test_integers_that_begin_anywhere():
+    """Tables, lengths, lists, scores and groups need no more than their type's alignment."""
+    paged, starts = grouped([3, 4], [2, 1], lambda i: 77 * i, seed=35)
+    q = queries(7, 52)
+    k, v, table = paged.dev()
+    k.nan_to_num_(0.5)
+    v.nan_to_num_(0.5)
+    codes, scale, _ = run_bounds(paged, [0] * 7, paged.lens, max(paged.lens))
+    sel = lists(paged.lens, 3, seed=13)
+
+    def off(t, by):
+        flat = torch.empty(t.numel() + by, dtype=t.dtype, device=DEV)
+        flat[by:] = t.reshape(-1)
+        return flat[by:].view(t.shape)
+
+    results = []
+    for by in (0, 1, 3):
+        tb, lens = off(table, by), off(ints(paged.lens), by)
+        score, chosen = off(torch.zeros(7, 8, 2 * paged.max_pages, device=DEV), by), off(ints(np.zeros((7, 8, 3))), by)
+        c, s = torch.zeros_like(codes), off(torch.zeros_like(scale), by)
+        a, z = torch.zeros_like(q, device=DEV), torch.zeros_like(q, device=DEV)
+        G.kv_bounds_paged(k, tb, off(ints([0] * 7), by), lens, max(paged.lens), c, s)
+        G.select_blocks_paged(q.to(DEV), c, s, tb, lens, 1, 1, score, chosen)
+        G.decode_sparse_paged(q.to(DEV), k, v, tb, lens, off(ints(sel), by), G.alloc_decode_sparse_workspace(7, 3), a)
+        G.decode_shared_paged(q.to(DEV), k, v, tb, lens, off(ints(starts), by), off(ints([2, 1]), by),
+                              G.alloc_decode_shared_workspace(7, paged.max_pages, 2), z)
+        results.append((c, s, score, chosen, a, z))
+    for other in results[1:]:
+        for x, y in zip(results[0], other):
+            assert torch.equal(x, y) and x.any()
