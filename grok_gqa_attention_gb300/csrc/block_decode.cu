@@ -688,11 +688,18 @@ grok_status block_decode_run(const BlockArgs& a, char* ws, const PrefixParts* pr
   p.status = a.status;
   p.out = a.out;
   if (a.sel && (long long)a.B * kKVHeads <= kBkCtas * sms) {
-    // One wave of clusters holds all pairs. The most blocks that an SM then has, against an equal share of all:
+    // One wave of clusters holds all pairs. That is faster than equal shares with a plan and a join
+    // - of short lists: where the most blocks that an SM has are few above an equal share of all (1 sequence: 16 blocks 6.9
+    //   us, 9.5 in equal shares; 256 blocks of 65536 rows 32 and 22);
+    // - where the clusters are CTAs enough to keep HBM busy and the lists probably full: the budget a quarter at most of the
+    //   blocks that a table holds (32 sequences: 32 of 256 blocks 47.8 us, 50.4 in equal shares; 20 of up to 16384 rows, 128 of
+    //   256 blocks, which the shorter ones do not have: 96 and 86).
     int ctas = 8;
     while (a.B * kKVHeads * ctas > kBkCtas * sms) ctas /= 2;
     const int most = (a.budget + ctas - 1) / ctas * (a.B * kKVHeads * ctas > sms ? 2 : 1);
-    if (most <= a.B * kKVHeads * a.budget / sms + kBkUneven) return bk_launch<kPairs>(a, p, sms, ctas);
+    if (most <= a.B * kKVHeads * a.budget / sms + kBkUneven ||
+        (a.B * kKVHeads * ctas >= sms * 3 / 4 && a.budget <= a.pm.max_pages * kBlkPerPage / 4))
+      return bk_launch<kPairs>(a, p, sms, ctas);
   }
   grok_status st = a.sel ? bk_launch<kLists>(a, p, sms, 1) : bk_launch<kOwn>(a, p, sms, 1);
   if (st != GROK_OK) return st;
