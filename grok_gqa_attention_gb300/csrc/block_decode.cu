@@ -40,7 +40,9 @@ constexpr int kBkQ = kGroup * kD * 2;        // a pair's queries
 constexpr int kBkPlan = 512;                 // entries of the table of block counts
 constexpr int kBkCtas = 2;                   // CTAs resident on an SM
 constexpr int kBkUneven = 5;                 // blocks an SM may have above its equal share to save the plan and the join
-constexpr int kBkFew = 8;                    // blocks per CTA up to which half of the CTAs take them (beside a prefix)
+// Beside the prefix kernel: blocks per CTA up to which half of the CTAs take them all; key tiles of the prefix in whose time a CTA
+// gets through a block; blocks in the time that a CTA behind the prefix takes to start.
+constexpr int kBkFew = 8, kBkBeside = 10, kBkStart = 6;
 
 template <int kRing>
 struct BkShared {
@@ -52,6 +54,7 @@ struct BkShared {
   int seq[kBkPlan];       // length | pages left out << 17, where an entry is a sequence
   GroupTable groups;
   int warp_sum[kBkWarps + 1];
+  int3 deal;              // CTAs of the first kind, blocks to each, blocks to each of the others
   int abort;
 };
 template <bool kList>
@@ -89,6 +92,30 @@ __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t x) {
 __device__ __forceinline__ int bk_blocks(const BkParams& p, int len, int share) {
   if (len < 1 || len > p.pm.max_pages * GROK_PAGE_TOKENS || len < share * GROK_PAGE_TOKENS) return -1;
   return min((len + kBlk - 1) / kBlk - share * kBlkPerPage, p.budget);
+}
+
+// How `total` blocks behind prefixes are dealt to the CTAs: (CTAs of the first kind, blocks to each, blocks to each of the others).
+// Beside the prefix kernel an SM has room for one CTA, which is slowed by it (its few warps wait for issue slots beside sixteen);
+// the second half of the CTAs starts behind the prefix. Little work is dealt to the first half (32 sequences behind 8192 rows, 5
+// blocks to a CTA: 30.6 us, 39 over all of them), of more work as much as lets both halves end together: 256 behind 16384 rows,
+// 20 blocks to a CTA of the first half and none to the others, 130.5 us (145 in equal shares); 128 behind 4096, 31 and 23, 75.8
+// (78.6). A function that is not inlined: with the same lines in the kernel the code of its loop comes out slower (140 and 77).
+__device__ __noinline__ int3 bk_deal(int total, int ctas, const GroupTable* groups, int n_groups) {
+  int early = ctas, late = 0;
+  if (total <= kBkFew * ctas) {
+    early /= kBkCtas;
+  } else {
+    int tiles = 0;  // key tiles of the prefix kernel
+    for (int i = threadIdx.x % 32; i < n_groups; i += 32)
+      tiles += (groups->start[i + 1] - groups->start[i] + kPxSeqs - 1) / kPxSeqs * groups->pages[i] * (kBlkPerPage * kKVHeads);
+    tiles = __reduce_add_sync(0xffffffffu, tiles);
+    if (tiles) {
+      early /= kBkCtas;
+      const int both = (total + early - 1) / early;  // blocks of a CTA of each half
+      late = max(0, both - tiles / early / kBkBeside - kBkStart) / 2;
+    }
+  }
+  return make_int3(early, max(1, (total - early * late + early - 1) / early), late);
 }
 
 // kOwn: the rows behind prefixes. (Registers: 112 a thread at most, for the same reason as in the prefix kernel.)
@@ -131,7 +158,7 @@ __global__ void __launch_bounds__(kMode != kOwn ? kBkThreads : 576, kMode != kOw
       asm volatile("prefetch.global.L2 [%0];" ::"l"(p.sel + line * 32));
   }
   const int cta = blockIdx.x;
-  int lo, hi, share_of;                    // this CTA's blocks; blocks per CTA
+  int lo, hi, share_of = 1;                    // this CTA's blocks; blocks per CTA
   int pair0 = 0, len0 = 0, n0 = 0, rank = 0, ctas = 1;  // kPairs: the pair, its sequence's rows, its blocks, the CTA's place
   int step = 1, entries = 0, n_groups = 0;
   if (kPair) {
@@ -207,16 +234,21 @@ __global__ void __launch_bounds__(kMode != kOwn ? kBkThreads : 576, kMode != kOw
     }
     __syncthreads();
     const int total = kKVHeads * sh->cum[entries];
-    // Beside the prefix kernel an SM has room for one CTA: little work is dealt to the first half of them (32 sequences behind
-    // 8192 rows, 5 blocks to a CTA: 30.6 us, 39 over all of them, of which the second half starts behind the prefix).
-    const int among = !kList && total <= kBkFew * int(gridDim.x) ? int(gridDim.x) / kBkCtas : int(gridDim.x);
-    share_of = max(1, (total + among - 1) / among);
-    lo = int(min((long long)cta * share_of, (long long)total));
-    hi = min(lo + share_of, total);
+    if (kList) {
+      share_of = max(1, (total + int(gridDim.x) - 1) / int(gridDim.x));
+      lo = int(min((long long)cta * share_of, (long long)total));
+      hi = min(lo + share_of, total);
+    } else {
+      const int3 d = bk_deal(total, int(gridDim.x), &sh->groups, n_groups);
+      if (tid == kBkWarps * 32) sh->deal = d;
+      lo = min(cta < d.x ? cta * d.y : d.x * d.y + (cta - d.x) * d.z, total);
+      hi = min(lo + (cta < d.x ? d.y : d.z), total);
+    }
   }
   if (lo < hi) {
     if (warp == kBkWarps) {
       // ------------------------------------------------------------ producer
+      __syncwarp();
       int st = 0, turn = 1, loads = 0;  // the ring's next place, the parity that frees it, places taken so far
       int cur = -1;        // the pair of the last block looked at
       bool sent = true;    // a token of that pair is out
@@ -275,7 +307,15 @@ __global__ void __launch_bounds__(kMode != kOwn ? kBkThreads : 576, kMode != kOw
             my_pair = b * kKVHeads + rest / n;
             k = rest % n;
             if (k == 0) {  // the pair's parts: one of each CTA from this one on that takes some of its blocks
-              const int last = (idx + n - 1) / share_of;
+              int last = 0, end = idx + n - 1, each = share_of;
+              if (!kList && end >= sh->deal.x * sh->deal.y) {
+                last = sh->deal.x;
+                end -= last * sh->deal.y;
+                each = sh->deal.z;
+              } else if (!kList) {
+                each = sh->deal.y;
+              }
+              last += end / each;
               p.parts.pair[my_pair] = make_int2(cta + my_pair, last - cta + 1);
             }
           }

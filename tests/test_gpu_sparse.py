@@ -788,3 +788,22 @@ def test_integers_that_begin_anywhere():
     for other in results[1:]:
         for x, y in zip(results[0], other):
             assert torch.equal(x, y) and x.any()
+
+
+@pytest.mark.parametrize("sizes,pages,mine", [
+    ([40], [1], lambda i: 500 + 11 * i), ([3, 30, 7], [2, 30, 0], lambda i: 1100 - 17 * i), ([200], [110], lambda i: 65 + i % 64),
+    ([2] * 30, [9] * 30, lambda i: 900 if i % 2 else 1)], ids=["short prefix", "unequal", "long prefix", "many groups"])
+def test_many_own_rows_behind_prefixes(sizes, pages, mine):
+    """More blocks than half of the CTAs take at once: the halves get unequal shares."""
+    paged, starts = grouped(sizes, pages, mine, seed=36)
+    B = len(paged.lens)
+    q = queries(B, 53)
+    out, st = run_shared(paged, q, starts, pages)
+    assert st == 0
+    some = sorted({0, 1, B // 3, B // 2, B // 2 + 1, B - 2, B - 1})
+    want, spread = expected(paged, q, lambda b, g: np.arange(paged.lens[b]) if b in some else [])
+    check(out[some], want[some], spread[some], 2.0 ** -10)
+    # the others, against every sequence by itself: two roundings of outputs below 1 or so, weights off by 2^-10
+    single, st = run_shared(paged, q, [0, B], [0])
+    assert st == 0
+    check(out, single.float().cpu().double().numpy(), np.full((B, 48, 128), 1.0), 2.0 ** -8)
