@@ -19,11 +19,12 @@
 // all are) and write one part; a second kernel, launched as a dependent, adds a pair's
 // parts in their order.
 //
-// Measured (graph replays): 8 sequences x 128 blocks per head (268 MB) 50.2 us, 5.3
-// TB/s, 0.79 of the copy rate: 2 us launch, 4 us to the first keys (lengths, list, table,
-// keys: four round trips), 40 us at 6.6 TB/s, 3 us the join. A second wave of small
-// shares, which evens out the SMs in the 8-bit decode, starts too late to pay here (54
-// us). One sequence, 16 blocks: 6.9 us in clusters (kPairs), 9.5 with a plan and a join.
+// Measured (graph replays): 8 sequences x 128 blocks per head (268 MB) in equal shares
+// 50.2 us: 2 us launch, 4 us to the first keys (lengths, list, table, keys: four round
+// trips), 40 us at 6.6 TB/s, 3 us the join. A second wave of small shares, which evens out
+// the SMs in the 8-bit decode, starts too late to pay here (54 us). In clusters of CTAs,
+// one to a pair (kPairs), which need neither plan nor join, 48.3 us, 5.6 TB/s, 0.82 of the
+// copy rate; one sequence, 16 blocks: 6.9 us, 9.5 with a plan and a join.
 #include <algorithm>
 
 #include "block_decode.cuh"
@@ -730,7 +731,7 @@ grok_status block_decode_run(const BlockArgs& a, char* ws, const PrefixParts* pr
   if (a.sel && (long long)a.B * kKVHeads <= kBkCtas * sms) {
     // One wave of clusters holds all pairs. That is faster than equal shares with a plan and a join
     // - of short lists: where the most blocks that an SM has are few above an equal share of all (1 sequence: 16 blocks 6.9
-    //   us, 9.5 in equal shares; 256 blocks of 65536 rows 32 and 22);
+    //   us, 9.5 in equal shares; 512 blocks 44.8 and 32.1);
     // - where the clusters are CTAs enough to keep HBM busy and the lists probably full: the budget a quarter at most of the
     //   blocks that a table holds (32 sequences: 32 of 256 blocks 47.8 us, 50.4 in equal shares; 20 of up to 16384 rows, 128 of
     //   256 blocks, which the shorter ones do not have: 96 and 86).
