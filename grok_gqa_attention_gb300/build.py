@@ -1,5 +1,6 @@
 """Build libgrok_attn.so (the C-ABI library) in-tree for sm_103a with nvcc, and _binding.so, the Python binding's
-checks of the calls over parts of a cache, with the host compiler.
+checks of the calls over parts of a cache, with the host compiler. The extension needs Python's C headers; where there
+are none the library is built without it, and sparse.py makes the checks.
 
 Each .cu file is compiled in parallel, then linked into one shared library
 next to this file. The CUDA runtime is linked statically; the driver's
@@ -46,13 +47,20 @@ def _inputs() -> list[str]:
     return files
 
 
+def _python_headers() -> str | None:
+    """The folder of Python.h, if it is installed."""
+    path = sysconfig.get_paths()["include"]
+    return path if os.path.exists(os.path.join(path, "Python.h")) else None
+
+
 def up_to_date() -> bool:
-    if not (os.path.exists(LIB) and os.path.exists(BINDING) and os.path.exists(_stamp_path())):
+    made = [LIB] + ([BINDING] if _python_headers() else [])
+    if not all(os.path.exists(p) for p in [*made, _stamp_path()]):
         return False
     with open(_stamp_path()) as f:
         if f.read().strip() != platform.machine():
             return False
-    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
+    t = min(os.path.getmtime(p) for p in made)
     return all(os.path.getmtime(p) <= t for p in _inputs())
 
 
@@ -73,7 +81,12 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
         return obj, r.stdout + r.stderr
 
     def compile_binding() -> None:
-        cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-I", INCLUDE, "-I", sysconfig.get_paths()["include"],
+        headers = _python_headers()
+        if headers is None:  # (an older one may not fit the library any more)
+            if os.path.exists(BINDING):
+                os.remove(BINDING)
+            return
+        cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-I", INCLUDE, "-I", headers,
                os.path.join(CSRC, "binding.cpp"), "-o", BINDING + ".tmp"]
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
@@ -93,7 +106,8 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
-    os.utime(BINDING)  # (as new as the library: what is built together is up to date together)
+    if os.path.exists(BINDING):
+        os.utime(BINDING)  # (as new as the library: what is built together is up to date together)
     with open(_stamp_path(), "w") as f:
         f.write(platform.machine())
     with open(os.path.join(BUILD, "ptxas.log"), "w") as f:
