@@ -1,5 +1,5 @@
-"""Build libgrok_attn.so (the C-ABI library) in-tree for sm_103a with nvcc, and _binding.so, the Python binding's
-checks of the calls over parts of a cache, with the host compiler. The extension needs Python's C headers; where there
+"""Build libgrok_attn.so (the C-ABI library) in-tree for sm_103a with nvcc, and _binding (a Python extension), the
+binding's checks of the calls over parts of a cache, with the host compiler. The extension needs Python's C headers; where there
 are none the library is built without it, and sparse.py makes the checks.
 
 Each .cu file is compiled in parallel, then linked into one shared library
@@ -21,7 +21,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build", platform.machine())
 LIB = os.path.join(PKG, "libgrok_attn.so")
-BINDING = os.path.join(PKG, "_binding.so")
+BINDING = os.path.join(PKG, "_binding" + sysconfig.get_config_var("EXT_SUFFIX"))  # (of this interpreter alone)
 SOURCES = ["abi.cu", "rope_append.cu", "prefill.cu", "decode.cu", "selftest.cu", "pipe.cu", "qkv.cu", "slots.cu", "int8_small.cu",
            "kv8_append.cu", "kv8_decode.cu", "kv8_prefill.cu", "kv8_evict.cu",
            "kv_bounds.cu", "block_decode.cu", "shared_prefix.cu"]

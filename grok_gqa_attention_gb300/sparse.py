@@ -3,8 +3,8 @@
 Bounds of the keys of each 64-token block, the choice of the blocks that a query reads, attention over a list of
 blocks, and attention for a batch whose sequences share prefixes (see grok_kv_bounds_paged in include/grok_attn.h).
 Every call runs on the device of its pools, on that device's current stream unless one is given. A call's arguments are
-checked by _binding.so where all is as it should be, and by the functions here otherwise, which say what is not. (Where
-the library was built without Python's headers there is no _binding.so: a call then takes about 3 us more.)
+checked by the extension _binding where all is as it should be, and by the functions here otherwise, which say what is not. (Where
+the library was built without Python's headers there is none: a call then takes about 3 us more.)
 """
 from __future__ import annotations
 
@@ -15,6 +15,7 @@ import os
 import torch
 
 from . import HEAD_DIM, N_KV_HEADS, N_Q_HEADS, PAGE_TOKENS, SPARSE_BLOCK, _check, load
+from .build import BINDING
 from .kv8 import _call, _maybe, _need, _raw_device, _raw_stream
 
 _BF16, _F32, _I32, _I8, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.int8, torch.uint8
@@ -32,15 +33,14 @@ _checked = None
 
 
 def _binding():
-    """The checks in _binding.so, with the library's functions."""
+    """The extension's checks, with the library's functions."""
     global _checked
     if _checked is None:
         lib = load()
-        path = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_binding.so")
-        if not os.path.exists(path):
+        if not os.path.exists(BINDING):
             _checked = _Unchecked()
             return _checked
-        spec = importlib.util.spec_from_file_location("_binding", path)
+        spec = importlib.util.spec_from_file_location("_binding", BINDING)
         module = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(module)
         calls = (lib.grok_kv_bounds_paged, lib.grok_attn_select_paged, lib.grok_attn_decode_sparse_paged,

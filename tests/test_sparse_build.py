@@ -83,3 +83,23 @@ def test_calls_without_the_extension(monkeypatch, tmp_path):
                  lambda: G.decode_shared_paged(q, pool, pool, table, one, one, one[:1], ws, q)):
         with pytest.raises(ValueError, match="CUDA tensor"):
             call()
+
+
+def test_extension_is_of_this_interpreter(monkeypatch, tmp_path, tree):
+    """It goes by the name that this Python gives its extensions: one that another Python built is neither loaded nor up to
+    date."""
+    from grok_gqa_attention_gb300 import sparse
+    suffix = sysconfig.get_config_var("EXT_SUFFIX")
+    assert os.path.basename(build.BINDING) == "_binding" + suffix
+    (tmp_path / "include").mkdir()
+    (tmp_path / "include" / "Python.h").write_text("")
+    _headers(monkeypatch, tmp_path / "include")
+    build.build(force=True)
+    assert build.up_to_date()
+    for other in ("_binding.so", "_binding.cpython-39-x86_64-linux-gnu.so"):
+        os.replace(build.BINDING, tmp_path / other)
+        assert not build.up_to_date()
+        os.replace(tmp_path / other, build.BINDING)
+    monkeypatch.undo()
+    build.build()
+    assert sparse._binding().__file__ == build.BINDING
