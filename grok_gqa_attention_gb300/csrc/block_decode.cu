@@ -20,11 +20,11 @@
 // parts in their order.
 //
 // Measured (graph replays): 8 sequences x 128 blocks per head (268 MB) in equal shares
-// 50.2 us: 2 us launch, 4 us to the first keys (lengths, list, table, keys: four round
-// trips), 40 us at 6.6 TB/s, 3 us the join. A second wave of small shares, which evens out
-// the SMs in the 8-bit decode, starts too late to pay here (54 us). In clusters of CTAs,
-// one to a pair (kPairs), which need neither plan nor join, 48.3 us, 5.6 TB/s, 0.82 of the
-// copy rate; one sequence, 16 blocks: 6.9 us, 9.5 with a plan and a join.
+// 49.5 us, 5.4 TB/s, 0.80 of the copy rate: 2 us launch, 4 us to the first keys (lengths, list,
+// table, keys: four round trips), 40 us at 6.6 TB/s, 3 us the join. A second wave of small shares,
+// which evens out the SMs in the 8-bit decode, starts too late to pay here (54 us). Short lists of
+// few pairs go to clusters of CTAs, one to a pair (kPairs), which need neither plan nor join:
+// one sequence, 16 blocks, 6.8 us, 9.2 with a plan and a join.
 #include <algorithm>
 
 #include "block_decode.cuh"
@@ -40,7 +40,7 @@ __host__ __device__ constexpr int bk_ring(bool list) { return list ? 5 : 4; }
 constexpr int kBkQ = kGroup * kD * 2;        // a pair's queries
 constexpr int kBkPlan = 512;                 // entries of the table of block counts
 constexpr int kBkCtas = 2;                   // CTAs resident on an SM
-constexpr int kBkUneven = 5;                 // blocks an SM may have above its equal share to save the plan and the join
+constexpr int kBkPairMost = 8;               // blocks of a list that a CTA of its pair's cluster may get
 // Beside the prefix kernel: blocks per CTA up to which half of the CTAs take them all; key tiles of the prefix in whose time a CTA
 // gets through a block; blocks in the time that a CTA behind the prefix takes to start.
 constexpr int kBkFew = 8, kBkBeside = 10, kBkStart = 6;
@@ -120,7 +120,7 @@ __device__ __noinline__ int3 bk_deal(int total, int ctas, const GroupTable* grou
 }
 
 // kOwn: the rows behind prefixes. (Registers: 112 a thread at most, for the same reason as in the prefix kernel.)
-// kLists: lists of blocks, dealt out to the CTAs in equal shares. kPairs: the same for few pairs: a cluster of CTAs takes a
+// kLists: lists of blocks, dealt out to the CTAs in equal shares. kPairs: the same for short lists of few pairs: a cluster of CTAs takes a
 // pair's list and joins its parts itself, so that there is neither a plan nor a second kernel.
 enum BkMode { kOwn, kLists, kPairs };
 template <int kMode>
@@ -729,17 +729,15 @@ grok_status block_decode_run(const BlockArgs& a, char* ws, const PrefixParts* pr
   p.status = a.status;
   p.out = a.out;
   if (a.sel && (long long)a.B * kKVHeads <= kBkCtas * sms) {
-    // One wave of clusters holds all pairs. That is faster than equal shares with a plan and a join
-    // - of short lists: where the most blocks that an SM has are few above an equal share of all (1 sequence: 16 blocks 6.9
-    //   us, 9.5 in equal shares; 512 blocks 44.8 and 32.1);
-    // - where the clusters are CTAs enough to keep HBM busy and the lists probably full: the budget a quarter at most of the
-    //   blocks that a table holds (32 sequences: 32 of 256 blocks 47.8 us, 50.4 in equal shares; 20 of up to 16384 rows, 128 of
-    //   256 blocks, which the shorter ones do not have: 96 and 86).
+    // One wave of clusters holds all pairs. That saves the plan and the join, but a pair's blocks stay with its cluster,
+    // whatever the other sequences' lengths, which are not known here: clusters take the call where no CTA can get more
+    // than kBkPairMost blocks. Equal shares against clusters, us, lists all full, and one sequence's full beside others of
+    // two blocks: budget 16, 2 sequences, 2 blocks to a CTA, 10.0 and 7.8, 9.5 and 7.2; 32, 8 sequences, 8 blocks, 19.0 and
+    // 17.5, 10.7 and 11.4; 8, 32 sequences, 8 blocks, 19.2 and 16.9, 10.7 and 11.8. Beyond, the gain stays (32, 32
+    // sequences, 32 blocks: 49.4 and 44.9) and the loss grows (12.7 and 26.0).
     int ctas = 8;
     while (a.B * kKVHeads * ctas > kBkCtas * sms) ctas /= 2;
-    const int most = (a.budget + ctas - 1) / ctas * (a.B * kKVHeads * ctas > sms ? 2 : 1);
-    if (most <= a.B * kKVHeads * a.budget / sms + kBkUneven ||
-        (a.B * kKVHeads * ctas >= sms * 3 / 4 && a.budget <= a.pm.max_pages * kBlkPerPage / 4))
+    if ((a.budget + ctas - 1) / ctas <= kBkPairMost)
       return bk_launch<kPairs>(a, p, sms, ctas);
   }
   grok_status st = a.sel ? bk_launch<kLists>(a, p, sms, 1) : bk_launch<kOwn>(a, p, sms, 1);

@@ -600,9 +600,9 @@ grok_status grok_qkv_rope_append_paged(const grok_bf16* x, const grok_bf16* w, c
  *   q_rot, out [B,48,128]; workspace: device memory, 256-byte aligned, of at least
  *   grok_attn_decode_shared_workspace(B, max_pages, n_groups) bytes for the current device.
  *
- * Sums are split where the shares of the GPU's SMs end, which the lengths in the batch
- * decide: the same call gives the same bits, and a sequence in another batch may
- * differ in the last place. Weights keep 2^-16 relative in the decode over blocks; over a
+ * Sums are split where the shares of the GPU's SMs end, which B, the budget and the lengths
+ * in the batch decide: the same call gives the same bits, and a sequence in another batch may
+ * differ in the last place. (What else the block table has room for changes nothing.) Weights keep 2^-16 relative in the decode over blocks; over a
  * shared prefix they carry the special-function unit's tanh, 4e-4 relative at most.
  * Calls that overlap on the GPU need separate workspaces; nothing is kept in one. out may
  * be q_rot. Bad table entries: GROK_DEV_BAD_PAGE, page 0 in their place, as above. Where
