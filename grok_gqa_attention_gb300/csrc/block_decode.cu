@@ -100,18 +100,17 @@ __device__ __forceinline__ int bk_blocks(const BkParams& p, int len, int share) 
 // the second half of the CTAs starts behind the prefix. Little work is dealt to the first half (32 sequences behind 8192 rows, 5
 // blocks to a CTA: 30.6 us, 39 over all of them), of more work as much as lets both halves end together: 256 behind 16384 rows,
 // 20 blocks to a CTA of the first half and none to the others, 130.5 us (145 in equal shares); 128 behind 4096, 31 and 23, 75.8
-// (78.6). A function that is not inlined: with the same lines in the kernel the code of its loop comes out slower (140 and 77).
+// (78.6). (kBkBeside and kBkStart were measured on those two, whose query tiles are full.) Where no group shares a page the
+// prefix kernel has nothing to do, and all CTAs take equal shares (64 sequences of up to 300 rows: 19.9 us, 24.2 over half of
+// them). A function that is not inlined: with the same lines in the kernel the code of its loop comes out slower (140 and 77).
 __device__ __noinline__ int3 bk_deal(int total, int ctas, const GroupTable* groups, int n_groups) {
-  int early = ctas, late = 0;
-  if (total <= kBkFew * ctas) {
+  int early = ctas, late = 0, tiles = 0;  // (key tiles of the prefix kernel)
+  for (int i = threadIdx.x % 32; i < n_groups; i += 32)
+    tiles += (groups->start[i + 1] - groups->start[i] + kPxSeqs - 1) / kPxSeqs * groups->pages[i] * (kBlkPerPage * kKVHeads);
+  tiles = __reduce_add_sync(0xffffffffu, tiles);
+  if (tiles) {
     early /= kBkCtas;
-  } else {
-    int tiles = 0;  // key tiles of the prefix kernel
-    for (int i = threadIdx.x % 32; i < n_groups; i += 32)
-      tiles += (groups->start[i + 1] - groups->start[i] + kPxSeqs - 1) / kPxSeqs * groups->pages[i] * (kBlkPerPage * kKVHeads);
-    tiles = __reduce_add_sync(0xffffffffu, tiles);
-    if (tiles) {
-      early /= kBkCtas;
+    if (total > kBkFew * ctas) {
       const int both = (total + early - 1) / early;  // blocks of a CTA of each half
       late = max(0, both - tiles / early / kBkBeside - kBkStart) / 2;
     }
