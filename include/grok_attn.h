@@ -602,8 +602,9 @@ grok_status grok_qkv_rope_append_paged(const grok_bf16* x, const grok_bf16* w, c
  *
  * Sums are split where the shares of the GPU's SMs end, which B, the budget and the lengths
  * in the batch decide: the same call gives the same bits, and a sequence in another batch may
- * differ in the last place. (What else the block table has room for changes nothing.) Weights keep 2^-16 relative in the decode over blocks; over a
- * shared prefix they carry the special-function unit's tanh, 4e-4 relative at most.
+ * differ in the last place. (What else the block table has room for changes nothing.) Weights are off by 3e-5 relative at most in the decode over
+ * blocks (two bf16 halves, 2^-16, and fp32 exponents); over a shared prefix they carry the
+ * special-function unit's tanh, 4e-4 relative at most, where grok_attn_decode_paged keeps 3e-5.
  * Calls that overlap on the GPU need separate workspaces; nothing is kept in one. out may
  * be q_rot. Bad table entries: GROK_DEV_BAD_PAGE, page 0 in their place, as above. Where
  * GROK_DEV_TIMEOUT is set the outputs are undefined.
