@@ -596,7 +596,8 @@ grok_status grok_qkv_rope_append_paged(const grok_bf16* x, const grok_bf16* w, c
  *   are others set the bit too, and their outputs are meaningless.
  *   kv_len[b] outside [1, max_pages * 128], or below the group's shared rows, sets
  *   GROK_DEV_BAD_KV_LEN, and the sequence's outputs are left as they were. (It may equal
- *   them: the sequence has no rows of its own then.)
+ *   them: the sequence has no rows of its own then.) A group of one sequence shares nothing:
+ *   the sequence is decoded by itself, also where its kv_len is below shared_pages[i] * 128.
  *   q_rot, out [B,48,128]; workspace: device memory, 256-byte aligned, of at least
  *   grok_attn_decode_shared_workspace(B, max_pages, n_groups) bytes for the current device.
  *

@@ -24,3 +24,19 @@ def test_nothing_is_shared(sizes, pages, rows, usable):
     some = sorted({0, 1, B // 2, B - 2, B - 1} & set(range(B)))
     want, spread = expected(paged, q, lambda b, g: np.arange(paged.lens[b]) if b in some else [])
     check(out[some], want[some], spread[some], 2.0 ** -12)
+
+
+def test_a_group_of_one_shares_nothing():
+    """Its sequence may be shorter than the pages given for the group; a sequence of a larger group may not."""
+    lens = [200, 300, 100, 300, 1]
+    paged, starts = grouped([1, 3, 1], [0, 0, 0], lambda i: lens[i], seed=42)
+    q = queries(5, 71)
+    out, st = run_shared(paged, q, starts, [3, 0, 2])
+    assert st == 0
+    check(out, *expected(paged, q, lambda b, g: np.arange(lens[b])), 2.0 ** -12)
+    paged, starts = grouped([1, 3], [0, 2], lambda i: [200, 40, 50, 60][i], seed=43)
+    q = queries(4, 72)
+    out, st = run_shared(paged, q, starts, [3, 2], lens=[200, 296, 255, 316])
+    assert st == G.DEV_BAD_KV_LEN and (out[2] == 5).all()
+    want, spread = expected(paged, q, lambda b, g: np.arange(paged.lens[b]))
+    check(out[[0, 1, 3]], want[[0, 1, 3]], spread[[0, 1, 3]], 2.0 ** -10)
