@@ -20,7 +20,7 @@
 // parts in their order.
 //
 // Measured (graph replays): 8 sequences x 128 blocks per head (268 MB) in equal shares
-// 49.5 us, 5.4 TB/s, 0.80 of the copy rate: 2 us launch, 4 us to the first keys (lengths, list,
+// 50.4 us, 5.3 TB/s, 0.79 of the copy rate: 2 us launch, 4 us to the first keys (lengths, list,
 // table, keys: four round trips), 40 us at 6.6 TB/s, 3 us the join. A second wave of small shares,
 // which evens out the SMs in the 8-bit decode, starts too late to pay here (54 us). Short lists of
 // few pairs go to clusters of CTAs, one to a pair (kPairs), which need neither plan nor join:
@@ -99,7 +99,7 @@ __device__ __forceinline__ int bk_blocks(const BkParams& p, int len, int share) 
 // Beside the prefix kernel an SM has room for one CTA, which is slowed by it (its few warps wait for issue slots beside sixteen);
 // the second half of the CTAs starts behind the prefix. Little work is dealt to the first half (32 sequences behind 8192 rows, 5
 // blocks to a CTA: 30.6 us, 39 over all of them), of more work as much as lets both halves end together: 256 behind 16384 rows,
-// 20 blocks to a CTA of the first half and none to the others, 130.5 us (145 in equal shares); 128 behind 4096, 31 and 23, 75.8
+// 20 blocks to a CTA of the first half and none to the others, 130 us (145 in equal shares); 128 behind 4096, 31 and 23, 75.3
 // (78.6). (kBkBeside and kBkStart were measured on those two, whose query tiles are full.) Where no group shares a page the
 // prefix kernel has nothing to do, and all CTAs take equal shares (64 sequences of up to 300 rows: 19.9 us, 24.2 over half of
 // them). A function that is not inlined: with the same lines in the kernel the code of its loop comes out slower (140 and 77).

@@ -23,7 +23,7 @@ namespace grok {
 // a maximum is one packed instruction for two features; NaNs order beyond the
 // infinities of their sign. Measured (graph replays): 8192 rows of a prompt, 16.8 MB, 5.5
 // us, which is the launch, the table's and the keys' latency and 2.5 us of HBM; the blocks
-// of a decode step, 32 sequences, 3.6 us.
+// of a decode step, 32 sequences, 4.0 us.
 constexpr int kBdThreads = 256;
 constexpr int kBdRows = kBlk / (kBdThreads / 32);  // rows per warp
 
@@ -108,7 +108,7 @@ __global__ void __launch_bounds__(kBdThreads) kv_bounds_kernel(const uint4* __re
 // over 256 codes of a block, the upper bounds against the query's positive codes and
 // the lower ones against its negative. A lane loads 16-byte words of two blocks; the order
 // of the contracted index is chosen to fit them. A warp has the next 16 blocks' codes
-// under way while it multiplies. Measured: 32 sequences of 65536 rows (68 MB of codes) 19.8
+// under way while it multiplies. Measured: 32 sequences of 65536 rows (68 MB of codes) 20.2
 // us, 3.4 TB/s, of which 3 us are the start, 13 the codes (SMs with two of the 256 CTAs
 // read 0.5 MB each, at 40 bytes a clock), 3 the choice; one of 8192 rows 5.5 us. With
 // integer products (mma s8) 22.3 us, with dp4a 32.7; with two to four CTAs to a pair,
