@@ -94,6 +94,16 @@ static EncodeTiledFn encode_fn() {
   return fn;
 }
 
+// The driver's encoder wants a context that is current in the calling thread, which a thread without any CUDA call so far
+// does not have: it gets its device's primary one then, as a kernel launch by the runtime would give it.
+template <typename Encode>
+static CUresult with_context(Encode encode) {
+  CUresult r = encode();
+  int dev = 0;
+  if (r == CUDA_ERROR_INVALID_CONTEXT && cudaGetDevice(&dev) == cudaSuccess && cudaSetDevice(dev) == cudaSuccess) r = encode();
+  return r;
+}
+
 static grok_status encode_tmap_16bit_4d(CUtensorMapDataType type, CUtensorMap* map, const void* base,
                                        const uint64_t dims[4], const uint64_t strides[3], const uint32_t box[4]) {
   EncodeTiledFn fn = encode_fn();
@@ -102,9 +112,10 @@ static grok_status encode_tmap_16bit_4d(CUtensorMapDataType type, CUtensorMap* m
   cuuint64_t gstr[3] = {strides[0], strides[1], strides[2]};
   cuuint32_t bdim[4] = {box[0], box[1], box[2], box[3]};
   cuuint32_t estr[4] = {1, 1, 1, 1};
-  CUresult r = fn(map, type, 4, const_cast<void*>(base), gdim, gstr, bdim, estr,
-                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  const CUresult r = with_context([&] {
+    return fn(map, type, 4, const_cast<void*>(base), gdim, gstr, bdim, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  });
   if (r != CUDA_SUCCESS) return fail(GROK_ERR_CUDA, "cuTensorMapEncodeTiled failed (CUresult %d)", int(r));
   return GROK_OK;
 }
@@ -127,9 +138,11 @@ grok_status encode_tmap_u8_2d(CUtensorMap* map, const void* base, const uint64_t
   cuuint64_t gstr[1] = {row_stride};
   cuuint32_t bdim[2] = {box[0], box[1]};
   cuuint32_t estr[2] = {1, 1};
-  CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), gdim, gstr, bdim, estr,
-                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  const CUresult r = with_context([&] {
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), gdim, gstr, bdim, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  });
   if (r != CUDA_SUCCESS) return fail(GROK_ERR_CUDA, "cuTensorMapEncodeTiled (uint8) failed (CUresult %d)", int(r));
   return GROK_OK;
 }
