@@ -15,7 +15,6 @@ import os
 import torch
 
 from . import HEAD_DIM, N_KV_HEADS, N_Q_HEADS, PAGE_TOKENS, SPARSE_BLOCK, _check, load
-from .build import BINDING
 from .kv8 import _call, _maybe, _need, _raw_device, _raw_stream
 
 _BF16, _F32, _I32, _I8, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.int8, torch.uint8
@@ -36,6 +35,7 @@ def _binding():
     """The extension's checks, with the library's functions."""
     global _checked
     if _checked is None:
+        from .build import BINDING  # (here: the package does not import what builds it)
         lib = load()
         if not os.path.exists(BINDING):
             _checked = _Unchecked()
